@@ -499,13 +499,14 @@ def exact(case, seed):
     y = torch.zeros(s["q"].shape, dtype=torch.float64, device="cuda")
     group = case["heads"] // case["kv"]
     for b, n in enumerate(_lens(case)):
+        first = None
         for t in range(case["cols"]):
             p = n - case["cols"] + t
             if p < 0:
                 continue
             lo = max(0, p - case["window"] + 1) if case["window"] else 0
             at = torch.arange(lo, p + 1, device="cuda")
-            if t == 0 or case["window"]:
+            if first is None or case["window"]:
                 first = lo
                 every = torch.arange(lo, n, device="cuda")
                 k, v = _token_record(case, s["pool"], table[b, every // ps], every % ps)
