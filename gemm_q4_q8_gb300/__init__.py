@@ -12,6 +12,8 @@ from __future__ import annotations
 import ctypes as C
 import os
 
+QG_F32 = 0
+QG_F16 = 1
 Q4_0 = 2
 Q8_0 = 8
 
@@ -20,7 +22,9 @@ LIB_PATH = os.path.join(_HERE, "libqgemm.so")
 
 EXPORTS = ("qg_status_str", "qgemv_q4_0", "qgemv_q8_0", "qgemm_cols", "qffn_gate_up_silu",
            "qmoe_workspace_bytes", "qmoe_experts", "qmoe_experts_noalloc", "qrepack",
-           "qargmax_f32", "qtopk_f32", "qmoe_router", "qg_kernel_launches", "qg_device_error",
+           "qargmax_f32", "qtopk_f32", "qmoe_router", "qrope_plan", "qrope",
+           "qkv_page_bytes", "qkv_append", "qkv_read", "qattn_workspace_bytes", "qattn_paged",
+           "qg_kernel_launches", "qg_device_error",
            "qg_wait_selftest", "qg_last_cuda_error", "qg_last_cuda_error_string")
 
 QG_MOE_NOALLOC_WS_BYTES = 1 << 20
@@ -44,6 +48,22 @@ class QGExpert(C.Structure):
     _fields_ = [("qg", C.c_void_p), ("sg", C.c_void_p), ("qu", C.c_void_p),
                 ("su", C.c_void_p), ("qd", C.c_void_p), ("sd", C.c_void_p)]
 
+
+class QGRope(C.Structure):
+    """A rotary plan (host memory), filled by qrope_plan."""
+    _fields_ = [("rot_dim", C.c_int32), ("interleaved", C.c_int32), ("mscale", C.c_float),
+                ("reserved", C.c_int32), ("step", C.c_uint64 * 128)]
+
+
+class QGKVCache(C.Structure):
+    """A paged key/value cache: device pointers and sizes (made by qkv_cache)."""
+    _fields_ = [("pool", C.c_void_p), ("page_table", C.c_void_p), ("type", C.c_int32),
+                ("n_kv_heads", C.c_int32), ("head_dim", C.c_int32), ("page_size", C.c_int32),
+                ("n_pages", C.c_int32), ("max_pages", C.c_int32), ("n_seq", C.c_int32)]
+
+
+# bits of the cache calls' error flag (include/qgemm.h)
+QG_KV_BAD_SEQ, QG_KV_BAD_POS, QG_KV_BAD_PAGE = 1, 2, 4
 
 _lib = None
 
@@ -75,6 +95,17 @@ def load(path: str | None = None):
     L.qargmax_f32.argtypes = [vp, i32, i32, vp, vp, vp]
     L.qtopk_f32.argtypes = [vp, i32, i32, i32, vp, vp, vp]
     L.qmoe_router.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    i64, f64 = C.c_int64, C.c_double
+    rope, cache = C.POINTER(QGRope), C.POINTER(QGKVCache)
+    L.qrope_plan.argtypes = [rope, i32, i32, f64, f64, i32, f64, f64, f64]
+    L.qrope.argtypes = [rope, i32, vp, i64, vp, i32, i32, i32, i32, vp, i64, vp]
+    L.qkv_page_bytes.argtypes = [i32, i32, i32, i32]
+    L.qkv_page_bytes.restype = sz
+    L.qkv_append.argtypes = [cache, rope, i32, vp, i64, vp, i64, vp, i64, i32, vp, vp, vp, i32, vp, vp]
+    L.qkv_read.argtypes = [cache, vp, vp, i32, i32, vp, vp, vp, vp]
+    L.qattn_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.qattn_workspace_bytes.restype = sz
+    L.qattn_paged.argtypes = [cache, vp, i32, i32, vp, i32, C.c_float, vp, vp, sz, vp, vp]
     L.qg_kernel_launches.argtypes = []
     L.qg_kernel_launches.restype = C.c_uint64
     L.qg_device_error.argtypes = [C.POINTER(C.c_int32)]
@@ -83,8 +114,8 @@ def load(path: str | None = None):
     L.qg_last_cuda_error_string.argtypes = []
     L.qg_last_cuda_error_string.restype = C.c_char_p
     for f in EXPORTS:
-        if f not in ("qg_status_str", "qmoe_workspace_bytes", "qg_kernel_launches",
-                     "qg_last_cuda_error_string"):
+        if f not in ("qg_status_str", "qmoe_workspace_bytes", "qkv_page_bytes",
+                     "qattn_workspace_bytes", "qg_kernel_launches", "qg_last_cuda_error_string"):
             getattr(L, f).restype = i32
     _lib = L
     return L
@@ -233,3 +264,140 @@ def qmoe_router(w_router, x, topk, ids_out, rw_out, logits_out=None, stream=None
     _check("qmoe_router", load().qmoe_router(_ptr(w_router), _ptr(x), n_expert, hidden, x.shape[0],
                                              int(topk), _ptr(logits_out), _ptr(ids_out),
                                              _ptr(rw_out), _stream(stream)))
+
+
+_ELEM = None
+
+
+def _elem(t, name):
+    """QG_F32 or QG_F16 of a tensor; the cache and rotary calls take nothing else."""
+    global _ELEM
+    if _ELEM is None:
+        import torch
+        _ELEM = {torch.float32: QG_F32, torch.float16: QG_F16}
+    if t.dtype not in _ELEM:
+        raise ValueError(f"{name}: float32 or float16 expected, got {t.dtype}")
+    return _ELEM[t.dtype]
+
+
+def _rows(t, name):
+    """Token stride of [ntok, heads, head_dim] whose heads are contiguous."""
+    heads, d = t.shape[1], t.shape[2]
+    s = t.stride()
+    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {s}")
+    return s[0]
+
+
+def _dense(t, name, dtype, shape):
+    """A contiguous tensor of the given type ("int32", "float16") and shape."""
+    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+        raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def _flag(t):
+    return None if t is None else _dense(t, "err_flag", "int32", t.shape if t.numel() else (1,))
+
+
+def qrope_plan(rot_dim, base=10000.0, interleaved=False, factor=1.0, orig_ctx=0, low_turns=1.0,
+               high_turns=32.0, mscale=1.0) -> QGRope:
+    """A rotary plan: pairs of the first rot_dim elements of a head turn by
+    pos * base^(-2i/rot_dim), the slow ones by 1/factor of it (all of them when
+    orig_ctx is 0). Host memory; keep it and pass it to any number of calls."""
+    plan = QGRope()
+    _check("qrope_plan", load().qrope_plan(C.byref(plan), rot_dim, int(interleaved), base, factor, orig_ctx,
+                                           low_turns, high_turns, mscale))
+    return plan
+
+
+def qrope(plan, x, pos, y, stream=None):
+    """Rotate x [ntok, heads, head_dim] (f32 or f16, any token stride) at int32
+    positions pos [ntok] into y (f32 or f16; y may be x itself)."""
+    ntok, heads, d = x.shape
+    if y.shape != x.shape:
+        raise ValueError(f"y: shape {tuple(x.shape)} expected, got {tuple(y.shape)}")
+    _check("qrope", load().qrope(plan, _elem(x, "x"), x.data_ptr(), _rows(x, "x"),
+                                 _dense(pos, "pos", "int32", (ntok,)), ntok, heads, d, _elem(y, "y"),
+                                 y.data_ptr(), _rows(y, "y"), _stream(stream)))
+
+
+def qkv_page_bytes(qtype, n_kv_heads, head_dim, page_size) -> int:
+    """Bytes of a cache page; 0 for sizes the cache does not take."""
+    return int(load().qkv_page_bytes(int(qtype), n_kv_heads, head_dim, page_size))
+
+
+def qkv_cache(qtype, pool, page_table, n_kv_heads, head_dim, page_size) -> QGKVCache:
+    """The cache over a pool (contiguous, a whole number of pages, any type) and an
+    int32 page_table [n_seq, max_pages]. It keeps both tensors alive."""
+    page = qkv_page_bytes(qtype, n_kv_heads, head_dim, page_size)
+    if page == 0:
+        raise ValueError(f"qkv_cache: no cache of type {qtype}, {n_kv_heads} heads of {head_dim}, "
+                         f"pages of {page_size}")
+    if not pool.is_contiguous() or pool.numel() * pool.element_size() % page:
+        raise ValueError(f"pool: contiguous, a multiple of {page} bytes expected")
+    c = QGKVCache(pool.data_ptr(), _dense(page_table, "page_table", "int32", page_table.shape[:2]), int(qtype),
+                  n_kv_heads, head_dim, page_size, pool.numel() * pool.element_size() // page,
+                  page_table.shape[1], page_table.shape[0])
+    c.tensors = (pool, page_table)
+    return c
+
+
+def qkv_append(cache, k, v, pos, seq=None, rope=None, q=None, q_out=None, err_flag=None, stream=None):
+    """Write k, v [ntok, n_kv_heads, head_dim] (f32 or f16, any token stride) at
+    int32 (seq, pos) [ntok]; with rope, k is rotated, and so is q [ntok, heads,
+    head_dim], which goes to q_out (f16, contiguous). seq None: the tokens are
+    the sequences' in turn, ntok / n_seq each."""
+    ntok, kind = k.shape[0], _elem(k, "k")
+    want = (ntok, cache.n_kv_heads, cache.head_dim)
+    for t, name in ((k, "k"), (v, "v")):
+        if tuple(t.shape) != want or t.dtype != k.dtype:
+            raise ValueError(f"{name}: {k.dtype} {want} expected, got {t.dtype} {tuple(t.shape)}")
+    qp = qs = qo = None
+    heads = 0
+    if q is not None:
+        heads = q.shape[1]
+        if q.dtype != k.dtype or tuple(q.shape) != (ntok, heads, cache.head_dim) or q_out is None:
+            raise ValueError(f"q: {k.dtype} {(ntok, 'heads', cache.head_dim)} and a q_out expected")
+        qp, qs, qo = q.data_ptr(), _rows(q, "q"), _dense(q_out, "q_out", "float16", q.shape)
+    _check("qkv_append",
+           load().qkv_append(cache, rope, kind, k.data_ptr(), _rows(k, "k"), v.data_ptr(), _rows(v, "v"), qp,
+                             qs or 0, heads, qo, None if seq is None else _dense(seq, "seq", "int32", (ntok,)),
+                             _dense(pos, "pos", "int32", (ntok,)), ntok, _flag(err_flag), _stream(stream)))
+
+
+def qkv_read(cache, pos, k_out=None, v_out=None, seq=None, err_flag=None, stream=None):
+    """Read the tokens at int32 (seq, pos) [ntok] back into k_out, v_out [ntok,
+    n_kv_heads, head_dim] (f16 or f32, contiguous; either may be None)."""
+    ntok = pos.shape[0]
+    some = k_out if k_out is not None else v_out
+    if some is None:
+        return
+    kind, name = _elem(some, "k_out / v_out"), str(some.dtype)[6:]
+    want = (ntok, cache.n_kv_heads, cache.head_dim)
+    _check("qkv_read",
+           load().qkv_read(cache, None if seq is None else _dense(seq, "seq", "int32", (ntok,)),
+                           _dense(pos, "pos", "int32", (ntok,)), ntok, kind,
+                           None if k_out is None else _dense(k_out, "k_out", name, want),
+                           None if v_out is None else _dense(v_out, "v_out", name, want), _flag(err_flag),
+                           _stream(stream)))
+
+
+def qattn_workspace_bytes(cache, n_heads, ncols) -> int:
+    """Workspace bytes of qattn_paged over this cache; 0 for a shape it rejects."""
+    return int(load().qattn_workspace_bytes(cache.n_seq, n_heads, cache.n_kv_heads, cache.head_dim, ncols))
+
+
+def qattn_paged(cache, q, lens, y, ws, scale=None, window=0, err_flag=None, stream=None):
+    """Attention of q f16 [n_seq, ncols, heads, head_dim], the last ncols tokens of
+    each sequence, over the cached tokens of lens int32 [n_seq] (the new ones
+    among them), causal, within `window` tokens if it is not 0; y f16 as q. scale
+    None: 1 / sqrt(head_dim)."""
+    n, ncols, heads, d = q.shape
+    if n != cache.n_seq or d != cache.head_dim:
+        raise ValueError(f"q: [{cache.n_seq}, ncols, heads, {cache.head_dim}] expected, got {tuple(q.shape)}")
+    _check("qattn_paged",
+           load().qattn_paged(cache, _dense(q, "q", "float16", q.shape), heads, ncols,
+                              _dense(lens, "lens", "int32", (n,)), window, d ** -0.5 if scale is None else scale,
+                              _dense(y, "y", "float16", q.shape), ws.data_ptr(), ws.numel() * ws.element_size(),
+                              _flag(err_flag), _stream(stream)))

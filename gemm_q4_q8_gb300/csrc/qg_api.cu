@@ -5,6 +5,7 @@
 #include <stdio.h>
 
 #include <atomic>
+#include <cmath>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -12,6 +13,7 @@
 #include <utility>
 
 #include "qg_internal.h"
+#include "qg_kv.cuh"
 #include "qgemm.h"
 
 namespace qg {
@@ -149,6 +151,36 @@ qg_status check_matmul(int t, const void* q, const uint16_t* scl, int rows, int 
   return QG_OK;
 }
 
+// Token rows of the rotary and cache calls: ntok rows of `row` elements, `stride` apart.
+bool float_type(int t) { return t == QG_F32 || t == QG_F16; }
+bool rows_ok(int ntok, int64_t row, int64_t stride) {
+  return ntok <= 1 || (stride >= row && stride <= ((int64_t)1 << 40) / ntok);
+}
+size_t rows_bytes(int ntok, int64_t row, int64_t stride, int t) {
+  return ((size_t)(ntok - 1) * (ntok > 1 ? stride : 0) + row) * (t == QG_F32 ? 4 : 2);
+}
+bool plan_ok(const qg_rope* p) {
+  return p->rot_dim >= 2 && p->rot_dim <= QG_ROPE_MAX_DIM && (p->rot_dim & 1) == 0;
+}
+qg_status kv_shape(int type, int n_kv_heads, int head_dim, int page_size) {
+  if (type != QG_F16 && type != QG_Q8_0) return QG_ERR_TYPE;
+  if (n_kv_heads < 1 || n_kv_heads > 256 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
+      page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
+    return QG_ERR_SHAPE;
+  return QG_OK;
+}
+qg_status check_cache(const qg_kvcache* c) {
+  if (!c) return QG_ERR_NULL;
+  const qg_status st = kv_shape(c->type, c->n_kv_heads, c->head_dim, c->page_size);
+  if (st != QG_OK) return st;
+  if (c->n_pages < 1 || c->n_seq < 1 || c->n_seq > QG_KV_MAX_SEQ || c->max_pages < 1 ||
+      (int64_t)c->max_pages * c->page_size >= ((int64_t)1 << 31))
+    return QG_ERR_SHAPE;
+  if (!c->pool || !c->page_table) return QG_ERR_NULL;
+  if (!aligned(c->pool, 16) || !aligned(c->page_table, 4)) return QG_ERR_ALIGN;
+  return QG_OK;
+}
+
 // Device readiness (a device must be present and current).
 qg_status check_device() {
   int dev = 0;
@@ -202,11 +234,11 @@ const char* qg_status_str(qg_status s) {
     case QG_OK: return "ok";
     case QG_ERR_NULL: return "a required pointer is NULL";
     case QG_ERR_SHAPE: return "invalid shape (k must be a positive multiple of 32; rows >= 0; ncols/topk/n_expert in range)";
-    case QG_ERR_ALIGN: return "misaligned pointer (quants, scales, x: 16 bytes; y, y0: 4 bytes; h: 2 bytes)";
-    case QG_ERR_TYPE: return "unknown quant type (expected Q4_0=2 or Q8_0=8)";
-    case QG_ERR_WORKSPACE: return "workspace missing or smaller than qmoe_workspace_bytes()";
+    case QG_ERR_ALIGN: return "misaligned pointer or stride (quants, scales, x: 16 bytes; y, y0: 4 bytes; h: 2 bytes)";
+    case QG_ERR_TYPE: return "a type the call does not take (weights: Q4_0=2 or Q8_0=8)";
+    case QG_ERR_WORKSPACE: return "workspace missing or smaller than the call's workspace_bytes()";
     case QG_ERR_CUDA: return "CUDA runtime error";
-    case QG_ERR_ALIAS: return "y0 partially overlaps y";
+    case QG_ERR_ALIAS: return "an input partially overlaps the output (such as y0 and y)";
   }
   return "unknown status";
 }
@@ -344,6 +376,183 @@ qg_status qrepack(qg_type t, const void* gguf, int rows, int k, void* q_out,
   qg_status st = check_device();
   if (st != QG_OK) return st;
   return from_cuda(qg::repack_launch((int)t, gguf, rows, k, q_out, scl_out, stream));
+}
+
+qg_status qrope_plan(qg_rope* plan, int rot_dim, int interleaved, double base, double factor,
+                     int orig_ctx, double low_turns, double high_turns, double mscale) {
+  if (!plan) return QG_ERR_NULL;
+  const double pi2 = 6.283185307179586476925;
+  if (rot_dim < 2 || rot_dim > QG_ROPE_MAX_DIM || (rot_dim & 1) || !(base > 0) || !std::isfinite(base) ||
+      !(factor > 0) || !std::isfinite(factor) || orig_ctx < 0 || !std::isfinite(mscale) ||
+      !std::isfinite((double)(float)mscale))
+    return QG_ERR_SHAPE;
+  if (orig_ctx > 0 &&
+      (!std::isfinite(low_turns) || !std::isfinite(high_turns) || !(high_turns > low_turns)))
+    return QG_ERR_SHAPE;
+  qg_rope p{};
+  p.rot_dim = rot_dim;
+  p.interleaved = interleaved != 0;
+  p.mscale = (float)mscale;
+  for (int i = 0; i < rot_dim / 2; ++i) {
+    double theta = std::pow(base, -2.0 * i / rot_dim);
+    if (factor != 1.0) {
+      double keep = 0.0;
+      if (orig_ctx > 0) {
+        keep = (orig_ctx * theta / pi2 - low_turns) / (high_turns - low_turns);
+        keep = keep < 0 ? 0 : keep > 1 ? 1 : keep;
+      }
+      theta = theta * keep + theta / factor * (1 - keep);
+    }
+    double turns = theta / pi2;
+    if (!std::isfinite(turns)) return QG_ERR_SHAPE;
+    turns -= std::floor(turns);  // whole turns do nothing
+    if (turns >= 1.0) turns = 0.0;
+    p.step[i] = (uint64_t)std::ldexp(turns, 64);
+  }
+  *plan = p;
+  return QG_OK;
+}
+
+qg_status qrope(const qg_rope* plan, qg_type xt, const void* x, int64_t x_stride,
+                const int32_t* pos, int ntok, int n_heads, int head_dim, qg_type yt, void* y,
+                int64_t y_stride, cudaStream_t stream) {
+  if (!float_type((int)xt) || !float_type((int)yt)) return QG_ERR_TYPE;
+  if (!plan) return QG_ERR_NULL;
+  if (!plan_ok(plan) || ntok < 0 || n_heads < 1 || n_heads > (1 << 20) || head_dim < 8 ||
+      head_dim > 256 || (head_dim % 8) || plan->rot_dim > head_dim)
+    return QG_ERR_SHAPE;
+  if (ntok == 0) return QG_OK;
+  const int64_t row = (int64_t)n_heads * head_dim;
+  if (!rows_ok(ntok, row, x_stride) || !rows_ok(ntok, row, y_stride)) return QG_ERR_SHAPE;
+  if (!x || !y || !pos) return QG_ERR_NULL;
+  if (!aligned(x, 16) || !aligned(y, 16) || !aligned(pos, 4) || (ntok > 1 && (x_stride % 8 || y_stride % 8)))
+    return QG_ERR_ALIGN;
+  const size_t xb = rows_bytes(ntok, row, x_stride, (int)xt), yb = rows_bytes(ntok, row, y_stride, (int)yt);
+  const bool in_place = x == y && xt == yt && (ntok == 1 || x_stride == y_stride);
+  if ((!in_place && overlaps(x, xb, y, yb)) || overlaps(pos, (size_t)ntok * 4, y, yb)) return QG_ERR_ALIAS;
+  qg_status st = check_device();
+  if (st != QG_OK) return st;
+  return from_cuda(qg::rope_launch(*plan, (int)xt, x, x_stride, pos, ntok, n_heads, head_dim, (int)yt, y,
+                                   y_stride, stream));
+}
+
+size_t qkv_page_bytes(qg_type type, int n_kv_heads, int head_dim, int page_size) {
+  if (kv_shape((int)type, n_kv_heads, head_dim, page_size) != QG_OK) return 0;
+  return qg::kv_page_bytes((int)type, n_kv_heads, head_dim, page_size);
+}
+
+qg_status qkv_append(const qg_kvcache* cache, const qg_rope* rope, qg_type xt, const void* k,
+                     int64_t k_stride, const void* v, int64_t v_stride, const void* q,
+                     int64_t q_stride, int n_q_heads, uint16_t* q_out, const int32_t* seq,
+                     const int32_t* pos, int ntok, int32_t* err_flag, cudaStream_t stream) {
+  qg_status st = check_cache(cache);
+  if (st != QG_OK) return st;
+  if (!float_type((int)xt)) return QG_ERR_TYPE;
+  if (ntok < 0 || (rope && (!plan_ok(rope) || rope->rot_dim > cache->head_dim)) ||
+      (q && (n_q_heads < 1 || n_q_heads > (1 << 20))) || (!seq && ntok % cache->n_seq))
+    return QG_ERR_SHAPE;
+  if (ntok == 0) return QG_OK;
+  const int64_t row = (int64_t)cache->n_kv_heads * cache->head_dim;
+  const int64_t qrow = q ? (int64_t)n_q_heads * cache->head_dim : 0;
+  if (!rows_ok(ntok, row, k_stride) || !rows_ok(ntok, row, v_stride) || (q && !rows_ok(ntok, qrow, q_stride)))
+    return QG_ERR_SHAPE;
+  if (!k || !v || !pos || (q && !q_out)) return QG_ERR_NULL;
+  if (!aligned(k, 16) || !aligned(v, 16) || !aligned(pos, 4) || !aligned(seq, 4) || !aligned(err_flag, 4) ||
+      (q && (!aligned(q, 16) || !aligned(q_out, 16))) ||
+      (ntok > 1 && (k_stride % 8 || v_stride % 8 || (q && q_stride % 8))))
+    return QG_ERR_ALIGN;
+  // what is written (q_out, the pool) must not be read: queries, keys, values, positions, table
+  struct Range { const void* p; size_t n; };
+  const Range in[] = {{k, rows_bytes(ntok, row, k_stride, (int)xt)},
+                      {v, rows_bytes(ntok, row, v_stride, (int)xt)},
+                      {q, q ? rows_bytes(ntok, qrow, q_stride, (int)xt) : 0},
+                      {pos, (size_t)ntok * 4},
+                      {seq, seq ? (size_t)ntok * 4 : 0},
+                      {cache->page_table, (size_t)cache->n_seq * cache->max_pages * 4}};
+  const Range out[] = {{q ? q_out : nullptr, q ? (size_t)ntok * qrow * 2 : 0},
+                       {cache->pool, (size_t)cache->n_pages * qg::kv_page_bytes(cache->type, cache->n_kv_heads,
+                                                                                cache->head_dim, cache->page_size)}};
+  for (const Range& o : out)
+    for (const Range& i : in)
+      if (o.n && i.n && overlaps(o.p, o.n, i.p, i.n)) return QG_ERR_ALIAS;
+  if (out[0].n && overlaps(out[0].p, out[0].n, out[1].p, out[1].n)) return QG_ERR_ALIAS;
+  if ((st = check_device()) != QG_OK) return st;
+  qg::KvAppendArgs a{};
+  a.c = *cache;
+  a.rope = rope;
+  a.xt = (int)xt;
+  a.q = q; a.k = k; a.v = v;
+  a.qs = q_stride; a.ks = k_stride; a.vs = v_stride;
+  a.n_q = q ? n_q_heads : 0;
+  a.q_out = q_out;
+  a.seq = seq; a.pos = pos; a.ntok = ntok;
+  a.err = err_flag;
+  return from_cuda(qg::kv_append_launch(a, stream));
+}
+
+qg_status qkv_read(const qg_kvcache* cache, const int32_t* seq, const int32_t* pos, int ntok,
+                   qg_type yt, void* k_out, void* v_out, int32_t* err_flag, cudaStream_t stream) {
+  qg_status st = check_cache(cache);
+  if (st != QG_OK) return st;
+  if (!float_type((int)yt)) return QG_ERR_TYPE;
+  if (ntok < 0 || (!seq && ntok % cache->n_seq)) return QG_ERR_SHAPE;
+  if (ntok == 0 || (!k_out && !v_out)) return QG_OK;
+  if (!pos) return QG_ERR_NULL;
+  if (!aligned(pos, 4) || !aligned(seq, 4) || !aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(err_flag, 4))
+    return QG_ERR_ALIGN;
+  const size_t nb = rows_bytes(ntok, (int64_t)cache->n_kv_heads * cache->head_dim,
+                               (int64_t)cache->n_kv_heads * cache->head_dim, (int)yt);
+  const size_t pool = (size_t)cache->n_pages *
+                      qg::kv_page_bytes(cache->type, cache->n_kv_heads, cache->head_dim, cache->page_size);
+  const size_t table = (size_t)cache->n_seq * cache->max_pages * 4;
+  if (k_out && v_out && overlaps(k_out, nb, v_out, nb)) return QG_ERR_ALIAS;
+  for (const void* o : {(const void*)k_out, (const void*)v_out})
+    if (o && (overlaps(o, nb, cache->pool, pool) || overlaps(o, nb, pos, (size_t)ntok * 4) ||
+              (seq && overlaps(o, nb, seq, (size_t)ntok * 4)) || overlaps(o, nb, cache->page_table, table)))
+      return QG_ERR_ALIAS;
+  if ((st = check_device()) != QG_OK) return st;
+  return from_cuda(qg::kv_read_launch(*cache, seq, pos, ntok, (int)yt, k_out, v_out, err_flag, stream));
+}
+
+size_t qattn_workspace_bytes(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols) {
+  if (!qg::attn_shape_ok(n_seq, n_heads, n_kv_heads, head_dim, ncols)) return 0;
+  return qg::attn_ws_bytes(n_seq, n_heads, n_kv_heads, head_dim, ncols);
+}
+
+qg_status qattn_paged(const qg_kvcache* cache, const uint16_t* q, int n_heads, int ncols,
+                      const int32_t* lens, int window, float scale, uint16_t* y, void* ws,
+                      size_t ws_bytes, int32_t* err_flag, cudaStream_t stream) {
+  qg_status st = check_cache(cache);
+  if (st != QG_OK) return st;
+  if (!qg::attn_shape_ok(cache->n_seq, n_heads, cache->n_kv_heads, cache->head_dim, ncols) || window < 0 ||
+      !std::isfinite(scale))
+    return QG_ERR_SHAPE;
+  if (!q || !lens || !y) return QG_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lens, 4) || !aligned(err_flag, 4)) return QG_ERR_ALIGN;
+  const size_t need = qg::attn_ws_bytes(cache->n_seq, n_heads, cache->n_kv_heads, cache->head_dim, ncols);
+  if (!ws || ws_bytes < need) return QG_ERR_WORKSPACE;
+  if (!aligned(ws, 16)) return QG_ERR_ALIGN;
+  const size_t nq = (size_t)cache->n_seq * ncols * n_heads * cache->head_dim * 2;
+  const size_t pool = (size_t)cache->n_pages *
+                      qg::kv_page_bytes(cache->type, cache->n_kv_heads, cache->head_dim, cache->page_size);
+  const size_t nl = (size_t)cache->n_seq * 4, table = nl * cache->max_pages;
+  struct Range { const void* p; size_t n; };
+  const Range in[] = {{q, nq}, {lens, nl}, {cache->pool, pool}, {cache->page_table, table}};
+  if (overlaps(ws, need, y, nq)) return QG_ERR_ALIAS;
+  for (const Range& r : in)
+    if (overlaps(r.p, r.n, y, nq) || overlaps(r.p, r.n, ws, need)) return QG_ERR_ALIAS;
+  if ((st = check_device()) != QG_OK) return st;
+  qg::AttnArgs a{};
+  a.c = *cache;
+  a.q = q;
+  a.n_heads = n_heads; a.ncols = ncols;
+  a.lens = lens;
+  a.window = window;
+  a.scale = scale;
+  a.y = y;
+  a.ws = ws;
+  a.err = err_flag;
+  return from_cuda(qg::attn_launch(a, stream));
 }
 
 uint64_t qg_kernel_launches(void) { return qg::g_launches.load(std::memory_order_relaxed); }

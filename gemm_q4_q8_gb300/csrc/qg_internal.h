@@ -138,4 +138,42 @@ bool router_shape_ok(int E, int hidden, int ncols, int topk);
 cudaError_t router_launch(const float* w, const uint16_t* x, int E, int hidden, int ncols,
                           int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s);
 
+// Rotary positions (qg_rope.cu). Arguments are those of the C calls, checked.
+cudaError_t rope_launch(const qg_rope& plan, int xt, const void* x, int64_t xs, const int32_t* pos,
+                        int ntok, int n_heads, int head_dim, int yt, void* y, int64_t ys,
+                        cudaStream_t s);
+
+// Paged key/value cache (qg_rope.cu: write; qg_kv.cu: read).
+struct KvAppendArgs {
+  qg_kvcache c;
+  const qg_rope* rope;  // host, or NULL
+  int xt;
+  const void *q, *k, *v;
+  int64_t qs, ks, vs;
+  int n_q;
+  uint16_t* q_out;
+  const int32_t *seq, *pos;
+  int ntok;
+  int32_t* err;
+};
+cudaError_t kv_append_launch(const KvAppendArgs& a, cudaStream_t s);
+cudaError_t kv_read_launch(const qg_kvcache& c, const int32_t* seq, const int32_t* pos, int ntok,
+                           int yt, void* k_out, void* v_out, int32_t* err, cudaStream_t s);
+
+// Attention over the paged cache (qg_attn.cu).
+struct AttnArgs {
+  qg_kvcache c;
+  const uint16_t* q;
+  int n_heads, ncols;
+  const int32_t* lens;
+  int window;
+  float scale;
+  uint16_t* y;
+  void* ws;
+  int32_t* err;
+};
+bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
+size_t attn_ws_bytes(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
+cudaError_t attn_launch(const AttnArgs& a, cudaStream_t s);
+
 }  // namespace qg

@@ -72,14 +72,16 @@ typedef enum {
   QG_OK = 0,
   QG_ERR_NULL = 1,      /* a required pointer is NULL */
   QG_ERR_SHAPE = 2,     /* k <= 0 or k % 32, rows < 0, ncols/topk/n_expert out of range */
-  QG_ERR_ALIGN = 3,     /* a pointer violates the alignment rule above */
-  QG_ERR_TYPE = 4,      /* unknown quant type */
-  QG_ERR_WORKSPACE = 5, /* workspace NULL or smaller than qmoe_workspace_bytes() */
+  QG_ERR_ALIGN = 3,     /* a pointer or stride violates the call's alignment rule */
+  QG_ERR_TYPE = 4,      /* a type the call does not take */
+  QG_ERR_WORKSPACE = 5, /* workspace NULL or smaller than the call's *_workspace_bytes() */
   QG_ERR_CUDA = 6,      /* a CUDA runtime error (launch failure, no device, ...) */
-  QG_ERR_ALIAS = 7      /* y0 partially overlaps y */
+  QG_ERR_ALIAS = 7      /* an input partially overlaps the output */
 } qg_status;
 
-typedef enum { QG_Q4_0 = 2, QG_Q8_0 = 8 } qg_type; /* GGUF type ids */
+/* GGUF type ids. Weights are Q4_0 or Q8_0; F32 and F16 are element types of the
+ * rotary and cache calls, F16 and Q8_0 the types of a key/value cache. */
+typedef enum { QG_F32 = 0, QG_F16 = 1, QG_Q4_0 = 2, QG_Q8_0 = 8 } qg_type;
 
 /* Static, NUL-terminated description of a status code. */
 const char *qg_status_str(qg_status s);
@@ -258,6 +260,173 @@ qg_status qargmax_f32(const float *x, int n, int ncols, int32_t *idx_out, float 
                       cudaStream_t stream);
 qg_status qtopk_f32(const float *x, int n, int ncols, int k, int32_t *idx_out,
                     float *val_out, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Rotary positions. A plan is host memory, filled once by qrope_plan and passed
+ * by pointer; a call copies it into its kernel's parameters, so it may be freed
+ * or changed after the call returns and calls that use it can be captured.
+ *
+ * The first rot_dim elements of a head form rot_dim / 2 pairs. Pair i is
+ * (x[i], x[i + rot_dim/2]) in the half layout and (x[2i], x[2i + 1]) in the
+ * interleaved one; at position p it turns by the angle p * theta_i:
+ *   (u, v) -> mscale * (u cos - v sin, u sin + v cos).
+ * The other elements of the head are copied.
+ *   theta_i = base^(-2i / rot_dim), then scaled for long contexts when
+ *   factor != 1: with n_i = orig_ctx * theta_i / (2 pi), the turns that pair i
+ *   makes over the original context, and
+ *   keep_i = clamp((n_i - low_turns) / (high_turns - low_turns), 0, 1),
+ *   theta_i <- theta_i * keep_i + theta_i / factor * (1 - keep_i).
+ *   orig_ctx == 0: every pair alike (keep_i = 0, plain position interpolation;
+ *   low_turns and high_turns are then ignored).
+ * Angles are exact for any int32 position: the plan holds theta_i in turns as
+ * a 64-bit fixed-point fraction, and the kernel multiplies it by the position
+ * modulo one turn. Sine, cosine and the rotation are f32.
+ *   rot_dim : even, 2..256;  base > 0;  factor > 0;  orig_ctx >= 0;
+ *   high_turns > low_turns when orig_ctx > 0; all finite (else QG_ERR_SHAPE).
+ * ------------------------------------------------------------------------- */
+#define QG_ROPE_MAX_DIM 256
+
+typedef struct qg_rope {
+  int32_t rot_dim;
+  int32_t interleaved; /* 0: half layout */
+  float mscale;
+  int32_t reserved;
+  uint64_t step[QG_ROPE_MAX_DIM / 2]; /* turns per position, times 2^64 */
+} qg_rope;
+
+qg_status qrope_plan(qg_rope *plan, int rot_dim, int interleaved, double base, double factor,
+                     int orig_ctx, double low_turns, double high_turns, double mscale);
+
+/* Rotate n_heads heads of ntok tokens.
+ *   x   : xt (QG_F32 or QG_F16), token t's heads at x + t * x_stride elements,
+ *         n_heads * head_dim elements each, contiguous
+ *   pos : int32 [ntok], any value
+ *   y   : yt (QG_F32 or QG_F16), token t's heads at y + t * y_stride
+ *   head_dim : a multiple of 8, <= 256, >= rot_dim; ntok >= 0; n_heads >= 1;
+ *         strides >= n_heads * head_dim (ignored when ntok <= 1).
+ *   x and y 16-byte aligned, strides multiples of 8 elements (QG_ERR_ALIGN).
+ *   y == x is allowed when xt == yt and the strides are equal (in place); any
+ *   other overlap is QG_ERR_ALIAS. */
+qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride,
+                const int32_t *pos, int ntok, int n_heads, int head_dim, qg_type yt, void *y,
+                int64_t y_stride, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Paged key/value cache ("Architecture", section "Memory and caching": the KV
+ * cache is f16 or int8). A pool of pages of page_size tokens; a page holds the
+ * keys and values of all n_kv_heads heads of one layer. page_table[s][j] is the
+ * pool index of the page with tokens j * page_size ... of sequence s.
+ *
+ * Pool bytes: [n_pages][n_kv_heads][page_size / 16] records, one for each group
+ * of 16 consecutive tokens of a head; a record is its key half, then its value
+ * half. D = head_dim:
+ *   QG_F16  half: f16 [D/32][16 tokens][32]                     (32 D bytes)
+ *   QG_Q8_0 half: [D/32][16 tokens][32] quants, stored as q + 128 (unsigned),
+ *           then f16 scales [D/32][16], token i of the group at place
+ *           4 * (i mod 4) + i / 4                               (17 D bytes)
+ * Q8_0 blocks (32 elements of one token's head, value q * d): d is
+ * max |x| / 127 rounded up to f16 (at most 65504), q the integer nearest to
+ * x / d (ties to even, within +-127). A block with a NaN or an infinity gets
+ * d = NaN, so that it is not silently lost.
+ *   type       : QG_F16 or QG_Q8_0 (QG_ERR_TYPE)
+ *   n_kv_heads : 1..256; head_dim: 64, 128 or 256; page_size: 16, 32, 64, 128
+ *                or 256; n_pages >= 1; n_seq: 1..1024; max_pages >= 1, with
+ *                max_pages * page_size < 2^31 (QG_ERR_SHAPE)
+ *   pool       : device, 16-byte aligned, n_pages * qkv_page_bytes(...) bytes
+ *   page_table : device int32 [n_seq][max_pages]. Only the entries of tokens
+ *                that a call touches are read.
+ * The struct is host memory, read during the call.
+ * What only the device can check is checked there: a sequence outside
+ * [0, n_seq), a position at or past max_pages * page_size, a page outside
+ * [0, n_pages) in the entry of a token that is used. Such a token is skipped
+ * (not written; read as zeros; not attended to) and the bit below is ORed into
+ * *err_flag (device int32 or NULL; the library never clears it).
+ * ------------------------------------------------------------------------- */
+typedef struct qg_kvcache {
+  void *pool;
+  const int32_t *page_table;
+  int32_t type; /* qg_type */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t n_pages;
+  int32_t max_pages;
+  int32_t n_seq;
+} qg_kvcache;
+
+#define QG_KV_BAD_SEQ 1
+#define QG_KV_BAD_POS 2
+#define QG_KV_BAD_PAGE 4
+#define QG_KV_MAX_SEQ 1024
+
+/* Bytes of one page; 0 for arguments that the calls below reject. */
+size_t qkv_page_bytes(qg_type type, int n_kv_heads, int head_dim, int page_size);
+
+/* Write the keys and values of ntok tokens into the cache, and rotate the
+ * queries of the same tokens in the same launch.
+ *   rope : host plan applied to k and q, or NULL (no rotation)
+ *   xt   : QG_F32 or QG_F16, the type of q, k and v
+ *   k, v : [ntok] tokens of n_kv_heads * head_dim contiguous elements, token t
+ *          at k + t * k_stride (elements). A fused QKV projection's output rows
+ *          are passed as three pointers with one stride.
+ *   q    : NULL, or the tokens' n_q_heads * head_dim query elements; then
+ *   q_out: f16 [ntok][n_q_heads][head_dim], written (rotated, rounded to f16).
+ *          It must not overlap the inputs (QG_ERR_ALIAS).
+ *   seq  : int32 [ntok] or NULL: then ntok is a multiple of n_seq and token t
+ *          belongs to sequence t / (ntok / n_seq)
+ *   pos  : int32 [ntok]. A negative position marks padding: nothing is written
+ *          to the cache (its query is rotated all the same).
+ * Two tokens of one call with the same sequence and position leave either's
+ * bytes. Other slots of the pool keep theirs. Pointers 16-byte aligned, strides
+ * multiples of 8 elements; pos, seq 4-byte aligned. */
+qg_status qkv_append(const qg_kvcache *cache, const qg_rope *rope, qg_type xt, const void *k,
+                     int64_t k_stride, const void *v, int64_t v_stride, const void *q,
+                     int64_t q_stride, int n_q_heads, uint16_t *q_out, const int32_t *seq,
+                     const int32_t *pos, int ntok, int32_t *err_flag, cudaStream_t stream);
+
+/* Read tokens back: k_out, v_out [ntok][n_kv_heads][head_dim] of type yt
+ * (QG_F16 or QG_F32; f16 rounds q * d once). Keys come as stored (rotated).
+ * seq, pos as in qkv_append; padding and skipped tokens give zeros. k_out and
+ * v_out may each be NULL (not wanted), 16-byte aligned. */
+qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *pos, int ntok,
+                   qg_type yt, void *k_out, void *v_out, int32_t *err_flag,
+                   cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Attention of new tokens over the paged cache ("Engine and kernels", section
+ * "Kernel families": attention split over the context): for every sequence s,
+ * column c < ncols and query head h, with L = lens[s] (the cached tokens, the
+ * ncols new ones included) and p = L - ncols + c the column's own position,
+ *   y[s][c][h] = sum_j w_j V_j,  w = softmax_j(scale * q[s][c][h] . K_j)
+ * over the tokens j <= p of the sequence, of kv head h / (n_heads / n_kv_heads),
+ * and j > p - window when window > 0. A row without a token (p < 0, or
+ * all its pages bad) gives zeros. ncols == 1 is decode, 2..16 speculative verify.
+ *   q     : f16 [n_seq][ncols][n_heads][head_dim], 16-byte aligned
+ *   lens  : device int32 [n_seq]; 0 is an empty sequence. A negative length or
+ *           one past max_pages * page_size sets QG_KV_BAD_POS; a negative one
+ *           counts as 0, of a long one the tokens past the table do not exist.
+ *   n_heads: a multiple of n_kv_heads, at most 64 per kv head; ncols: 1..16
+ *   scale : finite (QG_ERR_SHAPE otherwise)
+ *   y     : f16 [n_seq][ncols][n_heads][head_dim], 16-byte aligned
+ *   ws    : device workspace of at least qattn_workspace_bytes(...) bytes,
+ *           16-byte aligned; its contents on entry are ignored.
+ * Tokens that a row does not see (padding of the last page, later columns,
+ * outside the window) have no effect on it, whatever their bytes hold.
+ * Scores, softmax sums and the weighted sum are f32; a weight (times the
+ * block's scale for Q8_0) is rounded to f16 before it meets its value, and y
+ * is rounded to f16 once. Results are the same from run to run; the order of
+ * the sums depends on lens, so a column of a wider call need not equal the
+ * one-column call bit for bit.
+ * ------------------------------------------------------------------------- */
+#define QG_ATTN_MAX_COLS 16
+#define QG_ATTN_MAX_GROUP 64
+
+/* Workspace bytes; 0 for a shape that qattn_paged rejects with QG_ERR_SHAPE. */
+size_t qattn_workspace_bytes(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
+
+qg_status qattn_paged(const qg_kvcache *cache, const uint16_t *q, int n_heads, int ncols,
+                      const int32_t *lens, int window, float scale, uint16_t *y, void *ws,
+                      size_t ws_bytes, int32_t *err_flag, cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Diagnostics: number of kernels this library has launched in this process
