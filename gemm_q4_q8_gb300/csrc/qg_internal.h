@@ -175,5 +175,7 @@ struct AttnArgs {
 bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
 size_t attn_ws_bytes(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
 cudaError_t attn_launch(const AttnArgs& a, cudaStream_t s);
+// The attention kernel's device error word (QG_DEV_ERR_WAIT), read and cleared.
+cudaError_t attn_device_error(int32_t* bits);
 
 }  // namespace qg

@@ -727,6 +727,8 @@ extern "C" qg_status qg_device_error(int32_t* bits_out) {
   if (cudaMemcpyToSymbol(qg::g_tc_error, &zero, sizeof(zero)) != cudaSuccess) return QG_ERR_CUDA;
   int32_t m = 0;
   if (qg::moe_device_error(&m) != cudaSuccess) return QG_ERR_CUDA;
-  *bits_out = v | m;
+  int32_t at = 0;
+  if (qg::attn_device_error(&at) != cudaSuccess) return QG_ERR_CUDA;
+  *bits_out = v | m | at;
   return QG_OK;
 }
