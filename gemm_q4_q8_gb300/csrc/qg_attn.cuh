@@ -1,0 +1,929 @@
+// qg_attn.cuh -- attention of new tokens over the paged key/value cache
+// (qattn_paged): the kernel templates. Each head size is a translation unit
+// (qg_attn_64.cu ...); qg_attn.cu picks one.
+//
+// Mathematics. For a row (a query of one column and head) with scores s_j over
+// the tokens it sees, y = sum_j 2^(s_j - z) V_j / sum_j 2^(s_j - z) for any z,
+// scores in units of log 2. A run of tokens is summed with a reference z of its
+// own; two runs are joined by scaling each with 2^(z_run - z_both). So the tokens
+// may be cut into runs anywhere, and every byte of the cache is read once. z need
+// not be the maximum: it moves up to it only when a score passes z by more than 8
+// (weights then stay below 2^8, in the middle of f16), which is rare after the
+// first tokens, so most steps have no maximum to find and nothing to rescale.
+//
+// Work. The rows of one kv head (all its query heads, all columns; 8 NT to a
+// tile) share its keys and values. An item is a (sequence, kv head, row tile);
+// its tokens come in units of 64 (four warps x a record of 16 tokens). All
+// items' units in a row are cut into equal runs, one for each CTA of a grid that
+// fills the machine once, so a batch of ragged lengths and one very long sequence
+// load every SM alike. A CTA that covers an item whole writes y; where an item is
+// cut, each CTA writes its sum, reference and weight to the workspace, and a
+// second kernel joins them in CTA order. The cuts depend on lens and the shape
+// alone, and so do the results.
+//
+// Inside a CTA each warp is on its own: it has a ring of shared-memory slots,
+// fetches the key half and the value half of its records with bulk copies (one
+// lane for each, a slot refilled as soon as it is consumed), and keeps z, the sum
+// of weights and its accumulator in registers. The four warps meet only at the
+// end of an item. Page numbers of 32 steps are loaded by the 32 lanes at once, a
+// batch ahead.
+//
+// Products (mma m16n8k16, f16 in, f32 sums). Tokens and dimensions take the
+// 16-wide side, the rows the 8-wide one: the usual 1 to 8 query heads of a kv
+// head fill it, the keys and values are unpacked once for all row tiles, and the
+// accumulator is a fourth of D x rows registers. Scores: A = K, B = Q; the 32
+// dimensions of a block are given to the four lanes of a quad as 8 neighbouring
+// ones each, the same in A and B, so a lane's operands are one load. Values: A =
+// V^T, B = weights; the weights come out of the first product with tokens along
+// the lanes' rows and are turned by movmatrix, V's pairs of tokens are put
+// together by byte permutation after plain row loads.
+//
+// Q8_0: quants are stored as u = q + 128. As the low byte of an f16, u is the
+// subnormal u 2^-24, exact on the tensor cores, so K needs one byte permutation
+// for two elements: sum_d Q_d q_d = sum_d Q_d u_d - 128 sum_d Q_d, the last
+// term being the initial accumulator. A block's sum is then multiplied by its
+// scale in f32. V's u becomes the f16 integer q (exponent trick, exact), and the
+// block's scale is multiplied into the f32 weight before the weight is rounded
+// to f16 (so V itself is never rounded); a power of two that follows the largest
+// scale seen keeps that product in the normal range of f16.
+#pragma once
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qg_async.cuh"
+#include "qg_common.cuh"
+#include "qg_internal.h"
+#include "qg_kv.cuh"
+#include "qg_mma.cuh"
+
+namespace qg {
+
+// The device error word of this translation unit's kernels (QG_DEV_ERR_WAIT).
+static __device__ int32_t g_attn_error;
+
+namespace {
+
+constexpr int AT_WARPS = 4;
+constexpr int AT_THREADS = AT_WARPS * 32;
+constexpr int AT_UNIT = AT_WARPS * KV_GROUP;  // tokens of a unit
+constexpr int AT_SMS = 152;
+// An item's end (four warps' sums joined, the next queries loaded) costs a warp about as much as
+// this many units, and the runs are cut as if it were that many more.
+constexpr int AT_PAD = 2;
+constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
+
+template <int TYPE, int D, int NT>
+struct AttnCfg {
+  static constexpr int ROWS = 8 * NT;
+  static constexpr int NB = D / 32;
+  static constexpr int ACC = NT * D / 4;  // accumulator registers
+  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them)
+  static constexpr int CPS = ACC <= 32 ? 4 : ACC <= 64 ? 3 : 2;
+  static constexpr int GRID = AT_SMS * CPS;
+  static constexpr int HALF = kv_half_bytes(TYPE, D);
+  static constexpr int SLOT = (HALF + 127) / 128 * 128;
+  static constexpr bool QSMEM = NT * NB > 8;  // Q fragments in shared memory, not registers
+  static constexpr int OD = NT <= 2 ? 64 : 32;  // dimensions joined at a time
+  static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
+  static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
+  static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
+  static constexpr size_t qbuf = QSMEM ? (size_t)NB * NT * (32 * 16 + 8 * 4) : 0;
+  // slots of a warp's ring: as many as leave CPS CTAs on an SM (227 KB, with 1 KB of the system's
+  // and 1 KB for up to 80 sequences a CTA), at most 8
+  static constexpr size_t room = (size_t)(227 * 1024) / CPS - 2048 - obuf - stats - qbuf - 256;
+  static constexpr int FIT = (int)(room / ((size_t)AT_WARPS * SLOT));
+  static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
+  static_assert(SLOTS >= 2, "a warp needs a slot for keys and one for values");
+  static constexpr size_t ring = (size_t)AT_WARPS * SLOTS * SLOT;
+  static constexpr size_t bars = (size_t)AT_WARPS * SLOTS * 8;
+  static size_t smem(int n_seq) {
+    return ring + obuf + stats + qbuf + bars + (size_t)(n_seq + 1) * 8 + (size_t)n_seq * 4;
+  }
+};
+
+// What a CTA tells the joining kernel about the item that its run starts in.
+struct AttnCut {
+  int32_t first;   // 1: this CTA is the second that has a part of the item (and joins for it)
+  int32_t c0, c1;  // the item's CTAs
+  int32_t seq, head, tile;
+  int32_t pad[2];
+};
+
+struct AttnWs {
+  AttnCut* cut;  // [GRID]
+  float* ml;     // [GRID][2][ROWS][2]
+  float* o;      // [GRID][2][ROWS][D]
+};
+
+struct AttnDev {
+  AttnArgs a;
+  AttnWs ws;
+  int group;    // query heads of a kv head
+  int tiles;    // row tiles of a kv head
+  float scale;  // times log2 e
+};
+
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  uint32_t d;
+  asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
+  return d;
+}
+// Transpose of an 8 x 8 matrix of f16 held by a warp, two elements of a row a lane.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+  uint32_t d;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
+  return d;
+}
+
+// The CTA whose run holds place v of n, run c being [c n / N, (c+1) n / N).
+__device__ __forceinline__ int run_of(int64_t v, int64_t n, int64_t N) { return (int)(((v + 1) * N - 1) / n); }
+
+struct SeqSpan {
+  int lo;    // first token that any row sees
+  int hi;    // one past the last
+  int unit;  // first unit
+  int n;     // units (at least one, so that every item is written by some CTA)
+};
+__device__ __forceinline__ SeqSpan span_of(const AttnArgs& a, int len) {
+  SeqSpan s;
+  const int cap = a.c.max_pages * a.c.page_size;
+  s.hi = len < cap ? len : cap;
+  const int64_t lo = (int64_t)len - a.ncols - a.window + 1;
+  s.lo = a.window > 0 && lo > 0 ? (int)lo : 0;
+  s.unit = s.lo / AT_UNIT;
+  const int end = (int)(((int64_t)s.hi + AT_UNIT - 1) / AT_UNIT);
+  s.n = end - s.unit > 1 ? end - s.unit : 1;
+  return s;
+}
+
+template <int TYPE, int D, int NT>
+__global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
+    attn_kernel(const __grid_constant__ AttnDev p) {
+  using C = AttnCfg<TYPE, D, NT>;
+  constexpr int NB = C::NB, ROWS = C::ROWS;
+  extern __shared__ __align__(128) uint8_t smem[];
+  uint8_t* const s_ring = smem;
+  float* const s_o = reinterpret_cast<float*>(smem + C::ring);
+  float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
+  uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
+  uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
+  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::SLOTS);  // units before a sequence
+  int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
+  __shared__ int64_t s_part[AT_WARPS];
+
+  const AttnArgs& a = p.a;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int g = lane >> 2, t = lane & 3;
+  pdl_trigger();
+  if (tid < AT_WARPS * C::SLOTS) {
+    mbar_init(s_bar + tid, 1);
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+  }
+  pdl_wait();
+
+  // units of every sequence, and their running sum
+  const int n_seq = a.c.n_seq;
+  {
+    const int per = (n_seq + AT_THREADS - 1) / AT_THREADS;
+    const int b0 = tid * per, b1 = min(b0 + per, n_seq);
+    const int cap = a.c.max_pages * a.c.page_size;
+    int64_t sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      int len = a.lens[b];
+      if ((len < 0 || len > cap) && blockIdx.x == 0 && a.err) atomicOr(a.err, QG_KV_BAD_POS);
+      len = max(len, 0);
+      s_len[b] = len;
+      sum += span_of(a, len).n;
+    }
+    int64_t run = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int64_t up = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += up;
+    }
+    if (lane == 31) s_part[warp] = run;
+    __syncthreads();
+    int64_t before = run - sum;
+    for (int w = 0; w < warp; ++w) before += s_part[w];
+    for (int b = b0; b < b1; ++b) {
+      s_first[b] = before;
+      before += span_of(a, s_len[b]).n;
+    }
+    if (b1 == n_seq && b0 < n_seq) s_first[n_seq] = before;
+    __syncthreads();
+  }
+  // Two numberings: units in order, u, and places in order, v, where every item has
+  // AT_PAD places behind its units. Runs are equal in places.
+  const int items = a.c.n_kv_heads * p.tiles;  // of a sequence
+  auto u_first = [&](int b) { return s_first[b] * items; };
+  auto v_first = [&](int b) { return (s_first[b] + (int64_t)b * AT_PAD) * items; };
+  const int64_t places = v_first(n_seq);
+  const int64_t N = places < C::GRID ? places : C::GRID;
+  const int cta = blockIdx.x;
+  // the first unit at or behind a place
+  auto unit_at = [&](int64_t v) {
+    int lo = 0, hi = n_seq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (v_first(mid) <= v) lo = mid; else hi = mid;
+    }
+    const int64_t n = s_first[lo + 1] - s_first[lo], rem = v - v_first(lo);
+    const int64_t it = rem / (n + AT_PAD), in = rem - it * (n + AT_PAD);
+    return u_first(lo) + it * n + (in < n ? in : n);
+  };
+  const int64_t u0 = cta < N ? unit_at(cta * places / N) : 0, u1 = cta < N ? unit_at((cta + 1) * places / N) : 0;
+  const int steps = (int)(u1 - u0);
+
+  // the sequence that holds unit u: the last whose items start at or before it
+  auto seq_of = [&](int64_t u) {
+    int lo = 0, hi = n_seq;
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (u_first(mid) <= u) lo = mid; else hi = mid;
+    }
+    return lo;
+  };
+
+  if (tid == 0) {
+    AttnCut cut{};
+    if (steps > 0) {
+      const int b = seq_of(u0);
+      const int64_t nu = s_first[b + 1] - s_first[b], rem = u0 - u_first(b);
+      const int hr = (int)(rem / nu);
+      if (hr * nu < rem) {  // the item starts in an earlier run
+        const int64_t v = v_first(b) + hr * (nu + AT_PAD);
+        cut.c0 = run_of(v, places, N);
+        cut.c1 = run_of(v + nu - 1, places, N);
+        cut.first = cta == cut.c0 + 1;
+        cut.seq = b;
+        cut.head = hr / p.tiles;
+        cut.tile = hr % p.tiles;
+      }
+    }
+    p.ws.cut[cta] = cut;
+  }
+  if (steps == 0) return;
+
+  // ------------------------------------------------------------ the ring
+  const int gpp = a.c.page_size / KV_GROUP;  // records of a page and head
+  uint8_t* const ring = s_ring + (size_t)warp * C::SLOTS * C::SLOT;
+  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::SLOTS);
+  // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
+  // so that the load has the whole batch before to arrive.
+  int nx_page = -1, nx_off = 0;
+  bool nx_in = false;
+  auto look_up = [&](int base) {
+    nx_in = false;
+    nx_page = -1;
+    if (base + lane < steps) {
+      const int64_t u = u0 + base + lane;
+      const int b = seq_of(u);
+      const int64_t nu = s_first[b + 1] - s_first[b], rem = u - u_first(b);
+      const int hr = (int)(rem / nu), un = (int)(rem - hr * nu);
+      const SeqSpan sp = span_of(a, s_len[b]);
+      const int64_t grp = (int64_t)(sp.unit + un) * AT_WARPS + warp;
+      if (grp * KV_GROUP < sp.hi && grp * KV_GROUP + KV_GROUP > sp.lo) {
+        nx_in = true;
+        nx_page = a.c.page_table[(size_t)b * a.c.max_pages + (int)(grp / gpp)];
+        nx_off = (hr / p.tiles) * gpp + (int)(grp % gpp);
+      }
+    }
+  };
+  const uint8_t* my_rec = nullptr;         // this lane's record of the batch in issue
+  uint32_t valid_even = 0, valid_odd = 0;  // steps of the even / odd batches that have a record
+  auto enter = [&](int step) {             // step: a multiple of 32
+    my_rec = nullptr;
+    if (nx_in) {
+      if (nx_page >= 0 && nx_page < a.c.n_pages)
+        my_rec = static_cast<const uint8_t*>(a.c.pool) +
+                 ((size_t)nx_page * a.c.n_kv_heads * gpp + nx_off) * (2 * C::HALF);
+      else if (a.err)
+        atomicOr(a.err, QG_KV_BAD_PAGE);
+    }
+    const uint32_t v = __ballot_sync(0xffffffffu, my_rec != nullptr);
+    if (step & 32) valid_odd = v; else valid_even = v;
+    look_up(step + 32);
+  };
+  int is_step = 0, is_v = 0, is_slot = 0;  // the next half to fetch and its slot
+  auto issue = [&]() {
+    if (is_step < steps) {
+      if (!is_v && (is_step & 31) == 0) enter(is_step);
+      if (lane == (is_step & 31) && my_rec) {
+        const uint32_t bar = bar_at + 8 * is_slot;
+        mbar_expect_tx(bar, C::HALF);
+        bulk_g2s(ring_at + is_slot * C::SLOT, my_rec + is_v * C::HALF, C::HALF, bar);
+      }
+      is_step += is_v;
+      is_v ^= 1;
+      is_slot = is_slot + 1 == C::SLOTS ? 0 : is_slot + 1;
+    }
+  };
+  __syncwarp();
+  look_up(0);
+  for (int i = 0; i < C::SLOTS; ++i) issue();
+
+  int co_slot = 0;      // the slot of the next half to consume
+  uint32_t phases = 0;  // parity of each slot's next phase
+  bool ok = true;       // false (in all lanes) once a wait gave up: no more copies, no more waits
+  auto arrived = [&]() {
+    if (ok)
+      ok = __all_sync(0xffffffffu, mbar_wait(bar_at + 8 * co_slot, (phases >> co_slot) & 1, &g_attn_error));
+    phases ^= 1u << co_slot;
+    return ring_at + co_slot * C::SLOT;
+  };
+  // The slot's reads are over: every lane orders its own before the refill.
+  auto release = [&]() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+    __syncwarp();
+    if (ok) issue();
+    co_slot = co_slot + 1 == C::SLOTS ? 0 : co_slot + 1;
+  };
+
+  // Tokens of a lane. As a row of K and of the scores: tok_a and tok_a + 8. As a
+  // column of V^T: tok_v + {0, 8} and tok_w + {0, 8}. Position i of the 16-wide side
+  // is token i/2 (i even) or 4 + x (i odd); x is chosen so that the lanes of a
+  // shared-memory phase meet no bank twice: rows of 64 bytes (f16) want neighbours of
+  // different parity, rows of 32 bytes (Q8_0) four neighbours that differ modulo 4.
+  auto odd_tok = [](int i) { return 4 + (TYPE == QG_F16 ? (i ^ 1) : ((i + 2) & 3)); };
+  const int tok_a = (g & 1) ? odd_tok(g >> 1) : g >> 1;
+  const int tok_v = t, tok_w = odd_tok(t);
+  // the two scales of a lane's tokens, out of the four with the same i mod 4
+  const uint32_t scale_at = (tok_a & 3) * 8, scale_sel = (tok_a & 4) ? 0x7632u : 0x5410u;
+
+  // --------------------------------------------------------------- items
+  const int rows = p.group * a.ncols;
+  int parity = 0;
+  int64_t u = u0;
+  int step = 0;
+  int b = seq_of(u0);
+  while (u < u1) {
+    while (u_first(b + 1) <= u) ++b;
+    const int64_t nu = s_first[b + 1] - s_first[b], base = u_first(b);
+    const int hr = (int)((u - base) / nu);
+    const int64_t i0 = base + hr * nu, i1 = i0 + nu;
+    const int64_t uend = i1 < u1 ? i1 : u1;
+    const int head = hr / p.tiles, tile = hr % p.tiles;
+    const int len = s_len[b];
+    const SeqSpan sp = span_of(a, len);
+
+    // what row r of the tile sees: tokens lo < j <= hi
+    auto row_sees = [&](int i, int& lo, int& hi) {
+      const int r = tile * ROWS + i;
+      const int64_t pos = (int64_t)len - a.ncols + r / p.group;
+      hi = r < rows ? (int)(pos < sp.hi - 1 ? pos : sp.hi - 1) : -1;
+      lo = a.window > 0 && pos - a.window > -1 ? (int)(pos - a.window) : -1;
+    };
+    // tokens that all rows see: no mask needed from `lo_all` up to `hi_all`
+    const int hi_all = (int)min((int64_t)sp.hi - 1, (int64_t)len - a.ncols);
+    const int lo_all = a.window > 0 ? (int)max((int64_t)0, (int64_t)len - a.window) : 0;
+
+    // Q: the B fragments of a block and row tile, dimensions 8t .. 8t+7 of row g; and, for
+    // Q8_0, -128 2^-24 sum of the block's queries of rows 2t and 2t + 1.
+    uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : NT][4];
+    float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][2];
+    auto load_q = [&](int blk, int nt) {
+      const int r = tile * ROWS + nt * 8 + g;
+      if (r >= rows) return make_uint4(0, 0, 0, 0);
+      return *reinterpret_cast<const uint4*>(
+          a.q + (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + 32 * blk + 8 * t);
+    };
+    auto sum_q = [&](const uint4& x) {  // of row g
+      float s = ((lo_f32(x.x) + hi_f32(x.x)) + (lo_f32(x.y) + hi_f32(x.y))) +
+                ((lo_f32(x.z) + hi_f32(x.z)) + (lo_f32(x.w) + hi_f32(x.w)));
+      s += __shfl_xor_sync(0xffffffffu, s, 1);
+      s += __shfl_xor_sync(0xffffffffu, s, 2);
+      return s * -7.62939453125e-06f;  // -128 * 2^-24
+    };
+    if constexpr (C::QSMEM) {
+      // in fragment order [block][tile][lane][4 words]; the sums by row behind them
+      for (int i = warp; i < NB * NT; i += AT_WARPS) {
+        const uint4 x = load_q(i / NT, i % NT);
+        *reinterpret_cast<uint4*>(s_q + i * 512 + lane * 16) = x;
+        if constexpr (TYPE == QG_Q8_0) {
+          const float s = sum_q(x);
+          if (t == 0) reinterpret_cast<float*>(s_q + NB * NT * 512)[i * 8 + g] = s;
+        }
+      }
+      __syncthreads();
+    } else {
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const uint4 x = load_q(blk, nt);
+          qf[blk][nt][0] = x.x; qf[blk][nt][1] = x.y; qf[blk][nt][2] = x.z; qf[blk][nt][3] = x.w;
+        }
+      if constexpr (TYPE == QG_Q8_0) {
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            const float s = sum_q(make_uint4(qf[blk][nt][0], qf[blk][nt][1], qf[blk][nt][2], qf[blk][nt][3]));
+            qc[blk][nt][0] = __shfl_sync(0xffffffffu, s, 8 * t);
+            qc[blk][nt][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+          }
+      }
+    }
+
+    // o[blk][nt][i][c]: dimension 32 blk + 4g + 2i + c/2, row 8 nt + 2t + c%2
+    float o[NB][NT][2][4];
+#pragma unroll
+    for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
+    float z[NT][2], l[NT][2];  // of rows 2t, 2t + 1: reference; sum of this lane's tokens' weights
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt) {
+      z[nt][0] = z[nt][1] = -INFINITY;
+      l[nt][0] = l[nt][1] = 0.f;
+    }
+    // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
+    // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
+    float wmul = 1.f, wmax = 0.f, wback = 1.f;
+
+    for (; u < uend; ++u, ++step) {
+      const uint32_t valid = (step & 32) ? valid_odd : valid_even;
+      if (!((valid >> (step & 31)) & 1)) {  // nothing of this record is seen, or its page is bad
+        release();
+        release();
+        continue;
+      }
+      const int tok = (int)(((int64_t)sp.unit + (u - i0)) * AT_WARPS + warp) * KV_GROUP;
+      const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
+
+      // ---- scores: s[nt][c] of token tok_a + 8 (c/2), row 8 nt + 2t + c%2
+      float s[NT][4];
+#pragma unroll
+      for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] = 0.f;
+      const uint32_t kb = arrived();
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk) {
+        uint32_t a0[4], a1[4];
+        float e0 = 0.f, e1 = 0.f;
+        if constexpr (TYPE == QG_F16) {
+          const uint32_t at = kb + blk * 1024 + tok_a * 64 + t * 16;
+          lds128(at, a0[0], a0[2], a1[0], a1[2]);
+          lds128(at + 512, a0[1], a0[3], a1[1], a1[3]);
+        } else {
+          const uint32_t at = kb + blk * 512 + tok_a * 32 + t * 8;
+          uint32_t x, y, d0, d1;
+          lds64(at, x, y);
+          a0[0] = __byte_perm(x, 0, 0x4140);
+          a0[2] = __byte_perm(x, 0, 0x4342);
+          a1[0] = __byte_perm(y, 0, 0x4140);
+          a1[2] = __byte_perm(y, 0, 0x4342);
+          lds64(at + 256, x, y);
+          a0[1] = __byte_perm(x, 0, 0x4140);
+          a0[3] = __byte_perm(x, 0, 0x4342);
+          a1[1] = __byte_perm(y, 0, 0x4140);
+          a1[3] = __byte_perm(y, 0, 0x4342);
+          lds64(kb + KV_GROUP * D + blk * 32 + scale_at, d0, d1);
+          const uint32_t d = __byte_perm(d0, d1, scale_sel);
+          e0 = lo_f32(d);
+          e1 = hi_f32(d);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t q[4];
+          if constexpr (C::QSMEM) {
+            lds128(smem_u32(s_q) + (blk * NT + nt) * 512 + lane * 16, q[0], q[1], q[2], q[3]);
+          } else {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) q[i] = qf[blk][nt][i];
+          }
+          if constexpr (TYPE == QG_F16) {
+            mma16816_acc(s[nt], a0, q[0], q[1]);
+            mma16816_acc(s[nt], a1, q[2], q[3]);
+          } else {
+            float c0, c1;
+            if constexpr (C::QSMEM) {
+              const float2 c = *reinterpret_cast<const float2*>(s_q + NB * NT * 512 + ((blk * NT + nt) * 8 + 2 * t) * 4);
+              c0 = c.x;
+              c1 = c.y;
+            } else {
+              c0 = qc[blk][nt][0];
+              c1 = qc[blk][nt][1];
+            }
+            float part[4] = {c0, c1, c0, c1};
+            mma16816_acc(part, a0, q[0], q[1]);
+            mma16816_acc(part, a1, q[2], q[3]);
+            s[nt][0] = fmaf(part[0], e0, s[nt][0]);
+            s[nt][1] = fmaf(part[1], e0, s[nt][1]);
+            s[nt][2] = fmaf(part[2], e1, s[nt][2]);
+            s[nt][3] = fmaf(part[3], e1, s[nt][3]);
+          }
+        }
+      }
+      release();
+
+      // ---- weights
+      const float mul = TYPE == QG_F16 ? p.scale : p.scale * 16777216.f;  // Q8_0: u was u 2^-24
+      if (masked) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            int lo, hi;
+            row_sees(nt * 8 + 2 * t + c, lo, hi);
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              const int at = tok + tok_a + 8 * i;
+              float& x = s[nt][2 * i + c];
+              x = at <= hi && at > lo ? x * mul : -INFINITY;
+            }
+          }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] *= mul;
+      }
+      bool up = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][2 + c]) > z[nt][c] + AT_SLACK;
+      if (__any_sync(0xffffffffu, up)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float f[2];
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            float x = fmaxf(s[nt][c], s[nt][2 + c]);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            f[c] = x > z[nt][c] ? ex2(z[nt][c] - x) : 1.f;
+            z[nt][c] = fmaxf(z[nt][c], x);
+            l[nt][c] *= f[c];
+          }
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              o[blk][nt][i][0] *= f[0];
+              o[blk][nt][i][1] *= f[1];
+              o[blk][nt][i][2] *= f[0];
+              o[blk][nt][i][3] *= f[1];
+            }
+        }
+      }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          // a row that has seen nothing has z = -inf and scores of -inf only (or NaN)
+          const float zz = z[nt][c] == -INFINITY ? 0.f : z[nt][c];
+          s[nt][c] = ex2(s[nt][c] - zz);
+          s[nt][2 + c] = ex2(s[nt][2 + c] - zz);
+          l[nt][c] += s[nt][c] + s[nt][2 + c];
+        }
+
+      // ---- weights times values
+      const uint32_t vb = arrived();
+      uint8_t* const vp = ring + co_slot * C::SLOT;
+      if constexpr (TYPE == QG_F16) {
+        if (masked) {
+          // Zero weights do not silence a NaN or an infinity in the product. So the rows of tokens that no
+          // query row sees are cleared, and values that are not finite are taken out here and added, to the
+          // rows that see them.
+          uint32_t odd = 0;  // tokens with such values
+          for (int i = lane; i < KV_GROUP * D / 8; i += 32) {
+            uint4* at = reinterpret_cast<uint4*>(vp) + i;
+            const int tk = tok + ((i >> 2) & 15);
+            if (tk >= sp.hi || tk < sp.lo) {
+              *at = make_uint4(0, 0, 0, 0);
+            } else {
+              const uint4 w = *at;
+              const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+              for (int k = 0; k < 4; ++k)
+                if ((v[k] & 0x7C00u) == 0x7C00u || (v[k] & 0x7C000000u) == 0x7C000000u) odd |= 1u << ((i >> 2) & 15);
+            }
+          }
+          odd = __reduce_or_sync(0xffffffffu, odd);
+          while (odd) {
+            const int k = __ffs(odd) - 1;
+            odd &= odd - 1;
+            __half* const row = reinterpret_cast<__half*>(vp) + k * 32;
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+              for (int c = 0; c < 2; ++c) {
+                int lo, hi;
+                row_sees(nt * 8 + 2 * t + c, lo, hi);
+                const bool sees = tok + k <= hi && tok + k > lo;
+#pragma unroll
+                for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+                  for (int i = 0; i < 4; ++i) {
+                    const float x = __half2float(row[blk * 512 + 4 * g + i]);
+                    if (sees && !(fabsf(x) <= 65504.f)) o[blk][nt][i >> 1][2 * (i & 1) + c] += x;
+                  }
+              }
+            __syncwarp();
+            for (int e = lane; e < D; e += 32) {
+              __half* const x = row + (e >> 5) * 512 + (e & 31);
+              if (!(fabsf(__half2float(*x)) <= 65504.f)) *x = __ushort_as_half(0);
+            }
+          }
+          __syncwarp();
+        }
+        uint32_t w0[NT], w1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          w0[nt] = transpose8(pack_f16(s[nt][0], s[nt][1]));
+          w1[nt] = transpose8(pack_f16(s[nt][2], s[nt][3]));
+        }
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          uint32_t x[4], y[4];  // of four tokens: dimensions 4g, 4g+1 | 4g+2, 4g+3
+          const uint32_t at = vb + blk * 1024 + g * 8;
+          lds64(at + tok_v * 64, x[0], y[0]);
+          lds64(at + tok_w * 64, x[1], y[1]);
+          lds64(at + tok_v * 64 + 512, x[2], y[2]);
+          lds64(at + tok_w * 64 + 512, x[3], y[3]);
+          const uint32_t v0[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
+                                  __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
+          const uint32_t v1[4] = {__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[0], y[1], 0x7632),
+                                  __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[2], y[3], 0x7632)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma16816_acc(o[blk][nt][0], v0, w0[nt], w1[nt]);
+            mma16816_acc(o[blk][nt][1], v1, w0[nt], w1[nt]);
+          }
+        }
+      } else {
+        if (masked) {  // scales of tokens that no row sees may be anything
+          uint16_t* sc = reinterpret_cast<uint16_t*>(vp + KV_GROUP * D);
+          for (int i = lane; i < NB * KV_GROUP; i += 32) {
+            const int k = i & 15, tk = tok + (k >> 2) + 4 * (k & 3);
+            if (tk >= sp.hi || tk < sp.lo) sc[i] = 0;
+          }
+          __syncwarp();
+        }
+        uint32_t d[NB];
+        __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          uint32_t d0, d1;
+          lds64(vb + KV_GROUP * D + blk * 32 + scale_at, d0, d1);
+          d[blk] = __byte_perm(d0, d1, scale_sel);
+          big = __hmax2(big, *reinterpret_cast<__half2*>(&d[blk]));
+        }
+        float dmax = fmaxf(__low2float(big), __high2float(big));
+        if (__any_sync(0xffffffffu, dmax > wmax)) {
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 4));
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 8));
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
+          // dmax < 2^(e-1): scales may double before the next move
+          const int e = ((__float_as_int(dmax) >> 23) & 0xff) - 127 + 2;
+          const float to = __int_as_float((127 + 7 - e) << 23);  // 2^(7-e)
+          const float f = to * wback;  // at the first move there is nothing to scale yet
+          wmul = to;
+          wmax = __int_as_float((127 + e) << 23);
+          wback = __int_as_float((127 - 7 + e) << 23);
+#pragma unroll
+          for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
+        }
+        float w[NT][4];
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i) w[i >> 2][i & 3] = s[i >> 2][i & 3] * wmul;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          uint32_t v[4];  // of four tokens: dimensions 4g .. 4g+3
+          const uint32_t at = vb + blk * 512 + g * 4;
+          v[0] = lds32(at + tok_v * 32);
+          v[1] = lds32(at + tok_w * 32);
+          v[2] = lds32(at + tok_v * 32 + 256);
+          v[3] = lds32(at + tok_w * 32 + 256);
+          const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), lo1 = __byte_perm(v[2], v[3], 0x5140);
+          const uint32_t hi0 = __byte_perm(v[0], v[1], 0x7362), hi1 = __byte_perm(v[2], v[3], 0x7362);
+          const uint32_t k64 = 0x64646464u, k1152 = 0x64806480u;  // f16 1024 + u, less 1152
+          const uint32_t v0[4] = {hsub2_u(__byte_perm(lo0, k64, 0x4140), k1152), hsub2_u(__byte_perm(lo0, k64, 0x4342), k1152),
+                                  hsub2_u(__byte_perm(lo1, k64, 0x4140), k1152), hsub2_u(__byte_perm(lo1, k64, 0x4342), k1152)};
+          const uint32_t v1[4] = {hsub2_u(__byte_perm(hi0, k64, 0x4140), k1152), hsub2_u(__byte_perm(hi0, k64, 0x4342), k1152),
+                                  hsub2_u(__byte_perm(hi1, k64, 0x4140), k1152), hsub2_u(__byte_perm(hi1, k64, 0x4342), k1152)};
+          const float e0 = lo_f32(d[blk]), e1 = hi_f32(d[blk]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            float x[4] = {w[nt][0] * e0, w[nt][1] * e0, w[nt][2] * e1, w[nt][3] * e1};
+            if (masked) {  // a zero weight times a NaN scale (of a token that other rows see)
+#pragma unroll
+              for (int i = 0; i < 4; ++i) x[i] = w[nt][i] == 0.f ? 0.f : x[i];
+            }
+            const uint32_t w0 = transpose8(pack_f16(x[0], x[1])), w1 = transpose8(pack_f16(x[2], x[3]));
+            mma16816_acc(o[blk][nt][0], v0, w0, w1);
+            mma16816_acc(o[blk][nt][1], v1, w0, w1);
+          }
+        }
+      }
+      release();
+    }
+
+    // ------------------------------------------------ the four warps' sums
+    float* const s_z = s_stat + parity * (2 * AT_WARPS + 2) * ROWS;  // [warp][row]
+    float* const s_l = s_z + AT_WARPS * ROWS;                       // [warp][row]
+    float* const s_top = s_l + AT_WARPS * ROWS;                     // [row]
+    float* const s_sum = s_top + ROWS;                              // [row]
+    parity ^= 1;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        float x = l[nt][c];
+        x += __shfl_xor_sync(0xffffffffu, x, 4);
+        x += __shfl_xor_sync(0xffffffffu, x, 8);
+        x += __shfl_xor_sync(0xffffffffu, x, 16);
+        if (g == 0) {
+          s_z[warp * ROWS + nt * 8 + 2 * t + c] = z[nt][c];
+          s_l[warp * ROWS + nt * 8 + 2 * t + c] = x;
+        }
+      }
+    __syncthreads();
+    float f[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        const int row = nt * 8 + 2 * t + c;
+        float x = s_z[row];
+#pragma unroll
+        for (int w = 1; w < AT_WARPS; ++w) x = fmaxf(x, s_z[w * ROWS + row]);
+        f[nt][c] = z[nt][c] == -INFINITY ? 0.f : ex2(z[nt][c] - x) * wback;
+      }
+    if (tid < ROWS) {
+      float top = s_z[tid], sum = 0.f;
+#pragma unroll
+      for (int w = 1; w < AT_WARPS; ++w) top = fmaxf(top, s_z[w * ROWS + tid]);
+#pragma unroll
+      for (int w = 0; w < AT_WARPS; ++w) {
+        const float x = s_z[w * ROWS + tid];
+        sum += x == -INFINITY ? s_l[w * ROWS + tid] : s_l[w * ROWS + tid] * ex2(x - top);
+      }
+      s_top[tid] = top;
+      s_sum[tid] = sum;
+    }
+    const bool whole = u0 <= i0 && i1 <= u1;
+    const size_t part = (size_t)cta * 2 + (i0 < u0 ? 0 : 1);
+#pragma unroll
+    for (int pass = 0; pass < D / C::OD; ++pass) {
+      if (pass) __syncthreads();  // the buffer has been read
+#pragma unroll
+      for (int hb = 0; hb < C::OD / 32; ++hb) {
+        const int blk = pass * (C::OD / 32) + hb;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+            *reinterpret_cast<float4*>(s_o + (warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 4 * g) =
+                f[nt][c] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
+                                : make_float4(o[blk][nt][0][c] * f[nt][c], o[blk][nt][0][2 + c] * f[nt][c],
+                                              o[blk][nt][1][c] * f[nt][c], o[blk][nt][1][2 + c] * f[nt][c]);
+      }
+      __syncthreads();
+      constexpr int QUADS = C::OD / 4;  // float4 of a row
+#pragma unroll
+      for (int k = 0; k < ROWS * QUADS / AT_THREADS; ++k) {
+        const int row = (tid + k * AT_THREADS) / QUADS, dim = (tid % QUADS) * 4;
+        const int r = tile * ROWS + row;
+        if (r >= rows) continue;
+        float4 y = *reinterpret_cast<const float4*>(s_o + row * C::OPITCH + dim);
+#pragma unroll
+        for (int w = 1; w < AT_WARPS; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * C::OPITCH + dim);
+          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+        }
+        const int at = pass * C::OD + dim;
+        const float sum = s_sum[row];
+        if (whole) {
+          const float inv = sum == 0.f ? 0.f : 1.f / sum;
+          const size_t yo = (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + at;
+          *reinterpret_cast<uint2*>(a.y + yo) =
+              make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
+        } else {
+          *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
+          if (at == 0) *reinterpret_cast<float2*>(p.ws.ml + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
+        }
+      }
+    }
+  }
+  if (!ok) {  // a copy was late: wait for what is still in flight, each wait bounded
+    for (int i = 0; i < C::SLOTS; ++i) mbar_try_wait(bar_at + 8 * i, (phases >> i) & 1);
+  }
+}
+
+// Joins the parts of the items that are cut: one CTA for each (first cut of an
+// item, row); its warps share the parts out, the lanes the dimensions.
+template <int D, int ROWS>
+__global__ void __launch_bounds__(AT_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p) {
+  constexpr int V = D / 32;  // dimensions of a lane
+  extern __shared__ float s_w[];  // [grid] weights of the parts
+  __shared__ float s_y[AT_WARPS][D];
+  __shared__ float s_red[2][AT_WARPS];
+  pdl_trigger();
+  pdl_wait();
+  const AttnCut cut = p.ws.cut[blockIdx.x];
+  const int row = blockIdx.y, r = cut.tile * ROWS + row;
+  if (!cut.first || r >= p.group * p.a.ncols) return;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int n = cut.c1 - cut.c0 + 1;
+  // part i: the first CTA's run ends in the item (its second slot), the others' start in it
+  auto slot = [&](int i) { return ((size_t)(cut.c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+  float top = -INFINITY;
+  for (int i = tid; i < n; i += AT_THREADS) {
+    const float m = p.ws.ml[slot(i) * 2];
+    s_w[i] = m;
+    top = fmaxf(top, m);
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  if (lane == 0) s_red[0][warp] = top;
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, s_red[0][w]);
+  float sum = 0.f;
+  for (int i = tid; i < n; i += AT_THREADS) {
+    const float m = s_w[i], l = p.ws.ml[slot(i) * 2 + 1];
+    const float f = m == -INFINITY ? 0.f : ex2(m - top);
+    s_w[i] = f;
+    sum += m == -INFINITY ? l : l * f;
+  }
+#pragma unroll
+  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+  if (lane == 0) s_red[1][warp] = sum;
+  __syncthreads();
+  sum = 0.f;
+#pragma unroll
+  for (int w = 0; w < AT_WARPS; ++w) sum += s_red[1][w];
+  float y[V];
+#pragma unroll
+  for (int k = 0; k < V; ++k) y[k] = 0.f;
+#pragma unroll 4
+  for (int i = warp; i < n; i += AT_WARPS) {
+    const float f = s_w[i];
+    const float* o = p.ws.o + slot(i) * D + lane * V;
+    if (f != 0.f) {
+#pragma unroll
+      for (int k = 0; k < V; k += 2) {
+        const float2 x = *reinterpret_cast<const float2*>(o + k);
+        y[k] = fmaf(x.x, f, y[k]);
+        y[k + 1] = fmaf(x.y, f, y[k + 1]);
+      }
+    }
+  }
+#pragma unroll
+  for (int k = 0; k < V; ++k) s_y[warp][lane * V + k] = y[k];
+  __syncthreads();
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  for (int e = tid; e < D; e += AT_THREADS) {
+    float x = 0.f;
+#pragma unroll
+    for (int w = 0; w < AT_WARPS; ++w) x += s_y[w][e];
+    const size_t yo = (((size_t)cut.seq * p.a.ncols + r / p.group) * p.a.n_heads + cut.head * p.group + r % p.group) * D;
+    p.a.y[yo + e] = __half_as_ushort(__float2half_rn(x * inv));
+  }
+}
+
+
+template <int D, int NT>
+constexpr size_t attn_ws_of() {
+  constexpr int grid = AttnCfg<QG_F16, D, NT>::GRID;
+  static_assert(grid == AttnCfg<QG_Q8_0, D, NT>::GRID, "one workspace size for both types");
+  return (size_t)grid * (sizeof(AttnCut) + (size_t)2 * 8 * NT * (8 + D * 4));
+}
+
+template <int TYPE, int D, int NT>
+cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
+  using C = AttnCfg<TYPE, D, NT>;
+  AttnDev p;
+  p.a = a;
+  p.group = a.n_heads / a.c.n_kv_heads;
+  const int all = p.group * a.ncols;
+  p.tiles = (all + C::ROWS - 1) / C::ROWS;
+  p.scale = (float)((double)a.scale * 1.4426950408889634);
+  uint8_t* ws = static_cast<uint8_t*>(a.ws);
+  p.ws.cut = reinterpret_cast<AttnCut*>(ws);
+  ws += (size_t)C::GRID * sizeof(AttnCut);
+  p.ws.ml = reinterpret_cast<float*>(ws);
+  ws += (size_t)C::GRID * 2 * C::ROWS * 8;
+  p.ws.o = reinterpret_cast<float*>(ws);
+  const size_t smem = C::smem(a.c.n_seq);
+  cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT>, smem, false);
+  if (e != cudaSuccess) return e;
+  // both hold their SMs through shared memory, not L1
+  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_SMEM, p);
+  if (e != cudaSuccess) return e;
+  return launch_pdl(attn_join_kernel<D, C::ROWS>, dim3(C::GRID, all < C::ROWS ? all : C::ROWS), dim3(AT_THREADS),
+                    (size_t)C::GRID * 4, s, 0, LC_SMEM, p);
+}
+
+inline cudaError_t attn_error_word(int32_t* bits) {
+  const int32_t zero = 0;
+  cudaError_t e = cudaMemcpyFromSymbol(bits, g_attn_error, sizeof(*bits));
+  return e != cudaSuccess ? e : cudaMemcpyToSymbol(g_attn_error, &zero, sizeof(zero));
+}
+
+}  // namespace
+}  // namespace qg

@@ -1,0 +1,26 @@
+// qg_attn_256.cu -- attention over the paged cache, heads of 256 (kernels in qg_attn.cuh).
+#include "qg_attn.cuh"
+#include "qg_attn.h"
+
+namespace qg {
+
+cudaError_t attn_launch_256(const AttnArgs& a, int nt, cudaStream_t s) {
+  const bool f16 = a.c.type == QG_F16;
+  switch (nt) {
+    case 1: return f16 ? attn_typed<QG_F16, 256, 1>(a, s) : attn_typed<QG_Q8_0, 256, 1>(a, s);
+    case 2: return f16 ? attn_typed<QG_F16, 256, 2>(a, s) : attn_typed<QG_Q8_0, 256, 2>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
+size_t attn_ws_256(int nt) {
+  switch (nt) {
+    case 1: return attn_ws_of<256, 1>();
+    case 2: return attn_ws_of<256, 2>();
+  }
+  return 0;
+}
+
+cudaError_t attn_error_256(int32_t* bits) { return attn_error_word(bits); }
+
+}  // namespace qg

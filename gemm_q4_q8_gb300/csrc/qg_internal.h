@@ -160,7 +160,7 @@ cudaError_t kv_append_launch(const KvAppendArgs& a, cudaStream_t s);
 cudaError_t kv_read_launch(const qg_kvcache& c, const int32_t* seq, const int32_t* pos, int ntok,
                            int yt, void* k_out, void* v_out, int32_t* err, cudaStream_t s);
 
-// Attention over the paged cache (qg_attn.cu).
+// Attention over the paged cache (qg_attn.cu, qg_attn.cuh).
 struct AttnArgs {
   qg_kvcache c;
   const uint16_t* q;

@@ -1,6 +1,6 @@
 // qg_kv.cuh -- the byte layout of the paged key/value cache, shared by the
 // kernels that write it (qg_rope.cu), read it back (qg_kv.cu) and attend over
-// it (qg_attn.cu).
+// it (qg_attn.cuh).
 //
 // The unit is the record of 16 consecutive tokens of one head: its key half,
 // then its value half, each contiguous, so one bulk copy fetches either. Inside
