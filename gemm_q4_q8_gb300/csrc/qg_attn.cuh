@@ -50,6 +50,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <cmath>
+
 #include "qg_async.cuh"
 #include "qg_common.cuh"
 #include "qg_internal.h"
@@ -77,40 +79,40 @@ struct AttnCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int NB = D / 32;
   static constexpr int ACC = NT * D / 4;  // accumulator registers
-  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them)
-  static constexpr int CPS = ACC <= 32 ? 4 : ACC <= 64 ? 3 : 2;
+  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them) and, for f16
+  // heads of 256, by a warp's two slots
+  static constexpr int CPS = ACC <= 32 ? 4 : ACC <= 64 && kv_half_bytes(TYPE, D) <= 4608 ? 3 : 2;
   static constexpr int GRID = AT_SMS * CPS;
   static constexpr int HALF = kv_half_bytes(TYPE, D);
   static constexpr int SLOT = (HALF + 127) / 128 * 128;
-  static constexpr bool QSMEM = NT * NB > 8;  // Q fragments in shared memory, not registers
+  static constexpr bool QSMEM = NT * NB > 4;  // Q fragments in shared memory, not registers
   static constexpr int OD = NT <= 2 ? 64 : 32;  // dimensions joined at a time
   static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
   static constexpr size_t qbuf = QSMEM ? (size_t)NB * NT * (32 * 16 + 8 * 4) : 0;
-  // slots of a warp's ring: as many as leave CPS CTAs on an SM (227 KB, with 1 KB of the system's
-  // and 1 KB for up to 80 sequences a CTA), at most 8
+  // stages of a warp's ring: as many as leave CPS CTAs on an SM (227 KB, with 1 KB of the system's
+  // and 1 KB for up to 80 sequences a CTA), at most 4
   static constexpr size_t room = (size_t)(227 * 1024) / CPS - 2048 - obuf - stats - qbuf - 256;
-  static constexpr int FIT = (int)(room / ((size_t)AT_WARPS * SLOT));
-  static constexpr int SLOTS = FIT > 8 ? 8 : FIT;
-  static_assert(SLOTS >= 2, "a warp needs a slot for keys and one for values");
-  static constexpr size_t ring = (size_t)AT_WARPS * SLOTS * SLOT;
-  static constexpr size_t bars = (size_t)AT_WARPS * SLOTS * 8;
+  static constexpr int FIT = (int)(room / ((size_t)AT_WARPS * 2 * SLOT));
+  static constexpr int STAGES = FIT > 4 ? 4 : FIT;  // of a key slot and a value slot each
+  static_assert(STAGES >= 1, "a warp needs a slot for keys and one for values");
+  static constexpr size_t ring = (size_t)AT_WARPS * STAGES * 2 * SLOT;
+  static constexpr size_t bars = (size_t)AT_WARPS * STAGES * 2 * 8;
   static size_t smem(int n_seq) {
     return ring + obuf + stats + qbuf + bars + (size_t)(n_seq + 1) * 8 + (size_t)n_seq * 4;
   }
 };
 
-// What a CTA tells the joining kernel about the item that its run starts in.
+// What the main kernel tells the joining one: an item and the CTAs that have parts of it.
 struct AttnCut {
-  int32_t first;   // 1: this CTA is the second that has a part of the item (and joins for it)
-  int32_t c0, c1;  // the item's CTAs
+  int32_t c0, n;  // first CTA, number of parts; n == 0: nothing to join
   int32_t seq, head, tile;
-  int32_t pad[2];
+  int32_t pad[3];
 };
 
 struct AttnWs {
-  AttnCut* cut;  // [GRID]
+  AttnCut* cut;  // [GRID], of CTAs or of items
   float* ml;     // [GRID][2][ROWS][2]
   float* o;      // [GRID][2][ROWS][D]
 };
@@ -120,7 +122,9 @@ struct AttnDev {
   AttnWs ws;
   int group;    // query heads of a kv head
   int tiles;    // row tiles of a kv head
-  float scale;  // times log2 e
+  int by_item;  // the joining kernel goes by items, not by CTAs
+  float scale;  // |scale| log2 e; 1 for a scale of 0
+  uint32_t q_and, q_xor;  // and its sign, applied to the queries
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -138,6 +142,15 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   uint32_t d;
   asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(x));
   return d;
+}
+
+// D = A B + C with C's two columns the same in all rows.
+__device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
+                                              float c0, float c1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+      "{%8, %9}, {%10, %11, %10, %11};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
 // The CTA whose run holds place v of n, run c being [c n / N, (c+1) n / N).
@@ -172,7 +185,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
   uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
   uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
-  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::SLOTS);  // units before a sequence
+  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::STAGES * 2);  // units before a sequence
   int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
   __shared__ int64_t s_part[AT_WARPS];
 
@@ -180,7 +193,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_trigger();
-  if (tid < AT_WARPS * C::SLOTS) {
+  if (tid < AT_WARPS * C::STAGES * 2) {
     mbar_init(s_bar + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -249,21 +262,17 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     return lo;
   };
 
-  if (tid == 0) {
+  // The last item that starts in a run is the only one of them that may be cut: entry `cta` tells of it.
+  // (Where few items are joined one by one, item i's entry tells of item i.)
+  if (!p.by_item && tid == 0) {
     AttnCut cut{};
     if (steps > 0) {
-      const int b = seq_of(u0);
-      const int64_t nu = s_first[b + 1] - s_first[b], rem = u0 - u_first(b);
-      const int hr = (int)(rem / nu);
-      if (hr * nu < rem) {  // the item starts in an earlier run
-        const int64_t v = v_first(b) + hr * (nu + AT_PAD);
-        cut.c0 = run_of(v, places, N);
-        cut.c1 = run_of(v + nu - 1, places, N);
-        cut.first = cta == cut.c0 + 1;
-        cut.seq = b;
-        cut.head = hr / p.tiles;
-        cut.tile = hr % p.tiles;
-      }
+      const int b = seq_of(u1 - 1);
+      const int64_t nu = s_first[b + 1] - s_first[b];
+      const int hr = (int)((u1 - 1 - u_first(b)) / nu);
+      const int64_t v = v_first(b) + hr * (nu + AT_PAD), i0 = u_first(b) + hr * nu;
+      const int last = run_of(v + nu - 1, places, N);
+      if (i0 >= u0 && last > cta) cut = {cta, last - cta + 1, b, hr / p.tiles, hr % p.tiles};
     }
     p.ws.cut[cta] = cut;
   }
@@ -271,8 +280,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 
   // ------------------------------------------------------------ the ring
   const int gpp = a.c.page_size / KV_GROUP;  // records of a page and head
-  uint8_t* const ring = s_ring + (size_t)warp * C::SLOTS * C::SLOT;
-  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::SLOTS);
+  uint8_t* const ring = s_ring + (size_t)warp * C::STAGES * 2 * C::SLOT;
+  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::STAGES * 2);
   // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
   // so that the load has the whole batch before to arrive.
   int nx_page = -1, nx_off = 0;
@@ -309,39 +318,36 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     if (step & 32) valid_odd = v; else valid_even = v;
     look_up(step + 32);
   };
-  int is_step = 0, is_v = 0, is_slot = 0;  // the next half to fetch and its slot
-  auto issue = [&]() {
-    if (is_step < steps) {
-      if (!is_v && (is_step & 31) == 0) enter(is_step);
-      if (lane == (is_step & 31) && my_rec) {
-        const uint32_t bar = bar_at + 8 * is_slot;
+  // Fetch a half of the record of `step` into the slot whose barrier is `bar`: the lane that looked it up
+  // does. A step without a record completes the barrier at once.
+  bool ok = true;  // false once a wait gave up: no more copies, no more waits
+  auto fetch = [&](int step, int half, uint32_t slot, uint32_t bar) {
+    if (lane == (step & 31) && step < steps && ok) {
+      if (my_rec) {
         mbar_expect_tx(bar, C::HALF);
-        bulk_g2s(ring_at + is_slot * C::SLOT, my_rec + is_v * C::HALF, C::HALF, bar);
+        bulk_g2s(slot, my_rec + half * C::HALF, C::HALF, bar);
+      } else {
+        mbar_expect_tx(bar, 0);
       }
-      is_step += is_v;
-      is_v ^= 1;
-      is_slot = is_slot + 1 == C::SLOTS ? 0 : is_slot + 1;
     }
   };
   __syncwarp();
   look_up(0);
-  for (int i = 0; i < C::SLOTS; ++i) issue();
-
-  int co_slot = 0;      // the slot of the next half to consume
-  uint32_t phases = 0;  // parity of each slot's next phase
-  bool ok = true;       // false (in all lanes) once a wait gave up: no more copies, no more waits
-  auto arrived = [&]() {
-    if (ok)
-      ok = __all_sync(0xffffffffu, mbar_wait(bar_at + 8 * co_slot, (phases >> co_slot) & 1, &g_attn_error));
-    phases ^= 1u << co_slot;
-    return ring_at + co_slot * C::SLOT;
+  enter(0);
+#pragma unroll
+  for (int i = 0; i < C::STAGES; ++i) {
+    fetch(i, 0, ring_at + 2 * i * C::SLOT, bar_at + 16 * i);
+    fetch(i, 1, ring_at + (2 * i + 1) * C::SLOT, bar_at + 16 * i + 8);
+  }
+  int stage = 0;        // the stage in use
+  uint32_t parity = 0;  // of its barriers
+  auto arrived = [&](uint32_t bar) {
+    if (ok) ok = mbar_wait(bar, parity, &g_attn_error);
   };
-  // The slot's reads are over: every lane orders its own before the refill.
-  auto release = [&]() {
+  // A slot's reads are over: every lane orders its own before the refill.
+  auto slot_read = [&]() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
-    if (ok) issue();
-    co_slot = co_slot + 1 == C::SLOTS ? 0 : co_slot + 1;
   };
 
   // Tokens of a lane. As a row of K and of the scores: tok_a and tok_a + 8. As a
@@ -357,9 +363,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 
   // --------------------------------------------------------------- items
   const int rows = p.group * a.ncols;
-  int parity = 0;
+  int turn = 0;  // of the statistics' two buffers
   int64_t u = u0;
   int step = 0;
+  uint32_t valid = 0;
   int b = seq_of(u0);
   while (u < u1) {
     while (u_first(b + 1) <= u) ++b;
@@ -370,6 +377,13 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int head = hr / p.tiles, tile = hr % p.tiles;
     const int len = s_len[b];
     const SeqSpan sp = span_of(a, len);
+    if (p.by_item && tid == 0 && i0 >= u0) {
+      const int64_t v = v_first(b) + hr * (nu + AT_PAD);
+      const int last = run_of(v + nu - 1, places, N);
+      AttnCut cut{};
+      if (last > cta) cut = {cta, last - cta + 1, b, head, tile};
+      p.ws.cut[b * items + hr] = cut;
+    }
 
     // what row r of the tile sees: tokens lo < j <= hi
     auto row_sees = [&](int i, int& lo, int& hi) {
@@ -389,8 +403,13 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     auto load_q = [&](int blk, int nt) {
       const int r = tile * ROWS + nt * 8 + g;
       if (r >= rows) return make_uint4(0, 0, 0, 0);
-      return *reinterpret_cast<const uint4*>(
+      uint4 x = *reinterpret_cast<const uint4*>(
           a.q + (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + 32 * blk + 8 * t);
+      x.x = (x.x & p.q_and) ^ p.q_xor;
+      x.y = (x.y & p.q_and) ^ p.q_xor;
+      x.z = (x.z & p.q_and) ^ p.q_xor;
+      x.w = (x.w & p.q_and) ^ p.q_xor;
+      return x;
     };
     auto sum_q = [&](const uint4& x) {  // of row g
       float s = ((lo_f32(x.x) + hi_f32(x.x)) + (lo_f32(x.y) + hi_f32(x.y))) +
@@ -434,31 +453,53 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     float o[NB][NT][2][4];
 #pragma unroll
     for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
-    float z[NT][2], l[NT][2];  // of rows 2t, 2t + 1: reference; sum of this lane's tokens' weights
+    // of rows 2t, 2t + 1: the reference z, as -z (0 while there is none) and as the raw score above which it
+    // moves (-inf while there is none); the sum of this lane's tokens' weights
+    const float mul = TYPE == QG_F16 ? p.scale : p.scale * 16777216.f;  // Q8_0: u was u 2^-24
+    const float inv_mul = 1.f / mul;
+    float zneg[NT][2], limit[NT][2], l[NT][2];
+
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
-      z[nt][0] = z[nt][1] = -INFINITY;
-      l[nt][0] = l[nt][1] = 0.f;
-    }
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {
+        limit[nt][c] = -INFINITY;
+        zneg[nt][c] = l[nt][c] = 0.f;
+      }
+    auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : -zneg[nt][c]; };
     // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
     // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
 
-    for (; u < uend; ++u, ++step) {
-      const uint32_t valid = (step & 32) ? valid_odd : valid_even;
-      if (!((valid >> (step & 31)) & 1)) {  // nothing of this record is seen, or its page is bad
-        release();
-        release();
+    int tok = (int)(((int64_t)sp.unit + (u - i0)) * AT_WARPS + warp) * KV_GROUP - AT_UNIT;
+    for (int left = (int)(uend - u); left > 0; --left, ++step) {
+      tok += AT_UNIT;
+      if ((step & 31) == 0) valid = (step & 32) ? valid_odd : valid_even;
+      const uint32_t kb = ring_at + stage * (2 * C::SLOT), vb = kb + C::SLOT;
+      const uint32_t kbar = bar_at + stage * 16, vbar = kbar + 8;
+      // nothing to do where no token of the record is seen, or its page is bad
+      const bool live = (valid >> (step & 31)) & 1;
+      const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
+      const int ahead = step + C::STAGES;
+      arrived(kbar);
+      if (!live) {
+        __syncwarp();  // no lane re-arms a barrier that another still waits on
+        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        fetch(ahead, 0, kb, kbar);
+        arrived(vbar);
+        __syncwarp();
+        fetch(ahead, 1, vb, vbar);
+        if (++stage == C::STAGES) {
+          stage = 0;
+          parity ^= 1;
+        }
         continue;
       }
-      const int tok = (int)(((int64_t)sp.unit + (u - i0)) * AT_WARPS + warp) * KV_GROUP;
-      const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
 
       // ---- scores: s[nt][c] of token tok_a + 8 (c/2), row 8 nt + 2t + c%2
       float s[NT][4];
 #pragma unroll
       for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] = 0.f;
-      const uint32_t kb = arrived();
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
         uint32_t a0[4], a1[4];
@@ -507,8 +548,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
               c0 = qc[blk][nt][0];
               c1 = qc[blk][nt][1];
             }
-            float part[4] = {c0, c1, c0, c1};
-            mma16816_acc(part, a0, q[0], q[1]);
+            float part[4];
+            mma16816_from(part, a0, q[0], q[1], c0, c1);
             mma16816_acc(part, a1, q[2], q[3]);
             s[nt][0] = fmaf(part[0], e0, s[nt][0]);
             s[nt][1] = fmaf(part[1], e0, s[nt][1]);
@@ -517,10 +558,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       }
-      release();
+      slot_read();
+      if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+      fetch(ahead, 0, kb, kbar);
 
       // ---- weights
-      const float mul = TYPE == QG_F16 ? p.scale : p.scale * 16777216.f;  // Q8_0: u was u 2^-24
       if (masked) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -531,19 +573,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
               const int at = tok + tok_a + 8 * i;
-              float& x = s[nt][2 * i + c];
-              x = at <= hi && at > lo ? x * mul : -INFINITY;
+              if (at > hi || at <= lo) s[nt][2 * i + c] = -INFINITY;
             }
           }
-      } else {
-#pragma unroll
-        for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] *= mul;
       }
       bool up = false;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][2 + c]) > z[nt][c] + AT_SLACK;
+        for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][2 + c]) > limit[nt][c];
       if (__any_sync(0xffffffffu, up)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
@@ -553,10 +591,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             float x = fmaxf(s[nt][c], s[nt][2 + c]);
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
-            f[c] = x > z[nt][c] ? ex2(z[nt][c] - x) : 1.f;
-            z[nt][c] = fmaxf(z[nt][c], x);
-            l[nt][c] *= f[c];
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * mul;
+            const float z = ref(nt, c);
+            f[c] = 1.f;
+            if (x > z) {
+              f[c] = ex2(z - x);
+              zneg[nt][c] = -x;
+              limit[nt][c] = (x + AT_SLACK) * inv_mul;
+              l[nt][c] *= f[c];
+            }
           }
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk)
@@ -573,16 +616,14 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
-          // a row that has seen nothing has z = -inf and scores of -inf only (or NaN)
-          const float zz = z[nt][c] == -INFINITY ? 0.f : z[nt][c];
-          s[nt][c] = ex2(s[nt][c] - zz);
-          s[nt][2 + c] = ex2(s[nt][2 + c] - zz);
+          s[nt][c] = ex2(fmaf(s[nt][c], mul, zneg[nt][c]));
+          s[nt][2 + c] = ex2(fmaf(s[nt][2 + c], mul, zneg[nt][c]));
           l[nt][c] += s[nt][c] + s[nt][2 + c];
         }
 
       // ---- weights times values
-      const uint32_t vb = arrived();
-      uint8_t* const vp = ring + co_slot * C::SLOT;
+      arrived(vbar);
+      uint8_t* const vp = ring + stage * (2 * C::SLOT) + C::SLOT;
       if constexpr (TYPE == QG_F16) {
         if (masked) {
           // Zero weights do not silence a NaN or an infinity in the product. So the rows of tokens that no
@@ -719,15 +760,21 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       }
-      release();
+      slot_read();
+      fetch(ahead, 1, vb, vbar);
+      if (++stage == C::STAGES) {
+        stage = 0;
+        parity ^= 1;
+      }
     }
+    u = uend;
 
     // ------------------------------------------------ the four warps' sums
-    float* const s_z = s_stat + parity * (2 * AT_WARPS + 2) * ROWS;  // [warp][row]
+    float* const s_z = s_stat + turn * (2 * AT_WARPS + 2) * ROWS;  // [warp][row]
     float* const s_l = s_z + AT_WARPS * ROWS;                       // [warp][row]
     float* const s_top = s_l + AT_WARPS * ROWS;                     // [row]
     float* const s_sum = s_top + ROWS;                              // [row]
-    parity ^= 1;
+    turn ^= 1;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -737,7 +784,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         x += __shfl_xor_sync(0xffffffffu, x, 8);
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (g == 0) {
-          s_z[warp * ROWS + nt * 8 + 2 * t + c] = z[nt][c];
+          s_z[warp * ROWS + nt * 8 + 2 * t + c] = ref(nt, c);
           s_l[warp * ROWS + nt * 8 + 2 * t + c] = x;
         }
       }
@@ -751,7 +798,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         float x = s_z[row];
 #pragma unroll
         for (int w = 1; w < AT_WARPS; ++w) x = fmaxf(x, s_z[w * ROWS + row]);
-        f[nt][c] = z[nt][c] == -INFINITY ? 0.f : ex2(z[nt][c] - x) * wback;
+        f[nt][c] = limit[nt][c] == -INFINITY ? 0.f : ex2(-zneg[nt][c] - x) * wback;
       }
     if (tid < ROWS) {
       float top = s_z[tid], sum = 0.f;
@@ -810,87 +857,111 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     }
   }
   if (!ok) {  // a copy was late: wait for what is still in flight, each wait bounded
-    for (int i = 0; i < C::SLOTS; ++i) mbar_try_wait(bar_at + 8 * i, (phases >> i) & 1);
+    for (int i = 0; i < 2 * C::STAGES; ++i) mbar_try_wait(bar_at + 8 * i, parity);
   }
 }
 
-// Joins the parts of the items that are cut: one CTA for each (first cut of an
-// item, row); its warps share the parts out, the lanes the dimensions.
-template <int D, int ROWS>
-__global__ void __launch_bounds__(AT_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p) {
+// Joins the parts of the items that are cut. BY_ITEM: blockIdx.x is an item, its rows along y,
+// one to a CTA, whose warps share the parts out; for few items of many parts. Otherwise blockIdx.x is a
+// CTA of the main kernel and a warp joins a row; for many items of few parts.
+constexpr int JOIN_THREADS = 256;
+constexpr int JOIN_WARPS = JOIN_THREADS / 32;
+
+template <int D, int ROWS, bool BY_ITEM>
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p) {
   constexpr int V = D / 32;  // dimensions of a lane
-  extern __shared__ float s_w[];  // [grid] weights of the parts
-  __shared__ float s_y[AT_WARPS][D];
-  __shared__ float s_red[2][AT_WARPS];
+  __shared__ float s_y[BY_ITEM ? JOIN_WARPS : 1][D];
+  __shared__ float s_red[2][JOIN_WARPS];
   pdl_trigger();
   pdl_wait();
   const AttnCut cut = p.ws.cut[blockIdx.x];
-  const int row = blockIdx.y, r = cut.tile * ROWS + row;
-  if (!cut.first || r >= p.group * p.a.ncols) return;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int n = cut.c1 - cut.c0 + 1;
+  const int row = BY_ITEM ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+  const int r = cut.tile * ROWS + row;
+  if (cut.n == 0 || row >= ROWS || r >= p.group * p.a.ncols) return;
+  const int n = cut.n;
   // part i: the first CTA's run ends in the item (its second slot), the others' start in it
   auto slot = [&](int i) { return ((size_t)(cut.c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-  float top = -INFINITY;
-  for (int i = tid; i < n; i += AT_THREADS) {
-    const float m = p.ws.ml[slot(i) * 2];
-    s_w[i] = m;
-    top = fmaxf(top, m);
-  }
+  auto stat = [&](int i) {
+    return i < n ? *reinterpret_cast<const float2*>(p.ws.ml + slot(i) * 2) : make_float2(-INFINITY, 0.f);
+  };
+  // reference and sum over all parts
+  constexpr int SPREAD = BY_ITEM ? JOIN_THREADS : 32;
+  const int me = BY_ITEM ? tid : lane;
+  float top = -INFINITY, sum = 0.f;
+  for (int i = me; i < n; i += SPREAD) top = fmaxf(top, stat(i).x);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if (lane == 0) s_red[0][warp] = top;
-  __syncthreads();
+  if constexpr (BY_ITEM) {
+    if (lane == 0) s_red[0][warp] = top;
+    __syncthreads();
 #pragma unroll
-  for (int w = 0; w < AT_WARPS; ++w) top = fmaxf(top, s_red[0][w]);
-  float sum = 0.f;
-  for (int i = tid; i < n; i += AT_THREADS) {
-    const float m = s_w[i], l = p.ws.ml[slot(i) * 2 + 1];
-    const float f = m == -INFINITY ? 0.f : ex2(m - top);
-    s_w[i] = f;
-    sum += m == -INFINITY ? l : l * f;
+    for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, s_red[0][w]);
+  }
+  for (int i = me; i < n; i += SPREAD) {
+    const float2 x = stat(i);
+    sum += x.x == -INFINITY ? x.y : x.y * ex2(x.x - top);
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if (lane == 0) s_red[1][warp] = sum;
-  __syncthreads();
-  sum = 0.f;
+  if constexpr (BY_ITEM) {
+    if (lane == 0) s_red[1][warp] = sum;
+    __syncthreads();
+    sum = 0.f;
 #pragma unroll
-  for (int w = 0; w < AT_WARPS; ++w) sum += s_red[1][w];
+    for (int w = 0; w < JOIN_WARPS; ++w) sum += s_red[1][w];
+  }
   float y[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) y[k] = 0.f;
-#pragma unroll 4
-  for (int i = warp; i < n; i += AT_WARPS) {
-    const float f = s_w[i];
-    const float* o = p.ws.o + slot(i) * D + lane * V;
-    if (f != 0.f) {
+  // eight parts' loads in flight at a time
+  constexpr int STEP = BY_ITEM ? JOIN_WARPS : 1;
+  for (int i0 = BY_ITEM ? warp : 0; i0 < n; i0 += 8 * STEP) {
+    float x[8][V], f[8];
 #pragma unroll
-      for (int k = 0; k < V; k += 2) {
-        const float2 x = *reinterpret_cast<const float2*>(o + k);
-        y[k] = fmaf(x.x, f, y[k]);
-        y[k + 1] = fmaf(x.y, f, y[k + 1]);
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * STEP;
+      f[j] = stat(i).x;
+      if (i < n) {
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float2 v = *reinterpret_cast<const float2*>(p.ws.o + slot(i) * D + lane * V + k);
+          x[j][k] = v.x;
+          x[j][k + 1] = v.y;
+        }
       }
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const float w = f[j] == -INFINITY ? 0.f : ex2(f[j] - top);
+      if (w != 0.f)
+#pragma unroll
+        for (int k = 0; k < V; ++k) y[k] = fmaf(x[j][k], w, y[k]);
+    }
   }
-#pragma unroll
-  for (int k = 0; k < V; ++k) s_y[warp][lane * V + k] = y[k];
-  __syncthreads();
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  for (int e = tid; e < D; e += AT_THREADS) {
-    float x = 0.f;
+  const size_t yo = (((size_t)cut.seq * p.a.ncols + r / p.group) * p.a.n_heads + cut.head * p.group + r % p.group) * D;
+  if constexpr (BY_ITEM) {
 #pragma unroll
-    for (int w = 0; w < AT_WARPS; ++w) x += s_y[w][e];
-    const size_t yo = (((size_t)cut.seq * p.a.ncols + r / p.group) * p.a.n_heads + cut.head * p.group + r % p.group) * D;
-    p.a.y[yo + e] = __half_as_ushort(__float2half_rn(x * inv));
+    for (int k = 0; k < V; ++k) s_y[warp][lane * V + k] = y[k];
+    __syncthreads();
+    for (int e = tid; e < D; e += JOIN_THREADS) {
+      float x = 0.f;
+#pragma unroll
+      for (int w = 0; w < JOIN_WARPS; ++w) x += s_y[w][e];
+      p.a.y[yo + e] = __half_as_ushort(__float2half_rn(x * inv));
+    }
+  } else {
+#pragma unroll
+    for (int k = 0; k < V; k += 2)
+      *reinterpret_cast<uint32_t*>(p.a.y + yo + lane * V + k) = pack_f16(y[k] * inv, y[k + 1] * inv);
   }
 }
 
-
 template <int D, int NT>
 constexpr size_t attn_ws_of() {
-  constexpr int grid = AttnCfg<QG_F16, D, NT>::GRID;
-  static_assert(grid == AttnCfg<QG_Q8_0, D, NT>::GRID, "one workspace size for both types");
+  constexpr int grid = AttnCfg<QG_Q8_0, D, NT>::GRID;
+  static_assert(grid >= AttnCfg<QG_F16, D, NT>::GRID, "the workspace's size does not depend on the type");
   return (size_t)grid * (sizeof(AttnCut) + (size_t)2 * 8 * NT * (8 + D * 4));
 }
 
@@ -902,7 +973,14 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   p.group = a.n_heads / a.c.n_kv_heads;
   const int all = p.group * a.ncols;
   p.tiles = (all + C::ROWS - 1) / C::ROWS;
-  p.scale = (float)((double)a.scale * 1.4426950408889634);
+  // scores are compared before they are scaled, so the scale's sign goes to the queries
+  p.scale = a.scale == 0.f ? 1.f : (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+  p.q_and = a.scale == 0.f ? 0u : 0xffffffffu;
+  p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
+  const int n_items = a.c.n_seq * a.c.n_kv_heads * p.tiles;
+  const int tile_rows = all < C::ROWS ? all : C::ROWS;
+  // few items: they have many parts each
+  p.by_item = n_items <= C::GRID && n_items * tile_rows <= 8 * AT_SMS;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.ws.cut = reinterpret_cast<AttnCut*>(ws);
   ws += (size_t)C::GRID * sizeof(AttnCut);
@@ -915,8 +993,11 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   // both hold their SMs through shared memory, not L1
   e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_SMEM, p);
   if (e != cudaSuccess) return e;
-  return launch_pdl(attn_join_kernel<D, C::ROWS>, dim3(C::GRID, all < C::ROWS ? all : C::ROWS), dim3(AT_THREADS),
-                    (size_t)C::GRID * 4, s, 0, LC_SMEM, p);
+  if (p.by_item)
+    return launch_pdl(attn_join_kernel<D, C::ROWS, true>, dim3(n_items, tile_rows), dim3(JOIN_THREADS), 0, s, 0,
+                      LC_SMEM, p);
+  return launch_pdl(attn_join_kernel<D, C::ROWS, false>, dim3(C::GRID, (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS),
+                    dim3(JOIN_THREADS), 0, s, 0, LC_SMEM, p);
 }
 
 inline cudaError_t attn_error_word(int32_t* bits) {
