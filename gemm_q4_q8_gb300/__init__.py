@@ -266,38 +266,56 @@ def qmoe_router(w_router, x, topk, ids_out, rw_out, logits_out=None, stream=None
                                              _ptr(rw_out), _stream(stream)))
 
 
-_ELEM = None
+_ELEM = _INT32 = _FLOAT16 = None
+
+
+def _dtypes():
+    """torch's dtypes that the calls below take (torch is imported on first use)."""
+    global _ELEM, _INT32, _FLOAT16
+    import torch
+    _ELEM, _INT32, _FLOAT16 = {torch.float32: QG_F32, torch.float16: QG_F16}, torch.int32, torch.float16
 
 
 def _elem(t, name):
     """QG_F32 or QG_F16 of a tensor; the cache and rotary calls take nothing else."""
-    global _ELEM
     if _ELEM is None:
-        import torch
-        _ELEM = {torch.float32: QG_F32, torch.float16: QG_F16}
-    if t.dtype not in _ELEM:
+        _dtypes()
+    kind = _ELEM.get(t.dtype)
+    if kind is None:
         raise ValueError(f"{name}: float32 or float16 expected, got {t.dtype}")
-    return _ELEM[t.dtype]
+    return kind
 
 
-def _rows(t, name):
-    """Token stride of [ntok, heads, head_dim] whose heads are contiguous."""
-    heads, d = t.shape[1], t.shape[2]
-    s = t.stride()
-    if (d > 1 and s[2] != 1) or (heads > 1 and s[1] != d):
-        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {s}")
-    return s[0]
+def _rows(t, shape, name):
+    """Token stride of a tensor of `shape` [ntok, heads, head_dim] whose heads are contiguous."""
+    if t.shape != shape:
+        raise ValueError(f"{name}: shape {tuple(shape)} expected, got {tuple(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if (s2 != 1 and shape[2] > 1) or (s1 != shape[2] and shape[1] > 1):
+        raise ValueError(f"{name}: the heads of a token must be contiguous, got strides {t.stride()}")
+    return s0
 
 
 def _dense(t, name, dtype, shape):
-    """A contiguous tensor of the given type ("int32", "float16") and shape."""
-    if str(t.dtype) != "torch." + dtype or tuple(t.shape) != tuple(shape) or not t.is_contiguous():
+    """Address of a contiguous tensor of the given dtype and shape."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name}: contiguous {dtype} {tuple(shape)} expected, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
 
+def _int32s(t, name, n):
+    """Address of n contiguous int32, None for None."""
+    if t is None:
+        return None
+    if _INT32 is None:
+        _dtypes()
+    if t.dtype != _INT32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous int32 expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
 def _flag(t):
-    return None if t is None else _dense(t, "err_flag", "int32", t.shape if t.numel() else (1,))
+    return None if t is None else _int32s(t, "err_flag", 1)
 
 
 def qrope_plan(rot_dim, base=10000.0, interleaved=False, factor=1.0, orig_ctx=0, low_turns=1.0,
@@ -314,12 +332,12 @@ def qrope_plan(rot_dim, base=10000.0, interleaved=False, factor=1.0, orig_ctx=0,
 def qrope(plan, x, pos, y, stream=None):
     """Rotate x [ntok, heads, head_dim] (f32 or f16, any token stride) at int32
     positions pos [ntok] into y (f32 or f16; y may be x itself)."""
-    ntok, heads, d = x.shape
-    if y.shape != x.shape:
-        raise ValueError(f"y: shape {tuple(x.shape)} expected, got {tuple(y.shape)}")
-    _check("qrope", load().qrope(plan, _elem(x, "x"), x.data_ptr(), _rows(x, "x"),
-                                 _dense(pos, "pos", "int32", (ntok,)), ntok, heads, d, _elem(y, "y"),
-                                 y.data_ptr(), _rows(y, "y"), _stream(stream)))
+    shape = x.shape
+    ntok, heads, d = shape
+    st = (_lib or load()).qrope(plan, _elem(x, "x"), x.data_ptr(), _rows(x, shape, "x"), _int32s(pos, "pos", ntok),
+                                ntok, heads, d, _elem(y, "y"), y.data_ptr(), _rows(y, shape, "y"), _stream(stream))
+    if st:
+        _check("qrope", st)
 
 
 def qkv_page_bytes(qtype, n_kv_heads, head_dim, page_size) -> int:
@@ -334,11 +352,12 @@ def qkv_cache(qtype, pool, page_table, n_kv_heads, head_dim, page_size) -> QGKVC
     if page == 0:
         raise ValueError(f"qkv_cache: no cache of type {qtype}, {n_kv_heads} heads of {head_dim}, "
                          f"pages of {page_size}")
-    if not pool.is_contiguous() or pool.numel() * pool.element_size() % page:
+    nbytes = pool.numel() * pool.element_size()
+    if not pool.is_contiguous() or nbytes % page:
         raise ValueError(f"pool: contiguous, a multiple of {page} bytes expected")
-    c = QGKVCache(pool.data_ptr(), _dense(page_table, "page_table", "int32", page_table.shape[:2]), int(qtype),
-                  n_kv_heads, head_dim, page_size, pool.numel() * pool.element_size() // page,
-                  page_table.shape[1], page_table.shape[0])
+    n_seq, max_pages = page_table.shape
+    c = QGKVCache(pool.data_ptr(), _int32s(page_table, "page_table", n_seq * max_pages), int(qtype), n_kv_heads,
+                  head_dim, page_size, nbytes // page, max_pages, n_seq)
     c.tensors = (pool, page_table)
     return c
 
@@ -348,39 +367,39 @@ def qkv_append(cache, k, v, pos, seq=None, rope=None, q=None, q_out=None, err_fl
     int32 (seq, pos) [ntok]; with rope, k is rotated, and so is q [ntok, heads,
     head_dim], which goes to q_out (f16, contiguous). seq None: the tokens are
     the sequences' in turn, ntok / n_seq each."""
-    ntok, kind = k.shape[0], _elem(k, "k")
-    want = (ntok, cache.n_kv_heads, cache.head_dim)
-    for t, name in ((k, "k"), (v, "v")):
-        if tuple(t.shape) != want or t.dtype != k.dtype:
-            raise ValueError(f"{name}: {k.dtype} {want} expected, got {t.dtype} {tuple(t.shape)}")
-    qp = qs = qo = None
-    heads = 0
+    kind, ntok, d = _elem(k, "k"), k.shape[0], cache.head_dim
+    want = (ntok, cache.n_kv_heads, d)
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise ValueError("q, k and v must be of one type")
+    qp = qo = None
+    qs = heads = 0
     if q is not None:
         heads = q.shape[1]
-        if q.dtype != k.dtype or tuple(q.shape) != (ntok, heads, cache.head_dim) or q_out is None:
-            raise ValueError(f"q: {k.dtype} {(ntok, 'heads', cache.head_dim)} and a q_out expected")
-        qp, qs, qo = q.data_ptr(), _rows(q, "q"), _dense(q_out, "q_out", "float16", q.shape)
-    _check("qkv_append",
-           load().qkv_append(cache, rope, kind, k.data_ptr(), _rows(k, "k"), v.data_ptr(), _rows(v, "v"), qp,
-                             qs or 0, heads, qo, None if seq is None else _dense(seq, "seq", "int32", (ntok,)),
-                             _dense(pos, "pos", "int32", (ntok,)), ntok, _flag(err_flag), _stream(stream)))
+        if q_out is None:
+            raise ValueError("q needs a q_out")
+        shape = (ntok, heads, d)
+        qp, qs, qo = q.data_ptr(), _rows(q, shape, "q"), _dense(q_out, "q_out", _FLOAT16, shape)
+    st = (_lib or load()).qkv_append(cache, rope, kind, k.data_ptr(), _rows(k, want, "k"), v.data_ptr(),
+                                     _rows(v, want, "v"), qp, qs, heads, qo, _int32s(seq, "seq", ntok),
+                                     _int32s(pos, "pos", ntok), ntok, _flag(err_flag), _stream(stream))
+    if st:
+        _check("qkv_append", st)
 
 
 def qkv_read(cache, pos, k_out=None, v_out=None, seq=None, err_flag=None, stream=None):
     """Read the tokens at int32 (seq, pos) [ntok] back into k_out, v_out [ntok,
     n_kv_heads, head_dim] (f16 or f32, contiguous; either may be None)."""
-    ntok = pos.shape[0]
     some = k_out if k_out is not None else v_out
     if some is None:
         return
-    kind, name = _elem(some, "k_out / v_out"), str(some.dtype)[6:]
+    ntok, kind, dtype = pos.shape[0], _elem(some, "k_out / v_out"), some.dtype
     want = (ntok, cache.n_kv_heads, cache.head_dim)
-    _check("qkv_read",
-           load().qkv_read(cache, None if seq is None else _dense(seq, "seq", "int32", (ntok,)),
-                           _dense(pos, "pos", "int32", (ntok,)), ntok, kind,
-                           None if k_out is None else _dense(k_out, "k_out", name, want),
-                           None if v_out is None else _dense(v_out, "v_out", name, want), _flag(err_flag),
-                           _stream(stream)))
+    st = (_lib or load()).qkv_read(cache, _int32s(seq, "seq", ntok), _int32s(pos, "pos", ntok), ntok, kind,
+                                   None if k_out is None else _dense(k_out, "k_out", dtype, want),
+                                   None if v_out is None else _dense(v_out, "v_out", dtype, want), _flag(err_flag),
+                                   _stream(stream))
+    if st:
+        _check("qkv_read", st)
 
 
 def qattn_workspace_bytes(cache, n_heads, ncols) -> int:
@@ -393,11 +412,15 @@ def qattn_paged(cache, q, lens, y, ws, scale=None, window=0, err_flag=None, stre
     each sequence, over the cached tokens of lens int32 [n_seq] (the new ones
     among them), causal, within `window` tokens if it is not 0; y f16 as q. scale
     None: 1 / sqrt(head_dim)."""
-    n, ncols, heads, d = q.shape
+    shape = q.shape
+    n, ncols, heads, d = shape
     if n != cache.n_seq or d != cache.head_dim:
-        raise ValueError(f"q: [{cache.n_seq}, ncols, heads, {cache.head_dim}] expected, got {tuple(q.shape)}")
-    _check("qattn_paged",
-           load().qattn_paged(cache, _dense(q, "q", "float16", q.shape), heads, ncols,
-                              _dense(lens, "lens", "int32", (n,)), window, d ** -0.5 if scale is None else scale,
-                              _dense(y, "y", "float16", q.shape), ws.data_ptr(), ws.numel() * ws.element_size(),
-                              _flag(err_flag), _stream(stream)))
+        raise ValueError(f"q: [{cache.n_seq}, ncols, heads, {cache.head_dim}] expected, got {tuple(shape)}")
+    if not ws.is_contiguous():
+        raise ValueError("ws: contiguous workspace expected")
+    lens_at = _int32s(lens, "lens", n)  # (sets the dtypes up)
+    st = (_lib or load()).qattn_paged(cache, _dense(q, "q", _FLOAT16, shape), heads, ncols, lens_at, window,
+                                      d ** -0.5 if scale is None else scale, _dense(y, "y", _FLOAT16, shape),
+                                      ws.data_ptr(), ws.nbytes, _flag(err_flag), _stream(stream))
+    if st:
+        _check("qattn_paged", st)

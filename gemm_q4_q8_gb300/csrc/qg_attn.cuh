@@ -21,9 +21,9 @@
 // second kernel joins them in CTA order. The cuts depend on lens and the shape
 // alone, and so do the results.
 //
-// Inside a CTA each warp is on its own: it has a ring of shared-memory slots,
-// fetches the key half and the value half of its records with bulk copies (one
-// lane for each, a slot refilled as soon as it is consumed), and keeps z, the sum
+// Inside a CTA each warp is on its own: it has a ring of shared-memory stages,
+// fetches its records with bulk copies (one lane for each, a stage refilled as
+// soon as it is consumed), and keeps z, the sum
 // of weights and its accumulator in registers. The four warps meet only at the
 // end of an item. Page numbers of 32 steps are loaded by the 32 lanes at once, a
 // batch ahead.
@@ -35,8 +35,8 @@
 // dimensions of a block are given to the four lanes of a quad as 8 neighbouring
 // ones each, the same in A and B, so a lane's operands are one load. Values: A =
 // V^T, B = weights; the weights come out of the first product with tokens along
-// the lanes' rows and are turned by movmatrix, V's pairs of tokens are put
-// together by byte permutation after plain row loads.
+// the lanes' rows and are turned by movmatrix; V is turned by transposing
+// loads, of bytes for Q8_0.
 //
 // Q8_0: quants are stored as u = q + 128. As the low byte of an f16, u is the
 // subnormal u 2^-24, exact on the tensor cores, so K needs one byte permutation
@@ -79,26 +79,31 @@ struct AttnCfg {
   static constexpr int ROWS = 8 * NT;
   static constexpr int NB = D / 32;
   static constexpr int ACC = NT * D / 4;  // accumulator registers
-  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them) and, for f16
-  // heads of 256, by a warp's two slots
-  static constexpr int CPS = ACC <= 32 ? 4 : ACC <= 64 && kv_half_bytes(TYPE, D) <= 4608 ? 3 : 2;
-  static constexpr int GRID = AT_SMS * CPS;
   static constexpr int HALF = kv_half_bytes(TYPE, D);
-  static constexpr int SLOT = (HALF + 127) / 128 * 128;
+  static constexpr int STAGE = (2 * HALF + 127) / 128 * 128;  // a record
   static constexpr bool QSMEM = NT * NB > 4;  // Q fragments in shared memory, not registers
   static constexpr int OD = NT <= 2 ? 64 : 32;  // dimensions joined at a time
   static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
   static constexpr size_t qbuf = QSMEM ? (size_t)NB * NT * (32 * 16 + 8 * 4) : 0;
-  // stages of a warp's ring: as many as leave CPS CTAs on an SM (227 KB, with 1 KB of the system's
-  // and 1 KB for up to 80 sequences a CTA), at most 4
-  static constexpr size_t room = (size_t)(227 * 1024) / CPS - 2048 - obuf - stats - qbuf - 256;
-  static constexpr int FIT = (int)(room / ((size_t)AT_WARPS * 2 * SLOT));
-  static constexpr int STAGES = FIT > 4 ? 4 : FIT;  // of a key slot and a value slot each
-  static_assert(STAGES >= 1, "a warp needs a slot for keys and one for values");
-  static constexpr size_t ring = (size_t)AT_WARPS * STAGES * 2 * SLOT;
-  static constexpr size_t bars = (size_t)AT_WARPS * STAGES * 2 * 8;
+  // Stages of a warp's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 1 KB for up to
+  // 80 sequences a CTA).
+  static constexpr int fit(int n) {
+    return (int)(((size_t)(227 * 1024) / n - 2048 - obuf - stats - qbuf - 256) / ((size_t)AT_WARPS * STAGE));
+  }
+  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them), fewer while a warp
+  // has not two stages.
+  static constexpr int REGS = ACC <= 32 ? 4 : ACC <= 64 ? 3 : 2;
+  static constexpr int CPS = fit(REGS) >= 2 || REGS == 2 ? REGS : fit(REGS - 1) >= 2 || REGS == 3 ? REGS - 1 : 2;
+  static constexpr int GRID = AT_SMS * CPS;
+  static constexpr int STAGES = fit(CPS) > 4 ? 4 : fit(CPS);
+  static_assert(STAGES >= 1, "a warp needs room for a record");
+  // With one stage its halves come and go on their own: keys while values are in use, and the other way round.
+  static constexpr bool SPLIT = STAGES == 1;
+  static constexpr int BARS = SPLIT ? 2 : STAGES;
+  static constexpr size_t ring = (size_t)AT_WARPS * STAGES * STAGE;
+  static constexpr size_t bars = (size_t)AT_WARPS * BARS * 8;
   static size_t smem(int n_seq) {
     return ring + obuf + stats + qbuf + bars + (size_t)(n_seq + 1) * 8 + (size_t)n_seq * 4;
   }
@@ -136,6 +141,41 @@ __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   uint32_t d;
   asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(d) : "f"(hi), "f"(lo));
   return d;
+}
+__device__ __forceinline__ bool bar_ready(uint32_t bar, uint32_t parity) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(r)
+      : "r"(bar), "r"(parity)
+      : "memory");
+  return r != 0;
+}
+// One arrival on `bar` where `mine`, with a bulk copy of `bytes` to wait for where `has` (which implies `mine`).
+__device__ __forceinline__ void fetch_if(bool mine, bool has, uint32_t dst, const void* src, uint32_t bytes,
+                                         uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\t"
+      "setp.ne.u32 p, %0, 0;\n\tsetp.ne.u32 q, %1, 0;\n\t"
+      "selp.u32 n, %4, 0, q;\n\t"
+      "@p mbarrier.arrive.expect_tx.shared::cta.b64 _, [%5], n;\n\t"
+      "@q cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%2], [%3], %4, [%5];\n\t}" ::"r"((uint32_t)mine),
+      "r"((uint32_t)has), "r"(dst), "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+// V^T fragments of 32 dimensions x 16 tokens. f16: two 16 x 16 tiles by transposing loads of 8 x 8.
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
+}
+// Q8_0: two 16 x 16 byte matrices transposed; lane (g, t) gets bytes 4t .. 4t+3 of columns g, g + 8 of each.
+__device__ __forceinline__ void ldsm_bytes_trans(uint32_t at, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(at));
 }
 // Transpose of an 8 x 8 matrix of f16 held by a warp, two elements of a row a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -185,7 +225,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
   uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
   uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
-  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::STAGES * 2);  // units before a sequence
+  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::BARS);  // units before a sequence
   int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
   __shared__ int64_t s_part[AT_WARPS];
 
@@ -193,7 +233,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_trigger();
-  if (tid < AT_WARPS * C::STAGES * 2) {
+  if (tid < AT_WARPS * C::BARS) {
     mbar_init(s_bar + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
@@ -280,8 +320,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 
   // ------------------------------------------------------------ the ring
   const int gpp = a.c.page_size / KV_GROUP;  // records of a page and head
-  uint8_t* const ring = s_ring + (size_t)warp * C::STAGES * 2 * C::SLOT;
-  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::STAGES * 2);
+  uint8_t* const ring = s_ring + (size_t)warp * C::STAGES * C::STAGE;
+  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::BARS);
   // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
   // so that the load has the whole batch before to arrive.
   int nx_page = -1, nx_off = 0;
@@ -318,48 +358,51 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     if (step & 32) valid_odd = v; else valid_even = v;
     look_up(step + 32);
   };
-  // Fetch a half of the record of `step` into the slot whose barrier is `bar`: the lane that looked it up
-  // does. A step without a record completes the barrier at once.
+  // Fetch the record of `step` (from byte `from`, `bytes` of it) to `dst`: the lane that looked it up does. A
+  // step without a record completes the barrier at once.
   bool ok = true;  // false once a wait gave up: no more copies, no more waits
-  auto fetch = [&](int step, int half, uint32_t slot, uint32_t bar) {
-    if (lane == (step & 31) && step < steps && ok) {
-      if (my_rec) {
-        mbar_expect_tx(bar, C::HALF);
-        bulk_g2s(slot, my_rec + half * C::HALF, C::HALF, bar);
-      } else {
-        mbar_expect_tx(bar, 0);
-      }
-    }
+  auto fetch = [&](int step, int from, uint32_t bytes, uint32_t dst, uint32_t bar) {
+    const bool mine = lane == (step & 31) && step < steps && ok;
+    fetch_if(mine, mine && my_rec, dst, my_rec + from, bytes, bar);
   };
   __syncwarp();
   look_up(0);
   enter(0);
+  if constexpr (C::SPLIT) {
+    fetch(0, 0, C::HALF, ring_at, bar_at);
+    fetch(0, C::HALF, C::HALF, ring_at + C::HALF, bar_at + 8);
+  } else {
 #pragma unroll
-  for (int i = 0; i < C::STAGES; ++i) {
-    fetch(i, 0, ring_at + 2 * i * C::SLOT, bar_at + 16 * i);
-    fetch(i, 1, ring_at + (2 * i + 1) * C::SLOT, bar_at + 16 * i + 8);
+    for (int i = 0; i < C::STAGES; ++i) fetch(i, 0, 2 * C::HALF, ring_at + i * C::STAGE, bar_at + 8 * i);
   }
   int stage = 0;        // the stage in use
   uint32_t parity = 0;  // of its barriers
   auto arrived = [&](uint32_t bar) {
-    if (ok) ok = mbar_wait(bar, parity, &g_attn_error);
+    if (!bar_ready(bar, parity) && ok) ok = mbar_wait_slow(bar, parity, &g_attn_error);
   };
-  // A slot's reads are over: every lane orders its own before the refill.
-  auto slot_read = [&]() {
+  // Reads of a stage are over: every lane orders its own before the refill.
+  auto reads_done = [&]() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
   };
 
-  // Tokens of a lane. As a row of K and of the scores: tok_a and tok_a + 8. As a
-  // column of V^T: tok_v + {0, 8} and tok_w + {0, 8}. Position i of the 16-wide side
-  // is token i/2 (i even) or 4 + x (i odd); x is chosen so that the lanes of a
-  // shared-memory phase meet no bank twice: rows of 64 bytes (f16) want neighbours of
-  // different parity, rows of 32 bytes (Q8_0) four neighbours that differ modulo 4.
-  auto odd_tok = [](int i) { return 4 + (TYPE == QG_F16 ? (i ^ 1) : ((i + 2) & 3)); };
-  const int tok_a = (g & 1) ? odd_tok(g >> 1) : g >> 1;
-  const int tok_v = t, tok_w = odd_tok(t);
-  // the two scales of a lane's tokens, out of the four with the same i mod 4
+  // Which token of the record position i of the 16-wide side is. f16: token i. Q8_0: i/2 (i even) or
+  // 4 + (i/2 + 2) mod 4 (i odd), and 8 more for i >= 8: the rows of 32 bytes that the lanes of a shared-memory phase
+  // read then differ modulo 4 (no bank conflict), and a lane's two tokens, 8 apart, have their scales in one word.
+  auto token_of = [](int i) {
+    return TYPE == QG_F16 ? i : (i & 8) + ((i & 1) ? 4 + ((((i & 7) >> 1) + 2) & 3) : (i & 7) >> 1);
+  };
+  const int tok_a = token_of(g);  // this lane's tokens as rows of the scores: tok_a and tok_a + 8
   const uint32_t scale_at = (tok_a & 3) * 8, scale_sel = (tok_a & 4) ? 0x7632u : 0x5410u;
+  // this lane's row address for the transposing loads of V
+  uint32_t v_at;
+  if constexpr (TYPE == QG_F16) {
+    v_at = ((lane & 7) + ((lane >> 4) & 1) * 8) * 64 + ((lane >> 3) & 1) * 16;
+  } else {
+    // row j of the byte matrix goes to byte j mod 4 of lane j / 4: positions 2t, 2t+1, 2t+8, 2t+9
+    const int j = lane & 15, i = 2 * (j >> 2) + (j & 1) + 4 * (j & 2);
+    v_at = token_of(i) * 32 + (lane >> 4) * 16;
+  }
 
   // --------------------------------------------------------------- items
   const int rows = p.group * a.ncols;
@@ -449,7 +492,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       }
     }
 
-    // o[blk][nt][i][c]: dimension 32 blk + 4g + 2i + c/2, row 8 nt + 2t + c%2
+    // o[blk][nt][i][c]: dimension 32 blk + 16 i + 8 (c/2) + g, row 8 nt + 2t + c%2
     float o[NB][NT][2][4];
 #pragma unroll
     for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
@@ -475,24 +518,31 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     for (int left = (int)(uend - u); left > 0; --left, ++step) {
       tok += AT_UNIT;
       if ((step & 31) == 0) valid = (step & 32) ? valid_odd : valid_even;
-      const uint32_t kb = ring_at + stage * (2 * C::SLOT), vb = kb + C::SLOT;
-      const uint32_t kbar = bar_at + stage * 16, vbar = kbar + 8;
+      const uint32_t kb = ring_at + stage * C::STAGE, vb = kb + C::HALF;
+      const uint32_t kbar = bar_at + stage * 8, vbar = C::SPLIT ? kbar + 8 : kbar;
       // nothing to do where no token of the record is seen, or its page is bad
       const bool live = (valid >> (step & 31)) & 1;
       const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
       const int ahead = step + C::STAGES;
-      arrived(kbar);
-      if (!live) {
-        __syncwarp();  // no lane re-arms a barrier that another still waits on
-        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
-        fetch(ahead, 0, kb, kbar);
-        arrived(vbar);
-        __syncwarp();
-        fetch(ahead, 1, vb, vbar);
+      auto next = [&]() {
         if (++stage == C::STAGES) {
           stage = 0;
           parity ^= 1;
         }
+      };
+      arrived(kbar);
+      if (!live) {
+        __syncwarp();  // no lane re-arms a barrier that another still waits on
+        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        if constexpr (C::SPLIT) {
+          fetch(ahead, 0, C::HALF, kb, kbar);
+          arrived(vbar);
+          __syncwarp();
+          fetch(ahead, C::HALF, C::HALF, vb, vbar);
+        } else {
+          fetch(ahead, 0, 2 * C::HALF, kb, kbar);
+        }
+        next();
         continue;
       }
 
@@ -558,9 +608,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       }
-      slot_read();
-      if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
-      fetch(ahead, 0, kb, kbar);
+      if constexpr (C::SPLIT) {
+        reads_done();
+        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        fetch(ahead, 0, C::HALF, kb, kbar);
+      }
 
       // ---- weights
       if (masked) {
@@ -622,8 +674,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
 
       // ---- weights times values
-      arrived(vbar);
-      uint8_t* const vp = ring + stage * (2 * C::SLOT) + C::SLOT;
+      if constexpr (C::SPLIT) arrived(vbar);
+      uint8_t* const vp = ring + stage * C::STAGE + C::HALF;
       if constexpr (TYPE == QG_F16) {
         if (masked) {
           // Zero weights do not silence a NaN or an infinity in the product. So the rows of tokens that no
@@ -659,7 +711,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
                 for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
                   for (int i = 0; i < 4; ++i) {
-                    const float x = __half2float(row[blk * 512 + 4 * g + i]);
+                    const float x = __half2float(row[blk * 512 + 8 * i + g]);
                     if (sees && !(fabsf(x) <= 65504.f)) o[blk][nt][i >> 1][2 * (i & 1) + c] += x;
                   }
               }
@@ -679,16 +731,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          uint32_t x[4], y[4];  // of four tokens: dimensions 4g, 4g+1 | 4g+2, 4g+3
-          const uint32_t at = vb + blk * 1024 + g * 8;
-          lds64(at + tok_v * 64, x[0], y[0]);
-          lds64(at + tok_w * 64, x[1], y[1]);
-          lds64(at + tok_v * 64 + 512, x[2], y[2]);
-          lds64(at + tok_w * 64 + 512, x[3], y[3]);
-          const uint32_t v0[4] = {__byte_perm(x[0], x[1], 0x5410), __byte_perm(x[0], x[1], 0x7632),
-                                  __byte_perm(x[2], x[3], 0x5410), __byte_perm(x[2], x[3], 0x7632)};
-          const uint32_t v1[4] = {__byte_perm(y[0], y[1], 0x5410), __byte_perm(y[0], y[1], 0x7632),
-                                  __byte_perm(y[2], y[3], 0x5410), __byte_perm(y[2], y[3], 0x7632)};
+          uint32_t v0[4], v1[4];
+          ldsm_x4_trans(vb + blk * 1024 + v_at, v0);
+          ldsm_x4_trans(vb + blk * 1024 + 32 + v_at, v1);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
             mma16816_acc(o[blk][nt][0], v0, w0[nt], w1[nt]);
@@ -696,11 +741,35 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       } else {
-        if (masked) {  // scales of tokens that no row sees may be anything
+        if (masked) {
+          // As for f16: scales of tokens that no row sees may be anything, and a NaN scale (of a token that
+          // some rows do not see) is taken out and given to the rows that see it.
           uint16_t* sc = reinterpret_cast<uint16_t*>(vp + KV_GROUP * D);
-          for (int i = lane; i < NB * KV_GROUP; i += 32) {
-            const int k = i & 15, tk = tok + (k >> 2) + 4 * (k & 3);
-            if (tk >= sp.hi || tk < sp.lo) sc[i] = 0;
+#pragma unroll
+          for (int blk = 0; blk < NB; ++blk) {
+            bool nan = false;
+            if (lane < KV_GROUP) {
+              uint16_t& x = sc[blk * KV_GROUP + lane];
+              const int tk = tok + (lane >> 2) + 4 * (lane & 3);
+              const bool seen = tk < sp.hi && tk >= sp.lo;
+              nan = seen && (x & 0x7FFF) > 0x7C00;
+              if (!seen || nan) x = 0;
+            }
+            uint32_t odd = __ballot_sync(0xffffffffu, nan);
+            while (odd) {
+              const int j = __ffs(odd) - 1, tj = tok + (j >> 2) + 4 * (j & 3);
+              odd &= odd - 1;
+#pragma unroll
+              for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                  int lo, hi;
+                  row_sees(nt * 8 + 2 * t + c, lo, hi);
+                  const float add = tj <= hi && tj > lo ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+                  for (int e = 0; e < 4; ++e) o[blk][nt][e >> 1][2 * (e & 1) + c] += add;
+                }
+            }
           }
           __syncwarp();
         }
@@ -733,39 +802,31 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         for (int i = 0; i < NT * 4; ++i) w[i >> 2][i & 3] = s[i >> 2][i & 3] * wmul;
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          uint32_t v[4];  // of four tokens: dimensions 4g .. 4g+3
-          const uint32_t at = vb + blk * 512 + g * 4;
-          v[0] = lds32(at + tok_v * 32);
-          v[1] = lds32(at + tok_w * 32);
-          v[2] = lds32(at + tok_v * 32 + 256);
-          v[3] = lds32(at + tok_w * 32 + 256);
-          const uint32_t lo0 = __byte_perm(v[0], v[1], 0x5140), lo1 = __byte_perm(v[2], v[3], 0x5140);
-          const uint32_t hi0 = __byte_perm(v[0], v[1], 0x7362), hi1 = __byte_perm(v[2], v[3], 0x7362);
+          uint32_t v[4];  // of four tokens: dimensions g, g + 8, g + 16, g + 24
+          ldsm_bytes_trans(vb + blk * 512 + v_at, v);
           const uint32_t k64 = 0x64646464u, k1152 = 0x64806480u;  // f16 1024 + u, less 1152
-          const uint32_t v0[4] = {hsub2_u(__byte_perm(lo0, k64, 0x4140), k1152), hsub2_u(__byte_perm(lo0, k64, 0x4342), k1152),
-                                  hsub2_u(__byte_perm(lo1, k64, 0x4140), k1152), hsub2_u(__byte_perm(lo1, k64, 0x4342), k1152)};
-          const uint32_t v1[4] = {hsub2_u(__byte_perm(hi0, k64, 0x4140), k1152), hsub2_u(__byte_perm(hi0, k64, 0x4342), k1152),
-                                  hsub2_u(__byte_perm(hi1, k64, 0x4140), k1152), hsub2_u(__byte_perm(hi1, k64, 0x4342), k1152)};
+          const uint32_t v0[4] = {hsub2_u(__byte_perm(v[0], k64, 0x4140), k1152), hsub2_u(__byte_perm(v[1], k64, 0x4140), k1152),
+                                  hsub2_u(__byte_perm(v[0], k64, 0x4342), k1152), hsub2_u(__byte_perm(v[1], k64, 0x4342), k1152)};
+          const uint32_t v1[4] = {hsub2_u(__byte_perm(v[2], k64, 0x4140), k1152), hsub2_u(__byte_perm(v[3], k64, 0x4140), k1152),
+                                  hsub2_u(__byte_perm(v[2], k64, 0x4342), k1152), hsub2_u(__byte_perm(v[3], k64, 0x4342), k1152)};
           const float e0 = lo_f32(d[blk]), e1 = hi_f32(d[blk]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            float x[4] = {w[nt][0] * e0, w[nt][1] * e0, w[nt][2] * e1, w[nt][3] * e1};
-            if (masked) {  // a zero weight times a NaN scale (of a token that other rows see)
-#pragma unroll
-              for (int i = 0; i < 4; ++i) x[i] = w[nt][i] == 0.f ? 0.f : x[i];
-            }
-            const uint32_t w0 = transpose8(pack_f16(x[0], x[1])), w1 = transpose8(pack_f16(x[2], x[3]));
+            const uint32_t w0 = transpose8(pack_f16(w[nt][0] * e0, w[nt][1] * e0));
+            const uint32_t w1 = transpose8(pack_f16(w[nt][2] * e1, w[nt][3] * e1));
             mma16816_acc(o[blk][nt][0], v0, w0, w1);
             mma16816_acc(o[blk][nt][1], v1, w0, w1);
           }
         }
       }
-      slot_read();
-      fetch(ahead, 1, vb, vbar);
-      if (++stage == C::STAGES) {
-        stage = 0;
-        parity ^= 1;
+      reads_done();
+      if constexpr (C::SPLIT) {
+        fetch(ahead, C::HALF, C::HALF, vb, vbar);
+      } else {
+        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        fetch(ahead, 0, 2 * C::HALF, kb, kbar);
       }
+      next();
     }
     u = uend;
 
@@ -824,10 +885,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int c = 0; c < 2; ++c)
-            *reinterpret_cast<float4*>(s_o + (warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 4 * g) =
-                f[nt][c] == 0.f ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                : make_float4(o[blk][nt][0][c] * f[nt][c], o[blk][nt][0][2 + c] * f[nt][c],
-                                              o[blk][nt][1][c] * f[nt][c], o[blk][nt][1][2 + c] * f[nt][c]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s_o[(warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 8 * e + g] =
+                  f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
       }
       __syncthreads();
       constexpr int QUADS = C::OD / 4;  // float4 of a row
@@ -857,7 +918,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     }
   }
   if (!ok) {  // a copy was late: wait for what is still in flight, each wait bounded
-    for (int i = 0; i < 2 * C::STAGES; ++i) mbar_try_wait(bar_at + 8 * i, parity);
+    for (int i = 0; i < C::BARS; ++i) mbar_try_wait(bar_at + 8 * i, parity);
   }
 }
 
@@ -993,11 +1054,14 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   // both hold their SMs through shared memory, not L1
   e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_SMEM, p);
   if (e != cudaSuccess) return e;
+  // The join is not launched early: with both kernels early, a step's main kernel would start while the one
+  // before it is still running, on whatever SMs are free first, and its one wave of CTAs would be uneven
+  // (131,071 f16 tokens in a loop of calls: 104 us; with this rule 86).
   if (p.by_item)
     return launch_pdl(attn_join_kernel<D, C::ROWS, true>, dim3(n_items, tile_rows), dim3(JOIN_THREADS), 0, s, 0,
-                      LC_SMEM, p);
+                      LC_LATE, p);
   return launch_pdl(attn_join_kernel<D, C::ROWS, false>, dim3(C::GRID, (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS),
-                    dim3(JOIN_THREADS), 0, s, 0, LC_SMEM, p);
+                    dim3(JOIN_THREADS), 0, s, 0, LC_LATE, p);
 }
 
 inline cudaError_t attn_error_word(int32_t* bits) {

@@ -41,7 +41,8 @@ void note_launch(int n = 1);
 // life. So an LC_L1 kernel that directly follows an LC_SMEM kernel on the
 // same stream is launched without the programmatic attribute (it starts when
 // that grid completes); every other pair overlaps.
-enum LaunchClass { LC_L1 = 0, LC_SMEM = 1 };
+// LC_LATE: a kernel that never starts early itself (the attention's join).
+enum LaunchClass { LC_L1 = 0, LC_SMEM = 1, LC_LATE = 2 };
 
 // Records `cls` as the class of the latest launch on `s` and returns whether
 // this launch may use programmatic stream serialisation.
