@@ -19,7 +19,10 @@
 // load every SM alike. A CTA that covers an item whole writes y; where an item is
 // cut, each CTA writes its sum, reference and weight to the workspace, and a
 // second kernel joins them in CTA order. The cuts depend on lens and the shape
-// alone, and so do the results.
+// alone, and so do the results. (Joining in the CTA that finishes last needs no
+// second kernel but a first one that clears its counters, and has one CTA's loads
+// to work with: 1,000 tokens of two heads of 256 took 14.3 us so, 10.7 with the
+// second kernel.)
 //
 // Inside a CTA each warp is on its own: it has a ring of shared-memory stages,
 // fetches its records with bulk copies (one lane for each, a stage refilled as
@@ -71,7 +74,7 @@ constexpr int AT_UNIT = AT_WARPS * KV_GROUP;  // tokens of a unit
 constexpr int AT_SMS = 152;
 // An item's end (four warps' sums joined, the next queries loaded) costs a warp about as much as
 // this many units, and the runs are cut as if it were that many more.
-constexpr int AT_PAD = 2;
+constexpr int AT_PAD = 3;
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
 
 template <int TYPE, int D, int NT>
@@ -117,9 +120,9 @@ struct AttnCut {
 };
 
 struct AttnWs {
-  AttnCut* cut;  // [GRID], of CTAs or of items
-  float* ml;     // [GRID][2][ROWS][2]
-  float* o;      // [GRID][2][ROWS][D]
+  AttnCut* cut;   // [GRID], of CTAs or of items
+  float* zl;      // [GRID][2][ROWS][2] reference and sum of weights of a part
+  float* o;       // [GRID][2][ROWS][D] its weighted sum
 };
 
 struct AttnDev {
@@ -193,8 +196,13 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
+// a / b of numbers >= 0, in 32 bits where they fit (they nearly always do, and the division is several times shorter).
+__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
+  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
+  return a / b;
+}
 // The CTA whose run holds place v of n, run c being [c n / N, (c+1) n / N).
-__device__ __forceinline__ int run_of(int64_t v, int64_t n, int64_t N) { return (int)(((v + 1) * N - 1) / n); }
+__device__ __forceinline__ int run_of(int64_t v, int64_t n, int64_t N) { return (int)div_pos((v + 1) * N - 1, n); }
 
 struct SeqSpan {
   int lo;    // first token that any row sees
@@ -273,73 +281,92 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   // Two numberings: units in order, u, and places in order, v, where every item has
   // AT_PAD places behind its units. Runs are equal in places.
   const int items = a.c.n_kv_heads * p.tiles;  // of a sequence
-  auto u_first = [&](int b) { return s_first[b] * items; };
+  auto units_of = [&](int b) { return (int)(s_first[b + 1] - s_first[b]); };
   auto v_first = [&](int b) { return (s_first[b] + (int64_t)b * AT_PAD) * items; };
   const int64_t places = v_first(n_seq);
   const int64_t N = places < C::GRID ? places : C::GRID;
   const int cta = blockIdx.x;
+  // The last item that starts in a run is the only one of them that may be cut: entry `cta` tells of it.
+  // (Where few items are joined one by one, item i's entry tells of item i.)
+  if (!p.by_item && tid == 0) p.ws.cut[cta].n = 0;
+  if (cta >= N) return;
   // the first unit at or behind a place
-  auto unit_at = [&](int64_t v) {
+  struct Unit {
+    int seq, item, unit;  // item of the sequence, unit of the item
+  };
+  auto unit_at = [&](int64_t v, int64_t& number) {
     int lo = 0, hi = n_seq;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
       if (v_first(mid) <= v) lo = mid; else hi = mid;
     }
-    const int64_t n = s_first[lo + 1] - s_first[lo], rem = v - v_first(lo);
-    const int64_t it = rem / (n + AT_PAD), in = rem - it * (n + AT_PAD);
-    return u_first(lo) + it * n + (in < n ? in : n);
+    const int n = units_of(lo);
+    const int64_t rem = v - v_first(lo);
+    Unit x;
+    x.seq = lo;
+    x.item = (int)div_pos(rem, n + AT_PAD);
+    x.unit = (int)(rem - (int64_t)x.item * (n + AT_PAD));
+    if (x.unit >= n) {  // behind the item's units, or past the end
+      x.unit = 0;
+      if (++x.item == items) {
+        x.item = 0;
+        ++x.seq;
+      }
+    }
+    number = s_first[x.seq] * items + (x.seq < n_seq ? (int64_t)x.item * units_of(x.seq) : 0) + x.unit;
+    return x;
   };
-  const int64_t u0 = cta < N ? unit_at(cta * places / N) : 0, u1 = cta < N ? unit_at((cta + 1) * places / N) : 0;
+  int64_t u0, u1;
+  Unit at = unit_at(div_pos(cta * places, N), u0);  // the unit in hand
+  if (cta + 1 < N)
+    unit_at(div_pos((cta + 1) * places, N), u1);
+  else
+    u1 = s_first[n_seq] * items;
   const int steps = (int)(u1 - u0);
-
-  // the sequence that holds unit u: the last whose items start at or before it
-  auto seq_of = [&](int64_t u) {
-    int lo = 0, hi = n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (u_first(mid) <= u) lo = mid; else hi = mid;
-    }
-    return lo;
-  };
-
-  // The last item that starts in a run is the only one of them that may be cut: entry `cta` tells of it.
-  // (Where few items are joined one by one, item i's entry tells of item i.)
-  if (!p.by_item && tid == 0) {
-    AttnCut cut{};
-    if (steps > 0) {
-      const int b = seq_of(u1 - 1);
-      const int64_t nu = s_first[b + 1] - s_first[b];
-      const int hr = (int)((u1 - 1 - u_first(b)) / nu);
-      const int64_t v = v_first(b) + hr * (nu + AT_PAD), i0 = u_first(b) + hr * nu;
-      const int last = run_of(v + nu - 1, places, N);
-      if (i0 >= u0 && last > cta) cut = {cta, last - cta + 1, b, hr / p.tiles, hr % p.tiles};
-    }
-    p.ws.cut[cta] = cut;
-  }
   if (steps == 0) return;
 
   // ------------------------------------------------------------ the ring
-  const int gpp = a.c.page_size / KV_GROUP;  // records of a page and head
+  const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
   uint8_t* const ring = s_ring + (size_t)warp * C::STAGES * C::STAGE;
   const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::BARS);
   // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
   // so that the load has the whole batch before to arrive.
   int nx_page = -1, nx_off = 0;
   bool nx_in = false;
+  Unit ahead_at = at;  // of the batch's first step
   auto look_up = [&](int base) {
     nx_in = false;
     nx_page = -1;
-    if (base + lane < steps) {
-      const int64_t u = u0 + base + lane;
-      const int b = seq_of(u);
-      const int64_t nu = s_first[b + 1] - s_first[b], rem = u - u_first(b);
-      const int hr = (int)(rem / nu), un = (int)(rem - hr * nu);
-      const SeqSpan sp = span_of(a, s_len[b]);
-      const int64_t grp = (int64_t)(sp.unit + un) * AT_WARPS + warp;
+    Unit x = ahead_at;
+    x.unit += lane;
+    int n = units_of(x.seq);
+    const int most = steps - base;  // steps from here on
+    if (lane < most) {
+      while (x.unit >= n) {
+        x.unit -= n;
+        if (++x.item == items) {
+          x.item = 0;
+          n = units_of(++x.seq);
+        }
+      }
+      const SeqSpan sp = span_of(a, s_len[x.seq]);
+      const int64_t grp = (int64_t)(sp.unit + x.unit) * AT_WARPS + warp;
       if (grp * KV_GROUP < sp.hi && grp * KV_GROUP + KV_GROUP > sp.lo) {
         nx_in = true;
-        nx_page = a.c.page_table[(size_t)b * a.c.max_pages + (int)(grp / gpp)];
-        nx_off = (hr / p.tiles) * gpp + (int)(grp % gpp);
+        nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (int)(grp >> gpp_log)];
+        nx_off = x.item / p.tiles * gpp + ((int)grp & (gpp - 1));
+      }
+    }
+    if (most > 32) {  // on to the next batch: one behind lane 31's
+      ahead_at.seq = __shfl_sync(0xffffffffu, x.seq, 31);
+      ahead_at.item = __shfl_sync(0xffffffffu, x.item, 31);
+      ahead_at.unit = __shfl_sync(0xffffffffu, x.unit, 31) + 1;
+      if (ahead_at.unit == units_of(ahead_at.seq)) {
+        ahead_at.unit = 0;
+        if (++ahead_at.item == items) {
+          ahead_at.item = 0;
+          ++ahead_at.seq;
+        }
       }
     }
   };
@@ -407,25 +434,26 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   // --------------------------------------------------------------- items
   const int rows = p.group * a.ncols;
   int turn = 0;  // of the statistics' two buffers
-  int64_t u = u0;
   int step = 0;
   uint32_t valid = 0;
-  int b = seq_of(u0);
-  while (u < u1) {
-    while (u_first(b + 1) <= u) ++b;
-    const int64_t nu = s_first[b + 1] - s_first[b], base = u_first(b);
-    const int hr = (int)((u - base) / nu);
-    const int64_t i0 = base + hr * nu, i1 = i0 + nu;
-    const int64_t uend = i1 < u1 ? i1 : u1;
-    const int head = hr / p.tiles, tile = hr % p.tiles;
+  while (step < steps) {
+    const int b = at.seq, hr = at.item, nu = units_of(b);
+    const int todo = nu - at.unit < steps - step ? nu - at.unit : steps - step;  // units of this run in the item
+    const bool starts = at.unit == 0, whole = starts && todo == nu;
+    const int head = hr / p.tiles, tile = hr - head * p.tiles;
     const int len = s_len[b];
     const SeqSpan sp = span_of(a, len);
-    if (p.by_item && tid == 0 && i0 >= u0) {
-      const int64_t v = v_first(b) + hr * (nu + AT_PAD);
-      const int last = run_of(v + nu - 1, places, N);
+    int tok = (int)(((int64_t)sp.unit + at.unit) * AT_WARPS + warp) * KV_GROUP - AT_UNIT;
+    if (tid == 0 && starts && (p.by_item || !whole)) {
+      const int64_t v = v_first(b) + (int64_t)hr * (nu + AT_PAD);
       AttnCut cut{};
-      if (last > cta) cut = {cta, last - cta + 1, b, head, tile};
-      p.ws.cut[b * items + hr] = cut;
+      if (!whole) cut = {cta, run_of(v + nu - 1, places, N) - cta + 1, b, head, tile};
+      p.ws.cut[p.by_item ? b * items + hr : cta] = cut;
+    }
+    at.unit = 0;  // (the next item's first, if there is one)
+    if (++at.item == items) {
+      at.item = 0;
+      ++at.seq;
     }
 
     // what row r of the tile sees: tokens lo < j <= hi
@@ -514,8 +542,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
 
-    int tok = (int)(((int64_t)sp.unit + (u - i0)) * AT_WARPS + warp) * KV_GROUP - AT_UNIT;
-    for (int left = (int)(uend - u); left > 0; --left, ++step) {
+    for (const int end = step + todo; step < end; ++step) {
       tok += AT_UNIT;
       if ((step & 31) == 0) valid = (step & 32) ? valid_odd : valid_even;
       const uint32_t kb = ring_at + stage * C::STAGE, vb = kb + C::HALF;
@@ -828,9 +855,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       }
       next();
     }
-    u = uend;
 
     // ------------------------------------------------ the four warps' sums
+    const size_t part = (size_t)cta * 2 + (starts ? 1 : 0);
     float* const s_z = s_stat + turn * (2 * AT_WARPS + 2) * ROWS;  // [warp][row]
     float* const s_l = s_z + AT_WARPS * ROWS;                       // [warp][row]
     float* const s_top = s_l + AT_WARPS * ROWS;                     // [row]
@@ -873,8 +900,6 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s_top[tid] = top;
       s_sum[tid] = sum;
     }
-    const bool whole = u0 <= i0 && i1 <= u1;
-    const size_t part = (size_t)cta * 2 + (i0 < u0 ? 0 : 1);
 #pragma unroll
     for (int pass = 0; pass < D / C::OD; ++pass) {
       if (pass) __syncthreads();  // the buffer has been read
@@ -912,7 +937,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
               make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
         } else {
           *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
-          if (at == 0) *reinterpret_cast<float2*>(p.ws.ml + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
+          if (at == 0) *reinterpret_cast<float2*>(p.ws.zl + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
         }
       }
     }
@@ -944,7 +969,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
   // part i: the first CTA's run ends in the item (its second slot), the others' start in it
   auto slot = [&](int i) { return ((size_t)(cut.c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
   auto stat = [&](int i) {
-    return i < n ? *reinterpret_cast<const float2*>(p.ws.ml + slot(i) * 2) : make_float2(-INFINITY, 0.f);
+    return i < n ? *reinterpret_cast<const float2*>(p.ws.zl + slot(i) * 2) : make_float2(-INFINITY, 0.f);
   };
   // reference and sum over all parts
   constexpr int SPREAD = BY_ITEM ? JOIN_THREADS : 32;
@@ -1045,7 +1070,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.ws.cut = reinterpret_cast<AttnCut*>(ws);
   ws += (size_t)C::GRID * sizeof(AttnCut);
-  p.ws.ml = reinterpret_cast<float*>(ws);
+  p.ws.zl = reinterpret_cast<float*>(ws);
   ws += (size_t)C::GRID * 2 * C::ROWS * 8;
   p.ws.o = reinterpret_cast<float*>(ws);
   const size_t smem = C::smem(a.c.n_seq);
