@@ -17,6 +17,7 @@ namespace {
 
 constexpr int RD_THREADS = 256;
 constexpr int RD_WARPS = RD_THREADS / 32;
+constexpr int RD_UNROLL = 4;  // rows that a lane has in flight
 
 __device__ __forceinline__ uint32_t half2_bits(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
@@ -34,7 +35,7 @@ __device__ __forceinline__ void write8(__half* p, const float (&v)[8]) {
 template <int TYPE, class TO>
 __global__ void __launch_bounds__(RD_THREADS)
     kv_read_kernel(const __grid_constant__ qg_kvcache c, const int32_t* seqs, const int32_t* poss,
-                   int ntok, int per_seq, TO* k_out, TO* v_out, int32_t* err, int parts, int per_part) {
+                   int ntok, int per_seq, TO* k_out, TO* v_out, int32_t* err, int parts) {
   pdl_trigger();
   pdl_wait();
   const int lane = threadIdx.x & 31;
@@ -43,8 +44,8 @@ __global__ void __launch_bounds__(RD_THREADS)
   if (tok >= ntok) return;
   const int part = (int)(w - tok * parts);
   const int d = c.head_dim, lanes = d >> 3, at_once = 32 / lanes;
-  const int d0 = (lane & (lanes - 1)) * 8;
-  const int groups = c.page_size / KV_GROUP, rec = kv_record_bytes(TYPE, d);
+  const int d0 = (lane & (lanes - 1)) * 8, first = lane / lanes;
+  const int groups = c.page_size / KV_GROUP, head_bytes = groups * kv_record_bytes(TYPE, d);
   const int pos = poss[tok];
   const uint8_t* place = nullptr;
   if (pos >= 0) {
@@ -53,29 +54,53 @@ __global__ void __launch_bounds__(RD_THREADS)
     const int page = kv_page_of(c, seq, pos, &bits);
     const int slot = pos & (c.page_size - 1);
     if (page >= 0)
-      place = static_cast<const uint8_t*>(c.pool) +
-              ((size_t)page * c.n_kv_heads * groups + slot / KV_GROUP) * rec;
+      place = static_cast<const uint8_t*>(c.pool) + (size_t)page * c.n_kv_heads * head_bytes +
+              slot / KV_GROUP * kv_record_bytes(TYPE, d);
     else if (part == 0 && lane == 0 && err)
       atomicOr(err, bits);
   }
-  const int i = pos & (KV_GROUP - 1);
-  const int kv = c.n_kv_heads;
-  const int r0 = part * per_part * at_once + lane / lanes;
-#pragma unroll 4
-  for (int n = 0; n < per_part; ++n) {
-    const int r = r0 + n * at_once;
-    if (r >= 2 * kv) break;
-    const bool is_k = r < kv;
-    const int head = is_k ? r : r - kv;
-    TO* out = is_k ? k_out : v_out;
-    if (!out) continue;
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (place) {
-      const uint8_t* half = place + (size_t)head * groups * rec + (is_k ? 0 : kv_half_bytes(TYPE, d));
-      const int blk = d0 >> 5, at = blk * (KV_GROUP * 32) + i * 32 + (d0 & 31);
+  // this lane's eight elements of a half record, and their scale
+  const int i = pos & (KV_GROUP - 1), blk = d0 >> 5;
+  const int at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 2 : 1);
+  const int scale_at = KV_GROUP * d + (blk * KV_GROUP + kv_scale_place(i)) * 2;
+  const int kv = c.n_kv_heads, kg = (kv + at_once - 1) / at_once;  // row groups: keys, then values
+  TO* const ko = k_out ? k_out + tok * kv * d + d0 : nullptr;
+  TO* const vo = v_out ? v_out + tok * kv * d + d0 : nullptr;
+  for (int n = part; n < 2 * kg; n += RD_UNROLL * parts) {
+    uint4 q[RD_UNROLL];
+    uint16_t sc[RD_UNROLL];
+    TO* to[RD_UNROLL];
+#pragma unroll
+    for (int j = 0; j < RD_UNROLL; ++j) {
+      const int m = n + j * parts;
+      const bool is_v = m >= kg;
+      const int r = (is_v ? m - kg : m) * at_once + first;
+      TO* const out = is_v ? vo : ko;
+      to[j] = m < 2 * kg && r < kv && out ? out + r * d : nullptr;
+      q[j] = make_uint4(0, 0, 0, 0);
+      sc[j] = 0;
+      if (place && to[j]) {
+        const uint8_t* half = place + (size_t)((uint32_t)r * (uint32_t)head_bytes + (is_v ? kv_half_bytes(TYPE, d) : 0));
+        if constexpr (TYPE == QG_F16) {
+          q[j] = *reinterpret_cast<const uint4*>(half + at);
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(half + at);
+          q[j].x = x.x;
+          q[j].y = x.y;
+          sc[j] = *reinterpret_cast<const uint16_t*>(half + scale_at);
+        }
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < RD_UNROLL; ++j) {
+      if (!to[j]) continue;
+      if constexpr (TYPE == QG_F16 && sizeof(TO) == 2) {
+        *reinterpret_cast<uint4*>(to[j]) = q[j];
+        continue;
+      }
+      float y[8];
       if constexpr (TYPE == QG_F16) {
-        const uint4 q = *reinterpret_cast<const uint4*>(reinterpret_cast<const __half*>(half) + at);
-        const uint32_t u[4] = {q.x, q.y, q.z, q.w};
+        const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[e]));
@@ -83,16 +108,17 @@ __global__ void __launch_bounds__(RD_THREADS)
           y[2 * e + 1] = f.y;
         }
       } else {
-        const uint2 q = *reinterpret_cast<const uint2*>(half + at);
-        const float s = h2f(reinterpret_cast<const uint16_t*>(half + KV_GROUP * d)[blk * KV_GROUP + kv_scale_place(i)]);
+        // u = q + 128 as the low byte of the float 2^23 + u, exact (and 0 where there is no token)
+        const float s = h2f(sc[j]);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t b = ((e < 4 ? q.x : q.y) >> (8 * (e & 3))) & 0xffu;
-          y[e] = (float)((int)b - 128) * s;
-        }
+        for (int e = 0; e < 8; ++e)
+          y[e] = (u2f(__byte_perm(e < 4 ? q[j].x : q[j].y, MAGIC_2P23, 0x7440 + (e & 3))) - (F_2P23 + 128.f)) * s;
+        if (!place)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) y[e] = 0.f;
       }
+      write8(to[j], y);
     }
-    write8(out + (tok * kv + head) * (int64_t)d + d0, y);
   }
 }
 
@@ -100,15 +126,14 @@ template <int TYPE, class TO>
 cudaError_t read_typed(const qg_kvcache& c, const int32_t* seq, const int32_t* pos, int ntok,
                        void* k_out, void* v_out, int32_t* err, cudaStream_t s) {
   const int at_once = 256 / c.head_dim;
-  const int groups = (2 * c.n_kv_heads + at_once - 1) / at_once;
-  int parts = (152 * 32 + ntok - 1) / ntok;  // as in qg_rope.cu: rows spread over warps for few tokens
+  const int groups = 2 * ((c.n_kv_heads + at_once - 1) / at_once);
+  // a token's rows are spread over several warps while there are fewer tokens than fill the machine
+  int parts = (152 * 40 + ntok - 1) / ntok;
   if (parts > groups) parts = groups;
-  const int per_part = (groups + parts - 1) / parts;
-  parts = (groups + per_part - 1) / per_part;
   const int64_t warps = (int64_t)ntok * parts;
   return launch_pdl(kv_read_kernel<TYPE, TO>, dim3((unsigned)((warps + RD_WARPS - 1) / RD_WARPS)),
                     dim3(RD_THREADS), 0, s, 0, LC_L1, c, seq, pos, ntok, seq ? 1 : ntok / c.n_seq,
-                    static_cast<TO*>(k_out), static_cast<TO*>(v_out), err, parts, per_part);
+                    static_cast<TO*>(k_out), static_cast<TO*>(v_out), err, parts);
 }
 
 }  // namespace

@@ -1,19 +1,20 @@
 // qg_rope.cu -- rotary positions, alone (qrope) and fused with the write of the
 // paged key/value cache (qkv_append).
 //
-// Both kernels have one shape: a warp owns a token and walks over rows (heads)
-// of it. A row's D elements sit on D/8 neighbouring lanes, eight consecutive
-// elements a lane, so a warp covers 256 / D heads at a time (D rounded up to a
-// power of two). The angles depend on the token and the pair only, so a lane
-// computes the sines and cosines of its eight elements once and keeps them over
-// all heads.
+// Both kernels have one shape. A block of eight warps takes 8 / P tokens, P warps
+// each (and P x gridDim.y in all, so that few tokens still fill the machine). Its
+// threads first compute the tokens' sines and cosines, one pair each, into shared
+// memory; then each warp walks over rows (heads) of its token. A row's D elements
+// sit on D/8 neighbouring lanes, eight consecutive elements a lane, so a warp
+// covers 256 / D heads at a time (D rounded up to a power of two); a lane keeps
+// the sines and cosines of its eight elements over all rows.
 //
 // Angles: a pair's frequency is a 64-bit fixed-point fraction of a turn per
 // position. Frequency times position modulo 2^64 is then the exact fraction of
 // a turn (no large f32 angle, no f64), whose top 32 bits go to sincospif.
 //
-// Q8_0: the 32 elements of a block are on four lanes of the same quad of lanes,
-// so the block's largest magnitude is two shuffles away.
+// Q8_0: the 32 elements of a block are on four neighbouring lanes, so the
+// block's largest magnitude is two shuffles away.
 //
 // Bound by memory: 4 bytes read and 2 (f16) or 17/16 (Q8_0) written an element.
 #include <cuda_fp16.h>
@@ -29,6 +30,18 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
+constexpr int ROW_UNROLL = 2;  // rows that a lane has in flight
+
+// How the eight elements of a lane meet their partners.
+enum Layout {
+  PLAIN,   // no rotation
+  PAIRS,   // interleaved, rot_dim a multiple of 8: partners within the lane
+  HALVES,  // half layout, rot_dim a multiple of 16: partners in one other aligned group of eight
+  ANY      // everything else, element by element
+};
+Layout layout_of(const qg_rope& p) {
+  return p.interleaved ? (p.rot_dim % 8 ? ANY : PAIRS) : (p.rot_dim % 16 ? ANY : HALVES);
+}
 
 template <class T>
 __device__ __forceinline__ float elem(const T* p);
@@ -66,72 +79,97 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
       make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
 }
 
-// A lane's share of a token's rotation: y = x * c + partner * s, element by
-// element, s carrying the sign. Elements past rot_dim get c = 1, s = 0.
-struct Turn {
-  float c[8], s[8];
-};
-
-__device__ __forceinline__ void make_turn(const qg_rope& plan, const uint64_t* steps, int pos, int d0,
-                                          Turn& t) {
-  const int h = plan.rot_dim >> 1;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int d = d0 + e;
-    t.c[e] = 1.f;
-    t.s[e] = 0.f;
-    if (d < plan.rot_dim) {
-      const bool second = plan.interleaved ? (e & 1) : d >= h;
-      if (plan.interleaved && second) {  // the pair's angle is already there
-        t.c[e] = t.c[e - 1];
-        t.s[e] = -t.s[e - 1];
-        continue;
-      }
-      const int pair = plan.interleaved ? d >> 1 : (second ? d - h : d);
-      const uint64_t phase = steps[pair] * (uint64_t)(int64_t)pos;
+// Sines and cosines (times mscale) of the block's tokens: sc[token][pair].
+__device__ __forceinline__ void make_turns(const qg_rope& plan, float2* sc, const int32_t* pos, int64_t tok0,
+                                           int tokens, int64_t ntok) {
+  const int half = plan.rot_dim >> 1;
+  for (int i = threadIdx.x; i < tokens * half; i += ROW_THREADS) {
+    const int t = i / half, pair = i - t * half;
+    if (tok0 + t < ntok) {
+      const uint64_t phase = plan.step[pair] * (uint64_t)(int64_t)pos[tok0 + t];
       // the turn's fraction, signed, in half turns
       const float half_turns = (float)(int32_t)(phase >> 32) * 4.656612873077393e-10f;  // 2^-31
       float sn, cs;
       sincospif(half_turns, &sn, &cs);
-      t.c[e] = cs * plan.mscale;
-      t.s[e] = (second ? sn : -sn) * plan.mscale;
+      sc[t * (QG_ROPE_MAX_DIM / 2) + pair] = make_float2(sn * plan.mscale, cs * plan.mscale);
     }
   }
 }
 
-// The rotated values of a lane's eight elements; `row` points at the head.
-// Every element of the head is read before the caller's __syncwarp, so y may
-// overwrite x after it.
-template <class T>
-__device__ __forceinline__ void rotate8(const qg_rope& plan, const T* row, int d0, const Turn& t,
-                                        float (&y)[8]) {
-  float x[8];
-  load8(row + d0, x);
-  const int h = plan.rot_dim >> 1;
-  if (d0 >= plan.rot_dim) {
+// A lane's share of a token's rotation: elements d0 .. d0 + 7 of every row.
+template <int LAYOUT>
+struct Turn {
+  float c[LAYOUT == PAIRS ? 4 : 8], s[LAYOUT == PAIRS ? 4 : 8];
+  bool turned;   // the lane has elements that turn (all eight, but for ANY)
+  int partner;   // HALVES: offset of the other group; its sines carry the sign
+  __device__ __forceinline__ Turn(const qg_rope& plan, const float2* sc, int d0) {
+    const int rot = plan.rot_dim, h = rot >> 1;
+    turned = d0 < rot;
+    partner = 0;
+    if (!turned) return;
+    if constexpr (LAYOUT == PAIRS) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e];
-    return;
-  }
-  float o[8];
-  if (plan.interleaved) {
+      for (int i = 0; i < 4; ++i) {
+        const float2 x = sc[(d0 >> 1) + i];
+        s[i] = x.x;
+        c[i] = x.y;
+      }
+    } else if constexpr (LAYOUT == HALVES) {
+      partner = d0 < h ? h : -h;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) o[e] = x[e ^ 1];
-  } else if ((h & 7) == 0) {
-    load8(row + (d0 < h ? d0 + h : d0 - h), o);
-  } else {
+      for (int e = 0; e < 8; ++e) {
+        const float2 x = sc[(d0 < h ? d0 : d0 - h) + e];
+        s[e] = d0 < h ? -x.x : x.x;
+        c[e] = x.y;
+      }
+    } else if constexpr (LAYOUT == ANY) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int d = d0 + e;
-      o[e] = d < plan.rot_dim ? elem(row + (d < h ? d + h : d - h)) : 0.f;
+      for (int e = 0; e < 8; ++e) {
+        const int d = d0 + e;
+        c[e] = 1.f;
+        s[e] = 0.f;
+        if (d < rot) {
+          const bool second = plan.interleaved ? (d & 1) : d >= h;
+          const float2 x = sc[plan.interleaved ? d >> 1 : second ? d - h : d];
+          c[e] = x.y;
+          s[e] = second ? x.x : -x.x;
+        }
+      }
     }
   }
+  // The turned values of a lane's eight elements; `row` points at element 0 of the head. Every element of
+  // the head is read before the caller's __syncwarp, so the result may overwrite it after.
+  template <class T>
+  __device__ __forceinline__ void apply(const qg_rope& plan, const T* row, int d0, float (&y)[8]) const {
+    float x[8];
+    load8(row + d0, x);
+    if (LAYOUT == PLAIN || !turned) {
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const bool in = d0 + e < plan.rot_dim;
-    y[e] = in ? fmaf(x[e], t.c[e], o[e] * t.s[e]) : x[e];
+      for (int e = 0; e < 8; ++e) y[e] = x[e];
+      return;
+    }
+    if constexpr (LAYOUT == PAIRS) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        y[2 * i] = fmaf(x[2 * i], c[i], -(x[2 * i + 1] * s[i]));
+        y[2 * i + 1] = fmaf(x[2 * i + 1], c[i], x[2 * i] * s[i]);
+      }
+    } else if constexpr (LAYOUT == HALVES) {
+      float o[8];
+      load8(row + d0 + partner, o);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = fmaf(x[e], c[e], o[e] * s[e]);
+    } else {
+      const int rot = plan.rot_dim, h = rot >> 1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int d = d0 + e;
+        y[e] = x[e];
+        if (d < rot) y[e] = fmaf(x[e], c[e], elem(row + (plan.interleaved ? d ^ 1 : d < h ? d + h : d - h)) * s[e]);
+      }
+    }
   }
-}
+};
 
 // Lanes of a row: D/8 rounded up to a power of two.
 __host__ __device__ inline int row_lanes(int d) {
@@ -140,51 +178,58 @@ __host__ __device__ inline int row_lanes(int d) {
   return l;
 }
 
+// Warps of a token: as many as fill the machine (152 SMs x 40 warps) where there are few tokens, two at
+// least, no more than it has row groups.
 struct RowSplit {
-  int parts;      // warps of a token
-  int per_part;   // row groups (of 32 / row_lanes rows) of each
+  int parts;   // warps of a token in a block: 1, 2, 4 or 8
+  dim3 grid;
 };
-// A token's rows are spread over several warps while there are fewer tokens
-// than warps that fill the machine (152 SMs x 32 warps).
-RowSplit split_rows(int ntok, int rows, int rows_at_once) {
-  const int groups = (rows + rows_at_once - 1) / rows_at_once;
-  int parts = (152 * 32 + ntok - 1) / ntok;
-  if (parts > groups) parts = groups;
-  if (parts < 1) parts = 1;
-  RowSplit s;
-  s.per_part = (groups + parts - 1) / parts;
-  s.parts = (groups + s.per_part - 1) / s.per_part;
-  return s;
+RowSplit split_rows(int ntok, int groups) {
+  int want = (152 * 40 + ntok - 1) / ntok;
+  if (want < 2) want = 2;
+  if (want > groups) want = groups;
+  RowSplit r;
+  r.parts = 1;
+  while (r.parts < want && r.parts < ROW_WARPS) r.parts *= 2;
+  const int tokens = ROW_WARPS / r.parts;
+  r.grid = dim3((unsigned)((ntok + (int64_t)tokens - 1) / tokens), (unsigned)((want + r.parts - 1) / r.parts));
+  return r;
 }
 
 // ------------------------------------------------------------------- qrope
-template <class TI, class TO>
+template <class TI, class TO, int LAYOUT>
 __global__ void __launch_bounds__(ROW_THREADS) rope_kernel(
     const __grid_constant__ qg_rope plan, const TI* x, int64_t xs, const int32_t* pos, int ntok,
-    int n_heads, int d, TO* y, int64_t ys, int parts, int per_part) {
-  __shared__ uint64_t steps[QG_ROPE_MAX_DIM / 2];
+    int n_heads, int d, TO* y, int64_t ys, int parts) {
+  __shared__ float2 sc[ROW_WARPS * (QG_ROPE_MAX_DIM / 2)];
   pdl_trigger();
-  if (threadIdx.x < plan.rot_dim / 2) steps[threadIdx.x] = plan.step[threadIdx.x];
-  __syncthreads();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-  const int64_t tok = w / parts;
+  const int tokens = ROW_WARPS / parts;
+  const int64_t tok0 = (int64_t)blockIdx.x * tokens;
+  make_turns(plan, sc, pos, tok0, tokens, ntok);
+  __syncthreads();
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tok = tok0 + warp / parts;
   if (tok >= ntok) return;
-  const int part = (int)(w - tok * parts);
-  const int lanes = row_lanes(d), at_once = 32 / lanes;
-  const int d0 = (lane & (lanes - 1)) * 8;
-  const bool on = d0 < d;
-  Turn t;
-  make_turn(plan, steps, pos[tok], d0, t);
-  const int r0 = part * per_part * at_once + lane / lanes;
-  for (int i = 0; i < per_part; ++i) {
-    const int r = r0 + i * at_once;
-    const bool live = on && r < n_heads;
-    float v[8];
-    if (live) rotate8(plan, x + tok * xs + (int64_t)r * d, d0, t, v);
-    __syncwarp();
-    if (live) store8(y + tok * ys + (int64_t)r * d + d0, v);
+  const int lanes = row_lanes(d), at_once = 32 / lanes, d0 = (lane & (lanes - 1)) * 8;
+  const int step = at_once * parts * gridDim.y;
+  int r = (warp % parts + parts * blockIdx.y) * at_once + lane / lanes;
+  const Turn<LAYOUT> t(plan, sc + warp / parts * (QG_ROPE_MAX_DIM / 2), d0);
+  const TI* xr = x + tok * xs + (int64_t)r * d;
+  TO* yr = y + tok * ys + (int64_t)r * d + d0;
+  const int64_t hop = (int64_t)step * d;
+  if (d0 >= d) r = n_heads;  // no elements for this lane
+  for (; __any_sync(0xffffffffu, r < n_heads); r += ROW_UNROLL * step) {
+    float v[ROW_UNROLL][8];
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j)
+      if (r + j * step < n_heads) t.apply(plan, xr + j * hop, d0, v[j]);
+    __syncwarp();  // in place: the rows have been read
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j)
+      if (r + j * step < n_heads) store8(yr + j * hop, v[j]);
+    xr += ROW_UNROLL * hop;
+    yr += ROW_UNROLL * hop;
   }
 }
 
@@ -199,8 +244,7 @@ struct AppendParams {
   const int32_t *seq, *pos;
   int ntok, per_seq;  // per_seq: tokens of a sequence when seq is NULL
   int32_t* err;
-  int parts, per_part;
-  int rotate;
+  int parts;
 };
 
 // Eight elements of a row into the record of (token slot, head).
@@ -243,61 +287,83 @@ __device__ __forceinline__ void put8(uint8_t* half, int d0, int d, int i, float 
   }
 }
 
-template <class T, int TYPE>
+template <class T, int TYPE, int LAYOUT>
 __global__ void __launch_bounds__(ROW_THREADS)
     append_kernel(const __grid_constant__ qg_rope plan, const __grid_constant__ AppendParams<T> a) {
-  __shared__ uint64_t steps[QG_ROPE_MAX_DIM / 2];
+  __shared__ float2 sc[ROW_WARPS * (QG_ROPE_MAX_DIM / 2)];
   pdl_trigger();
-  if (threadIdx.x < plan.rot_dim / 2) steps[threadIdx.x] = plan.step[threadIdx.x];
-  __syncthreads();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t w = (int64_t)blockIdx.x * ROW_WARPS + (threadIdx.x >> 5);
-  const int64_t tok = w / a.parts;
-  if (tok >= a.ntok) return;
-  const int part = (int)(w - tok * a.parts);
-  const int d = a.c.head_dim;
-  const int lanes = d >> 3, at_once = 32 / lanes;
-  const int d0 = (lane & (lanes - 1)) * 8;
-  const int pos = a.pos[tok];
-  Turn t;
-  if (a.rotate) make_turn(plan, steps, pos, d0, t);
-
+  const int tokens = ROW_WARPS / a.parts;
+  const int64_t tok0 = (int64_t)blockIdx.x * tokens;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int64_t tok = tok0 + warp / a.parts;
+  const int d = a.c.head_dim, lanes = d >> 3, at_once = 32 / lanes, d0 = (lane & (lanes - 1)) * 8;
   // the token's place in the cache (NULL: nowhere)
   uint8_t* place = nullptr;
   const int groups = a.c.page_size / KV_GROUP, rec = kv_record_bytes(TYPE, d);
-  if (pos >= 0) {
-    int bits = 0;
-    const int seq = a.seq ? a.seq[tok] : (int)(tok / a.per_seq);
-    const int page = kv_page_of(a.c, seq, pos, &bits);
-    const int slot = pos & (a.c.page_size - 1);
-    if (page >= 0)
-      place = static_cast<uint8_t*>(a.c.pool) +
-              ((size_t)page * a.c.n_kv_heads * groups + slot / KV_GROUP) * rec;
-    else if (part == 0 && lane == 0 && a.err)
-      atomicOr(a.err, bits);
-  }
-  const int in_group = pos & (KV_GROUP - 1);
-  const int kv = a.c.n_kv_heads, rows = a.n_q + 2 * kv;
-  const int r0 = part * a.per_part * at_once + lane / lanes;
-  for (int i = 0; i < a.per_part; ++i) {
-    const int r = r0 + i * at_once;
-    if (r - lane / lanes >= rows) break;  // the whole warp is past the end
-    const bool in = r < rows;
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    const bool is_q = r < a.n_q, is_k = !is_q && r < a.n_q + kv;
-    const int head = is_q ? r : is_k ? r - a.n_q : r - a.n_q - kv;
-    if (in) {
-      const T* row = is_q ? a.q + tok * a.qs : is_k ? a.k + tok * a.ks : a.v + tok * a.vs;
-      row += (int64_t)head * d;
-      if (a.rotate && (is_q || is_k))
-        rotate8(plan, row, d0, t, y);
-      else
-        load8(row + d0, y);
+  int in_group = 0;
+  const int part = warp % a.parts + a.parts * blockIdx.y, all_parts = a.parts * gridDim.y;
+  if (tok < a.ntok) {
+    const int pos = a.pos[tok];
+    if (pos >= 0) {
+      int bits = 0;
+      const int seq = a.seq ? a.seq[tok] : (int)(tok / a.per_seq);
+      const int page = kv_page_of(a.c, seq, pos, &bits);
+      const int slot = pos & (a.c.page_size - 1);
+      in_group = slot & (KV_GROUP - 1);
+      if (page >= 0)
+        place = static_cast<uint8_t*>(a.c.pool) + ((size_t)page * a.c.n_kv_heads * groups + slot / KV_GROUP) * rec;
+      else if (part == 0 && lane == 0 && a.err)
+        atomicOr(a.err, bits);
     }
-    if (in && is_q) store8(a.q_out + (tok * a.n_q + head) * (int64_t)d + d0, y);
-    uint8_t* half = place + (size_t)head * groups * rec + (is_k ? 0 : kv_half_bytes(TYPE, d));
-    put8<TYPE>(half, d0, d, in_group, y, in && !is_q && place != nullptr);
+  }
+  if (LAYOUT != PLAIN) {
+    make_turns(plan, sc, a.pos, tok0, tokens, a.ntok);
+    __syncthreads();
+  }
+  if (tok >= a.ntok) return;
+  const Turn<LAYOUT> t(plan, sc + warp / a.parts * (QG_ROPE_MAX_DIM / 2), d0);
+  // Row groups of the token in order: queries, keys, values; the parts take them in turn.
+  const int first = lane / lanes;
+  const int qg = (a.n_q + at_once - 1) / at_once, kg = (a.c.n_kv_heads + at_once - 1) / at_once;
+  int n = part;
+  for (; n < qg; n += ROW_UNROLL * all_parts) {
+    float y[ROW_UNROLL][8];
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j) {
+      const int r = (n + j * all_parts) * at_once + first;
+      if (r < a.n_q) t.apply(plan, a.q + tok * a.qs + (int64_t)r * d, d0, y[j]);
+    }
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j) {
+      const int r = (n + j * all_parts) * at_once + first;
+      if (r < a.n_q) store8(a.q_out + (tok * a.n_q + r) * (int64_t)d + d0, y[j]);
+    }
+  }
+  // (the unrolled loop may have stepped over this part's first key group)
+  n = part;
+  if (qg > part) n += (qg - part + all_parts - 1) / all_parts * all_parts;
+  for (n -= qg; n < 2 * kg; n += ROW_UNROLL * all_parts) {
+    float y[ROW_UNROLL][8];
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j) {
+      const int m = n + j * all_parts, is_v = m >= kg, r = (is_v ? m - kg : m) * at_once + first;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[j][e] = 0.f;
+      if (m < 2 * kg && r < a.c.n_kv_heads) {
+        if (is_v)
+          load8(a.v + tok * a.vs + (int64_t)r * d + d0, y[j]);
+        else
+          t.apply(plan, a.k + tok * a.ks + (int64_t)r * d, d0, y[j]);
+      }
+    }
+#pragma unroll
+    for (int j = 0; j < ROW_UNROLL; ++j) {
+      const int m = n + j * all_parts, is_v = m >= kg, r = (is_v ? m - kg : m) * at_once + first;
+      const bool live = m < 2 * kg && r < a.c.n_kv_heads && place != nullptr;
+      uint8_t* const half = live ? place + (size_t)r * groups * rec + (is_v ? kv_half_bytes(TYPE, d) : 0) : nullptr;
+      put8<TYPE>(half, d0, d, in_group, y[j], live);
+    }
   }
 }
 
@@ -315,25 +381,31 @@ cudaError_t append_typed(const KvAppendArgs& a, cudaStream_t s) {
   p.ntok = a.ntok;
   p.per_seq = a.seq ? 1 : a.ntok / a.c.n_seq;
   p.err = a.err;
-  p.rotate = a.rope != nullptr;
-  const RowSplit sp = split_rows(a.ntok, a.n_q + 2 * a.c.n_kv_heads, 256 / a.c.head_dim);
+  const int at_once = 256 / a.c.head_dim;
+  const int kg = (a.c.n_kv_heads + at_once - 1) / at_once, qg = (a.n_q + at_once - 1) / at_once;
+  const RowSplit sp = split_rows(a.ntok, qg + 2 * kg);
   p.parts = sp.parts;
-  p.per_part = sp.per_part;
   qg_rope plan{};
   if (a.rope) plan = *a.rope;
-  const int64_t warps = (int64_t)a.ntok * sp.parts;
-  return launch_pdl(append_kernel<T, TYPE>, dim3((unsigned)((warps + ROW_WARPS - 1) / ROW_WARPS)),
-                    dim3(ROW_THREADS), 0, s, 0, LC_L1, plan, p);
+  const Layout l = a.rope ? layout_of(plan) : PLAIN;
+  const auto kern = l == PLAIN    ? append_kernel<T, TYPE, PLAIN>
+                    : l == PAIRS  ? append_kernel<T, TYPE, PAIRS>
+                    : l == HALVES ? append_kernel<T, TYPE, HALVES>
+                                  : append_kernel<T, TYPE, ANY>;
+  return launch_pdl(kern, sp.grid, dim3(ROW_THREADS), 0, s, 0, LC_L1, plan, p);
 }
 
 template <class TI, class TO>
 cudaError_t rope_typed(const qg_rope& plan, const void* x, int64_t xs, const int32_t* pos, int ntok,
                        int n_heads, int d, void* y, int64_t ys, cudaStream_t s) {
-  const RowSplit sp = split_rows(ntok, n_heads, 32 / row_lanes(d));
-  const int64_t warps = (int64_t)ntok * sp.parts;
-  return launch_pdl(rope_kernel<TI, TO>, dim3((unsigned)((warps + ROW_WARPS - 1) / ROW_WARPS)),
-                    dim3(ROW_THREADS), 0, s, 0, LC_L1, plan, static_cast<const TI*>(x), xs, pos, ntok,
-                    n_heads, d, static_cast<TO*>(y), ys, sp.parts, sp.per_part);
+  const int at_once = 32 / row_lanes(d);
+  const RowSplit sp = split_rows(ntok, (n_heads + at_once - 1) / at_once);
+  const Layout l = layout_of(plan);
+  const auto kern = l == PAIRS    ? rope_kernel<TI, TO, PAIRS>
+                    : l == HALVES ? rope_kernel<TI, TO, HALVES>
+                                  : rope_kernel<TI, TO, ANY>;
+  return launch_pdl(kern, sp.grid, dim3(ROW_THREADS), 0, s, 0, LC_L1, plan, static_cast<const TI*>(x), xs, pos, ntok,
+                    n_heads, d, static_cast<TO*>(y), ys, sp.parts);
 }
 
 }  // namespace
