@@ -133,11 +133,19 @@ def _ptr(t):
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = _device = None
+
+
 def _stream(stream):
+    """The stream's handle; None: the current stream of the current device."""
+    global _raw_stream, _device
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-    return torch.cuda.current_stream().cuda_stream
+    if _raw_stream is None:
+        import torch
+        torch.cuda.current_stream()  # sets torch's CUDA side up
+        _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+    return _raw_stream(_device())  # the handle itself, without a Stream object (2.9 us against 0.1)
 
 
 def qgemv_q4_0(nib, scl, x, y, y0=None, stream=None):

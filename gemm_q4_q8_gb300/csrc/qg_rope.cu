@@ -30,7 +30,10 @@ namespace {
 
 constexpr int ROW_THREADS = 256;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
-constexpr int ROW_UNROLL = 2;  // rows that a lane has in flight
+// Blocks that share an SM: the rows' loads hide behind other warps (48 of them), not behind more rows a lane; 8,191 x 40
+// x 128 from f32 to f16 takes 40.1 us so, 42.5 with two rows and 46.6 with four rows a lane in flight.
+constexpr int ROW_BLOCKS = 6;
+constexpr int APPEND_BLOCKS = 5;  // its rows need more registers (a prompt of 16,382 tokens: 153 us with 5, 154 with 6, 166 with 7)
 
 // How the eight elements of a lane meet their partners.
 enum Layout {
@@ -66,6 +69,17 @@ __device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
     v[2 * i + 1] = f.y;
   }
 }
+// Four consecutive elements, aligned to four.
+__device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
+  const float4 a = *reinterpret_cast<const float4*>(p);
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+}
+__device__ __forceinline__ void load4(const __half* p, float (&v)[4]) {
+  const uint2 w = *reinterpret_cast<const uint2*>(p);
+  const float2 a = __half22float2(*reinterpret_cast<const __half2*>(&w.x));
+  const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
+  v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
+}
 __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const __half2 h = __floats2half2_rn(a, b);
   return *reinterpret_cast<const uint32_t*>(&h);
@@ -73,6 +87,12 @@ __device__ __forceinline__ uint32_t pack2(float a, float b) {
 __device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
   reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
   reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+__device__ __forceinline__ void store4(float* p, const float* v) {
+  *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+}
+__device__ __forceinline__ void store4(__half* p, const float* v) {
+  *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
 __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
@@ -171,6 +191,54 @@ struct Turn {
   }
 };
 
+// Where a row need not come out as aligned groups of eight, HALVES is done by quads: lane l < rot_dim / 8 turns the
+// pairs 4l .. 4l+3, elements 4l .. and rot_dim/2 + 4l .., and every element is read once.
+template <int LAYOUT>
+struct RowTurn : Turn<LAYOUT> {
+  using Turn<LAYOUT>::Turn;
+  template <class TI>
+  __device__ __forceinline__ void read(const qg_rope& plan, const TI* row, int d0, float (&y)[8]) const {
+    this->apply(plan, row, d0, y);
+  }
+  template <class TO>
+  __device__ __forceinline__ void write(TO* row, int d0, const float (&y)[8]) const {
+    store8(row + d0, y);
+  }
+};
+template <>
+struct RowTurn<HALVES> {
+  float c[4], s[4];
+  int a, b;  // the lane's two quads
+  bool turned;
+  __device__ __forceinline__ RowTurn(const qg_rope& plan, const float2* sc, int d0) {
+    turned = d0 < plan.rot_dim;
+    a = turned ? d0 >> 1 : d0;
+    b = turned ? (plan.rot_dim + d0) >> 1 : d0 + 4;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const float2 x = turned ? sc[a + i] : make_float2(0.f, 1.f);
+      s[i] = x.x;
+      c[i] = x.y;
+    }
+  }
+  template <class TI>
+  __device__ __forceinline__ void read(const qg_rope&, const TI* row, int, float (&y)[8]) const {
+    float u[4], v[4];
+    load4(row + a, u);
+    load4(row + b, v);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = turned ? fmaf(u[i], c[i], -(v[i] * s[i])) : u[i];
+      y[4 + i] = turned ? fmaf(v[i], c[i], u[i] * s[i]) : v[i];
+    }
+  }
+  template <class TO>
+  __device__ __forceinline__ void write(TO* row, int, const float (&y)[8]) const {
+    store4(row + a, y);
+    store4(row + b, y + 4);
+  }
+};
+
 // Lanes of a row: D/8 rounded up to a power of two.
 __host__ __device__ inline int row_lanes(int d) {
   int l = 1;
@@ -198,7 +266,7 @@ RowSplit split_rows(int ntok, int groups) {
 
 // ------------------------------------------------------------------- qrope
 template <class TI, class TO, int LAYOUT>
-__global__ void __launch_bounds__(ROW_THREADS) rope_kernel(
+__global__ void __launch_bounds__(ROW_THREADS, ROW_BLOCKS) rope_kernel(
     const __grid_constant__ qg_rope plan, const TI* x, int64_t xs, const int32_t* pos, int ntok,
     int n_heads, int d, TO* y, int64_t ys, int parts) {
   __shared__ float2 sc[ROW_WARPS * (QG_ROPE_MAX_DIM / 2)];
@@ -214,22 +282,18 @@ __global__ void __launch_bounds__(ROW_THREADS) rope_kernel(
   const int lanes = row_lanes(d), at_once = 32 / lanes, d0 = (lane & (lanes - 1)) * 8;
   const int step = at_once * parts * gridDim.y;
   int r = (warp % parts + parts * blockIdx.y) * at_once + lane / lanes;
-  const Turn<LAYOUT> t(plan, sc + warp / parts * (QG_ROPE_MAX_DIM / 2), d0);
+  const RowTurn<LAYOUT> t(plan, sc + warp / parts * (QG_ROPE_MAX_DIM / 2), d0);
   const TI* xr = x + tok * xs + (int64_t)r * d;
-  TO* yr = y + tok * ys + (int64_t)r * d + d0;
+  TO* yr = y + tok * ys + (int64_t)r * d;
   const int64_t hop = (int64_t)step * d;
   if (d0 >= d) r = n_heads;  // no elements for this lane
-  for (; __any_sync(0xffffffffu, r < n_heads); r += ROW_UNROLL * step) {
-    float v[ROW_UNROLL][8];
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j)
-      if (r + j * step < n_heads) t.apply(plan, xr + j * hop, d0, v[j]);
-    __syncwarp();  // in place: the rows have been read
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j)
-      if (r + j * step < n_heads) store8(yr + j * hop, v[j]);
-    xr += ROW_UNROLL * hop;
-    yr += ROW_UNROLL * hop;
+  for (; __any_sync(0xffffffffu, r < n_heads); r += step) {
+    float v[8];
+    if (r < n_heads) t.read(plan, xr, d0, v);
+    __syncwarp();  // in place: the row has been read
+    if (r < n_heads) t.write(yr, d0, v);
+    xr += hop;
+    yr += hop;
   }
 }
 
@@ -268,15 +332,26 @@ __device__ __forceinline__ void put8(uint8_t* half, int d0, int d, int i, float 
     uint16_t bits = __half_as_ushort(__float2half_ru(__fdiv_rn(top, 127.f)));
     if (bits > 0x7BFF) bits = 0x7BFF;
     if (bad) bits = 0x7FFF;
-    const float ds = __half2float(__ushort_as_half(bits));
     uint32_t w[2] = {0x80808080u, 0x80808080u};
     if (!bad && bits != 0) {
+      // x / d by the reciprocal is off by less than 1e-4; only next to a half is the division needed to know
+      // its nearest integer q. 1.5 2^23 + 128 + q has q + 128 as its low byte.
+      const float ds = __half2float(__ushort_as_half(bits)), inv = __frcp_rn(ds), magic = 12582912.f + 128.f;
+      uint32_t b[8];
+      bool close = false;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const float r = fminf(fmaxf(rintf(__fdiv_rn(y[e], ds)), -127.f), 127.f);
-        const uint32_t b = (uint32_t)((int)r + 128);
-        w[e >> 2] = (w[e >> 2] & ~(0xffu << (8 * (e & 3)))) | (b << (8 * (e & 3)));
+        const float q = fminf(fmaxf(y[e] * inv, -127.f), 127.f);
+        const float m = q + magic;
+        close |= fabsf(q - (m - magic)) > 0.4998f;
+        b[e] = __float_as_uint(m);
       }
+      if (close)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(fminf(fmaxf(__fdiv_rn(y[e], ds), -127.f), 127.f) + magic);
+#pragma unroll
+      for (int h = 0; h < 2; ++h)
+        w[h] = __byte_perm(__byte_perm(b[4 * h], b[4 * h + 1], 0x0040), __byte_perm(b[4 * h + 2], b[4 * h + 3], 0x0040), 0x5410);
     }
     if (live) {
       const int blk = d0 >> 5;
@@ -288,7 +363,7 @@ __device__ __forceinline__ void put8(uint8_t* half, int d0, int d, int i, float 
 }
 
 template <class T, int TYPE, int LAYOUT>
-__global__ void __launch_bounds__(ROW_THREADS)
+__global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     append_kernel(const __grid_constant__ qg_rope plan, const __grid_constant__ AppendParams<T> a) {
   __shared__ float2 sc[ROW_WARPS * (QG_ROPE_MAX_DIM / 2)];
   pdl_trigger();
@@ -322,48 +397,36 @@ __global__ void __launch_bounds__(ROW_THREADS)
     __syncthreads();
   }
   if (tok >= a.ntok) return;
-  const Turn<LAYOUT> t(plan, sc + warp / a.parts * (QG_ROPE_MAX_DIM / 2), d0);
   // Row groups of the token in order: queries, keys, values; the parts take them in turn.
   const int first = lane / lanes;
   const int qg = (a.n_q + at_once - 1) / at_once, kg = (a.c.n_kv_heads + at_once - 1) / at_once;
+  const float2* const my_sc = sc + warp / a.parts * (QG_ROPE_MAX_DIM / 2);
   int n = part;
-  for (; n < qg; n += ROW_UNROLL * all_parts) {
-    float y[ROW_UNROLL][8];
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j) {
-      const int r = (n + j * all_parts) * at_once + first;
-      if (r < a.n_q) t.apply(plan, a.q + tok * a.qs + (int64_t)r * d, d0, y[j]);
-    }
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j) {
-      const int r = (n + j * all_parts) * at_once + first;
-      if (r < a.n_q) store8(a.q_out + (tok * a.n_q + r) * (int64_t)d + d0, y[j]);
-    }
-  }
-  // (the unrolled loop may have stepped over this part's first key group)
-  n = part;
-  if (qg > part) n += (qg - part + all_parts - 1) / all_parts * all_parts;
-  for (n -= qg; n < 2 * kg; n += ROW_UNROLL * all_parts) {
-    float y[ROW_UNROLL][8];
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j) {
-      const int m = n + j * all_parts, is_v = m >= kg, r = (is_v ? m - kg : m) * at_once + first;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[j][e] = 0.f;
-      if (m < 2 * kg && r < a.c.n_kv_heads) {
-        if (is_v)
-          load8(a.v + tok * a.vs + (int64_t)r * d + d0, y[j]);
-        else
-          t.apply(plan, a.k + tok * a.ks + (int64_t)r * d, d0, y[j]);
+  {
+    const RowTurn<LAYOUT> t(plan, my_sc, d0);
+    for (; n < qg; n += all_parts) {
+      const int r = n * at_once + first;
+      if (r < a.n_q) {
+        float y[8];
+        t.read(plan, a.q + tok * a.qs + (int64_t)r * d, d0, y);
+        t.write(a.q_out + (tok * a.n_q + r) * (int64_t)d, d0, y);
       }
     }
-#pragma unroll
-    for (int j = 0; j < ROW_UNROLL; ++j) {
-      const int m = n + j * all_parts, is_v = m >= kg, r = (is_v ? m - kg : m) * at_once + first;
-      const bool live = m < 2 * kg && r < a.c.n_kv_heads && place != nullptr;
-      uint8_t* const half = live ? place + (size_t)r * groups * rec + (is_v ? kv_half_bytes(TYPE, d) : 0) : nullptr;
-      put8<TYPE>(half, d0, d, in_group, y[j], live);
+  }
+  const Turn<LAYOUT> t(plan, my_sc, d0);
+  for (n -= qg; n < 2 * kg; n += all_parts) {
+    const bool is_v = n >= kg;
+    const int r = (is_v ? n - kg : n) * at_once + first;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < a.c.n_kv_heads) {
+      if (is_v)
+        load8(a.v + tok * a.vs + (int64_t)r * d + d0, y);
+      else
+        t.apply(plan, a.k + tok * a.ks + (int64_t)r * d, d0, y);
     }
+    const bool live = r < a.c.n_kv_heads && place != nullptr;
+    uint8_t* const half = live ? place + (size_t)r * groups * rec + (is_v ? kv_half_bytes(TYPE, d) : 0) : nullptr;
+    put8<TYPE>(half, d0, d, in_group, y, live);
   }
 }
 
