@@ -237,6 +237,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
   __shared__ int64_t s_part[AT_WARPS];
 
+  uint32_t k64;  // the high bytes of f16 1024 + u, in a register that is not made anew at each use
+  asm volatile("mov.b32 %0, 0x64646464;" : "=r"(k64));
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
@@ -290,38 +292,39 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   // (Where few items are joined one by one, item i's entry tells of item i.)
   if (!p.by_item && tid == 0) p.ws.cut[cta].n = 0;
   if (cta >= N) return;
-  // the first unit at or behind a place
+  // the first unit at or behind a place; `before`: sequences that start at or before the place
   struct Unit {
     int seq, item, unit;  // item of the sequence, unit of the item
   };
-  auto unit_at = [&](int64_t v, int64_t& number) {
-    int lo = 0, hi = n_seq;
-    while (hi - lo > 1) {
-      const int mid = (lo + hi) >> 1;
-      if (v_first(mid) <= v) lo = mid; else hi = mid;
-    }
-    const int n = units_of(lo);
-    const int64_t rem = v - v_first(lo);
+  auto unit_at = [&](int64_t v, int before, int64_t& number) {
     Unit x;
-    x.seq = lo;
+    x.seq = before - 1;
+    int n = units_of(x.seq);
+    const int64_t rem = v - v_first(x.seq);
     x.item = (int)div_pos(rem, n + AT_PAD);
     x.unit = (int)(rem - (int64_t)x.item * (n + AT_PAD));
     if (x.unit >= n) {  // behind the item's units, or past the end
       x.unit = 0;
       if (++x.item == items) {
         x.item = 0;
-        ++x.seq;
+        n = ++x.seq < n_seq ? units_of(x.seq) : 0;
       }
     }
-    number = s_first[x.seq] * items + (x.seq < n_seq ? (int64_t)x.item * units_of(x.seq) : 0) + x.unit;
+    number = s_first[x.seq] * items + (int64_t)x.item * n + x.unit;
     return x;
   };
+  const int64_t v0 = div_pos(cta * places, N), v1 = div_pos((cta + 1) * places, N);
+  int before0 = 0, before1 = 0;
+  for (int b0 = 0; b0 < n_seq; b0 += 32) {
+    const int64_t v = b0 + lane < n_seq ? v_first(b0 + lane) : places;
+    const uint32_t m1 = __ballot_sync(0xffffffffu, v <= v1 && v < places);
+    before0 += __popc(__ballot_sync(0xffffffffu, v <= v0));
+    before1 += __popc(m1);
+    if (m1 != 0xffffffffu) break;
+  }
   int64_t u0, u1;
-  Unit at = unit_at(div_pos(cta * places, N), u0);  // the unit in hand
-  if (cta + 1 < N)
-    unit_at(div_pos((cta + 1) * places, N), u1);
-  else
-    u1 = s_first[n_seq] * items;
+  Unit at = unit_at(v0, before0, u0);  // the unit in hand
+  unit_at(v1, before1, u1);
   const int steps = (int)(u1 - u0);
   if (steps == 0) return;
 
@@ -383,7 +386,6 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     }
     const uint32_t v = __ballot_sync(0xffffffffu, my_rec != nullptr);
     if (step & 32) valid_odd = v; else valid_even = v;
-    look_up(step + 32);
   };
   // Fetch the record of `step` (from byte `from`, `bytes` of it) to `dst`: the lane that looked it up does. A
   // step without a record completes the barrier at once.
@@ -402,6 +404,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
     for (int i = 0; i < C::STAGES; ++i) fetch(i, 0, 2 * C::HALF, ring_at + i * C::STAGE, bar_at + 8 * i);
   }
+  look_up(32);
   int stage = 0;        // the stage in use
   uint32_t parity = 0;  // of its barriers
   auto arrived = [&](uint32_t bar) {
@@ -551,6 +554,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       const bool live = (valid >> (step & 31)) & 1;
       const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
       const int ahead = step + C::STAGES;
+      const bool new_batch = (ahead & 31) == 0 && ahead < steps;
       auto next = [&]() {
         if (++stage == C::STAGES) {
           stage = 0;
@@ -558,9 +562,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
       };
       arrived(kbar);
-      if (!live) {
+      if (__builtin_expect(!live, 0)) {
         __syncwarp();  // no lane re-arms a barrier that another still waits on
-        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        if (new_batch) enter(ahead);
         if constexpr (C::SPLIT) {
           fetch(ahead, 0, C::HALF, kb, kbar);
           arrived(vbar);
@@ -569,6 +573,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         } else {
           fetch(ahead, 0, 2 * C::HALF, kb, kbar);
         }
+        if (new_batch) look_up(ahead + 32);
         next();
         continue;
       }
@@ -637,12 +642,12 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       }
       if constexpr (C::SPLIT) {
         reads_done();
-        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        if (new_batch) enter(ahead);
         fetch(ahead, 0, C::HALF, kb, kbar);
       }
 
       // ---- weights
-      if (masked) {
+      if (__builtin_expect(masked, 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -661,7 +666,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int c = 0; c < 2; ++c) up |= fmaxf(s[nt][c], s[nt][2 + c]) > limit[nt][c];
-      if (__any_sync(0xffffffffu, up)) {
+      if (__builtin_expect(__any_sync(0xffffffffu, up), 0)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float f[2];
@@ -704,7 +709,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       if constexpr (C::SPLIT) arrived(vbar);
       uint8_t* const vp = ring + stage * C::STAGE + C::HALF;
       if constexpr (TYPE == QG_F16) {
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           // Zero weights do not silence a NaN or an infinity in the product. So the rows of tokens that no
           // query row sees are cleared, and values that are not finite are taken out here and added, to the
           // rows that see them.
@@ -768,7 +773,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       } else {
-        if (masked) {
+        if (__builtin_expect(masked, 0)) {
           // As for f16: scales of tokens that no row sees may be anything, and a NaN scale (of a token that
           // some rows do not see) is taken out and given to the rows that see it.
           uint16_t* sc = reinterpret_cast<uint16_t*>(vp + KV_GROUP * D);
@@ -810,7 +815,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           big = __hmax2(big, *reinterpret_cast<__half2*>(&d[blk]));
         }
         float dmax = fmaxf(__low2float(big), __high2float(big));
-        if (__any_sync(0xffffffffu, dmax > wmax)) {
+        if (__builtin_expect(__any_sync(0xffffffffu, dmax > wmax), 0)) {
           dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 4));
           dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 8));
           dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
@@ -831,7 +836,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         for (int blk = 0; blk < NB; ++blk) {
           uint32_t v[4];  // of four tokens: dimensions g, g + 8, g + 16, g + 24
           ldsm_bytes_trans(vb + blk * 512 + v_at, v);
-          const uint32_t k64 = 0x64646464u, k1152 = 0x64806480u;  // f16 1024 + u, less 1152
+          const uint32_t k1152 = 0x64806480u;  // f16 1024 + u, less 1152
           const uint32_t v0[4] = {hsub2_u(__byte_perm(v[0], k64, 0x4140), k1152), hsub2_u(__byte_perm(v[1], k64, 0x4140), k1152),
                                   hsub2_u(__byte_perm(v[0], k64, 0x4342), k1152), hsub2_u(__byte_perm(v[1], k64, 0x4342), k1152)};
           const uint32_t v1[4] = {hsub2_u(__byte_perm(v[2], k64, 0x4140), k1152), hsub2_u(__byte_perm(v[3], k64, 0x4140), k1152),
@@ -850,9 +855,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       if constexpr (C::SPLIT) {
         fetch(ahead, C::HALF, C::HALF, vb, vbar);
       } else {
-        if ((ahead & 31) == 0 && ahead < steps) enter(ahead);
+        if (new_batch) enter(ahead);
         fetch(ahead, 0, 2 * C::HALF, kb, kbar);
       }
+      if (new_batch) look_up(ahead + 32);
       next();
     }
 
