@@ -525,7 +525,7 @@ qg_status qattn_paged(const qg_kvcache* cache, const uint16_t* q, int n_heads, i
   qg_status st = check_cache(cache);
   if (st != QG_OK) return st;
   if (!qg::attn_shape_ok(cache->n_seq, n_heads, cache->n_kv_heads, cache->head_dim, ncols) || window < 0 ||
-      !std::isfinite(scale))
+      !std::isfinite(scale) || !qg::attn_size_ok(*cache, n_heads, ncols))
     return QG_ERR_SHAPE;
   if (!q || !lens || !y) return QG_ERR_NULL;
   if (!aligned(q, 16) || !aligned(y, 16) || !aligned(lens, 4) || !aligned(err_flag, 4)) return QG_ERR_ALIGN;

@@ -26,6 +26,14 @@ bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int nco
          (head_dim == 64 || head_dim == 128 || head_dim == 256) && ncols >= 1 && ncols <= QG_ATTN_MAX_COLS;
 }
 
+// The kernel numbers units (64 tokens), with up to three places behind each item's, in 32 bits.
+bool attn_size_ok(const qg_kvcache& c, int n_heads, int ncols) {
+  const int nt = tiles_of(n_heads, c.n_kv_heads, c.head_dim, ncols), rows = n_heads / c.n_kv_heads * ncols;
+  const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
+  const int64_t units = (int64_t)c.max_pages * c.page_size / 64 + 4;
+  return units * c.n_seq * c.n_kv_heads * tiles < ((int64_t)1 << 31);
+}
+
 size_t attn_ws_bytes(int, int n_heads, int n_kv_heads, int head_dim, int ncols) {
   const int nt = tiles_of(n_heads, n_kv_heads, head_dim, ncols);
   return head_dim == 64 ? attn_ws_64(nt) : head_dim == 128 ? attn_ws_128(nt) : attn_ws_256(nt);

@@ -84,16 +84,18 @@ struct AttnCfg {
   static constexpr int ACC = NT * D / 4;  // accumulator registers
   static constexpr int HALF = kv_half_bytes(TYPE, D);
   static constexpr int STAGE = (2 * HALF + 127) / 128 * 128;  // a record
-  static constexpr bool QSMEM = NT * NB > 4;  // Q fragments in shared memory, not registers
-  static constexpr int OD = NT <= 2 ? 64 : 32;  // dimensions joined at a time
+  static constexpr bool QSMEM = NT * NB > 4;  // Q fragments read from shared memory each time, not kept in registers
+  static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
+  // dimensions joined at a time (32 also where 64 would leave one stage less)
+  static constexpr int OD = NT > 2 || (NT == 1 && kv_half_bytes(TYPE, D) == 4096) ? 32 : 64;
   static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
-  static constexpr size_t qbuf = QSMEM ? (size_t)NB * NT * (32 * 16 + 8 * 4) : 0;
-  // Stages of a warp's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 1 KB for up to
-  // 80 sequences a CTA).
+  static constexpr size_t qbuf = (size_t)2 * ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)NB * ROWS * 4 : 0);
+  // Stages of a warp's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 600 bytes for up to
+  // 72 sequences a CTA).
   static constexpr int fit(int n) {
-    return (int)(((size_t)(227 * 1024) / n - 2048 - obuf - stats - qbuf - 256) / ((size_t)AT_WARPS * STAGE));
+    return (int)(((size_t)(227 * 1024) / n - 1024 - 600 - obuf - stats - qbuf - 256) / ((size_t)AT_WARPS * STAGE));
   }
   // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them), fewer while a warp
   // has not two stages.
@@ -108,7 +110,7 @@ struct AttnCfg {
   static constexpr size_t ring = (size_t)AT_WARPS * STAGES * STAGE;
   static constexpr size_t bars = (size_t)AT_WARPS * BARS * 8;
   static size_t smem(int n_seq) {
-    return ring + obuf + stats + qbuf + bars + (size_t)(n_seq + 1) * 8 + (size_t)n_seq * 4;
+    return ring + obuf + stats + qbuf + bars + (size_t)(2 * n_seq + 1) * 4;
   }
 };
 
@@ -156,6 +158,11 @@ __device__ __forceinline__ bool bar_ready(uint32_t bar, uint32_t parity) {
       : "memory");
   return r != 0;
 }
+// 16 bytes to shared memory behind the thread's back; `bytes` 0: zeros instead.
+__device__ __forceinline__ void copy16_async(uint32_t dst, const void* src, int bytes) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
+}
+__device__ __forceinline__ void copies_done() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 // One arrival on `bar` where `mine`, with a bulk copy of `bytes` to wait for where `has` (which implies `mine`).
 __device__ __forceinline__ void fetch_if(bool mine, bool has, uint32_t dst, const void* src, uint32_t bytes,
                                          uint32_t bar) {
@@ -196,14 +203,6 @@ __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)
       : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-// a / b of numbers >= 0, in 32 bits where they fit (they nearly always do, and the division is several times shorter).
-__device__ __forceinline__ int64_t div_pos(int64_t a, int64_t b) {
-  if ((((uint64_t)a | (uint64_t)b) >> 32) == 0) return (uint32_t)a / (uint32_t)b;
-  return a / b;
-}
-// The CTA whose run holds place v of n, run c being [c n / N, (c+1) n / N).
-__device__ __forceinline__ int run_of(int64_t v, int64_t n, int64_t N) { return (int)div_pos((v + 1) * N - 1, n); }
-
 struct SeqSpan {
   int lo;    // first token that any row sees
   int hi;    // one past the last
@@ -233,9 +232,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
   uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
   uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
-  int64_t* const s_first = reinterpret_cast<int64_t*>(s_bar + AT_WARPS * C::BARS);  // units before a sequence
+  int32_t* const s_first = reinterpret_cast<int32_t*>(s_bar + AT_WARPS * C::BARS);  // units before a sequence
   int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
-  __shared__ int64_t s_part[AT_WARPS];
+  __shared__ int s_part[AT_WARPS];
 
   uint32_t k64;  // the high bytes of f16 1024 + u, in a register that is not made anew at each use
   asm volatile("mov.b32 %0, 0x64646464;" : "=r"(k64));
@@ -255,7 +254,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int per = (n_seq + AT_THREADS - 1) / AT_THREADS;
     const int b0 = tid * per, b1 = min(b0 + per, n_seq);
     const int cap = a.c.max_pages * a.c.page_size;
-    int64_t sum = 0;
+    int sum = 0;
     for (int b = b0; b < b1; ++b) {
       int len = a.lens[b];
       if ((len < 0 || len > cap) && blockIdx.x == 0 && a.err) atomicOr(a.err, QG_KV_BAD_POS);
@@ -263,15 +262,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s_len[b] = len;
       sum += span_of(a, len).n;
     }
-    int64_t run = sum;
+    int run = sum;
 #pragma unroll
     for (int off = 1; off < 32; off <<= 1) {
-      const int64_t up = __shfl_up_sync(0xffffffffu, run, off);
+      const int up = __shfl_up_sync(0xffffffffu, run, off);
       if (lane >= off) run += up;
     }
     if (lane == 31) s_part[warp] = run;
     __syncthreads();
-    int64_t before = run - sum;
+    int before = run - sum;
     for (int w = 0; w < warp; ++w) before += s_part[w];
     for (int b = b0; b < b1; ++b) {
       s_first[b] = before;
@@ -283,26 +282,30 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   // Two numberings: units in order, u, and places in order, v, where every item has
   // AT_PAD places behind its units. Runs are equal in places.
   const int items = a.c.n_kv_heads * p.tiles;  // of a sequence
-  auto units_of = [&](int b) { return (int)(s_first[b + 1] - s_first[b]); };
-  auto v_first = [&](int b) { return (s_first[b] + (int64_t)b * AT_PAD) * items; };
-  const int64_t places = v_first(n_seq);
-  const int64_t N = places < C::GRID ? places : C::GRID;
+  auto units_of = [&](int b) { return s_first[b + 1] - s_first[b]; };
+  auto v_first = [&](int b) { return (s_first[b] + b * AT_PAD) * items; };
+  const int places = v_first(n_seq);  // below 2^31 (attn_places)
+  const int N = places < C::GRID ? places : C::GRID;
   const int cta = blockIdx.x;
   // The last item that starts in a run is the only one of them that may be cut: entry `cta` tells of it.
   // (Where few items are joined one by one, item i's entry tells of item i.)
   if (!p.by_item && tid == 0) p.ws.cut[cta].n = 0;
   if (cta >= N) return;
+  // run c is [c places / N, (c+1) places / N)
+  const int each = places / N, over = places - each * N;
+  auto run_start = [&](int c) { return c * each + c * over / N; };
+  auto run_of = [&](int v) { return (int)((((int64_t)v + 1) * N - 1) / places); };
   // the first unit at or behind a place; `before`: sequences that start at or before the place
   struct Unit {
     int seq, item, unit;  // item of the sequence, unit of the item
   };
-  auto unit_at = [&](int64_t v, int before, int64_t& number) {
+  auto unit_at = [&](int v, int before, int& number) {
     Unit x;
     x.seq = before - 1;
     int n = units_of(x.seq);
-    const int64_t rem = v - v_first(x.seq);
-    x.item = (int)div_pos(rem, n + AT_PAD);
-    x.unit = (int)(rem - (int64_t)x.item * (n + AT_PAD));
+    const uint32_t rem = v - v_first(x.seq);
+    x.item = rem / (uint32_t)(n + AT_PAD);
+    x.unit = rem - x.item * (n + AT_PAD);
     if (x.unit >= n) {  // behind the item's units, or past the end
       x.unit = 0;
       if (++x.item == items) {
@@ -310,23 +313,38 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         n = ++x.seq < n_seq ? units_of(x.seq) : 0;
       }
     }
-    number = s_first[x.seq] * items + (int64_t)x.item * n + x.unit;
+    number = s_first[x.seq] * items + x.item * n + x.unit;
     return x;
   };
-  const int64_t v0 = div_pos(cta * places, N), v1 = div_pos((cta + 1) * places, N);
+  const int v0 = run_start(cta), v1 = cta + 1 < N ? run_start(cta + 1) : places;
   int before0 = 0, before1 = 0;
   for (int b0 = 0; b0 < n_seq; b0 += 32) {
-    const int64_t v = b0 + lane < n_seq ? v_first(b0 + lane) : places;
-    const uint32_t m1 = __ballot_sync(0xffffffffu, v <= v1 && v < places);
+    const int v = b0 + lane < n_seq ? v_first(b0 + lane) : 0x7fffffff;
     before0 += __popc(__ballot_sync(0xffffffffu, v <= v0));
-    before1 += __popc(m1);
-    if (m1 != 0xffffffffu) break;
+    const uint32_t m = __ballot_sync(0xffffffffu, v <= v1);
+    before1 += __popc(m);
+    if (m != 0xffffffffu) break;
   }
-  int64_t u0, u1;
+  int u0, u1;
   Unit at = unit_at(v0, before0, u0);  // the unit in hand
   unit_at(v1, before1, u1);
-  const int steps = (int)(u1 - u0);
+  const int steps = u1 - u0;
   if (steps == 0) return;
+
+  // Queries of an item into one of two buffers, [row][D] f16, asynchronously: the first before any keys are
+  // asked for, the others an item ahead (in the middle of the stream a load takes microseconds).
+  const int rows = p.group * a.ncols;
+  auto stage_q = [&](const Unit& x, int buf) {
+    const int head = x.item / p.tiles, r0 = (x.item - head * p.tiles) * ROWS;
+    for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
+      const int row = i / (D / 8), c = i % (D / 8), r = r0 + row;
+      const uint16_t* src = a.q;
+      if (r < rows)
+        src += (((size_t)x.seq * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + 8 * c;
+      copy16_async(smem_u32(s_q) + (buf * ROWS + row) * C::QPITCH + 16 * c, src, r < rows ? 16 : 0);
+    }
+  };
+  stage_q(at, 0);
 
   // ------------------------------------------------------------ the ring
   const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
@@ -353,11 +371,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
       }
       const SeqSpan sp = span_of(a, s_len[x.seq]);
-      const int64_t grp = (int64_t)(sp.unit + x.unit) * AT_WARPS + warp;
-      if (grp * KV_GROUP < sp.hi && grp * KV_GROUP + KV_GROUP > sp.lo) {
+      const int grp = (sp.unit + x.unit) * AT_WARPS + warp;  // group of 16 tokens, hence the comparisons in groups
+      if (grp < (sp.hi + KV_GROUP - 1) / KV_GROUP && grp >= sp.lo / KV_GROUP) {
         nx_in = true;
-        nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (int)(grp >> gpp_log)];
-        nx_off = x.item / p.tiles * gpp + ((int)grp & (gpp - 1));
+        nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (grp >> gpp_log)];
+        nx_off = x.item / p.tiles * gpp + (grp & (gpp - 1));
       }
     }
     if (most > 32) {  // on to the next batch: one behind lane 31's
@@ -435,9 +453,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   }
 
   // --------------------------------------------------------------- items
-  const int rows = p.group * a.ncols;
   int turn = 0;  // of the statistics' two buffers
-  int step = 0;
+  int step = 0, q_buf = 0;
   uint32_t valid = 0;
   while (step < steps) {
     const int b = at.seq, hr = at.item, nu = units_of(b);
@@ -446,11 +463,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int head = hr / p.tiles, tile = hr - head * p.tiles;
     const int len = s_len[b];
     const SeqSpan sp = span_of(a, len);
-    int tok = (int)(((int64_t)sp.unit + at.unit) * AT_WARPS + warp) * KV_GROUP - AT_UNIT;
+    // (the last unit's end may pass 2^31, but not the records that are looked at)
+    int tok = (int)(((uint32_t)(sp.unit + at.unit) * AT_WARPS + warp) * KV_GROUP - AT_UNIT);
     if (tid == 0 && starts && (p.by_item || !whole)) {
-      const int64_t v = v_first(b) + (int64_t)hr * (nu + AT_PAD);
       AttnCut cut{};
-      if (!whole) cut = {cta, run_of(v + nu - 1, places, N) - cta + 1, b, head, tile};
+      if (!whole) cut = {cta, run_of(v_first(b) + hr * (nu + AT_PAD) + nu - 1) - cta + 1, b, head, tile};
       p.ws.cut[p.by_item ? b * items + hr : cta] = cut;
     }
     at.unit = 0;  // (the next item's first, if there is one)
@@ -474,54 +491,53 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // Q8_0, -128 2^-24 sum of the block's queries of rows 2t and 2t + 1.
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : NT][4];
     float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][2];
-    auto load_q = [&](int blk, int nt) {
-      const int r = tile * ROWS + nt * 8 + g;
-      if (r >= rows) return make_uint4(0, 0, 0, 0);
-      uint4 x = *reinterpret_cast<const uint4*>(
-          a.q + (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + 32 * blk + 8 * t);
-      x.x = (x.x & p.q_and) ^ p.q_xor;
-      x.y = (x.y & p.q_and) ^ p.q_xor;
-      x.z = (x.z & p.q_and) ^ p.q_xor;
-      x.w = (x.w & p.q_and) ^ p.q_xor;
-      return x;
+    const uint32_t q_at = smem_u32(s_q) + (q_buf * ROWS + g) * C::QPITCH + 16 * t;  // this lane's, of block 0 and tile 0
+    auto load_q = [&](int blk, int nt, uint32_t (&q)[4]) {
+      lds128(q_at + nt * 8 * C::QPITCH + blk * 64, q[0], q[1], q[2], q[3]);
     };
-    auto sum_q = [&](const uint4& x) {  // of row g
-      float s = ((lo_f32(x.x) + hi_f32(x.x)) + (lo_f32(x.y) + hi_f32(x.y))) +
-                ((lo_f32(x.z) + hi_f32(x.z)) + (lo_f32(x.w) + hi_f32(x.w)));
+    auto sum_q = [&](const uint32_t (&q)[4]) {  // of row g
+      float s = ((lo_f32(q[0]) + hi_f32(q[0])) + (lo_f32(q[1]) + hi_f32(q[1]))) +
+                ((lo_f32(q[2]) + hi_f32(q[2])) + (lo_f32(q[3]) + hi_f32(q[3])));
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       return s * -7.62939453125e-06f;  // -128 * 2^-24
     };
-    if constexpr (C::QSMEM) {
-      // in fragment order [block][tile][lane][4 words]; the sums by row behind them
-      for (int i = warp; i < NB * NT; i += AT_WARPS) {
-        const uint4 x = load_q(i / NT, i % NT);
-        *reinterpret_cast<uint4*>(s_q + i * 512 + lane * 16) = x;
-        if constexpr (TYPE == QG_Q8_0) {
-          const float s = sum_q(x);
-          if (t == 0) reinterpret_cast<float*>(s_q + NB * NT * 512)[i * 8 + g] = s;
-        }
+    float* const s_qsum = reinterpret_cast<float*>(s_q + 2 * ROWS * C::QPITCH);  // [block][row]
+    copies_done();
+    if (p.q_and != 0xffffffffu || p.q_xor) {  // a scale that is not positive: each thread on what it copied
+      for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
+        uint4* const x = reinterpret_cast<uint4*>(s_q + (q_buf * ROWS + i / (D / 8)) * C::QPITCH + 16 * (i % (D / 8)));
+        *x = make_uint4((x->x & p.q_and) ^ p.q_xor, (x->y & p.q_and) ^ p.q_xor, (x->z & p.q_and) ^ p.q_xor,
+                        (x->w & p.q_and) ^ p.q_xor);
       }
-      __syncthreads();
+    }
+    __syncthreads();
+    if constexpr (C::QSMEM) {
+      if constexpr (TYPE == QG_Q8_0) {
+        for (int i = warp; i < NB * NT; i += AT_WARPS) {
+          uint32_t q[4];
+          load_q(i / NT, i % NT, q);
+          const float s = sum_q(q);
+          if (t == 0) s_qsum[i * 8 + g] = s;
+        }
+        __syncthreads();
+      }
     } else {
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
-          const uint4 x = load_q(blk, nt);
-          qf[blk][nt][0] = x.x; qf[blk][nt][1] = x.y; qf[blk][nt][2] = x.z; qf[blk][nt][3] = x.w;
-        }
-      if constexpr (TYPE == QG_Q8_0) {
-#pragma unroll
-        for (int blk = 0; blk < NB; ++blk)
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) {
-            const float s = sum_q(make_uint4(qf[blk][nt][0], qf[blk][nt][1], qf[blk][nt][2], qf[blk][nt][3]));
+          load_q(blk, nt, qf[blk][nt]);
+          if constexpr (TYPE == QG_Q8_0) {
+            const float s = sum_q(qf[blk][nt]);
             qc[blk][nt][0] = __shfl_sync(0xffffffffu, s, 8 * t);
             qc[blk][nt][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
           }
-      }
+        }
     }
+    // (the other buffer was read before the last item's end, which all warps have passed)
+    q_buf ^= 1;
+    if (step + todo < steps) stage_q(at, q_buf);
 
     // o[blk][nt][i][c]: dimension 32 blk + 16 i + 8 (c/2) + g, row 8 nt + 2t + c%2
     float o[NB][NT][2][4];
@@ -612,7 +628,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         for (int nt = 0; nt < NT; ++nt) {
           uint32_t q[4];
           if constexpr (C::QSMEM) {
-            lds128(smem_u32(s_q) + (blk * NT + nt) * 512 + lane * 16, q[0], q[1], q[2], q[3]);
+            load_q(blk, nt, q);
           } else {
 #pragma unroll
             for (int i = 0; i < 4; ++i) q[i] = qf[blk][nt][i];
@@ -623,7 +639,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           } else {
             float c0, c1;
             if constexpr (C::QSMEM) {
-              const float2 c = *reinterpret_cast<const float2*>(s_q + NB * NT * 512 + ((blk * NT + nt) * 8 + 2 * t) * 4);
+              const float2 c = *reinterpret_cast<const float2*>(s_qsum + (blk * NT + nt) * 8 + 2 * t);
               c0 = c.x;
               c1 = c.y;
             } else {
@@ -924,10 +940,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       __syncthreads();
       constexpr int QUADS = C::OD / 4;  // float4 of a row
 #pragma unroll
-      for (int k = 0; k < ROWS * QUADS / AT_THREADS; ++k) {
+      for (int k = 0; k < (ROWS * QUADS + AT_THREADS - 1) / AT_THREADS; ++k) {
         const int row = (tid + k * AT_THREADS) / QUADS, dim = (tid % QUADS) * 4;
         const int r = tile * ROWS + row;
-        if (r >= rows) continue;
+        if (row >= ROWS || r >= rows) continue;
         float4 y = *reinterpret_cast<const float4*>(s_o + row * C::OPITCH + dim);
 #pragma unroll
         for (int w = 1; w < AT_WARPS; ++w) {

@@ -174,6 +174,7 @@ struct AttnArgs {
   int32_t* err;
 };
 bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
+bool attn_size_ok(const qg_kvcache& c, int n_heads, int ncols);  // of a shape that is ok
 size_t attn_ws_bytes(int n_seq, int n_heads, int n_kv_heads, int head_dim, int ncols);
 cudaError_t attn_launch(const AttnArgs& a, cudaStream_t s);
 // The attention kernel's device error word (QG_DEV_ERR_WAIT), read and cleared.

@@ -182,6 +182,7 @@ def test_attention_refusals(lib):
     assert attn(lib, heads=41) == SHAPE and attn(lib, heads=0) == SHAPE and attn(lib, heads=8 * 65) == SHAPE
     assert attn(lib, ncols=0) == SHAPE and attn(lib, ncols=17) == SHAPE and attn(lib, window=-1) == SHAPE
     assert attn(lib, scale=math.nan) == SHAPE and attn(lib, scale=math.inf) == SHAPE
+    assert attn(lib, cache(max_pages=1 << 24, n_kv_heads=256, n_seq=1024), heads=256, wsb=1 << 35) == SHAPE
     assert attn(lib, q=None) == NULL and attn(lib, lens=None) == NULL and attn(lib, y=None) == NULL
     assert attn(lib, q=at(3) + 2) == ALIGN and attn(lib, y=at(4) + 8) == ALIGN and attn(lib, lens=at(5) + 2) == ALIGN
     assert attn(lib, ws=None) == WORKSPACE and attn(lib, wsb=need - 1) == WORKSPACE
