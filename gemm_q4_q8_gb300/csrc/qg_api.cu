@@ -110,7 +110,7 @@ bool pdl_allowed(cudaStream_t s, LaunchClass cls) {
   } else {
     it->second = (int)cls;
   }
-  return !(cls == LC_LATE || (cls == LC_L1 && prev == LC_SMEM));
+  return !(cls == LC_FULL || (cls == LC_L1 && prev > LC_L1));
 }
 
 }  // namespace qg

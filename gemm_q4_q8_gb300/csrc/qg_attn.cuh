@@ -114,15 +114,7 @@ struct AttnCfg {
   }
 };
 
-// What the main kernel tells the joining one: an item and the CTAs that have parts of it.
-struct AttnCut {
-  int32_t c0, n;  // first CTA, number of parts; n == 0: nothing to join
-  int32_t seq, head, tile;
-  int32_t pad[3];
-};
-
 struct AttnWs {
-  AttnCut* cut;   // [GRID], of CTAs or of items
   float* zl;      // [GRID][2][ROWS][2] reference and sum of weights of a part
   float* o;       // [GRID][2][ROWS][D] its weighted sum
 };
@@ -132,7 +124,6 @@ struct AttnDev {
   AttnWs ws;
   int group;    // query heads of a kv head
   int tiles;    // row tiles of a kv head
-  int by_item;  // the joining kernel goes by items, not by CTAs
   float scale;  // |scale| log2 e; 1 for a scale of 0
   uint32_t q_and, q_xor;  // and its sign, applied to the queries
 };
@@ -221,6 +212,93 @@ __device__ __forceinline__ SeqSpan span_of(const AttnArgs& a, int len) {
   return s;
 }
 
+// Which CTA does what. Two numberings: units in order, u, and places in order, v, where every item has AT_PAD
+// places behind its units. Run c of N is the places [c places / N, (c+1) places / N), and the CTA's units are those
+// among them. Both kernels of a call work this out for themselves, from lens in shared memory.
+struct Unit {
+  int seq, item, unit;  // item of the sequence, unit of the item
+};
+template <int THREADS>
+struct Runs {
+  int32_t* first;  // [n_seq + 1] units before a sequence (times its items)
+  int32_t* len;    // [n_seq] lengths, none negative
+  int n_seq, items, places, N, each, over;
+
+  // By all threads; `part`: shared, one int a warp. Ends with a barrier.
+  __device__ __forceinline__ Runs(const AttnArgs& a, int tiles, int grid, int32_t* mem, int* part, bool report)
+      : first(mem), len(mem + a.c.n_seq + 1), n_seq(a.c.n_seq), items(a.c.n_kv_heads * tiles) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int per = (n_seq + THREADS - 1) / THREADS;
+    const int b0 = tid * per, b1 = min(b0 + per, n_seq);
+    const int cap = a.c.max_pages * a.c.page_size;
+    int sum = 0;
+    for (int b = b0; b < b1; ++b) {
+      int l = a.lens[b];
+      if ((l < 0 || l > cap) && report && a.err) atomicOr(a.err, QG_KV_BAD_POS);
+      l = max(l, 0);
+      len[b] = l;
+      sum += span_of(a, l).n;
+    }
+    int run = sum;
+#pragma unroll
+    for (int off = 1; off < 32; off <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, run, off);
+      if (lane >= off) run += up;
+    }
+    if (lane == 31) part[warp] = run;
+    __syncthreads();
+    int before = run - sum;
+    for (int w = 0; w < warp; ++w) before += part[w];
+    for (int b = b0; b < b1; ++b) {
+      first[b] = before;
+      before += span_of(a, len[b]).n;
+    }
+    if (b1 == n_seq && b0 < n_seq) first[n_seq] = before;
+    __syncthreads();
+    places = v_first(n_seq);  // below 2^31 (attn_size_ok)
+    N = places < grid ? places : grid;
+    each = places / N;
+    over = places - each * N;
+  }
+  __device__ __forceinline__ int units_of(int b) const { return first[b + 1] - first[b]; }
+  __device__ __forceinline__ int v_first(int b) const { return (first[b] + b * AT_PAD) * items; }
+  __device__ __forceinline__ int v_item(int b, int item) const { return v_first(b) + item * (units_of(b) + AT_PAD); }
+  __device__ __forceinline__ int run_start(int c) const { return c < N ? c * each + c * over / N : places; }
+  __device__ __forceinline__ int run_of(int v) const { return (int)((((int64_t)v + 1) * N - 1) / places); }
+  // The first units at or behind run c's first place and its last place's successor, and their numbers; by a warp.
+  __device__ __forceinline__ void find(int c, Unit& x0, int& u0, Unit& x1, int& u1) const {
+    const int lane = threadIdx.x & 31;
+    const int v0 = run_start(c), v1 = run_start(c + 1);
+    int before0 = 0, before1 = 0;  // sequences that start at or before the place
+    for (int b0 = 0; b0 < n_seq; b0 += 32) {
+      const int v = b0 + lane < n_seq ? v_first(b0 + lane) : 0x7fffffff;
+      before0 += __popc(__ballot_sync(0xffffffffu, v <= v0));
+      const uint32_t m = __ballot_sync(0xffffffffu, v <= v1);
+      before1 += __popc(m);
+      if (m != 0xffffffffu) break;
+    }
+    // even lanes take v0, odd ones v1
+    Unit x;
+    x.seq = ((lane & 1) ? before1 : before0) - 1;
+    int n = units_of(x.seq);
+    const uint32_t rem = ((lane & 1) ? v1 : v0) - v_first(x.seq);
+    x.item = rem / (uint32_t)(n + AT_PAD);
+    x.unit = rem - x.item * (n + AT_PAD);
+    if (x.unit >= n) {  // behind the item's units, or past the end
+      x.unit = 0;
+      if (++x.item == items) {
+        x.item = 0;
+        n = ++x.seq < n_seq ? units_of(x.seq) : 0;
+      }
+    }
+    const int u = first[x.seq] * items + x.item * n + x.unit;
+    x0 = {__shfl_sync(0xffffffffu, x.seq, 0), __shfl_sync(0xffffffffu, x.item, 0), __shfl_sync(0xffffffffu, x.unit, 0)};
+    x1 = {__shfl_sync(0xffffffffu, x.seq, 1), __shfl_sync(0xffffffffu, x.item, 1), __shfl_sync(0xffffffffu, x.unit, 1)};
+    u0 = __shfl_sync(0xffffffffu, u, 0);
+    u1 = __shfl_sync(0xffffffffu, u, 1);
+  }
+};
+
 template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     attn_kernel(const __grid_constant__ AttnDev p) {
@@ -232,8 +310,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
   uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
   uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
-  int32_t* const s_first = reinterpret_cast<int32_t*>(s_bar + AT_WARPS * C::BARS);  // units before a sequence
-  int32_t* const s_len = reinterpret_cast<int32_t*>(s_first + p.a.c.n_seq + 1);
+  int32_t* const s_runs = reinterpret_cast<int32_t*>(s_bar + AT_WARPS * C::BARS);
   __shared__ int s_part[AT_WARPS];
 
   uint32_t k64;  // the high bytes of f16 1024 + u, in a register that is not made anew at each use
@@ -248,86 +325,14 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   }
   pdl_wait();
 
-  // units of every sequence, and their running sum
-  const int n_seq = a.c.n_seq;
-  {
-    const int per = (n_seq + AT_THREADS - 1) / AT_THREADS;
-    const int b0 = tid * per, b1 = min(b0 + per, n_seq);
-    const int cap = a.c.max_pages * a.c.page_size;
-    int sum = 0;
-    for (int b = b0; b < b1; ++b) {
-      int len = a.lens[b];
-      if ((len < 0 || len > cap) && blockIdx.x == 0 && a.err) atomicOr(a.err, QG_KV_BAD_POS);
-      len = max(len, 0);
-      s_len[b] = len;
-      sum += span_of(a, len).n;
-    }
-    int run = sum;
-#pragma unroll
-    for (int off = 1; off < 32; off <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, run, off);
-      if (lane >= off) run += up;
-    }
-    if (lane == 31) s_part[warp] = run;
-    __syncthreads();
-    int before = run - sum;
-    for (int w = 0; w < warp; ++w) before += s_part[w];
-    for (int b = b0; b < b1; ++b) {
-      s_first[b] = before;
-      before += span_of(a, s_len[b]).n;
-    }
-    if (b1 == n_seq && b0 < n_seq) s_first[n_seq] = before;
-    __syncthreads();
-  }
-  // Two numberings: units in order, u, and places in order, v, where every item has
-  // AT_PAD places behind its units. Runs are equal in places.
-  const int items = a.c.n_kv_heads * p.tiles;  // of a sequence
-  auto units_of = [&](int b) { return s_first[b + 1] - s_first[b]; };
-  auto v_first = [&](int b) { return (s_first[b] + b * AT_PAD) * items; };
-  const int places = v_first(n_seq);  // below 2^31 (attn_places)
-  const int N = places < C::GRID ? places : C::GRID;
   const int cta = blockIdx.x;
-  // The last item that starts in a run is the only one of them that may be cut: entry `cta` tells of it.
-  // (Where few items are joined one by one, item i's entry tells of item i.)
-  if (!p.by_item && tid == 0) p.ws.cut[cta].n = 0;
-  if (cta >= N) return;
-  // run c is [c places / N, (c+1) places / N)
-  const int each = places / N, over = places - each * N;
-  auto run_start = [&](int c) { return c * each + c * over / N; };
-  auto run_of = [&](int v) { return (int)((((int64_t)v + 1) * N - 1) / places); };
-  // the first unit at or behind a place; `before`: sequences that start at or before the place
-  struct Unit {
-    int seq, item, unit;  // item of the sequence, unit of the item
-  };
-  auto unit_at = [&](int v, int before, int& number) {
-    Unit x;
-    x.seq = before - 1;
-    int n = units_of(x.seq);
-    const uint32_t rem = v - v_first(x.seq);
-    x.item = rem / (uint32_t)(n + AT_PAD);
-    x.unit = rem - x.item * (n + AT_PAD);
-    if (x.unit >= n) {  // behind the item's units, or past the end
-      x.unit = 0;
-      if (++x.item == items) {
-        x.item = 0;
-        n = ++x.seq < n_seq ? units_of(x.seq) : 0;
-      }
-    }
-    number = s_first[x.seq] * items + x.item * n + x.unit;
-    return x;
-  };
-  const int v0 = run_start(cta), v1 = cta + 1 < N ? run_start(cta + 1) : places;
-  int before0 = 0, before1 = 0;
-  for (int b0 = 0; b0 < n_seq; b0 += 32) {
-    const int v = b0 + lane < n_seq ? v_first(b0 + lane) : 0x7fffffff;
-    before0 += __popc(__ballot_sync(0xffffffffu, v <= v0));
-    const uint32_t m = __ballot_sync(0xffffffffu, v <= v1);
-    before1 += __popc(m);
-    if (m != 0xffffffffu) break;
-  }
+  const Runs<AT_THREADS> runs(a, p.tiles, C::GRID, s_runs, s_part, cta == 0);
+  if (cta >= runs.N) return;
+  const int items = runs.items;
+  const int32_t* const s_len = runs.len;
+  Unit at, end_at;  // the unit in hand
   int u0, u1;
-  Unit at = unit_at(v0, before0, u0);  // the unit in hand
-  unit_at(v1, before1, u1);
+  runs.find(cta, at, u0, end_at, u1);
   const int steps = u1 - u0;
   if (steps == 0) return;
 
@@ -360,14 +365,14 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     nx_page = -1;
     Unit x = ahead_at;
     x.unit += lane;
-    int n = units_of(x.seq);
+    int n = runs.units_of(x.seq);
     const int most = steps - base;  // steps from here on
     if (lane < most) {
       while (x.unit >= n) {
         x.unit -= n;
         if (++x.item == items) {
           x.item = 0;
-          n = units_of(++x.seq);
+          n = runs.units_of(++x.seq);
         }
       }
       const SeqSpan sp = span_of(a, s_len[x.seq]);
@@ -382,7 +387,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       ahead_at.seq = __shfl_sync(0xffffffffu, x.seq, 31);
       ahead_at.item = __shfl_sync(0xffffffffu, x.item, 31);
       ahead_at.unit = __shfl_sync(0xffffffffu, x.unit, 31) + 1;
-      if (ahead_at.unit == units_of(ahead_at.seq)) {
+      if (ahead_at.unit == runs.units_of(ahead_at.seq)) {
         ahead_at.unit = 0;
         if (++ahead_at.item == items) {
           ahead_at.item = 0;
@@ -457,7 +462,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   int step = 0, q_buf = 0;
   uint32_t valid = 0;
   while (step < steps) {
-    const int b = at.seq, hr = at.item, nu = units_of(b);
+    const int b = at.seq, hr = at.item, nu = runs.units_of(b);
     const int todo = nu - at.unit < steps - step ? nu - at.unit : steps - step;  // units of this run in the item
     const bool starts = at.unit == 0, whole = starts && todo == nu;
     const int head = hr / p.tiles, tile = hr - head * p.tiles;
@@ -465,11 +470,6 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const SeqSpan sp = span_of(a, len);
     // (the last unit's end may pass 2^31, but not the records that are looked at)
     int tok = (int)(((uint32_t)(sp.unit + at.unit) * AT_WARPS + warp) * KV_GROUP - AT_UNIT);
-    if (tid == 0 && starts && (p.by_item || !whole)) {
-      AttnCut cut{};
-      if (!whole) cut = {cta, run_of(v_first(b) + hr * (nu + AT_PAD) + nu - 1) - cta + 1, b, head, tile};
-      p.ws.cut[p.by_item ? b * items + hr : cta] = cut;
-    }
     at.unit = 0;  // (the next item's first, if there is one)
     if (++at.item == items) {
       at.item = 0;
@@ -969,38 +969,81 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   }
 }
 
-// Joins the parts of the items that are cut. BY_ITEM: blockIdx.x is an item, its rows along y,
-// one to a CTA, whose warps share the parts out; for few items of many parts. Otherwise blockIdx.x is a
-// CTA of the main kernel and a warp joins a row; for many items of few parts.
+// Joins the parts of the items that are cut. blockIdx.x is an item (by_item) or, where there are more items than CTAs of
+// the main kernel, one of those CTAs: the last item that starts in its run is the only one that may be cut. WIDE: a CTA
+// joins a row and its warps share the parts out, for few items of many parts; otherwise a warp joins a row.
 constexpr int JOIN_THREADS = 256;
 constexpr int JOIN_WARPS = JOIN_THREADS / 32;
 
-template <int D, int ROWS, bool BY_ITEM>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p) {
+template <int D, int ROWS, bool WIDE>
+__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p, int grid, int by_item) {
   constexpr int V = D / 32;  // dimensions of a lane
-  __shared__ float s_y[BY_ITEM ? JOIN_WARPS : 1][D];
+  __shared__ float s_y[WIDE ? JOIN_WARPS : 1][D];
   __shared__ float s_red[2][JOIN_WARPS];
-  pdl_trigger();
-  pdl_wait();
-  const AttnCut cut = p.ws.cut[blockIdx.x];
+  __shared__ int s_part[JOIN_WARPS];
+  extern __shared__ int32_t s_runs[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = BY_ITEM ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
-  const int r = cut.tile * ROWS + row;
-  if (cut.n == 0 || row >= ROWS || r >= p.group * p.a.ncols) return;
-  const int n = cut.n;
+  const int row = WIDE ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+  pdl_trigger();
+  // The main kernel is not launched early, so what came before it is complete; its parts are not before pdl_wait.
+  const Runs<JOIN_THREADS> runs(p.a, p.tiles, grid, s_runs, s_part, false);
+  Unit x;
+  int c0 = blockIdx.x, n = 0;
+  if (by_item) {
+    x.seq = blockIdx.x / runs.items;
+    x.item = blockIdx.x - x.seq * runs.items;
+    const int v = runs.v_item(x.seq, x.item);
+    c0 = runs.run_of(v);
+    n = runs.run_of(v + runs.units_of(x.seq) - 1) - c0 + 1;
+    if (n == 1) n = 0;
+  } else if (c0 < runs.N) {
+    // cut is the item that run c0 ends in the middle of, if it starts in that run
+    Unit first;
+    int u0, u1;
+    runs.find(c0, first, u0, x, u1);
+    if (x.unit > 0) {
+      const int v = runs.v_item(x.seq, x.item);
+      if (v >= runs.run_start(c0)) n = runs.run_of(v + runs.units_of(x.seq) - 1) - c0 + 1;
+    }
+  }
+  const int head = x.item / p.tiles, tile = x.item - head * p.tiles;
+  const int r = tile * ROWS + row;
+  pdl_wait();
+  if (n == 0 || row >= ROWS || r >= p.group * p.a.ncols) return;
   // part i: the first CTA's run ends in the item (its second slot), the others' start in it
-  auto slot = [&](int i) { return ((size_t)(cut.c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
+  auto slot = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
   auto stat = [&](int i) {
-    return i < n ? *reinterpret_cast<const float2*>(p.ws.zl + slot(i) * 2) : make_float2(-INFINITY, 0.f);
+    return i < n ? __ldcg(reinterpret_cast<const float2*>(p.ws.zl + slot(i) * 2)) : make_float2(-INFINITY, 0.f);
   };
+  // eight parts' loads in flight at a time, the first eight while reference and sum over all parts are found
+  constexpr int STEP = WIDE ? JOIN_WARPS : 1;
+  float part[8][V], z[8];
+  auto load = [&](int i0) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int i = i0 + j * STEP;
+      z[j] = -INFINITY;
+      if (i < n) {
+        z[j] = __ldcg(p.ws.zl + slot(i) * 2);
+#pragma unroll
+        for (int k = 0; k < V; k += 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws.o + slot(i) * D + lane * V + k));
+          part[j][k] = v.x;
+          part[j][k + 1] = v.y;
+        }
+      }
+    }
+  };
+  const int mine = WIDE ? warp : 0;
+  load(mine);
   // reference and sum over all parts
-  constexpr int SPREAD = BY_ITEM ? JOIN_THREADS : 32;
-  const int me = BY_ITEM ? tid : lane;
+  constexpr int SPREAD = WIDE ? JOIN_THREADS : 32;
+  const int me = WIDE ? tid : lane;
   float top = -INFINITY, sum = 0.f;
   for (int i = me; i < n; i += SPREAD) top = fmaxf(top, stat(i).x);
 #pragma unroll
   for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if constexpr (BY_ITEM) {
+  if constexpr (WIDE) {
     if (lane == 0) s_red[0][warp] = top;
     __syncthreads();
 #pragma unroll
@@ -1012,7 +1055,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
   }
 #pragma unroll
   for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if constexpr (BY_ITEM) {
+  if constexpr (WIDE) {
     if (lane == 0) s_red[1][warp] = sum;
     __syncthreads();
     sum = 0.f;
@@ -1022,34 +1065,19 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
   float y[V];
 #pragma unroll
   for (int k = 0; k < V; ++k) y[k] = 0.f;
-  // eight parts' loads in flight at a time
-  constexpr int STEP = BY_ITEM ? JOIN_WARPS : 1;
-  for (int i0 = BY_ITEM ? warp : 0; i0 < n; i0 += 8 * STEP) {
-    float x[8][V], f[8];
+  for (int i0 = mine; i0 < n; i0 += 8 * STEP) {
+    if (i0 != mine) load(i0);
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
-      const int i = i0 + j * STEP;
-      f[j] = stat(i).x;
-      if (i < n) {
-#pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 v = *reinterpret_cast<const float2*>(p.ws.o + slot(i) * D + lane * V + k);
-          x[j][k] = v.x;
-          x[j][k + 1] = v.y;
-        }
-      }
-    }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float w = f[j] == -INFINITY ? 0.f : ex2(f[j] - top);
+      const float w = z[j] == -INFINITY ? 0.f : ex2(z[j] - top);
       if (w != 0.f)
 #pragma unroll
-        for (int k = 0; k < V; ++k) y[k] = fmaf(x[j][k], w, y[k]);
+        for (int k = 0; k < V; ++k) y[k] = fmaf(part[j][k], w, y[k]);
     }
   }
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
-  const size_t yo = (((size_t)cut.seq * p.a.ncols + r / p.group) * p.a.n_heads + cut.head * p.group + r % p.group) * D;
-  if constexpr (BY_ITEM) {
+  const size_t yo = (((size_t)x.seq * p.a.ncols + r / p.group) * p.a.n_heads + head * p.group + r % p.group) * D;
+  if constexpr (WIDE) {
 #pragma unroll
     for (int k = 0; k < V; ++k) s_y[warp][lane * V + k] = y[k];
     __syncthreads();
@@ -1070,7 +1098,7 @@ template <int D, int NT>
 constexpr size_t attn_ws_of() {
   constexpr int grid = AttnCfg<QG_Q8_0, D, NT>::GRID;
   static_assert(grid >= AttnCfg<QG_F16, D, NT>::GRID, "the workspace's size does not depend on the type");
-  return (size_t)grid * (sizeof(AttnCut) + (size_t)2 * 8 * NT * (8 + D * 4));
+  return (size_t)grid * ((size_t)2 * 8 * NT * (8 + D * 4));
 }
 
 template <int TYPE, int D, int NT>
@@ -1087,28 +1115,20 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
   const int n_items = a.c.n_seq * a.c.n_kv_heads * p.tiles;
   const int tile_rows = all < C::ROWS ? all : C::ROWS;
-  // few items: they have many parts each
-  p.by_item = n_items <= C::GRID && n_items * tile_rows <= 8 * AT_SMS;
+  const bool by_item = n_items <= C::GRID, wide = n_items <= 4 * AT_SMS / tile_rows;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
-  p.ws.cut = reinterpret_cast<AttnCut*>(ws);
-  ws += (size_t)C::GRID * sizeof(AttnCut);
   p.ws.zl = reinterpret_cast<float*>(ws);
   ws += (size_t)C::GRID * 2 * C::ROWS * 8;
   p.ws.o = reinterpret_cast<float*>(ws);
   const size_t smem = C::smem(a.c.n_seq);
   cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT>, smem, false);
   if (e != cudaSuccess) return e;
-  // both hold their SMs through shared memory, not L1
-  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_SMEM, p);
+  const auto join = wide ? attn_join_kernel<D, C::ROWS, true> : attn_join_kernel<D, C::ROWS, false>;
+  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_FULL, p);
   if (e != cudaSuccess) return e;
-  // The join is not launched early: with both kernels early, a step's main kernel would start while the one
-  // before it is still running, on whatever SMs are free first, and its one wave of CTAs would be uneven
-  // (131,071 f16 tokens in a loop of calls: 104 us; with this rule 86).
-  if (p.by_item)
-    return launch_pdl(attn_join_kernel<D, C::ROWS, true>, dim3(n_items, tile_rows), dim3(JOIN_THREADS), 0, s, 0,
-                      LC_LATE, p);
-  return launch_pdl(attn_join_kernel<D, C::ROWS, false>, dim3(C::GRID, (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS),
-                    dim3(JOIN_THREADS), 0, s, 0, LC_LATE, p);
+  const dim3 grid(by_item ? n_items : C::GRID, wide ? tile_rows : (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS);
+  return launch_pdl(join, grid, dim3(JOIN_THREADS), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p, C::GRID,
+                    (int)by_item);
 }
 
 inline cudaError_t attn_error_word(int32_t* bits) {
