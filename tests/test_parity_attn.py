@@ -673,3 +673,43 @@ def test_guard_bands(qtype, d, heads, ncols, lens):
     qg.qkv_append(c, x[:2, :kv], x[:2, :kv], torch.tensor([0, min(lens) - 1], dtype=torch.int32, device="cuda"),
                   rope=qg.qrope_plan(d), q=x[:2], q_out=qo[:2 * 3 * d * 2].view(torch.float16).view(2, 3, d))
     assert intact(qo_buf) and intact(pool_buf)
+
+
+# ------------------------------------------------- scale, many sequences, threads
+@pytest.mark.parametrize("qtype", [F16, Q8])
+@pytest.mark.parametrize("scale", [0.0, -0.125, 1.0, 1e-30])
+@pytest.mark.parametrize("heads,d", [(3, 64), (12, 256)])
+def test_attention_any_scale(qtype, scale, heads, d):
+    """A scale of zero (the mean of the values), a negative, a large and a vanishing one."""
+    c, ks, vs = filled(qtype, 1, d, 16, [70, 3], 9)
+    q = rng(14, heads).standard_normal((2, 2, heads, d)).astype(np.float16)
+    y, err = attend(c, q, [70, 3], scale=scale)
+    want, bound = ref.attention(q, ks, vs, [70, 3], 2, 0, scale)
+    assert err == 0
+    assert_within(y, want, bound, f"scale {scale}")
+
+
+def test_attention_1024_sequences():
+    """The most sequences a call takes, of lengths 0 to 40."""
+    n, kv, heads, d, ps = 1024, 1, 2, 64, 16
+    lens = [(7 * i) % 41 for i in range(n)]
+    pages = 3
+    table = torch.randperm(n * pages, device="cuda").to(torch.int32).view(n, pages)
+    pool = torch.full((n * pages * qg.qkv_page_bytes(F16, kv, d, ps),), 0xFF, dtype=torch.uint8, device="cuda")
+    c = qg.qkv_cache(F16, pool, table, kv, d, ps)
+    seq = torch.tensor([s for s in range(n) for _ in range(lens[s])], dtype=torch.int32, device="cuda")
+    pos = torch.tensor([j for s in range(n) for j in range(lens[s])], dtype=torch.int32, device="cuda")
+    k, v = torch.randn(2, len(pos), kv, d, device="cuda")
+    qg.qkv_append(c, k, v, pos, seq=seq)
+    q = torch.randn(n, 1, heads, d, device="cuda").half()
+    y = torch.empty_like(q)
+    ws = torch.empty(qg.qattn_workspace_bytes(c, heads, 1), dtype=torch.uint8, device="cuda")
+    qg.qattn_paged(c, q, torch.tensor(lens, dtype=torch.int32, device="cuda"), y, ws)
+    want, bound = big_reference(c, q, lens, 1)
+    assert ((y.double() - want).abs() <= bound).all()
+
+
+def test_no_wait_was_given_up():
+    """After all calls of this file the device error word is 0."""
+    torch.cuda.synchronize()
+    assert qg.qg_device_error() == 0
