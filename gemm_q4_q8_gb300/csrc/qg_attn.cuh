@@ -91,7 +91,7 @@ struct AttnCfg {
   static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
-  static constexpr size_t qbuf = (size_t)2 * ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)NB * ROWS * 4 : 0);
+  static constexpr size_t qbuf = (size_t)2 * ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)NB * ROWS * 8 : 0);
   // Stages of a warp's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 600 bytes for up to
   // 72 sequences a CTA).
   static constexpr int fit(int n) {
@@ -185,13 +185,13 @@ __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
   return d;
 }
 
-// D = A B + C with C's two columns the same in all rows.
+// D = A B + C, C kept.
 __device__ __forceinline__ void mma16816_from(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1,
-                                              float c0, float c1) {
+                                              const float (&c)[4]) {
   asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
-      "{%8, %9}, {%10, %11, %10, %11};"
+      "{%8, %9}, {%10, %11, %12, %13};"
       : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c[0]), "f"(c[1]), "f"(c[2]), "f"(c[3]));
 }
 
 struct SeqSpan {
@@ -313,12 +313,12 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   int32_t* const s_runs = reinterpret_cast<int32_t*>(s_bar + AT_WARPS * C::BARS);
   __shared__ int s_part[AT_WARPS];
 
-  uint32_t k64;  // the high bytes of f16 1024 + u, in a register that is not made anew at each use
-  asm volatile("mov.b32 %0, 0x64646464;" : "=r"(k64));
+  __shared__ uint32_t s_k64[32];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   pdl_trigger();
+  if (tid < 32) s_k64[tid] = 0x64646464u;
   if (tid < AT_WARPS * C::BARS) {
     mbar_init(s_bar + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -350,6 +350,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     }
   };
   stage_q(at, 0);
+  // The high bytes of f16 1024 + u. Read from shared memory it stays in a register of each lane; as a constant it is
+  // moved from a uniform register at every use (eight moves a block).
+  const uint32_t k64 = s_k64[lane];
 
   // ------------------------------------------------------------ the ring
   const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
@@ -490,7 +493,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // Q: the B fragments of a block and row tile, dimensions 8t .. 8t+7 of row g; and, for
     // Q8_0, -128 2^-24 sum of the block's queries of rows 2t and 2t + 1.
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : NT][4];
-    float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][2];
+    float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][4];  // (each twice, as the mma's C)
     const uint32_t q_at = smem_u32(s_q) + (q_buf * ROWS + g) * C::QPITCH + 16 * t;  // this lane's, of block 0 and tile 0
     auto load_q = [&](int blk, int nt, uint32_t (&q)[4]) {
       lds128(q_at + nt * 8 * C::QPITCH + blk * 64, q[0], q[1], q[2], q[3]);
@@ -502,7 +505,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       return s * -7.62939453125e-06f;  // -128 * 2^-24
     };
-    float* const s_qsum = reinterpret_cast<float*>(s_q + 2 * ROWS * C::QPITCH);  // [block][row]
+    float* const s_qsum = reinterpret_cast<float*>(s_q + 2 * ROWS * C::QPITCH);  // [block][tile][t][4]
     copies_done();
     if (p.q_and != 0xffffffffu || p.q_xor) {  // a scale that is not positive: each thread on what it copied
       for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
@@ -518,7 +521,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           uint32_t q[4];
           load_q(i / NT, i % NT, q);
           const float s = sum_q(q);
-          if (t == 0) s_qsum[i * 8 + g] = s;
+          if (t < 2) s_qsum[i * 16 + (g >> 1) * 4 + 2 * t + (g & 1)] = s;
         }
         __syncthreads();
       }
@@ -530,8 +533,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           load_q(blk, nt, qf[blk][nt]);
           if constexpr (TYPE == QG_Q8_0) {
             const float s = sum_q(qf[blk][nt]);
-            qc[blk][nt][0] = __shfl_sync(0xffffffffu, s, 8 * t);
-            qc[blk][nt][1] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
+            qc[blk][nt][0] = qc[blk][nt][2] = __shfl_sync(0xffffffffu, s, 8 * t);
+            qc[blk][nt][1] = qc[blk][nt][3] = __shfl_sync(0xffffffffu, s, 8 * t + 4);
           }
         }
     }
@@ -637,17 +640,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             mma16816_acc(s[nt], a0, q[0], q[1]);
             mma16816_acc(s[nt], a1, q[2], q[3]);
           } else {
-            float c0, c1;
+            float part[4], c[4];
             if constexpr (C::QSMEM) {
-              const float2 c = *reinterpret_cast<const float2*>(s_qsum + (blk * NT + nt) * 8 + 2 * t);
-              c0 = c.x;
-              c1 = c.y;
+              const float4 x = *reinterpret_cast<const float4*>(s_qsum + (blk * NT + nt) * 16 + 4 * t);
+              c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
             } else {
-              c0 = qc[blk][nt][0];
-              c1 = qc[blk][nt][1];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) c[i] = qc[blk][nt][i];
             }
-            float part[4];
-            mma16816_from(part, a0, q[0], q[1], c0, c1);
+            mma16816_from(part, a0, q[0], q[1], c);
             mma16816_acc(part, a1, q[2], q[3]);
             s[nt][0] = fmaf(part[0], e0, s[nt][0]);
             s[nt][1] = fmaf(part[1], e0, s[nt][1]);
