@@ -70,7 +70,13 @@ namespace {
 
 constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
-constexpr int AT_UNIT = AT_WARPS * KV_GROUP;  // tokens of a unit
+// Warps that share a record: 32 rows of heads of 256 are split between two, 128 dimensions each, which add their scores
+// up; each then has the registers of a warp on heads of 128. (16 sequences of 8,191 f16 tokens, two kv heads, 32 rows:
+// 70 us, against 90 for two tiles of 16 rows that read everything twice. For fewer rows, and for Q8_0, a warp on its own
+// is faster: 48 us against 50 for 8 rows, f16; 61 against 67 or 81 for 32 rows, Q8_0.)
+__host__ __device__ constexpr int at_team(int d, int nt) { return d == 256 && nt == 4 ? 2 : 1; }
+// Tokens of a unit: a record of 16 for every team of the CTA.
+__host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_team(d, nt) * KV_GROUP; }
 constexpr int AT_SMS = 152;
 // An item's end (four warps' sums joined, the next queries loaded) costs a warp about as much as
 // this many units, and the runs are cut as if it were that many more.
@@ -80,35 +86,36 @@ constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this
 template <int TYPE, int D, int NT>
 struct AttnCfg {
   static constexpr int ROWS = 8 * NT;
-  static constexpr int NB = D / 32;
-  static constexpr int ACC = NT * D / 4;  // accumulator registers
-  static constexpr int HALF = kv_half_bytes(TYPE, D);
-  static constexpr int STAGE = (2 * HALF + 127) / 128 * 128;  // a record
+  static constexpr int TEAM = at_team(D, NT), TEAMS = AT_WARPS / TEAM;
+  static constexpr int NB = D / 32 / TEAM;      // blocks of a warp
+  static constexpr int ACC = NT * NB * 8;       // accumulator registers
+  static constexpr int RECORD = kv_record_bytes(TYPE, D), STAGE = (RECORD + 127) / 128 * 128;
   static constexpr bool QSMEM = NT * NB > 4;  // Q fragments read from shared memory each time, not kept in registers
   static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
   // dimensions joined at a time (32 also where 64 would leave one stage less)
-  static constexpr int OD = NT > 2 || (NT == 1 && kv_half_bytes(TYPE, D) == 4096) ? 32 : 64;
+  static constexpr int OD = NT > 2 || (NT == 1 && RECORD == 8192) ? 32 : 64;
   static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
+  static_assert(TEAM == 1 || obuf >= (size_t)2 * AT_WARPS * NT * 512, "a team's scores pass through the join buffer");
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
-  static constexpr size_t qbuf = (size_t)2 * ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)NB * ROWS * 8 : 0);
-  // Stages of a warp's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 600 bytes for up to
+  static constexpr size_t qbuf = (size_t)ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)(D / 32) * ROWS * 8 : 0);
+  // Stages of a team's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 600 bytes for up to
   // 72 sequences a CTA).
   static constexpr int fit(int n) {
-    return (int)(((size_t)(227 * 1024) / n - 1024 - 600 - obuf - stats - qbuf - 256) / ((size_t)AT_WARPS * STAGE));
+    return (int)(((size_t)(227 * 1024) / n - 1024 - 600 - obuf - stats - qbuf - 256) / ((size_t)TEAMS * STAGE));
   }
-  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them), fewer while a warp
+  // CTAs per SM, by the registers a thread needs (128 threads: 128, 168 or 255 of them), fewer while a team
   // has not two stages.
   static constexpr int REGS = ACC <= 32 ? 4 : ACC <= 64 ? 3 : 2;
-  static constexpr int CPS = fit(REGS) >= 2 || REGS == 2 ? REGS : fit(REGS - 1) >= 2 || REGS == 3 ? REGS - 1 : 2;
+  static constexpr int CPS = fit(REGS) >= 2 || REGS == 2 ? REGS : fit(REGS - 1) >= 2 ? REGS - 1 : 2;
   static constexpr int GRID = AT_SMS * CPS;
   static constexpr int STAGES = fit(CPS) > 4 ? 4 : fit(CPS);
-  static_assert(STAGES >= 1, "a warp needs room for a record");
   // With one stage its halves come and go on their own: keys while values are in use, and the other way round.
   static constexpr bool SPLIT = STAGES == 1;
+  static_assert(STAGES >= 1 && (TEAM == 1 || !SPLIT), "room for the records in use");
   static constexpr int BARS = SPLIT ? 2 : STAGES;
-  static constexpr size_t ring = (size_t)AT_WARPS * STAGES * STAGE;
-  static constexpr size_t bars = (size_t)AT_WARPS * BARS * 8;
+  static constexpr size_t ring = (size_t)TEAMS * STAGES * STAGE;
+  static constexpr size_t bars = (size_t)TEAMS * BARS * 8;
   static size_t smem(int n_seq) {
     return ring + obuf + stats + qbuf + bars + (size_t)(2 * n_seq + 1) * 4;
   }
@@ -200,14 +207,15 @@ struct SeqSpan {
   int unit;  // first unit
   int n;     // units (at least one, so that every item is written by some CTA)
 };
+template <int UNIT>
 __device__ __forceinline__ SeqSpan span_of(const AttnArgs& a, int len) {
   SeqSpan s;
   const int cap = a.c.max_pages * a.c.page_size;
   s.hi = len < cap ? len : cap;
   const int64_t lo = (int64_t)len - a.ncols - a.window + 1;
   s.lo = a.window > 0 && lo > 0 ? (int)lo : 0;
-  s.unit = s.lo / AT_UNIT;
-  const int end = (int)(((int64_t)s.hi + AT_UNIT - 1) / AT_UNIT);
+  s.unit = s.lo / UNIT;
+  const int end = (int)(((int64_t)s.hi + UNIT - 1) / UNIT);
   s.n = end - s.unit > 1 ? end - s.unit : 1;
   return s;
 }
@@ -218,7 +226,7 @@ __device__ __forceinline__ SeqSpan span_of(const AttnArgs& a, int len) {
 struct Unit {
   int seq, item, unit;  // item of the sequence, unit of the item
 };
-template <int THREADS>
+template <int THREADS, int UNIT>
 struct Runs {
   int32_t* first;  // [n_seq + 1] units before a sequence (times its items)
   int32_t* len;    // [n_seq] lengths, none negative
@@ -237,7 +245,7 @@ struct Runs {
       if ((l < 0 || l > cap) && report && a.err) atomicOr(a.err, QG_KV_BAD_POS);
       l = max(l, 0);
       len[b] = l;
-      sum += span_of(a, l).n;
+      sum += span_of<UNIT>(a, l).n;
     }
     int run = sum;
 #pragma unroll
@@ -251,7 +259,7 @@ struct Runs {
     for (int w = 0; w < warp; ++w) before += part[w];
     for (int b = b0; b < b1; ++b) {
       first[b] = before;
-      before += span_of(a, len[b]).n;
+      before += span_of<UNIT>(a, len[b]).n;
     }
     if (b1 == n_seq && b0 < n_seq) first[n_seq] = before;
     __syncthreads();
@@ -303,30 +311,31 @@ template <int TYPE, int D, int NT>
 __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     attn_kernel(const __grid_constant__ AttnDev p) {
   using C = AttnCfg<TYPE, D, NT>;
-  constexpr int NB = C::NB, ROWS = C::ROWS;
+  constexpr int NB = C::NB, ROWS = C::ROWS, TEAM = C::TEAM, UNIT = at_unit(D, NT);
   extern __shared__ __align__(128) uint8_t smem[];
   uint8_t* const s_ring = smem;
   float* const s_o = reinterpret_cast<float*>(smem + C::ring);
   float* const s_stat = reinterpret_cast<float*>(smem + C::ring + C::obuf);
   uint8_t* const s_q = smem + C::ring + C::obuf + C::stats;
   uint64_t* const s_bar = reinterpret_cast<uint64_t*>(s_q + C::qbuf);
-  int32_t* const s_runs = reinterpret_cast<int32_t*>(s_bar + AT_WARPS * C::BARS);
+  int32_t* const s_runs = reinterpret_cast<int32_t*>(s_bar + C::TEAMS * C::BARS);
   __shared__ int s_part[AT_WARPS];
 
   __shared__ uint32_t s_k64[32];
   const AttnArgs& a = p.a;
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
+  const int team = warp / TEAM, share = warp % TEAM;  // the warp has blocks share * NB ... of the team's records
   pdl_trigger();
   if (tid < 32) s_k64[tid] = 0x64646464u;
-  if (tid < AT_WARPS * C::BARS) {
+  if (tid < C::TEAMS * C::BARS) {
     mbar_init(s_bar + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
 
   const int cta = blockIdx.x;
-  const Runs<AT_THREADS> runs(a, p.tiles, C::GRID, s_runs, s_part, cta == 0);
+  const Runs<AT_THREADS, UNIT> runs(a, p.tiles, C::GRID, s_runs, s_part, cta == 0);
   if (cta >= runs.N) return;
   const int items = runs.items;
   const int32_t* const s_len = runs.len;
@@ -336,28 +345,31 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   const int steps = u1 - u0;
   if (steps == 0) return;
 
-  // Queries of an item into one of two buffers, [row][D] f16, asynchronously: the first before any keys are
-  // asked for, the others an item ahead (in the middle of the stream a load takes microseconds).
+  // Queries of an item into shared memory, [row][D] f16, asynchronously: the first before any keys are asked for, the
+  // others as soon as the buffer is free (in the middle of the stream a load takes microseconds).
   const int rows = p.group * a.ncols;
-  auto stage_q = [&](const Unit& x, int buf) {
+  auto stage_q = [&](const Unit& x) {
     const int head = x.item / p.tiles, r0 = (x.item - head * p.tiles) * ROWS;
     for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
       const int row = i / (D / 8), c = i % (D / 8), r = r0 + row;
       const uint16_t* src = a.q;
       if (r < rows)
         src += (((size_t)x.seq * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + 8 * c;
-      copy16_async(smem_u32(s_q) + (buf * ROWS + row) * C::QPITCH + 16 * c, src, r < rows ? 16 : 0);
+      copy16_async(smem_u32(s_q) + row * C::QPITCH + 16 * c, src, r < rows ? 16 : 0);
     }
   };
-  stage_q(at, 0);
+  stage_q(at);
   // The high bytes of f16 1024 + u. Read from shared memory it stays in a register of each lane; as a constant it is
   // moved from a uniform register at every use (eight moves a block).
   const uint32_t k64 = s_k64[lane];
 
   // ------------------------------------------------------------ the ring
   const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
-  uint8_t* const ring = s_ring + (size_t)warp * C::STAGES * C::STAGE;
-  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + warp * C::BARS);
+  uint8_t* const ring = s_ring + (size_t)team * C::STAGES * C::STAGE;
+  const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + team * C::BARS);
+  // In a half record: where this warp's blocks are, and (Q8_0) from there their scales.
+  constexpr int BLOCKS = NB * 32 * KV_GROUP * (TYPE == QG_F16 ? 2 : 1);
+  const int own = share * BLOCKS, scales = TEAM * BLOCKS - share * (BLOCKS - NB * 32);
   // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
   // so that the load has the whole batch before to arrive.
   int nx_page = -1, nx_off = 0;
@@ -378,8 +390,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           n = runs.units_of(++x.seq);
         }
       }
-      const SeqSpan sp = span_of(a, s_len[x.seq]);
-      const int grp = (sp.unit + x.unit) * AT_WARPS + warp;  // group of 16 tokens, hence the comparisons in groups
+      const SeqSpan sp = span_of<UNIT>(a, s_len[x.seq]);
+      const int grp = (sp.unit + x.unit) * C::TEAMS + team;  // group of 16 tokens, hence the comparisons in groups
       if (grp < (sp.hi + KV_GROUP - 1) / KV_GROUP && grp >= sp.lo / KV_GROUP) {
         nx_in = true;
         nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (grp >> gpp_log)];
@@ -406,37 +418,38 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     if (nx_in) {
       if (nx_page >= 0 && nx_page < a.c.n_pages)
         my_rec = static_cast<const uint8_t*>(a.c.pool) +
-                 ((size_t)nx_page * a.c.n_kv_heads * gpp + nx_off) * (2 * C::HALF);
+                 ((size_t)nx_page * a.c.n_kv_heads * gpp + nx_off) * kv_record_bytes(TYPE, D);
       else if (a.err)
         atomicOr(a.err, QG_KV_BAD_PAGE);
     }
     const uint32_t v = __ballot_sync(0xffffffffu, my_rec != nullptr);
     if (step & 32) valid_odd = v; else valid_even = v;
   };
-  // Fetch the record of `step` (from byte `from`, `bytes` of it) to `dst`: the lane that looked it up does. A
-  // step without a record completes the barrier at once.
+  // Fetch the record of `step` into a stage: the lane that looked it up does, of the team's first warp. A step without a
+  // record completes the barrier at once.
   bool ok = true;  // false once a wait gave up: no more copies, no more waits
-  auto fetch = [&](int step, int from, uint32_t bytes, uint32_t dst, uint32_t bar) {
-    const bool mine = lane == (step & 31) && step < steps && ok;
-    fetch_if(mine, mine && my_rec, dst, my_rec + from, bytes, bar);
+  constexpr int HALF = kv_half_bytes(TYPE, D);
+  auto fetch = [&](int step, int to) {  // SPLIT: `to` is the half
+    const bool mine = lane == (step & 31) && step < steps && ok && share == 0;
+    if constexpr (C::SPLIT)
+      fetch_if(mine, mine && my_rec, ring_at + to * HALF, my_rec + to * HALF, HALF, bar_at + 8 * to);
+    else
+      fetch_if(mine, mine && my_rec, ring_at + to * C::STAGE, my_rec, C::RECORD, bar_at + 8 * to);
   };
   __syncwarp();
   look_up(0);
   enter(0);
-  if constexpr (C::SPLIT) {
-    fetch(0, 0, C::HALF, ring_at, bar_at);
-    fetch(0, C::HALF, C::HALF, ring_at + C::HALF, bar_at + 8);
-  } else {
 #pragma unroll
-    for (int i = 0; i < C::STAGES; ++i) fetch(i, 0, 2 * C::HALF, ring_at + i * C::STAGE, bar_at + 8 * i);
-  }
+  for (int i = 0; i < C::BARS; ++i) fetch(C::SPLIT ? 0 : i, i);
   look_up(32);
   int stage = 0;        // the stage in use
   uint32_t parity = 0;  // of its barriers
   auto arrived = [&](uint32_t bar) {
     if (!bar_ready(bar, parity) && ok) ok = mbar_wait_slow(bar, parity, &g_attn_error);
   };
-  // Reads of a stage are over: every lane orders its own before the refill.
+  auto team_barrier = [&]() { asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "n"(32 * TEAM) : "memory"); };
+  // A stage's reads are over: every lane orders its own before the refill. A warp on its own then refills the stage at
+  // once; of a team, the first warp does after the next step's barrier, which both pass behind their reads.
   auto reads_done = [&]() {
     asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
     __syncwarp();
@@ -462,7 +475,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 
   // --------------------------------------------------------------- items
   int turn = 0;  // of the statistics' two buffers
-  int step = 0, q_buf = 0;
+  int step = 0;
   uint32_t valid = 0;
   while (step < steps) {
     const int b = at.seq, hr = at.item, nu = runs.units_of(b);
@@ -470,9 +483,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const bool starts = at.unit == 0, whole = starts && todo == nu;
     const int head = hr / p.tiles, tile = hr - head * p.tiles;
     const int len = s_len[b];
-    const SeqSpan sp = span_of(a, len);
+    const SeqSpan sp = span_of<UNIT>(a, len);
     // (the last unit's end may pass 2^31, but not the records that are looked at)
-    int tok = (int)(((uint32_t)(sp.unit + at.unit) * AT_WARPS + warp) * KV_GROUP - AT_UNIT);
+    int tok = (int)(((uint32_t)(sp.unit + at.unit) * C::TEAMS + team) * KV_GROUP - UNIT);
     at.unit = 0;  // (the next item's first, if there is one)
     if (++at.item == items) {
       at.item = 0;
@@ -494,7 +507,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // Q8_0, -128 2^-24 sum of the block's queries of rows 2t and 2t + 1.
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : NT][4];
     float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][4];  // (each twice, as the mma's C)
-    const uint32_t q_at = smem_u32(s_q) + (q_buf * ROWS + g) * C::QPITCH + 16 * t;  // this lane's, of block 0 and tile 0
+    const uint32_t q_at = smem_u32(s_q) + g * C::QPITCH + 16 * t + share * (NB * 64);  // this lane's, of the warp's first block
     auto load_q = [&](int blk, int nt, uint32_t (&q)[4]) {
       lds128(q_at + nt * 8 * C::QPITCH + blk * 64, q[0], q[1], q[2], q[3]);
     };
@@ -505,11 +518,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s += __shfl_xor_sync(0xffffffffu, s, 2);
       return s * -7.62939453125e-06f;  // -128 * 2^-24
     };
-    float* const s_qsum = reinterpret_cast<float*>(s_q + 2 * ROWS * C::QPITCH);  // [block][tile][t][4]
+    float* const s_qsum = reinterpret_cast<float*>(s_q + ROWS * C::QPITCH);  // [block][tile][t][4]
     copies_done();
     if (p.q_and != 0xffffffffu || p.q_xor) {  // a scale that is not positive: each thread on what it copied
       for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
-        uint4* const x = reinterpret_cast<uint4*>(s_q + (q_buf * ROWS + i / (D / 8)) * C::QPITCH + 16 * (i % (D / 8)));
+        uint4* const x = reinterpret_cast<uint4*>(s_q + i / (D / 8) * C::QPITCH + 16 * (i % (D / 8)));
         *x = make_uint4((x->x & p.q_and) ^ p.q_xor, (x->y & p.q_and) ^ p.q_xor, (x->z & p.q_and) ^ p.q_xor,
                         (x->w & p.q_and) ^ p.q_xor);
       }
@@ -517,11 +530,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     __syncthreads();
     if constexpr (C::QSMEM) {
       if constexpr (TYPE == QG_Q8_0) {
-        for (int i = warp; i < NB * NT; i += AT_WARPS) {
+        for (int i = team; i < NB * NT; i += C::TEAMS) {
           uint32_t q[4];
           load_q(i / NT, i % NT, q);
           const float s = sum_q(q);
-          if (t < 2) s_qsum[i * 16 + (g >> 1) * 4 + 2 * t + (g & 1)] = s;
+          if (t < 2) s_qsum[(share * NB * NT + i) * 16 + (g >> 1) * 4 + 2 * t + (g & 1)] = s;
         }
         __syncthreads();
       }
@@ -538,9 +551,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
     }
-    // (the other buffer was read before the last item's end, which all warps have passed)
-    q_buf ^= 1;
-    if (step + todo < steps) stage_q(at, q_buf);
+    if (!C::QSMEM && step + todo < steps) {
+      __syncthreads();  // the buffer is in all warps' registers
+      stage_q(at);
+    }
 
     // o[blk][nt][i][c]: dimension 32 blk + 16 i + 8 (c/2) + g, row 8 nt + 2t + c%2
     float o[NB][NT][2][4];
@@ -565,34 +579,37 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
 
     for (const int end = step + todo; step < end; ++step) {
-      tok += AT_UNIT;
+      tok += UNIT;
       if ((step & 31) == 0) valid = (step & 32) ? valid_odd : valid_even;
-      const uint32_t kb = ring_at + stage * C::STAGE, vb = kb + C::HALF;
-      const uint32_t kbar = bar_at + stage * 8, vbar = C::SPLIT ? kbar + 8 : kbar;
+      const uint32_t kb = ring_at + stage * C::STAGE + own, vb = kb + HALF;
       // nothing to do where no token of the record is seen, or its page is bad
       const bool live = (valid >> (step & 31)) & 1;
       const bool masked = tok + KV_GROUP - 1 > hi_all || tok < lo_all;
-      const int ahead = step + C::STAGES;
-      const bool new_batch = (ahead & 31) == 0 && ahead < steps;
+      // SPLIT: the half just read; otherwise this stage, or a team's stage of the step before
+      auto refill = [&](int half) {
+        const int ahead = step + C::STAGES - (TEAM > 1);
+        const bool new_batch = (ahead & 31) == 0 && ahead < steps;
+        if (TEAM > 1 && step == 0) return;
+        if (new_batch && half == 0) enter(ahead);
+        fetch(ahead, C::SPLIT ? half : TEAM == 1 ? stage : stage ? stage - 1 : C::STAGES - 1);
+        if (new_batch && half == (C::SPLIT ? 1 : 0)) look_up(ahead + 32);
+      };
       auto next = [&]() {
         if (++stage == C::STAGES) {
           stage = 0;
           parity ^= 1;
         }
       };
-      arrived(kbar);
+      arrived(bar_at + stage * 8);
       if (__builtin_expect(!live, 0)) {
         __syncwarp();  // no lane re-arms a barrier that another still waits on
-        if (new_batch) enter(ahead);
+        if constexpr (TEAM > 1) team_barrier();  // (both warps pass as many, whatever they made of the page table)
+        refill(0);
         if constexpr (C::SPLIT) {
-          fetch(ahead, 0, C::HALF, kb, kbar);
-          arrived(vbar);
+          arrived(bar_at + 8);
           __syncwarp();
-          fetch(ahead, C::HALF, C::HALF, vb, vbar);
-        } else {
-          fetch(ahead, 0, 2 * C::HALF, kb, kbar);
+          refill(1);
         }
-        if (new_batch) look_up(ahead + 32);
         next();
         continue;
       }
@@ -622,7 +639,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           a0[3] = __byte_perm(x, 0, 0x4342);
           a1[1] = __byte_perm(y, 0, 0x4140);
           a1[3] = __byte_perm(y, 0, 0x4342);
-          lds64(kb + KV_GROUP * D + blk * 32 + scale_at, d0, d1);
+          lds64(kb + scales + blk * 32 + scale_at, d0, d1);
           const uint32_t d = __byte_perm(d0, d1, scale_sel);
           e0 = lo_f32(d);
           e1 = hi_f32(d);
@@ -642,7 +659,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           } else {
             float part[4], c[4];
             if constexpr (C::QSMEM) {
-              const float4 x = *reinterpret_cast<const float4*>(s_qsum + (blk * NT + nt) * 16 + 4 * t);
+              const float4 x = *reinterpret_cast<const float4*>(s_qsum + ((share * NB + blk) * NT + nt) * 16 + 4 * t);
               c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
             } else {
 #pragma unroll
@@ -657,10 +674,26 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
       }
+      if constexpr (TEAM > 1) {
+        // the other half of every sum; two buffers, so one barrier of the team a step
+        float4* const x = reinterpret_cast<float4*>(s_o) + ((step & 1) * AT_WARPS + warp) * (NT * 32) + lane;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) x[nt * 32] = make_float4(s[nt][0], s[nt][1], s[nt][2], s[nt][3]);
+        team_barrier();
+        const float4* const y = x + (share ? -1 : 1) * (NT * 32);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          const float4 v = y[nt * 32];
+          s[nt][0] += v.x;
+          s[nt][1] += v.y;
+          s[nt][2] += v.z;
+          s[nt][3] += v.w;
+        }
+        refill(0);
+      }
       if constexpr (C::SPLIT) {
         reads_done();
-        if (new_batch) enter(ahead);
-        fetch(ahead, 0, C::HALF, kb, kbar);
+        refill(0);
       }
 
       // ---- weights
@@ -723,15 +756,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
 
       // ---- weights times values
-      if constexpr (C::SPLIT) arrived(vbar);
-      uint8_t* const vp = ring + stage * C::STAGE + C::HALF;
+      if constexpr (C::SPLIT) arrived(bar_at + 8);
+      uint8_t* const vp = ring + stage * C::STAGE + HALF + own;
       if constexpr (TYPE == QG_F16) {
         if (__builtin_expect(masked, 0)) {
           // Zero weights do not silence a NaN or an infinity in the product. So the rows of tokens that no
           // query row sees are cleared, and values that are not finite are taken out here and added, to the
           // rows that see them.
           uint32_t odd = 0;  // tokens with such values
-          for (int i = lane; i < KV_GROUP * D / 8; i += 32) {
+          for (int i = lane; i < NB * KV_GROUP * 4; i += 32) {
             uint4* at = reinterpret_cast<uint4*>(vp) + i;
             const int tk = tok + ((i >> 2) & 15);
             if (tk >= sp.hi || tk < sp.lo) {
@@ -765,7 +798,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
                   }
               }
             __syncwarp();
-            for (int e = lane; e < D; e += 32) {
+            for (int e = lane; e < NB * 32; e += 32) {
               __half* const x = row + (e >> 5) * 512 + (e & 31);
               if (!(fabsf(__half2float(*x)) <= 65504.f)) *x = __ushort_as_half(0);
             }
@@ -793,7 +826,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         if (__builtin_expect(masked, 0)) {
           // As for f16: scales of tokens that no row sees may be anything, and a NaN scale (of a token that
           // some rows do not see) is taken out and given to the rows that see it.
-          uint16_t* sc = reinterpret_cast<uint16_t*>(vp + KV_GROUP * D);
+          uint16_t* sc = reinterpret_cast<uint16_t*>(vp + scales);
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk) {
             bool nan = false;
@@ -827,7 +860,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
           uint32_t d0, d1;
-          lds64(vb + KV_GROUP * D + blk * 32 + scale_at, d0, d1);
+          lds64(vb + scales + blk * 32 + scale_at, d0, d1);
           d[blk] = __byte_perm(d0, d1, scale_sel);
           big = __hmax2(big, *reinterpret_cast<__half2*>(&d[blk]));
         }
@@ -869,13 +902,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
       }
       reads_done();
-      if constexpr (C::SPLIT) {
-        fetch(ahead, C::HALF, C::HALF, vb, vbar);
-      } else {
-        if (new_batch) enter(ahead);
-        fetch(ahead, 0, 2 * C::HALF, kb, kbar);
-      }
-      if (new_batch) look_up(ahead + 32);
+      if constexpr (TEAM == 1) refill(C::SPLIT);
       next();
     }
 
@@ -896,10 +923,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         x += __shfl_xor_sync(0xffffffffu, x, 16);
         if (g == 0) {
           s_z[warp * ROWS + nt * 8 + 2 * t + c] = ref(nt, c);
-          s_l[warp * ROWS + nt * 8 + 2 * t + c] = x;
+          s_l[warp * ROWS + nt * 8 + 2 * t + c] = share ? 0.f : x;  // (a team's warps have the same weights)
         }
       }
     __syncthreads();
+    if (C::QSMEM && step < steps) stage_q(at);  // (all warps are through with the queries)
     float f[NT][2];
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
@@ -924,7 +952,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s_sum[tid] = sum;
     }
 #pragma unroll
-    for (int pass = 0; pass < D / C::OD; ++pass) {
+    for (int pass = 0; pass < NB * 32 / C::OD; ++pass) {
       if (pass) __syncthreads();  // the buffer has been read
 #pragma unroll
       for (int hb = 0; hb < C::OD / 32; ++hb) {
@@ -939,19 +967,19 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
                   f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
       }
       __syncthreads();
-      constexpr int QUADS = C::OD / 4;  // float4 of a row
+      constexpr int QUADS = C::OD / 4;  // float4 of a row of each share
 #pragma unroll
-      for (int k = 0; k < (ROWS * QUADS + AT_THREADS - 1) / AT_THREADS; ++k) {
-        const int row = (tid + k * AT_THREADS) / QUADS, dim = (tid % QUADS) * 4;
+      for (int k = 0; k < (TEAM * ROWS * QUADS + AT_THREADS - 1) / AT_THREADS; ++k) {
+        const int i = tid + k * AT_THREADS, of = i / (ROWS * QUADS), row = i / QUADS % ROWS, dim = (i % QUADS) * 4;
         const int r = tile * ROWS + row;
-        if (row >= ROWS || r >= rows) continue;
-        float4 y = *reinterpret_cast<const float4*>(s_o + row * C::OPITCH + dim);
+        if (of >= TEAM || r >= rows) continue;
+        float4 y = *reinterpret_cast<const float4*>(s_o + (of * ROWS + row) * C::OPITCH + dim);
 #pragma unroll
-        for (int w = 1; w < AT_WARPS; ++w) {
-          const float4 x = *reinterpret_cast<const float4*>(s_o + (w * ROWS + row) * C::OPITCH + dim);
+        for (int w = TEAM; w < AT_WARPS; w += TEAM) {
+          const float4 x = *reinterpret_cast<const float4*>(s_o + ((of + w) * ROWS + row) * C::OPITCH + dim);
           y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
         }
-        const int at = pass * C::OD + dim;
+        const int at = of * (NB * 32) + pass * C::OD + dim;
         const float sum = s_sum[row];
         if (whole) {
           const float inv = sum == 0.f ? 0.f : 1.f / sum;
@@ -987,7 +1015,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
   const int row = WIDE ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
   pdl_trigger();
   // The main kernel is not launched early, so what came before it is complete; its parts are not before pdl_wait.
-  const Runs<JOIN_THREADS> runs(p.a, p.tiles, grid, s_runs, s_part, false);
+  const Runs<JOIN_THREADS, at_unit(D, ROWS / 8)> runs(p.a, p.tiles, grid, s_runs, s_part, false);
   Unit x;
   int c0 = blockIdx.x, n = 0;
   if (by_item) {

@@ -1,5 +1,6 @@
 // qg_attn.h -- the attention's launchers by head size, between its translation
-// units. nt: row tiles of 8 that a CTA handles together.
+// units. nt: row tiles of 8 that a CTA handles together, a power of two: up to 8 at
+// heads of 64 and 4 above, half of that for Q8_0.
 #pragma once
 #include "qg_internal.h"
 

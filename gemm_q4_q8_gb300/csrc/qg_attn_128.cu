@@ -9,7 +9,7 @@ cudaError_t attn_launch_128(const AttnArgs& a, int nt, cudaStream_t s) {
   switch (nt) {
     case 1: return f16 ? attn_typed<QG_F16, 128, 1>(a, s) : attn_typed<QG_Q8_0, 128, 1>(a, s);
     case 2: return f16 ? attn_typed<QG_F16, 128, 2>(a, s) : attn_typed<QG_Q8_0, 128, 2>(a, s);
-    case 4: return f16 ? attn_typed<QG_F16, 128, 4>(a, s) : attn_typed<QG_Q8_0, 128, 4>(a, s);
+    case 4: return f16 ? attn_typed<QG_F16, 128, 4>(a, s) : cudaErrorInvalidValue;
   }
   return cudaErrorInvalidValue;
 }

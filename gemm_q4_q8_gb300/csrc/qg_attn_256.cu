@@ -9,6 +9,7 @@ cudaError_t attn_launch_256(const AttnArgs& a, int nt, cudaStream_t s) {
   switch (nt) {
     case 1: return f16 ? attn_typed<QG_F16, 256, 1>(a, s) : attn_typed<QG_Q8_0, 256, 1>(a, s);
     case 2: return f16 ? attn_typed<QG_F16, 256, 2>(a, s) : attn_typed<QG_Q8_0, 256, 2>(a, s);
+    case 4: return f16 ? attn_typed<QG_F16, 256, 4>(a, s) : cudaErrorInvalidValue;
   }
   return cudaErrorInvalidValue;
 }
@@ -17,6 +18,7 @@ size_t attn_ws_256(int nt) {
   switch (nt) {
     case 1: return attn_ws_of<256, 1>();
     case 2: return attn_ws_of<256, 2>();
+    case 4: return attn_ws_of<256, 4>();
   }
   return 0;
 }

@@ -10,7 +10,7 @@ cudaError_t attn_launch_64(const AttnArgs& a, int nt, cudaStream_t s) {
     case 1: return f16 ? attn_typed<QG_F16, 64, 1>(a, s) : attn_typed<QG_Q8_0, 64, 1>(a, s);
     case 2: return f16 ? attn_typed<QG_F16, 64, 2>(a, s) : attn_typed<QG_Q8_0, 64, 2>(a, s);
     case 4: return f16 ? attn_typed<QG_F16, 64, 4>(a, s) : attn_typed<QG_Q8_0, 64, 4>(a, s);
-    case 8: return f16 ? attn_typed<QG_F16, 64, 8>(a, s) : attn_typed<QG_Q8_0, 64, 8>(a, s);
+    case 8: return f16 ? attn_typed<QG_F16, 64, 8>(a, s) : cudaErrorInvalidValue;
   }
   return cudaErrorInvalidValue;
 }
