@@ -326,16 +326,16 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int g = lane >> 2, t = lane & 3;
   const int team = warp / TEAM, share = warp % TEAM;  // the warp has blocks share * NB ... of the team's records
-  pdl_trigger();
   if (tid < 32) s_k64[tid] = 0x64646464u;
   if (tid < C::TEAMS * C::BARS) {
     mbar_init(s_bar + tid, 1);
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
   }
   pdl_wait();
+  pdl_trigger();  // (not before: the join reads lens at once)
 
   const int cta = blockIdx.x;
-  const Runs<AT_THREADS, UNIT> runs(a, p.tiles, C::GRID, s_runs, s_part, cta == 0);
+  const Runs<AT_THREADS, UNIT> runs(a, p.tiles, gridDim.x, s_runs, s_part, cta == 0);
   if (cta >= runs.N) return;
   const int items = runs.items;
   const int32_t* const s_len = runs.len;
@@ -1014,7 +1014,7 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int row = WIDE ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
   pdl_trigger();
-  // The main kernel is not launched early, so what came before it is complete; its parts are not before pdl_wait.
+  // The main kernel lets this one start once what came before it is complete; so before pdl_wait only its parts are not.
   const Runs<JOIN_THREADS, at_unit(D, ROWS / 8)> runs(p.a, p.tiles, grid, s_runs, s_part, false);
   Unit x;
   int c0 = blockIdx.x, n = 0;
@@ -1144,7 +1144,14 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
   const int n_items = a.c.n_seq * a.c.n_kv_heads * p.tiles;
   const int tile_rows = all < C::ROWS ? all : C::ROWS;
-  const bool by_item = n_items <= C::GRID, wide = n_items <= 4 * AT_SMS / tile_rows;
+  // As many CTAs as there can be places. Where they leave every SM room for another, the kernel is launched early.
+  constexpr int unit = at_unit(D, NT);
+  int64_t most = ((int64_t)a.c.max_pages * a.c.page_size + unit - 1) / unit;  // units of a sequence
+  if (a.window > 0 && a.window / unit + 3 < most) most = a.window / unit + 3;
+  most = (most + AT_PAD) * n_items;
+  const int grid = most < C::GRID ? (int)most : C::GRID;
+  const bool early = grid <= AT_SMS;
+  const bool by_item = n_items <= grid, wide = n_items <= 4 * AT_SMS / tile_rows;
   uint8_t* ws = static_cast<uint8_t*>(a.ws);
   p.ws.zl = reinterpret_cast<float*>(ws);
   ws += (size_t)C::GRID * 2 * C::ROWS * 8;
@@ -1153,10 +1160,10 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT>, smem, false);
   if (e != cudaSuccess) return e;
   const auto join = wide ? attn_join_kernel<D, C::ROWS, true> : attn_join_kernel<D, C::ROWS, false>;
-  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(C::GRID), dim3(AT_THREADS), smem, s, 0, LC_FULL, p);
+  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(grid), dim3(AT_THREADS), smem, s, 0, early ? LC_SMEM : LC_FULL, p);
   if (e != cudaSuccess) return e;
-  const dim3 grid(by_item ? n_items : C::GRID, wide ? tile_rows : (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS);
-  return launch_pdl(join, grid, dim3(JOIN_THREADS), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p, C::GRID,
+  const dim3 join_grid(by_item ? n_items : grid, wide ? tile_rows : (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS);
+  return launch_pdl(join, join_grid, dim3(JOIN_THREADS), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p, grid,
                     (int)by_item);
 }
 

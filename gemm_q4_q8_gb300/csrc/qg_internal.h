@@ -41,7 +41,7 @@ void note_launch(int n = 1);
 // life. So an LC_L1 kernel that directly follows an LC_SMEM kernel on the
 // same stream is launched without the programmatic attribute (it starts when
 // that grid completes); every other pair overlaps.
-// LC_FULL: the attention kernel, whose one wave of CTAs fills the registers and the shared memory of every SM. Launched
+// LC_FULL: the attention kernel, where its one wave of CTAs fills the registers and the shared memory of every SM. Launched
 // early it finds CTAs of its predecessor still there; the hole that one leaves in the shared memory is too
 // small for a CTA, and a few CTAs start only when others of their own wave end (64 ragged sequences, Q8_0: 64 us
 // instead of 52). So it is never launched early.
