@@ -98,6 +98,19 @@ __global__ void __launch_bounds__(RD_THREADS)
         *reinterpret_cast<uint4*>(to[j]) = q[j];
         continue;
       }
+      if constexpr (TYPE == QG_Q8_0 && sizeof(TO) == 2) {
+        // f16 1024 + u, less 1152, is the integer q exactly, and q * d is rounded once: the same as through f32
+        const __half2 s = __half2half2(__ushort_as_half(sc[j]));
+        uint32_t w[4];
+#pragma unroll
+        for (int h = 0; h < 4; ++h) {
+          const uint32_t u = __byte_perm(h < 2 ? q[j].x : q[j].y, 0x64646464u, h & 1 ? 0x4342 : 0x4140);
+          const __half2 v = __hmul2(__hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6480))), s);
+          w[h] = place ? *reinterpret_cast<const uint32_t*>(&v) : 0u;
+        }
+        *reinterpret_cast<uint4*>(to[j]) = make_uint4(w[0], w[1], w[2], w[3]);
+        continue;
+      }
       float y[8];
       if constexpr (TYPE == QG_F16) {
         const uint32_t u[4] = {q[j].x, q[j].y, q[j].z, q[j].w};

@@ -122,6 +122,7 @@ struct Turn {
   float c[LAYOUT == PAIRS ? 4 : 8], s[LAYOUT == PAIRS ? 4 : 8];
   bool turned;   // the lane has elements that turn (all eight, but for ANY)
   int partner;   // HALVES: offset of the other group; its sines carry the sign
+  Turn() = default;
   __device__ __forceinline__ Turn(const qg_rope& plan, const float2* sc, int d0) {
     const int rot = plan.rot_dim, h = rot >> 1;
     turned = d0 < rot;
@@ -160,9 +161,8 @@ struct Turn {
   // The turned values of a lane's eight elements; `row` points at element 0 of the head. Every element of
   // the head is read before the caller's __syncwarp, so the result may overwrite it after.
   template <class T>
-  __device__ __forceinline__ void apply(const qg_rope& plan, const T* row, int d0, float (&y)[8]) const {
-    float x[8];
-    load8(row + d0, x);
+  __device__ __forceinline__ void apply(const qg_rope& plan, const T* row, int d0, const float (&x)[8],
+                                        float (&y)[8]) const {
     if (LAYOUT == PLAIN || !turned) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) y[e] = x[e];
@@ -195,10 +195,19 @@ struct Turn {
 // pairs 4l .. 4l+3, elements 4l .. and rot_dim/2 + 4l .., and every element is read once.
 template <int LAYOUT>
 struct RowTurn : Turn<LAYOUT> {
-  using Turn<LAYOUT>::Turn;
+  __device__ __forceinline__ RowTurn(const qg_rope&, int) {}
+  __device__ __forceinline__ void angles(const qg_rope& plan, const float2* sc, int d0) {
+    Turn<LAYOUT>::operator=(Turn<LAYOUT>(plan, sc, d0));
+  }
+  // load: the lane's elements of a row; turn: the turned values of what was loaded from it; write: to where they belong.
   template <class TI>
-  __device__ __forceinline__ void read(const qg_rope& plan, const TI* row, int d0, float (&y)[8]) const {
-    this->apply(plan, row, d0, y);
+  __device__ __forceinline__ void load(const TI* row, int d0, float (&x)[8]) const {
+    load8(row + d0, x);
+  }
+  template <class TI>
+  __device__ __forceinline__ void turn(const qg_rope& plan, const TI* row, int d0, const float (&x)[8],
+                                       float (&y)[8]) const {
+    this->apply(plan, row, d0, x, y);
   }
   template <class TO>
   __device__ __forceinline__ void write(TO* row, int d0, const float (&y)[8]) const {
@@ -210,10 +219,12 @@ struct RowTurn<HALVES> {
   float c[4], s[4];
   int a, b;  // the lane's two quads
   bool turned;
-  __device__ __forceinline__ RowTurn(const qg_rope& plan, const float2* sc, int d0) {
+  __device__ __forceinline__ RowTurn(const qg_rope& plan, int d0) {
     turned = d0 < plan.rot_dim;
     a = turned ? d0 >> 1 : d0;
     b = turned ? (plan.rot_dim + d0) >> 1 : d0 + 4;
+  }
+  __device__ __forceinline__ void angles(const qg_rope&, const float2* sc, int) {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const float2 x = turned ? sc[a + i] : make_float2(0.f, 1.f);
@@ -222,14 +233,22 @@ struct RowTurn<HALVES> {
     }
   }
   template <class TI>
-  __device__ __forceinline__ void read(const qg_rope&, const TI* row, int, float (&y)[8]) const {
+  __device__ __forceinline__ void load(const TI* row, int, float (&x)[8]) const {
     float u[4], v[4];
     load4(row + a, u);
     load4(row + b, v);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      y[i] = turned ? fmaf(u[i], c[i], -(v[i] * s[i])) : u[i];
-      y[4 + i] = turned ? fmaf(v[i], c[i], u[i] * s[i]) : v[i];
+      x[i] = u[i];
+      x[4 + i] = v[i];
+    }
+  }
+  template <class TI>
+  __device__ __forceinline__ void turn(const qg_rope&, const TI*, int, const float (&x)[8], float (&y)[8]) const {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      y[i] = turned ? fmaf(x[i], c[i], -(x[4 + i] * s[i])) : x[i];
+      y[4 + i] = turned ? fmaf(x[4 + i], c[i], x[i] * s[i]) : x[4 + i];
     }
   }
   template <class TO>
@@ -274,26 +293,29 @@ __global__ void __launch_bounds__(ROW_THREADS, ROW_BLOCKS) rope_kernel(
   pdl_wait();
   const int tokens = ROW_WARPS / parts;
   const int64_t tok0 = (int64_t)blockIdx.x * tokens;
-  make_turns(plan, sc, pos, tok0, tokens, ntok);
-  __syncthreads();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tok = tok0 + warp / parts;
-  if (tok >= ntok) return;
   const int lanes = row_lanes(d), at_once = 32 / lanes, d0 = (lane & (lanes - 1)) * 8;
   const int step = at_once * parts * gridDim.y;
   int r = (warp % parts + parts * blockIdx.y) * at_once + lane / lanes;
-  const RowTurn<LAYOUT> t(plan, sc + warp / parts * (QG_ROPE_MAX_DIM / 2), d0);
   const TI* xr = x + tok * xs + (int64_t)r * d;
   TO* yr = y + tok * ys + (int64_t)r * d;
   const int64_t hop = (int64_t)step * d;
-  if (d0 >= d) r = n_heads;  // no elements for this lane
-  for (; __any_sync(0xffffffffu, r < n_heads); r += step) {
-    float v[8];
-    if (r < n_heads) t.read(plan, xr, d0, v);
+  if (d0 >= d || tok >= ntok) r = n_heads;  // no elements for this lane
+  RowTurn<LAYOUT> t(plan, d0);
+  float x8[8], v[8];
+  if (r < n_heads) t.load(xr, d0, x8);  // the first row is on its way while the angles are found
+  make_turns(plan, sc, pos, tok0, tokens, ntok);
+  __syncthreads();
+  t.angles(plan, sc + warp / parts * (QG_ROPE_MAX_DIM / 2), d0);
+  while (__any_sync(0xffffffffu, r < n_heads)) {
+    if (r < n_heads) t.turn(plan, xr, d0, x8, v);
     __syncwarp();  // in place: the row has been read
     if (r < n_heads) t.write(yr, d0, v);
+    r += step;
     xr += hop;
     yr += hop;
+    if (r < n_heads) t.load(xr, d0, x8);
   }
 }
 
@@ -373,11 +395,19 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int64_t tok = tok0 + warp / a.parts;
   const int d = a.c.head_dim, lanes = d >> 3, at_once = 32 / lanes, d0 = (lane & (lanes - 1)) * 8;
+  // Row groups of the token in order: queries, keys, values; the parts take them in turn. The first queries are on
+  // their way while the place and the angles are found.
+  const int part = warp % a.parts + a.parts * blockIdx.y, all_parts = a.parts * gridDim.y;
+  const int first = lane / lanes;
+  const int qg = (a.n_q + at_once - 1) / at_once, kg = (a.c.n_kv_heads + at_once - 1) / at_once;
+  const T* row = a.q + tok * a.qs + (int64_t)(part * at_once + first) * d;
+  float next[8];
+  RowTurn<LAYOUT> tq(plan, d0);
+  if (tok < a.ntok && part * at_once + first < a.n_q) tq.load(row, d0, next);
   // the token's place in the cache (NULL: nowhere)
   uint8_t* place = nullptr;
   const int groups = a.c.page_size / KV_GROUP, rec = kv_record_bytes(TYPE, d);
   int in_group = 0;
-  const int part = warp % a.parts + a.parts * blockIdx.y, all_parts = a.parts * gridDim.y;
   if (tok < a.ntok) {
     const int pos = a.pos[tok];
     if (pos >= 0) {
@@ -397,19 +427,20 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     __syncthreads();
   }
   if (tok >= a.ntok) return;
-  // Row groups of the token in order: queries, keys, values; the parts take them in turn.
-  const int first = lane / lanes;
-  const int qg = (a.n_q + at_once - 1) / at_once, kg = (a.c.n_kv_heads + at_once - 1) / at_once;
   const float2* const my_sc = sc + warp / a.parts * (QG_ROPE_MAX_DIM / 2);
   int n = part;
   {
-    const RowTurn<LAYOUT> t(plan, my_sc, d0);
-    for (; n < qg; n += all_parts) {
+    tq.angles(plan, my_sc, d0);
+    const int64_t hop = (int64_t)all_parts * at_once * d;
+    for (; n < qg; n += all_parts, row += hop) {
       const int r = n * at_once + first;
+      float x[8], y[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = next[e];
+      if (r + all_parts * at_once < a.n_q) tq.load(row + hop, d0, next);
       if (r < a.n_q) {
-        float y[8];
-        t.read(plan, a.q + tok * a.qs + (int64_t)r * d, d0, y);
-        t.write(a.q_out + (tok * a.n_q + r) * (int64_t)d, d0, y);
+        tq.turn(plan, row, d0, x, y);
+        tq.write(a.q_out + (tok * a.n_q + r) * (int64_t)d, d0, y);
       }
     }
   }
@@ -419,10 +450,14 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     const int r = (is_v ? n - kg : n) * at_once + first;
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r < a.c.n_kv_heads) {
-      if (is_v)
+      if (is_v) {
         load8(a.v + tok * a.vs + (int64_t)r * d + d0, y);
-      else
-        t.apply(plan, a.k + tok * a.ks + (int64_t)r * d, d0, y);
+      } else {
+        const T* const row = a.k + tok * a.ks + (int64_t)r * d;
+        float x[8];
+        load8(row + d0, x);
+        t.apply(plan, row, d0, x, y);
+      }
     }
     const bool live = r < a.c.n_kv_heads && place != nullptr;
     uint8_t* const half = live ? place + (size_t)r * groups * rec + (is_v ? kv_half_bytes(TYPE, d) : 0) : nullptr;
