@@ -1,7 +1,7 @@
 // qg_rope.cu -- rotary positions, alone (qrope) and fused with the write of the
 // paged key/value cache (qkv_append).
 //
-// Both kernels have one shape. A block of eight warps takes 8 / P tokens, P warps
+// Both kernels have one shape. A block of four warps takes 4 / P tokens, P warps
 // each (and P x gridDim.y in all, so that few tokens still fill the machine). Its
 // threads first compute the tokens' sines and cosines, one pair each, into shared
 // memory; then each warp walks over rows (heads) of its token. A row's D elements
@@ -28,12 +28,13 @@ namespace qg {
 
 namespace {
 
-constexpr int ROW_THREADS = 256;
+constexpr int ROW_THREADS = 128;
 constexpr int ROW_WARPS = ROW_THREADS / 32;
 // Blocks that share an SM: the rows' loads hide behind other warps (48 of them), not behind more rows a lane; 8,191 x 40
-// x 128 from f32 to f16 takes 40.1 us so, 42.5 with two rows and 46.6 with four rows a lane in flight.
-constexpr int ROW_BLOCKS = 6;
-constexpr int APPEND_BLOCKS = 5;  // its rows need more registers (a prompt of 16,382 tokens: 153 us with 5, 154 with 6, 166 with 7)
+// x 128 from f32 to f16 took 40.1 us so, 42.5 with two rows and 46.6 with four rows a lane in flight. Blocks of eight warps:
+// 40.8, and 145 us instead of 142 for a prompt of 16,382 tokens appended and read back.
+constexpr int ROW_BLOCKS = 12;
+constexpr int APPEND_BLOCKS = 10;  // (its rows need more registers)
 
 // How the eight elements of a lane meet their partners.
 enum Layout {
@@ -268,7 +269,7 @@ __host__ __device__ inline int row_lanes(int d) {
 // Warps of a token: as many as fill the machine (152 SMs x 40 warps) where there are few tokens, two at
 // least, no more than it has row groups.
 struct RowSplit {
-  int parts;   // warps of a token in a block: 1, 2, 4 or 8
+  int parts;   // warps of a token in a block: 1, 2 or 4
   dim3 grid;
 };
 RowSplit split_rows(int ntok, int groups) {
