@@ -78,9 +78,9 @@ __host__ __device__ constexpr int at_team(int d, int nt) { return d == 256 && nt
 // Tokens of a unit: a record of 16 for every team of the CTA.
 __host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_team(d, nt) * KV_GROUP; }
 constexpr int AT_SMS = 152;
-// An item's end (four warps' sums joined, the next queries loaded) costs a warp about as much as
-// this many units, and the runs are cut as if it were that many more.
-constexpr int AT_PAD = 3;
+// An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
+// the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64).
+constexpr int at_pad(int nt) { return nt == 1 ? 2 : 4; }
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
 
 template <int TYPE, int D, int NT>
@@ -132,6 +132,7 @@ struct AttnDev {
   int group;    // query heads of a kv head
   int tiles;    // row tiles of a kv head
   float scale;  // |scale| log2 e; 1 for a scale of 0
+  __device__ __forceinline__ int head_of(int item) const { return tiles == 1 ? item : item / tiles; }
   uint32_t q_and, q_xor;  // and its sign, applied to the queries
 };
 
@@ -220,20 +221,20 @@ __device__ __forceinline__ SeqSpan span_of(const AttnArgs& a, int len) {
   return s;
 }
 
-// Which CTA does what. Two numberings: units in order, u, and places in order, v, where every item has AT_PAD
+// Which CTA does what. Two numberings: units in order, u, and places in order, v, where every item has PAD
 // places behind its units. Run c of N is the places [c places / N, (c+1) places / N), and the CTA's units are those
 // among them. Both kernels of a call work this out for themselves, from lens in shared memory.
 struct Unit {
   int seq, item, unit;  // item of the sequence, unit of the item
 };
-template <int THREADS, int UNIT>
+template <int THREADS, int UNIT, int PAD, int GRID>
 struct Runs {
   int32_t* first;  // [n_seq + 1] units before a sequence (times its items)
   int32_t* len;    // [n_seq] lengths, none negative
-  int n_seq, items, places, N, each, over;
+  int n_seq, items, places, N, each, over;  // N: GRID, or less where there are fewer places
 
   // By all threads; `part`: shared, one int a warp. Ends with a barrier.
-  __device__ __forceinline__ Runs(const AttnArgs& a, int tiles, int grid, int32_t* mem, int* part, bool report)
+  __device__ __forceinline__ Runs(const AttnArgs& a, int tiles, int32_t* mem, int* part, bool report)
       : first(mem), len(mem + a.c.n_seq + 1), n_seq(a.c.n_seq), items(a.c.n_kv_heads * tiles) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int per = (n_seq + THREADS - 1) / THREADS;
@@ -264,34 +265,40 @@ struct Runs {
     if (b1 == n_seq && b0 < n_seq) first[n_seq] = before;
     __syncthreads();
     places = v_first(n_seq);  // below 2^31 (attn_size_ok)
-    N = places < grid ? places : grid;
-    each = places / N;
+    N = places < GRID ? places : GRID;
+    each = places < GRID ? 1 : places / GRID;
     over = places - each * N;
   }
   __device__ __forceinline__ int units_of(int b) const { return first[b + 1] - first[b]; }
-  __device__ __forceinline__ int v_first(int b) const { return (first[b] + b * AT_PAD) * items; }
-  __device__ __forceinline__ int v_item(int b, int item) const { return v_first(b) + item * (units_of(b) + AT_PAD); }
-  __device__ __forceinline__ int run_start(int c) const { return c < N ? c * each + c * over / N : places; }
-  __device__ __forceinline__ int run_of(int v) const { return (int)((((int64_t)v + 1) * N - 1) / places); }
+  __device__ __forceinline__ int v_first(int b) const { return (first[b] + b * PAD) * items; }
+  __device__ __forceinline__ int v_item(int b, int item) const { return v_first(b) + item * (units_of(b) + PAD); }
+  __device__ __forceinline__ int run_start(int c) const { return c < N ? c * each + c * over / GRID : places; }
+  __device__ __forceinline__ int run_of(int v) const {
+    int c = (int)((float)v * ((float)N / (float)places));  // right, or one off
+    c = min(c, N - 1);
+    if (run_start(c) > v) --c;
+    if (run_start(c + 1) <= v) ++c;
+    return c;
+  }
   // The first units at or behind run c's first place and its last place's successor, and their numbers; by a warp.
   __device__ __forceinline__ void find(int c, Unit& x0, int& u0, Unit& x1, int& u1) const {
     const int lane = threadIdx.x & 31;
-    const int v0 = run_start(c), v1 = run_start(c + 1);
+    const int v = run_start(c + (lane & 1));  // even lanes take the first, odd ones the second
+    const int v0 = __shfl_sync(0xffffffffu, v, 0), v1 = __shfl_sync(0xffffffffu, v, 1);
     int before0 = 0, before1 = 0;  // sequences that start at or before the place
     for (int b0 = 0; b0 < n_seq; b0 += 32) {
-      const int v = b0 + lane < n_seq ? v_first(b0 + lane) : 0x7fffffff;
-      before0 += __popc(__ballot_sync(0xffffffffu, v <= v0));
-      const uint32_t m = __ballot_sync(0xffffffffu, v <= v1);
+      const int f = b0 + lane < n_seq ? v_first(b0 + lane) : 0x7fffffff;
+      before0 += __popc(__ballot_sync(0xffffffffu, f <= v0));
+      const uint32_t m = __ballot_sync(0xffffffffu, f <= v1);
       before1 += __popc(m);
       if (m != 0xffffffffu) break;
     }
-    // even lanes take v0, odd ones v1
     Unit x;
     x.seq = ((lane & 1) ? before1 : before0) - 1;
     int n = units_of(x.seq);
-    const uint32_t rem = ((lane & 1) ? v1 : v0) - v_first(x.seq);
-    x.item = rem / (uint32_t)(n + AT_PAD);
-    x.unit = rem - x.item * (n + AT_PAD);
+    const uint32_t rem = v - v_first(x.seq);
+    x.item = rem / (uint32_t)(n + PAD);
+    x.unit = rem - x.item * (n + PAD);
     if (x.unit >= n) {  // behind the item's units, or past the end
       x.unit = 0;
       if (++x.item == items) {
@@ -335,7 +342,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   pdl_trigger();  // (not before: the join reads lens at once)
 
   const int cta = blockIdx.x;
-  const Runs<AT_THREADS, UNIT> runs(a, p.tiles, gridDim.x, s_runs, s_part, cta == 0);
+  const Runs<AT_THREADS, UNIT, at_pad(NT), C::GRID> runs(a, p.tiles, s_runs, s_part, cta == 0);
   if (cta >= runs.N) return;
   const int items = runs.items;
   const int32_t* const s_len = runs.len;
@@ -349,7 +356,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   // others as soon as the buffer is free (in the middle of the stream a load takes microseconds).
   const int rows = p.group * a.ncols;
   auto stage_q = [&](const Unit& x) {
-    const int head = x.item / p.tiles, r0 = (x.item - head * p.tiles) * ROWS;
+    const int head = p.head_of(x.item), r0 = (x.item - head * p.tiles) * ROWS;
     for (int i = tid; i < ROWS * (D / 8); i += AT_THREADS) {
       const int row = i / (D / 8), c = i % (D / 8), r = r0 + row;
       const uint16_t* src = a.q;
@@ -358,7 +365,6 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       copy16_async(smem_u32(s_q) + row * C::QPITCH + 16 * c, src, r < rows ? 16 : 0);
     }
   };
-  stage_q(at);
   // The high bytes of f16 1024 + u. Read from shared memory it stays in a register of each lane; as a constant it is
   // moved from a uniform register at every use (eight moves a block).
   const uint32_t k64 = s_k64[lane];
@@ -395,7 +401,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       if (grp < (sp.hi + KV_GROUP - 1) / KV_GROUP && grp >= sp.lo / KV_GROUP) {
         nx_in = true;
         nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (grp >> gpp_log)];
-        nx_off = x.item / p.tiles * gpp + (grp & (gpp - 1));
+        nx_off = p.head_of(x.item) * gpp + (grp & (gpp - 1));
       }
     }
     if (most > 32) {  // on to the next batch: one behind lane 31's
@@ -438,6 +444,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   };
   __syncwarp();
   look_up(0);
+  stage_q(at);
   enter(0);
 #pragma unroll
   for (int i = 0; i < C::BARS; ++i) fetch(C::SPLIT ? 0 : i, i);
@@ -481,7 +488,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int b = at.seq, hr = at.item, nu = runs.units_of(b);
     const int todo = nu - at.unit < steps - step ? nu - at.unit : steps - step;  // units of this run in the item
     const bool starts = at.unit == 0, whole = starts && todo == nu;
-    const int head = hr / p.tiles, tile = hr - head * p.tiles;
+    const int head = p.head_of(hr), tile = hr - head * p.tiles;
     const int len = s_len[b];
     const SeqSpan sp = span_of<UNIT>(a, len);
     // (the last unit's end may pass 2^31, but not the records that are looked at)
@@ -1001,21 +1008,20 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 // Joins the parts of the items that are cut. blockIdx.x is an item (by_item) or, where there are more items than CTAs of
 // the main kernel, one of those CTAs: the last item that starts in its run is the only one that may be cut. WIDE: a CTA
 // joins a row and its warps share the parts out, for few items of many parts; otherwise a warp joins a row.
-constexpr int JOIN_THREADS = 256;
-constexpr int JOIN_WARPS = JOIN_THREADS / 32;
-
-template <int D, int ROWS, bool WIDE>
-__global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_constant__ AttnDev p, int grid, int by_item) {
-  constexpr int V = D / 32;  // dimensions of a lane
-  __shared__ float s_y[WIDE ? JOIN_WARPS : 1][D];
-  __shared__ float s_red[2][JOIN_WARPS];
-  __shared__ int s_part[JOIN_WARPS];
+template <int D, int ROWS, bool WIDE, int GRID>
+__global__ void __launch_bounds__(WIDE ? 256 : 128) attn_join_kernel(const __grid_constant__ AttnDev p, int by_item) {
+  constexpr int THREADS = WIDE ? 256 : 128, WARPS = THREADS / 32;
+  constexpr int V = D / 32;               // dimensions of a lane
+  constexpr int BATCH = V == 8 ? 4 : 8;   // parts in flight
+  __shared__ float s_y[WIDE ? WARPS : 1][D];
+  __shared__ float2 s_zl[WARPS];
+  __shared__ int s_part[WARPS];
   extern __shared__ int32_t s_runs[];
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int row = WIDE ? blockIdx.y : blockIdx.y * JOIN_WARPS + warp;
+  const int row = WIDE ? blockIdx.y : blockIdx.y * WARPS + warp;
   pdl_trigger();
   // The main kernel lets this one start once what came before it is complete; so before pdl_wait only its parts are not.
-  const Runs<JOIN_THREADS, at_unit(D, ROWS / 8)> runs(p.a, p.tiles, grid, s_runs, s_part, false);
+  const Runs<THREADS, at_unit(D, ROWS / 8), at_pad(ROWS / 8), GRID> runs(p.a, p.tiles, s_runs, s_part, false);
   Unit x;
   int c0 = blockIdx.x, n = 0;
   if (by_item) {
@@ -1035,88 +1041,80 @@ __global__ void __launch_bounds__(JOIN_THREADS) attn_join_kernel(const __grid_co
       if (v >= runs.run_start(c0)) n = runs.run_of(v + runs.units_of(x.seq) - 1) - c0 + 1;
     }
   }
-  const int head = x.item / p.tiles, tile = x.item - head * p.tiles;
+  const int head = p.head_of(x.item), tile = x.item - head * p.tiles;
   const int r = tile * ROWS + row;
   pdl_wait();
   if (n == 0 || row >= ROWS || r >= p.group * p.a.ncols) return;
   // part i: the first CTA's run ends in the item (its second slot), the others' start in it
   auto slot = [&](int i) { return ((size_t)(c0 + i) * 2 + (i == 0 ? 1 : 0)) * ROWS + row; };
-  auto stat = [&](int i) {
-    return i < n ? __ldcg(reinterpret_cast<const float2*>(p.ws.zl + slot(i) * 2)) : make_float2(-INFINITY, 0.f);
-  };
-  // eight parts' loads in flight at a time, the first eight while reference and sum over all parts are found
-  constexpr int STEP = WIDE ? JOIN_WARPS : 1;
-  float part[8][V], z[8];
-  auto load = [&](int i0) {
+  // a warp's parts, with a reference that moves as they come
+  float top = -INFINITY, sum = 0.f, y[V];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
+  for (int k = 0; k < V; ++k) y[k] = 0.f;
+  constexpr int STEP = WIDE ? WARPS : 1;
+  for (int i0 = WIDE ? warp : 0; i0 < n; i0 += BATCH * STEP) {
+    float part[BATCH][V];
+    float2 zl[BATCH];
+#pragma unroll
+    for (int j = 0; j < BATCH; ++j) {
       const int i = i0 + j * STEP;
-      z[j] = -INFINITY;
+      zl[j] = make_float2(-INFINITY, 0.f);
       if (i < n) {
-        z[j] = __ldcg(p.ws.zl + slot(i) * 2);
+        zl[j] = __ldcg(reinterpret_cast<const float2*>(p.ws.zl + slot(i) * 2));
+        const float* const o = p.ws.o + slot(i) * D + lane * V;
+        if constexpr (V == 2) {
+          const float2 v = __ldcg(reinterpret_cast<const float2*>(o));
+          part[j][0] = v.x; part[j][1] = v.y;
+        } else {
 #pragma unroll
-        for (int k = 0; k < V; k += 2) {
-          const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ws.o + slot(i) * D + lane * V + k));
-          part[j][k] = v.x;
-          part[j][k + 1] = v.y;
+          for (int k = 0; k < V; k += 4) {
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(o + k));
+            part[j][k] = v.x; part[j][k + 1] = v.y; part[j][k + 2] = v.z; part[j][k + 3] = v.w;
+          }
         }
       }
     }
-  };
-  const int mine = WIDE ? warp : 0;
-  load(mine);
-  // reference and sum over all parts
-  constexpr int SPREAD = WIDE ? JOIN_THREADS : 32;
-  const int me = WIDE ? tid : lane;
-  float top = -INFINITY, sum = 0.f;
-  for (int i = me; i < n; i += SPREAD) top = fmaxf(top, stat(i).x);
+    float z = top;
 #pragma unroll
-  for (int off = 16; off; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-  if constexpr (WIDE) {
-    if (lane == 0) s_red[0][warp] = top;
-    __syncthreads();
+    for (int j = 0; j < BATCH; ++j) z = fmaxf(z, zl[j].x);
+    const float f = top == -INFINITY ? 0.f : ex2(top - z);
+    sum = top == -INFINITY ? sum : sum * f;  // (a part that has seen nothing but NaN has a sum of its own)
 #pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) top = fmaxf(top, s_red[0][w]);
-  }
-  for (int i = me; i < n; i += SPREAD) {
-    const float2 x = stat(i);
-    sum += x.x == -INFINITY ? x.y : x.y * ex2(x.x - top);
-  }
+    for (int k = 0; k < V; ++k) y[k] *= f;
+    top = z;
 #pragma unroll
-  for (int off = 16; off; off >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-  if constexpr (WIDE) {
-    if (lane == 0) s_red[1][warp] = sum;
-    __syncthreads();
-    sum = 0.f;
-#pragma unroll
-    for (int w = 0; w < JOIN_WARPS; ++w) sum += s_red[1][w];
-  }
-  float y[V];
-#pragma unroll
-  for (int k = 0; k < V; ++k) y[k] = 0.f;
-  for (int i0 = mine; i0 < n; i0 += 8 * STEP) {
-    if (i0 != mine) load(i0);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float w = z[j] == -INFINITY ? 0.f : ex2(z[j] - top);
+    for (int j = 0; j < BATCH; ++j) {
+      const float w = zl[j].x == -INFINITY ? 0.f : ex2(zl[j].x - top);
+      sum += zl[j].x == -INFINITY ? zl[j].y : zl[j].y * w;
       if (w != 0.f)
 #pragma unroll
         for (int k = 0; k < V; ++k) y[k] = fmaf(part[j][k], w, y[k]);
     }
   }
-  const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const size_t yo = (((size_t)x.seq * p.a.ncols + r / p.group) * p.a.n_heads + head * p.group + r % p.group) * D;
   if constexpr (WIDE) {
 #pragma unroll
     for (int k = 0; k < V; ++k) s_y[warp][lane * V + k] = y[k];
+    if (lane == 0) s_zl[warp] = make_float2(top, sum);
     __syncthreads();
-    for (int e = tid; e < D; e += JOIN_THREADS) {
-      float x = 0.f;
+    float z = -INFINITY, l = 0.f, w[WARPS];
 #pragma unroll
-      for (int w = 0; w < JOIN_WARPS; ++w) x += s_y[w][e];
-      p.a.y[yo + e] = __half_as_ushort(__float2half_rn(x * inv));
+    for (int i = 0; i < WARPS; ++i) z = fmaxf(z, s_zl[i].x);
+#pragma unroll
+    for (int i = 0; i < WARPS; ++i) {
+      const float2 t = s_zl[i];
+      w[i] = t.x == -INFINITY ? 0.f : ex2(t.x - z);
+      l += t.x == -INFINITY ? t.y : t.y * w[i];
+    }
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+    for (int e = tid; e < D; e += THREADS) {
+      float v = 0.f;
+#pragma unroll
+      for (int i = 0; i < WARPS; ++i) v += w[i] == 0.f ? 0.f : s_y[i][e] * w[i];
+      p.a.y[yo + e] = __half_as_ushort(__float2half_rn(v * inv));
     }
   } else {
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
 #pragma unroll
     for (int k = 0; k < V; k += 2)
       *reinterpret_cast<uint32_t*>(p.a.y + yo + lane * V + k) = pack_f16(y[k] * inv, y[k + 1] * inv);
@@ -1148,7 +1146,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   constexpr int unit = at_unit(D, NT);
   int64_t most = ((int64_t)a.c.max_pages * a.c.page_size + unit - 1) / unit;  // units of a sequence
   if (a.window > 0 && a.window / unit + 3 < most) most = a.window / unit + 3;
-  most = (most + AT_PAD) * n_items;
+  most = (most + at_pad(NT)) * n_items;
   const int grid = most < C::GRID ? (int)most : C::GRID;
   const bool early = grid <= AT_SMS;
   const bool by_item = n_items <= grid, wide = n_items <= 4 * AT_SMS / tile_rows;
@@ -1159,11 +1157,11 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   const size_t smem = C::smem(a.c.n_seq);
   cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT>, smem, false);
   if (e != cudaSuccess) return e;
-  const auto join = wide ? attn_join_kernel<D, C::ROWS, true> : attn_join_kernel<D, C::ROWS, false>;
+  const auto join = wide ? attn_join_kernel<D, C::ROWS, true, C::GRID> : attn_join_kernel<D, C::ROWS, false, C::GRID>;
   e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(grid), dim3(AT_THREADS), smem, s, 0, early ? LC_SMEM : LC_FULL, p);
   if (e != cudaSuccess) return e;
-  const dim3 join_grid(by_item ? n_items : grid, wide ? tile_rows : (tile_rows + JOIN_WARPS - 1) / JOIN_WARPS);
-  return launch_pdl(join, join_grid, dim3(JOIN_THREADS), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p, grid,
+  const dim3 join_grid(by_item ? n_items : grid, wide ? tile_rows : (tile_rows + 3) / 4);
+  return launch_pdl(join, join_grid, dim3(wide ? 256 : 128), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p,
                     (int)by_item);
 }
 
