@@ -36,7 +36,7 @@ bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int nco
 bool attn_size_ok(const qg_kvcache& c, int n_heads, int ncols) {
   const int rows = n_heads / c.n_kv_heads * ncols, nt = tiles_of(c.type, rows, c.head_dim);
   const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
-  const int64_t units = (int64_t)c.max_pages * c.page_size / 32 + 4;
+  const int64_t units = (int64_t)c.max_pages * c.page_size / 32 + 8;
   return units * c.n_seq * c.n_kv_heads * tiles < ((int64_t)1 << 31);
 }
 

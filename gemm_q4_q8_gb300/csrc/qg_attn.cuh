@@ -1009,10 +1009,12 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 // the main kernel, one of those CTAs: the last item that starts in its run is the only one that may be cut. WIDE: a CTA
 // joins a row and its warps share the parts out, for few items of many parts; otherwise a warp joins a row.
 template <int D, int ROWS, bool WIDE, int GRID>
-__global__ void __launch_bounds__(WIDE ? 256 : 128) attn_join_kernel(const __grid_constant__ AttnDev p, int by_item) {
+__global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kernel(const __grid_constant__ AttnDev p, int by_item) {
   constexpr int THREADS = WIDE ? 256 : 128, WARPS = THREADS / 32;
   constexpr int V = D / 32;               // dimensions of a lane
-  constexpr int BATCH = V == 8 ? 4 : 8;   // parts in flight
+  // Parts in flight. A row of its own warp has few parts, and with few registers most of the CTAs find room (and get
+  // through their first part) before the main kernel's last CTAs end.
+  constexpr int BATCH = V == 2 ? 12 : WIDE && V == 4 ? 8 : 4;
   __shared__ float s_y[WIDE ? WARPS : 1][D];
   __shared__ float2 s_zl[WARPS];
   __shared__ int s_part[WARPS];
