@@ -674,10 +674,12 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             }
             mma16816_from(part, a0, q[0], q[1], c);
             mma16816_acc(part, a1, q[2], q[3]);
-            s[nt][0] = fmaf(part[0], e0, s[nt][0]);
-            s[nt][1] = fmaf(part[1], e0, s[nt][1]);
-            s[nt][2] = fmaf(part[2], e1, s[nt][2]);
-            s[nt][3] = fmaf(part[3], e1, s[nt][3]);
+            const float2 lo = fma2(make_float2(part[0], part[1]), make_float2(e0, e0), make_float2(s[nt][0], s[nt][1]));
+            const float2 hi = fma2(make_float2(part[2], part[3]), make_float2(e1, e1), make_float2(s[nt][2], s[nt][3]));
+            s[nt][0] = lo.x;
+            s[nt][1] = lo.y;
+            s[nt][2] = hi.x;
+            s[nt][3] = hi.y;
           }
         }
       }
@@ -901,8 +903,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           const float e0 = lo_f32(d[blk]), e1 = hi_f32(d[blk]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) {
-            const uint32_t w0 = transpose8(pack_f16(w[nt][0] * e0, w[nt][1] * e0));
-            const uint32_t w1 = transpose8(pack_f16(w[nt][2] * e1, w[nt][3] * e1));
+            const float2 lo = mul2(make_float2(w[nt][0], w[nt][1]), make_float2(e0, e0));
+            const float2 hi = mul2(make_float2(w[nt][2], w[nt][3]), make_float2(e1, e1));
+            const uint32_t w0 = transpose8(pack_f16(lo.x, lo.y));
+            const uint32_t w1 = transpose8(pack_f16(hi.x, hi.y));
             mma16816_acc(o[blk][nt][0], v0, w0, w1);
             mma16816_acc(o[blk][nt][1], v1, w0, w1);
           }
