@@ -34,7 +34,9 @@ constexpr int ROW_WARPS = ROW_THREADS / 32;
 // x 128 from f32 to f16 took 40.1 us so, 42.5 with two rows and 46.6 with four rows a lane in flight. Blocks of eight warps:
 // 40.8, and 145 us instead of 142 for a prompt of 16,382 tokens appended and read back.
 constexpr int ROW_BLOCKS = 12;
-constexpr int APPEND_BLOCKS = 10;  // (its rows need more registers)
+// qkv_append's rows need more registers: that prompt takes 137 us with 10 blocks (which spill), 135 with 9, 138 with 8. The
+// next key or value row in flight as well is no gain (142 with 9, 141 with 8), nor are prefetches into L2 (149).
+constexpr int APPEND_BLOCKS = 9;
 
 // How the eight elements of a lane meet their partners.
 enum Layout {
@@ -98,6 +100,13 @@ __device__ __forceinline__ void store4(__half* p, const float* v) {
 __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
   *reinterpret_cast<uint4*>(p) =
       make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
+}
+
+// The larger of two magnitudes; a NaN if either is one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
 }
 
 // Sines and cosines (times mscale) of the block's tokens: sc[token][pair].
@@ -334,53 +343,67 @@ struct AppendParams {
   int parts;
 };
 
-// Eight elements of a row into the record of (token slot, head).
+// Where a lane's eight elements of a row, and their block's scale, go in a half record.
 template <int TYPE>
-__device__ __forceinline__ void put8(uint8_t* half, int d0, int d, int i, float (&y)[8], bool live) {
+struct Spot {
+  int at, scale_at;  // bytes; scale_at < 0: another lane writes it
+  __device__ __forceinline__ Spot(int d0, int d, int i) {
+    const int blk = d0 >> 5;
+    at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 2 : 1);
+    scale_at = (d0 & 31) == 0 ? KV_GROUP * d + 2 * (blk * KV_GROUP + kv_scale_place(i)) : -1;
+  }
+};
+
+// Eight elements of a row into its half record (NULL: nowhere; the lanes of a block call together).
+//
+// Q8_0. The scale is the smallest f16 h with 127 h >= the block's largest magnitude. The product with R, a little
+// above 1/127, rounded up is that h or the f16 behind it, and 127 h is exact in f32 (18 bits), so one comparison
+// decides. x / h by an approximate reciprocal is off by at most 127 (2^-23 + 2^-24) < 2.3e-5; only next to a half is the
+// division needed to know the nearest integer q. 1.5 2^23 + 128 + q has q + 128 as its low byte.
+// (With two IEEE divisions a block, a clamp and a test an element, key and value rows took most of the kernel's issue
+// slots: a prompt of 16,382 tokens, appended and read back, 142 us instead of 135.)
+template <int TYPE>
+__device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, float (&y)[8]) {
   if constexpr (TYPE == QG_F16) {
-    if (live)
-      store8(reinterpret_cast<__half*>(half) + (d0 >> 5) * (KV_GROUP * 32) + i * 32 + (d0 & 31), y);
+    if (half) store8(reinterpret_cast<__half*>(half + spot.at), y);
   } else {
-    // largest magnitude of the block; a NaN or an infinity makes it infinite
-    float top = 0.f;
+    float top = fabsf(y[0]);  // an infinity or a NaN stays one
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float a = fabsf(y[e]);
-      top = fmaxf(top, a <= 3.402823466e38f ? a : __int_as_float(0x7f800000));
-    }
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    const bool bad = top > 3.402823466e38f;
-    // rounded up, so that no quant of the block passes 127
-    uint16_t bits = __half_as_ushort(__float2half_ru(__fdiv_rn(top, 127.f)));
-    if (bits > 0x7BFF) bits = 0x7BFF;
+    for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(y[e]));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    constexpr float R = 0x1.02040cp-7f;
+    uint32_t bits = __half_as_ushort(__float2half_ru(top * R));
+    if (127.f * __half2float(__ushort_as_half(bits - 1)) >= top) --bits;  // (false for 0 - 1, a NaN)
+    const bool bad = !(top <= 3.402823466e38f), high = bits > 0x7BFF;
+    if (high) bits = 0x7BFF;
     if (bad) bits = 0x7FFF;
     uint32_t w[2] = {0x80808080u, 0x80808080u};
     if (!bad && bits != 0) {
-      // x / d by the reciprocal is off by less than 1e-4; only next to a half is the division needed to know
-      // its nearest integer q. 1.5 2^23 + 128 + q has q + 128 as its low byte.
-      const float ds = __half2float(__ushort_as_half(bits)), inv = __frcp_rn(ds), magic = 12582912.f + 128.f;
-      uint32_t b[8];
-      bool close = false;
+      const float ds = __half2float(__ushort_as_half(bits)), magic = 12582912.f + 128.f;
+      float inv;
+      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ds));
+      float b[8], off = 0.f;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float q = fminf(fmaxf(y[e] * inv, -127.f), 127.f);
-        const float m = q + magic;
-        close |= fabsf(q - (m - magic)) > 0.4998f;
-        b[e] = __float_as_uint(m);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 q = mul2(make_float2(y[e], y[e + 1]), make_float2(inv, inv));
+        const float2 m = sub2(q, make_float2(-magic, -magic));
+        const float2 r = sub2(q, sub2(m, make_float2(magic, magic)));
+        off = fmaxf(off, fmaxf(fabsf(r.x), fabsf(r.y)));
+        b[e] = m.x;
+        b[e + 1] = m.y;
       }
-      if (close)
+      if (off > 0.49996f || high)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = __float_as_uint(fminf(fmaxf(__fdiv_rn(y[e], ds), -127.f), 127.f) + magic);
+        for (int e = 0; e < 8; ++e) b[e] = fminf(fmaxf(__fdiv_rn(y[e], ds), -127.f), 127.f) + magic;
 #pragma unroll
       for (int h = 0; h < 2; ++h)
-        w[h] = __byte_perm(__byte_perm(b[4 * h], b[4 * h + 1], 0x0040), __byte_perm(b[4 * h + 2], b[4 * h + 3], 0x0040), 0x5410);
+        w[h] = __byte_perm(__byte_perm(__float_as_uint(b[4 * h]), __float_as_uint(b[4 * h + 1]), 0x0040),
+                           __byte_perm(__float_as_uint(b[4 * h + 2]), __float_as_uint(b[4 * h + 3]), 0x0040), 0x5410);
     }
-    if (live) {
-      const int blk = d0 >> 5;
-      *reinterpret_cast<uint2*>(half + blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) = make_uint2(w[0], w[1]);
-      if ((d0 & 31) == 0)
-        reinterpret_cast<uint16_t*>(half + KV_GROUP * d)[blk * KV_GROUP + kv_scale_place(i)] = bits;
+    if (half) {
+      *reinterpret_cast<uint2*>(half + spot.at) = make_uint2(w[0], w[1]);
+      if (spot.scale_at >= 0) *reinterpret_cast<uint16_t*>(half + spot.scale_at) = (uint16_t)bits;
     }
   }
 }
@@ -446,23 +469,25 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     }
   }
   const Turn<LAYOUT> t(plan, my_sc, d0);
-  for (n -= qg; n < 2 * kg; n += all_parts) {
-    const bool is_v = n >= kg;
-    const int r = (is_v ? n - kg : n) * at_once + first;
-    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (r < a.c.n_kv_heads) {
-      if (is_v) {
-        load8(a.v + tok * a.vs + (int64_t)r * d + d0, y);
-      } else {
-        const T* const row = a.k + tok * a.ks + (int64_t)r * d;
-        float x[8];
-        load8(row + d0, x);
-        t.apply(plan, row, d0, x, y);
-      }
+  const Spot<TYPE> spot(d0, d, in_group);
+  const uint32_t head_bytes = groups * rec;
+  const int kv = a.c.n_kv_heads;
+  const T* const kr = a.k + tok * a.ks;
+  for (n -= qg; n < kg; n += all_parts) {
+    const int r = n * at_once + first;
+    float x[8], y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < kv) {
+      load8(kr + r * d + d0, x);
+      t.apply(plan, kr + r * d, d0, x, y);
     }
-    const bool live = r < a.c.n_kv_heads && place != nullptr;
-    uint8_t* const half = live ? place + (size_t)r * groups * rec + (is_v ? kv_half_bytes(TYPE, d) : 0) : nullptr;
-    put8<TYPE>(half, d0, d, in_group, y, live);
+    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes : nullptr, spot, y);
+  }
+  const T* const vr = a.v + tok * a.vs + d0;
+  for (n -= kg; n < kg; n += all_parts) {
+    const int r = n * at_once + first;
+    float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    if (r < kv) load8(vr + r * d, y);
+    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes + kv_half_bytes(TYPE, d) : nullptr, spot, y);
   }
 }
 
