@@ -13,10 +13,11 @@
 //
 // Work. The rows of one kv head (all its query heads, all columns; 8 NT to a
 // tile) share its keys and values. An item is a (sequence, kv head, row tile);
-// its tokens come in units of 64 (four warps x a record of 16 tokens). All
-// items' units in a row are cut into equal runs, one for each CTA of a grid that
-// fills the machine once, so a batch of ragged lengths and one very long sequence
-// load every SM alike. A CTA that covers an item whole writes y; where an item is
+// its tokens come in units of 64 (four warps x a record of 16 tokens; 32 where two
+// warps share a record). All items' units in a row, with a few empty places behind
+// each item for what its end costs, are cut into equal runs, one for each CTA of a
+// grid that fills the machine once, so a batch of ragged lengths and one very long
+// sequence load every SM alike. A CTA that covers an item whole writes y; where an item is
 // cut, each CTA writes its sum, reference and weight to the workspace, and a
 // second kernel joins them in CTA order. The cuts depend on lens and the shape
 // alone, and so do the results. (Joining in the CTA that finishes last needs no
@@ -49,6 +50,15 @@
 // block's scale is multiplied into the f32 weight before the weight is rounded
 // to f16 (so V itself is never rounded); a power of two that follows the largest
 // scale seen keeps that product in the normal range of f16.
+//
+// Bound. One tile of 8 rows: by memory, at 6.1 TB/s in f16 (131,071 tokens of 8 kv
+// heads of 128 in 88 us; the bytes alone take 79 at the rate of a large copy), and
+// nearly so in Q8_0 (64 ragged sequences, 279 MB, in 50 us, issue slots half
+// used). More rows: by the latency of the instructions between two matrix
+// products, with the 8 to 16 warps that the accumulators leave room for (Q8_0, 32 rows of heads
+// of 256: 800 instructions a record and tile of 16 rows, issue slots 38% and
+// tensor pipe 24% used, 37 us for 82 MB). One short sequence: by the chain of
+// dependent loads lens, page, record, and by the join (1,000 tokens: 8.4 us).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -72,8 +82,9 @@ constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
 // Warps that share a record: 32 rows of heads of 256 are split between two, 128 dimensions each, which add their scores
 // up; each then has the registers of a warp on heads of 128. (16 sequences of 8,191 f16 tokens, two kv heads, 32 rows:
-// 70 us, against 90 for two tiles of 16 rows that read everything twice. For fewer rows, and for Q8_0, a warp on its own
-// is faster: 48 us against 50 for 8 rows, f16; 61 against 67 or 81 for 32 rows, Q8_0.)
+// 68 us, against 90 for two tiles of 16 rows that read everything twice. For fewer rows, and for Q8_0, a warp on its own
+// is faster: f16, 8 rows 47 us against 50, 16 rows 51 against 56; Q8_0, 16 rows 36 against 42, 32 rows 56 as two tiles
+// of 16 against 65 or, as one, 68.)
 __host__ __device__ constexpr int at_team(int d, int nt) { return d == 256 && nt == 4 ? 2 : 1; }
 // Tokens of a unit: a record of 16 for every team of the CTA.
 __host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_team(d, nt) * KV_GROUP; }

@@ -406,9 +406,9 @@ qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *p
  *           one past max_pages * page_size sets QG_KV_BAD_POS; a negative one
  *           counts as 0, of a long one the tokens past the table do not exist.
  *   n_heads: a multiple of n_kv_heads, at most 64 per kv head; ncols: 1..16.
- *           (max_pages * page_size / 64 + 4) * n_seq * n_kv_heads * (n_heads /
- *           n_kv_heads * ncols / 8 + 1) below 2^31 is enough for any problem
- *           (QG_ERR_SHAPE where it is far above).
+ *           (max_pages * page_size / 32 + 8) * n_seq * n_kv_heads * (n_heads /
+ *           n_kv_heads * ncols / 8 + 1) below 2^31 is always accepted; a
+ *           problem above it may be refused (QG_ERR_SHAPE).
  *   scale : finite (QG_ERR_SHAPE otherwise)
  *   y     : f16 [n_seq][ncols][n_heads][head_dim], 16-byte aligned
  *   ws    : device workspace of at least qattn_workspace_bytes(...) bytes,
