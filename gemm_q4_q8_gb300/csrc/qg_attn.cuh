@@ -92,6 +92,8 @@ constexpr int AT_SMS = 152;
 // An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
 // the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64).
 constexpr int at_pad(int nt) { return nt == 1 ? 2 : 4; }
+constexpr int AT_CLUSTER = 16;      // CTAs of a cluster, at most
+constexpr int AT_CLUSTER_UNITS = 4; // units of a CTA of a cluster, at most
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
 
 template <int TYPE, int D, int NT>
@@ -281,6 +283,7 @@ struct Runs {
     over = places - each * N;
   }
   __device__ __forceinline__ int units_of(int b) const { return first[b + 1] - first[b]; }
+  __device__ __forceinline__ int len_of(int b) const { return len[b]; }
   __device__ __forceinline__ int v_first(int b) const { return (first[b] + b * PAD) * items; }
   __device__ __forceinline__ int v_item(int b, int item) const { return v_first(b) + item * (units_of(b) + PAD); }
   __device__ __forceinline__ int run_start(int c) const { return c < N ? c * each + c * over / GRID : places; }
@@ -325,7 +328,53 @@ struct Runs {
   }
 };
 
-template <int TYPE, int D, int NT>
+// The same for a cluster of CTAs that has an item to itself: the item's units in equal runs, in order of rank. One
+// length is looked at, and there is nothing to add up.
+template <int UNIT>
+struct ClusterRun {
+  int N, items, seq, item, len, n, u0, u1;
+  __device__ __forceinline__ ClusterRun(const AttnArgs& a, int tiles, uint32_t rank, uint32_t ctas)
+      : N(1 << 30), items(a.c.n_kv_heads * tiles) {
+    const uint32_t i = blockIdx.x / ctas;
+    seq = i / (uint32_t)items;
+    item = i - seq * items;
+    len = a.lens[seq];
+    if ((len < 0 || len > a.c.max_pages * a.c.page_size) && item == 0 && rank == 0 && threadIdx.x == 0 && a.err)
+      atomicOr(a.err, QG_KV_BAD_POS);
+    len = max(len, 0);
+    n = span_of<UNIT>(a, len).n;  // (few: the host has looked at what a sequence can hold)
+    u0 = n * rank / ctas;
+    u1 = n * (rank + 1) / ctas;
+  }
+  __device__ __forceinline__ int units_of(int) const { return n; }
+  __device__ __forceinline__ int len_of(int) const { return len; }
+  __device__ __forceinline__ void find(int, Unit& x0, int& v0, Unit&, int& v1) const {
+    x0 = {seq, item, u0};
+    v0 = u0;
+    v1 = u1;
+  }
+};
+__device__ __forceinline__ void cluster_barrier() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint32_t at_rank(const void* mine, uint32_t rank) {
+  uint32_t d;
+  asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(d) : "r"(smem_u32(mine)), "r"(rank));
+  return d;
+}
+__device__ __forceinline__ float ld_rank(uint32_t at) {
+  float v;
+  asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(at) : "memory");
+  return v;
+}
+__device__ __forceinline__ float2 ld_rank2(uint32_t at) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(at) : "memory");
+  return v;
+}
+
+// CLUSTER: short contexts; each item is a cluster's, whose CTAs read one another's sums from shared memory and join them.
+template <int TYPE, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     attn_kernel(const __grid_constant__ AttnDev p) {
   using C = AttnCfg<TYPE, D, NT>;
@@ -353,15 +402,26 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   pdl_trigger();  // (not before: the join reads lens at once)
 
   const int cta = blockIdx.x;
-  const Runs<AT_THREADS, UNIT, at_pad(NT), C::GRID> runs(a, p.tiles, s_runs, s_part, cta == 0);
+  uint32_t rank = 0, ctas = 1;
+  if constexpr (CLUSTER) {
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
+    asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
+  }
+  const auto runs = [&] {
+    if constexpr (CLUSTER)
+      return ClusterRun<UNIT>(a, p.tiles, rank, ctas);
+    else
+      return Runs<AT_THREADS, UNIT, at_pad(NT), C::GRID>(a, p.tiles, s_runs, s_part, cta == 0);
+  }();
   if (cta >= runs.N) return;
   const int items = runs.items;
-  const int32_t* const s_len = runs.len;
   Unit at, end_at;  // the unit in hand
   int u0, u1;
   runs.find(cta, at, u0, end_at, u1);
   const int steps = u1 - u0;
-  if (steps == 0) return;
+  if (!CLUSTER && steps == 0) return;
+  if constexpr (CLUSTER) __syncthreads();  // the barriers are ready (Runs has a barrier of its own)
+  const Unit whose = at;
 
   // Queries of an item into shared memory, [row][D] f16, asynchronously: the first before any keys are asked for, the
   // others as soon as the buffer is free (in the middle of the stream a load takes microseconds).
@@ -407,7 +467,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           n = runs.units_of(++x.seq);
         }
       }
-      const SeqSpan sp = span_of<UNIT>(a, s_len[x.seq]);
+      const SeqSpan sp = span_of<UNIT>(a, runs.len_of(x.seq));
       const int grp = (sp.unit + x.unit) * C::TEAMS + team;  // group of 16 tokens, hence the comparisons in groups
       if (grp < (sp.hi + KV_GROUP - 1) / KV_GROUP && grp >= sp.lo / KV_GROUP) {
         nx_in = true;
@@ -498,9 +558,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   while (step < steps) {
     const int b = at.seq, hr = at.item, nu = runs.units_of(b);
     const int todo = nu - at.unit < steps - step ? nu - at.unit : steps - step;  // units of this run in the item
-    const bool starts = at.unit == 0, whole = starts && todo == nu;
+    const bool starts = at.unit == 0, whole = !CLUSTER && starts && todo == nu;
     const int head = p.head_of(hr), tile = hr - head * p.tiles;
-    const int len = s_len[b];
+    const int len = runs.len_of(b);
     const SeqSpan sp = span_of<UNIT>(a, len);
     // (the last unit's end may pass 2^31, but not the records that are looked at)
     int tok = (int)(((uint32_t)(sp.unit + at.unit) * C::TEAMS + team) * KV_GROUP - UNIT);
@@ -1008,12 +1068,63 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           const size_t yo = (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + at;
           *reinterpret_cast<uint2*>(a.y + yo) =
               make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
+        } else if constexpr (CLUSTER) {
+          *reinterpret_cast<float4*>(reinterpret_cast<float*>(s_ring) + row * D + at) = y;
         } else {
           *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
           if (at == 0) *reinterpret_cast<float2*>(p.ws.zl + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
         }
       }
     }
+  }
+  if constexpr (CLUSTER) {
+    // The CTAs' sums are in the rings (their only item is over), references and weights where the item's end left them.
+    static_assert((size_t)ROWS * D * 4 <= C::ring, "the sums fit the ring");
+    float* const s_top = s_stat + 2 * AT_WARPS * ROWS;
+    float* const s_sum = s_top + ROWS;
+    if (steps == 0) {
+      copies_done();
+      if (tid < ROWS) {
+        s_top[tid] = -INFINITY;
+        s_sum[tid] = 0.f;
+      }
+    }
+    __syncwarp();
+    cluster_barrier();
+    const int head = p.head_of(whose.item), r0 = (whose.item - head * p.tiles) * ROWS;
+    const int pairs = (rows - r0 < ROWS ? rows - r0 : ROWS) * (D / 2);
+    for (int i = rank * AT_THREADS + tid; i < pairs; i += ctas * AT_THREADS) {
+      const int row = i / (D / 2), dim = i % (D / 2) * 2, r = r0 + row;
+      float z[AT_CLUSTER], l[AT_CLUSTER], top = -INFINITY;
+      float2 v[AT_CLUSTER];
+#pragma unroll
+      for (int j = 0; j < AT_CLUSTER; ++j) {
+        z[j] = -INFINITY;
+        l[j] = 0.f;
+        if (j < ctas) {
+          z[j] = ld_rank(at_rank(s_top + row, j));
+          l[j] = ld_rank(at_rank(s_sum + row, j));
+          v[j] = ld_rank2(at_rank(reinterpret_cast<float*>(s_ring) + row * D + dim, j));
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < AT_CLUSTER; ++j) top = fmaxf(top, z[j]);
+      float sum = 0.f, y0 = 0.f, y1 = 0.f;
+#pragma unroll
+      for (int j = 0; j < AT_CLUSTER; ++j) {
+        const float w = z[j] == -INFINITY ? 0.f : ex2(z[j] - top);
+        sum += z[j] == -INFINITY ? l[j] : l[j] * w;
+        if (w != 0.f) {
+          y0 = fmaf(v[j].x, w, y0);
+          y1 = fmaf(v[j].y, w, y1);
+        }
+      }
+      const float inv = sum == 0.f ? 0.f : 1.f / sum;
+      const size_t yo = (((size_t)whose.seq * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + dim;
+      *reinterpret_cast<uint32_t*>(a.y + yo) = pack_f16(y0 * inv, y1 * inv);
+    }
+    __syncwarp();
+    cluster_barrier();  // nobody leaves while the others read
   }
   if (!ok) {  // a copy was late: wait for what is still in flight, each wait bounded
     for (int i = 0; i < C::BARS; ++i) mbar_try_wait(bar_at + 8 * i, parity);
@@ -1163,6 +1274,16 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   constexpr int unit = at_unit(D, NT);
   int64_t most = ((int64_t)a.c.max_pages * a.c.page_size + unit - 1) / unit;  // units of a sequence
   if (a.window > 0 && a.window / unit + 3 < most) most = a.window / unit + 3;
+  if constexpr (NT <= 2) {
+    int ctas = AT_CLUSTER;
+    while (ctas > 1 && ((int64_t)n_items * ctas > 2 * AT_SMS || ctas >= 2 * most)) ctas /= 2;
+    if (most <= AT_CLUSTER_UNITS * ctas && (int64_t)n_items * ctas <= C::GRID) {
+      const cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT, true>, C::smem(0), true);
+      if (e != cudaSuccess) return e;
+      return launch_pdl(attn_kernel<TYPE, D, NT, true>, dim3(n_items * ctas), dim3(AT_THREADS), C::smem(0), s, ctas,
+                        n_items * ctas <= AT_SMS ? LC_SMEM : LC_FULL, p);
+    }
+  }
   most = (most + at_pad(NT)) * n_items;
   const int grid = most < C::GRID ? (int)most : C::GRID;
   const bool early = grid <= AT_SMS;
@@ -1172,10 +1293,10 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   ws += (size_t)C::GRID * 2 * C::ROWS * 8;
   p.ws.o = reinterpret_cast<float*>(ws);
   const size_t smem = C::smem(a.c.n_seq);
-  cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT>, smem, false);
+  cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT, false>, smem, false);
   if (e != cudaSuccess) return e;
   const auto join = wide ? attn_join_kernel<D, C::ROWS, true, C::GRID> : attn_join_kernel<D, C::ROWS, false, C::GRID>;
-  e = launch_pdl(attn_kernel<TYPE, D, NT>, dim3(grid), dim3(AT_THREADS), smem, s, 0, early ? LC_SMEM : LC_FULL, p);
+  e = launch_pdl(attn_kernel<TYPE, D, NT, false>, dim3(grid), dim3(AT_THREADS), smem, s, 0, early ? LC_SMEM : LC_FULL, p);
   if (e != cudaSuccess) return e;
   const dim3 join_grid(by_item ? n_items : grid, wide ? tile_rows : (tile_rows + 3) / 4);
   return launch_pdl(join, join_grid, dim3(wide ? 256 : 128), (size_t)(2 * a.c.n_seq + 1) * 4, s, 0, LC_SMEM, p,
