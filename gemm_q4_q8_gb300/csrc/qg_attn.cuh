@@ -328,8 +328,9 @@ struct Runs {
   }
 };
 
-// The same for a cluster of CTAs that has an item to itself: the item's units in equal runs, in order of rank. One
-// length is looked at, and there is nothing to add up.
+// The same for a cluster of CTAs that has an item to itself. Without a window the units that the table has room for are
+// dealt out, in order of rank: where a CTA starts does not depend on the length, and its pages are looked up at
+// the same time. With one, the units that are seen.
 template <int UNIT>
 struct ClusterRun {
   int N, items, seq, item, len, n, u0, u1;
@@ -338,21 +339,21 @@ struct ClusterRun {
     const uint32_t i = blockIdx.x / ctas;
     seq = i / (uint32_t)items;
     item = i - seq * items;
+    const int cap = a.c.max_pages * a.c.page_size;
     len = a.lens[seq];
-    if ((len < 0 || len > a.c.max_pages * a.c.page_size) && item == 0 && rank == 0 && threadIdx.x == 0 && a.err)
-      atomicOr(a.err, QG_KV_BAD_POS);
+    uint32_t all = (uint32_t)(cap + UNIT - 1) / UNIT;  // (few: the host has looked)
+    if (a.window > 0) all = span_of<UNIT>(a, max(len, 0)).n;
+    u0 = all * rank / ctas;
+    u1 = all * (rank + 1) / ctas;
+  }
+  __device__ __forceinline__ void arrived(const AttnArgs& a, bool report) {
+    if (report && (len < 0 || len > a.c.max_pages * a.c.page_size) && item == 0 && a.err) atomicOr(a.err, QG_KV_BAD_POS);
     len = max(len, 0);
-    n = span_of<UNIT>(a, len).n;  // (few: the host has looked at what a sequence can hold)
-    u0 = n * rank / ctas;
-    u1 = n * (rank + 1) / ctas;
+    n = span_of<UNIT>(a, len).n;
+    u1 = max(min(u1, n), u0);
   }
   __device__ __forceinline__ int units_of(int) const { return n; }
   __device__ __forceinline__ int len_of(int) const { return len; }
-  __device__ __forceinline__ void find(int, Unit& x0, int& v0, Unit&, int& v1) const {
-    x0 = {seq, item, u0};
-    v0 = u0;
-    v1 = u1;
-  }
 };
 __device__ __forceinline__ void cluster_barrier() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
@@ -407,7 +408,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(rank));
     asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(ctas));
   }
-  const auto runs = [&] {
+  auto runs = [&] {
     if constexpr (CLUSTER)
       return ClusterRun<UNIT>(a, p.tiles, rank, ctas);
     else
@@ -417,11 +418,12 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   const int items = runs.items;
   Unit at, end_at;  // the unit in hand
   int u0, u1;
-  runs.find(cta, at, u0, end_at, u1);
-  const int steps = u1 - u0;
-  if (!CLUSTER && steps == 0) return;
-  if constexpr (CLUSTER) __syncthreads();  // the barriers are ready (Runs has a barrier of its own)
-  const Unit whose = at;
+  if constexpr (CLUSTER) {
+    at = {runs.seq, runs.item, u0 = runs.u0};
+  } else {
+    runs.find(cta, at, u0, end_at, u1);
+    if (u1 == u0) return;
+  }
 
   // Queries of an item into shared memory, [row][D] f16, asynchronously: the first before any keys are asked for, the
   // others as soon as the buffer is free (in the middle of the stream a load takes microseconds).
@@ -436,12 +438,23 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       copy16_async(smem_u32(s_q) + row * C::QPITCH + 16 * c, src, r < rows ? 16 : 0);
     }
   };
+  const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
+  int near_page = -1;  // CLUSTER without a window: the page of lane's step, whether or not there is one
+  if constexpr (CLUSTER) {
+    const int j = ((u0 + lane) * C::TEAMS + team) >> gpp_log;
+    if (a.window <= 0 && j < a.c.max_pages) near_page = a.c.page_table[(size_t)at.seq * a.c.max_pages + j];
+    stage_q(at);
+    __syncthreads();  // the barriers are ready (Runs has a barrier of its own)
+    runs.arrived(a, rank == 0 && tid == 0);
+    u1 = runs.u1;
+  }
+  const int steps = u1 - u0;
+  const Unit whose = at;
   // The high bytes of f16 1024 + u. Read from shared memory it stays in a register of each lane; as a constant it is
   // moved from a uniform register at every use (eight moves a block).
   const uint32_t k64 = s_k64[lane];
 
   // ------------------------------------------------------------ the ring
-  const int gpp = a.c.page_size / KV_GROUP, gpp_log = __ffs(gpp) - 1;  // records of a page and head
   uint8_t* const ring = s_ring + (size_t)team * C::STAGES * C::STAGE;
   const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + team * C::BARS);
   // In a half record: where this warp's blocks are, and (Q8_0) from there their scales.
@@ -471,7 +484,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       const int grp = (sp.unit + x.unit) * C::TEAMS + team;  // group of 16 tokens, hence the comparisons in groups
       if (grp < (sp.hi + KV_GROUP - 1) / KV_GROUP && grp >= sp.lo / KV_GROUP) {
         nx_in = true;
-        nx_page = a.c.page_table[(size_t)x.seq * a.c.max_pages + (grp >> gpp_log)];
+        nx_page = CLUSTER && a.window <= 0 ? near_page : a.c.page_table[(size_t)x.seq * a.c.max_pages + (grp >> gpp_log)];
         nx_off = p.head_of(x.item) * gpp + (grp & (gpp - 1));
       }
     }
@@ -515,11 +528,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   };
   __syncwarp();
   look_up(0);
-  stage_q(at);
+  if constexpr (!CLUSTER) stage_q(at);
   enter(0);
 #pragma unroll
   for (int i = 0; i < C::BARS; ++i) fetch(C::SPLIT ? 0 : i, i);
-  look_up(32);
+  if constexpr (!CLUSTER) look_up(32);
   int stage = 0;        // the stage in use
   uint32_t parity = 0;  // of its barriers
   auto arrived = [&](uint32_t bar) {
@@ -550,6 +563,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int j = lane & 15, i = 2 * (j >> 2) + (j & 1) + 4 * (j & 2);
     v_at = token_of(i) * 32 + (lane >> 4) * 16;
   }
+
+  // CLUSTER: place of (row, dimension) among a warp's sums; the exclusive or keeps a quad's rows on different banks
+  auto in_sums = [](int row, int dim) { return row * D + (dim ^ ((row & 6) << 2)); };
 
   // --------------------------------------------------------------- items
   int turn = 0;  // of the statistics' two buffers
@@ -1033,6 +1049,31 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       s_top[tid] = top;
       s_sum[tid] = sum;
     }
+    if constexpr (CLUSTER) {
+      // The CTA's only item: the ring is free, and takes all four sums at once.
+      float* const s_all = reinterpret_cast<float*>(s_ring);
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              s_all[warp * (ROWS * D) + in_sums(nt * 8 + 2 * t + c, blk * 32 + 8 * e + g)] =
+                  f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
+      __syncthreads();
+      for (int i = tid * 4; i < ROWS * D; i += AT_THREADS * 4) {
+        float4 y = *reinterpret_cast<const float4*>(s_all + i);
+#pragma unroll
+        for (int w = 1; w < AT_WARPS; ++w) {
+          const float4 x = *reinterpret_cast<const float4*>(s_all + w * (ROWS * D) + i);
+          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+        }
+        *reinterpret_cast<float4*>(s_all + i) = y;
+      }
+      continue;
+    }
 #pragma unroll
     for (int pass = 0; pass < NB * 32 / C::OD; ++pass) {
       if (pass) __syncthreads();  // the buffer has been read
@@ -1068,8 +1109,6 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           const size_t yo = (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + at;
           *reinterpret_cast<uint2*>(a.y + yo) =
               make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
-        } else if constexpr (CLUSTER) {
-          *reinterpret_cast<float4*>(reinterpret_cast<float*>(s_ring) + row * D + at) = y;
         } else {
           *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
           if (at == 0) *reinterpret_cast<float2*>(p.ws.zl + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
@@ -1079,7 +1118,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   }
   if constexpr (CLUSTER) {
     // The CTAs' sums are in the rings (their only item is over), references and weights where the item's end left them.
-    static_assert((size_t)ROWS * D * 4 <= C::ring, "the sums fit the ring");
+    static_assert((size_t)AT_WARPS * ROWS * D * 4 <= C::ring && TEAM == 1, "the sums fit the ring");
     float* const s_top = s_stat + 2 * AT_WARPS * ROWS;
     float* const s_sum = s_top + ROWS;
     if (steps == 0) {
@@ -1104,7 +1143,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         if (j < ctas) {
           z[j] = ld_rank(at_rank(s_top + row, j));
           l[j] = ld_rank(at_rank(s_sum + row, j));
-          v[j] = ld_rank2(at_rank(reinterpret_cast<float*>(s_ring) + row * D + dim, j));
+          v[j] = ld_rank2(at_rank(reinterpret_cast<float*>(s_ring) + in_sums(row, dim), j));
         }
       }
 #pragma unroll
@@ -1276,7 +1315,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   if (a.window > 0 && a.window / unit + 3 < most) most = a.window / unit + 3;
   if constexpr (NT <= 2) {
     int ctas = AT_CLUSTER;
-    while (ctas > 1 && ((int64_t)n_items * ctas > 2 * AT_SMS || ctas >= 2 * most)) ctas /= 2;
+    while (ctas > 1 && (int64_t)n_items * ctas > 2 * AT_SMS) ctas /= 2;
     if (most <= AT_CLUSTER_UNITS * ctas && (int64_t)n_items * ctas <= C::GRID) {
       const cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT, true>, C::smem(0), true);
       if (e != cudaSuccess) return e;

@@ -333,8 +333,8 @@ qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride
  *                or 256; n_pages >= 1; n_seq: 1..1024; max_pages >= 1, with
  *                max_pages * page_size < 2^31 (QG_ERR_SHAPE)
  *   pool       : device, 16-byte aligned, n_pages * qkv_page_bytes(...) bytes
- *   page_table : device int32 [n_seq][max_pages]. Only the entries of tokens
- *                that a call touches are read.
+ *   page_table : device int32 [n_seq][max_pages]. Entries of tokens that a call
+ *                does not touch may hold anything.
  * The struct is host memory, read during the call.
  * What only the device can check is checked there: a sequence outside
  * [0, n_seq), a position at or past max_pages * page_size, a page outside
