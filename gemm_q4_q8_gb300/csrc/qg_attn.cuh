@@ -23,7 +23,9 @@
 // alone, and so do the results. (Joining in the CTA that finishes last needs no
 // second kernel but a first one that clears its counters, and has one CTA's loads
 // to work with: 1,000 tokens of two heads of 256 took 14.3 us so, 10.7 with the
-// second kernel.)
+// second kernel.) Where the page table has room for little, each item is a cluster's
+// of up to 16 CTAs instead, which join their sums through shared memory: one
+// launch, and one length to wait for (ClusterRun).
 //
 // Inside a CTA each warp is on its own: it has a ring of shared-memory stages,
 // fetches its records with bulk copies (one lane for each, a stage refilled as
@@ -58,7 +60,9 @@
 // products, with the 8 to 16 warps that the accumulators leave room for (Q8_0, 32 rows of heads
 // of 256: 800 instructions a record and tile of 16 rows, issue slots 38% and
 // tensor pipe 24% used, 37 us for 82 MB). One short sequence: by the chain of
-// dependent loads lens, page, record, and by the join (1,000 tokens: 8.4 us).
+// dependent loads length and page, record, and by 1,500 to 2,000 instructions a warp
+// that run once (1,000 Q8_0 tokens of two heads of 256: 6.4 us; 8.4 with runs and the
+// second kernel).
 #pragma once
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -92,8 +96,10 @@ constexpr int AT_SMS = 152;
 // An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
 // the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64).
 constexpr int at_pad(int nt) { return nt == 1 ? 2 : 4; }
-constexpr int AT_CLUSTER = 16;      // CTAs of a cluster, at most
-constexpr int AT_CLUSTER_UNITS = 4; // units of a CTA of a cluster, at most
+constexpr int AT_CLUSTER = 16;  // CTAs of a cluster, at most
+// Units of a CTA of a cluster, at most: what its join saves (1.9 us of 8.4 at 1,000 tokens, two Q8_0 heads of 256; 0.7 of 7.7 at
+// 2,000) is gone at four (4,000 tokens: 8.6 us against 8.5; f16, 8 heads of 128: 9.45 against 9.4).
+constexpr int AT_CLUSTER_UNITS = 3;
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
 
 template <int TYPE, int D, int NT>
@@ -126,6 +132,7 @@ struct AttnCfg {
   // With one stage its halves come and go on their own: keys while values are in use, and the other way round.
   static constexpr bool SPLIT = STAGES == 1;
   static_assert(STAGES >= 1 && (TEAM == 1 || !SPLIT), "room for the records in use");
+  static_assert(NB % 2 == 0, "blocks are looked through in pairs");
   static constexpr int BARS = SPLIT ? 2 : STAGES;
   static constexpr size_t ring = (size_t)TEAMS * STAGES * STAGE;
   static constexpr size_t bars = (size_t)TEAMS * BARS * 8;
@@ -672,6 +679,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
 
+    const int begin = step;
     for (const int end = step + todo; step < end; ++step) {
       tok += UNIT;
       if ((step & 31) == 0) valid = (step & 32) ? valid_odd : valid_even;
@@ -831,6 +839,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
               l[nt][c] *= f[c];
             }
           }
+          if (step == begin) continue;  // nothing is there yet
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
@@ -924,29 +933,31 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           // some rows do not see) is taken out and given to the rows that see it.
           uint16_t* sc = reinterpret_cast<uint16_t*>(vp + scales);
 #pragma unroll
-          for (int blk = 0; blk < NB; ++blk) {
-            bool nan = false;
-            if (lane < KV_GROUP) {
-              uint16_t& x = sc[blk * KV_GROUP + lane];
-              const int tk = tok + (lane >> 2) + 4 * (lane & 3);
-              const bool seen = tk < sp.hi && tk >= sp.lo;
-              nan = seen && (x & 0x7FFF) > 0x7C00;
-              if (!seen || nan) x = 0;
-            }
-            uint32_t odd = __ballot_sync(0xffffffffu, nan);
-            while (odd) {
-              const int j = __ffs(odd) - 1, tj = tok + (j >> 2) + 4 * (j & 3);
-              odd &= odd - 1;
+          for (int two = 0; two < NB; two += 2) {  // the 16 scales of each by a half of the warp
+            uint16_t& x = sc[two * KV_GROUP + lane];
+            const int tk = tok + ((lane & 15) >> 2) + 4 * (lane & 3);
+            const bool seen = tk < sp.hi && tk >= sp.lo;
+            const bool nan = seen && (x & 0x7FFF) > 0x7C00;
+            if (!seen || nan) x = 0;
+            const uint32_t both = __ballot_sync(0xffffffffu, nan);
+            if (__builtin_expect(both == 0, 1)) continue;
 #pragma unroll
-              for (int nt = 0; nt < NT; ++nt)
+            for (int blk = two; blk < two + 2; ++blk) {
+              uint32_t odd = blk == two ? both & 0xffffu : both >> 16;
+              while (odd) {
+                const int j = __ffs(odd) - 1, tj = tok + (j >> 2) + 4 * (j & 3);
+                odd &= odd - 1;
 #pragma unroll
-                for (int c = 0; c < 2; ++c) {
-                  int lo, hi;
-                  row_sees(nt * 8 + 2 * t + c, lo, hi);
-                  const float add = tj <= hi && tj > lo ? __int_as_float(0x7fffffff) : 0.f;
+                for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-                  for (int e = 0; e < 4; ++e) o[blk][nt][e >> 1][2 * (e & 1) + c] += add;
-                }
+                  for (int c = 0; c < 2; ++c) {
+                    int lo, hi;
+                    row_sees(nt * 8 + 2 * t + c, lo, hi);
+                    const float add = tj <= hi && tj > lo ? __int_as_float(0x7fffffff) : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[blk][nt][e >> 1][2 * (e & 1) + c] += add;
+                  }
+              }
             }
           }
           __syncwarp();
@@ -972,8 +983,9 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           wmul = to;
           wmax = __int_as_float((127 + e) << 23);
           wback = __int_as_float((127 - 7 + e) << 23);
+          if (step != begin)
 #pragma unroll
-          for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
+            for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
         }
         float w[NT][4];
 #pragma unroll
@@ -1053,15 +1065,16 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       // The CTA's only item: the ring is free, and takes all four sums at once.
       float* const s_all = reinterpret_cast<float*>(s_ring);
 #pragma unroll
-      for (int blk = 0; blk < NB; ++blk)
+      for (int e = 0; e < 4; ++e) {
+        float* const to = s_all + warp * (ROWS * D) + in_sums(2 * t, 8 * e + g);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s_all[warp * (ROWS * D) + in_sums(nt * 8 + 2 * t + c, blk * 32 + 8 * e + g)] =
-                  f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
+            for (int c = 0; c < 2; ++c)
+              to[(nt * 8 + c) * D + blk * 32] = f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
+      }
       __syncthreads();
       for (int i = tid * 4; i < ROWS * D; i += AT_THREADS * 4) {
         float4 y = *reinterpret_cast<const float4*>(s_all + i);
@@ -1072,46 +1085,46 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         }
         *reinterpret_cast<float4*>(s_all + i) = y;
       }
-      continue;
-    }
+    } else {
 #pragma unroll
-    for (int pass = 0; pass < NB * 32 / C::OD; ++pass) {
-      if (pass) __syncthreads();  // the buffer has been read
+      for (int pass = 0; pass < NB * 32 / C::OD; ++pass) {
+        if (pass) __syncthreads();  // the buffer has been read
 #pragma unroll
-      for (int hb = 0; hb < C::OD / 32; ++hb) {
-        const int blk = pass * (C::OD / 32) + hb;
+        for (int hb = 0; hb < C::OD / 32; ++hb) {
+          const int blk = pass * (C::OD / 32) + hb;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+          for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int c = 0; c < 2; ++c)
+            for (int c = 0; c < 2; ++c)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-              s_o[(warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 8 * e + g] =
-                  f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
-      }
-      __syncthreads();
-      constexpr int QUADS = C::OD / 4;  // float4 of a row of each share
-#pragma unroll
-      for (int k = 0; k < (TEAM * ROWS * QUADS + AT_THREADS - 1) / AT_THREADS; ++k) {
-        const int i = tid + k * AT_THREADS, of = i / (ROWS * QUADS), row = i / QUADS % ROWS, dim = (i % QUADS) * 4;
-        const int r = tile * ROWS + row;
-        if (of >= TEAM || r >= rows) continue;
-        float4 y = *reinterpret_cast<const float4*>(s_o + (of * ROWS + row) * C::OPITCH + dim);
-#pragma unroll
-        for (int w = TEAM; w < AT_WARPS; w += TEAM) {
-          const float4 x = *reinterpret_cast<const float4*>(s_o + ((of + w) * ROWS + row) * C::OPITCH + dim);
-          y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+              for (int e = 0; e < 4; ++e)
+                s_o[(warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 8 * e + g] =
+                    f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
         }
-        const int at = of * (NB * 32) + pass * C::OD + dim;
-        const float sum = s_sum[row];
-        if (whole) {
-          const float inv = sum == 0.f ? 0.f : 1.f / sum;
-          const size_t yo = (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + at;
-          *reinterpret_cast<uint2*>(a.y + yo) =
-              make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
-        } else {
-          *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
-          if (at == 0) *reinterpret_cast<float2*>(p.ws.zl + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
+        __syncthreads();
+        constexpr int QUADS = C::OD / 4;  // float4 of a row of each share
+#pragma unroll
+        for (int k = 0; k < (TEAM * ROWS * QUADS + AT_THREADS - 1) / AT_THREADS; ++k) {
+          const int i = tid + k * AT_THREADS, of = i / (ROWS * QUADS), row = i / QUADS % ROWS, dim = (i % QUADS) * 4;
+          const int r = tile * ROWS + row;
+          if (of >= TEAM || r >= rows) continue;
+          float4 y = *reinterpret_cast<const float4*>(s_o + (of * ROWS + row) * C::OPITCH + dim);
+#pragma unroll
+          for (int w = TEAM; w < AT_WARPS; w += TEAM) {
+            const float4 x = *reinterpret_cast<const float4*>(s_o + ((of + w) * ROWS + row) * C::OPITCH + dim);
+            y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
+          }
+          const int at = of * (NB * 32) + pass * C::OD + dim;
+          const float sum = s_sum[row];
+          if (whole) {
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const size_t yo = (((size_t)b * a.ncols + r / p.group) * a.n_heads + head * p.group + r % p.group) * D + at;
+            *reinterpret_cast<uint2*>(a.y + yo) =
+                make_uint2(pack_f16(y.x * inv, y.y * inv), pack_f16(y.z * inv, y.w * inv));
+          } else {
+            *reinterpret_cast<float4*>(p.ws.o + (part * ROWS + row) * D + at) = y;
+            if (at == 0) *reinterpret_cast<float2*>(p.ws.zl + (part * ROWS + row) * 2) = make_float2(s_top[row], sum);
+          }
         }
       }
     }
@@ -1134,6 +1147,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     const int pairs = (rows - r0 < ROWS ? rows - r0 : ROWS) * (D / 2);
     for (int i = rank * AT_THREADS + tid; i < pairs; i += ctas * AT_THREADS) {
       const int row = i / (D / 2), dim = i % (D / 2) * 2, r = r0 + row;
+      const uint32_t v_at = in_sums(row, dim) * 4, z_at = (uint32_t)(reinterpret_cast<uint8_t*>(s_top + row) - smem);
       float z[AT_CLUSTER], l[AT_CLUSTER], top = -INFINITY;
       float2 v[AT_CLUSTER];
 #pragma unroll
@@ -1141,9 +1155,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         z[j] = -INFINITY;
         l[j] = 0.f;
         if (j < ctas) {
-          z[j] = ld_rank(at_rank(s_top + row, j));
-          l[j] = ld_rank(at_rank(s_sum + row, j));
-          v[j] = ld_rank2(at_rank(reinterpret_cast<float*>(s_ring) + in_sums(row, dim), j));
+          const uint32_t its = at_rank(smem, j);
+          z[j] = ld_rank(its + z_at);
+          l[j] = ld_rank(its + z_at + ROWS * 4);
+          v[j] = ld_rank2(its + v_at);
         }
       }
 #pragma unroll

@@ -9,6 +9,8 @@ torch = pytest.importorskip("torch")
 
 import gemm_q4_q8_gb300 as qg  # noqa: E402
 
+from test_parity_attn import _lib  # noqa: E402, F401
+
 pytestmark = pytest.mark.gpu
 
 ONE = np.float32(1)
