@@ -839,7 +839,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
               l[nt][c] *= f[c];
             }
           }
-          if (step == begin) continue;  // nothing is there yet
+          if (CLUSTER && step == begin) continue;  // nothing is there yet (with more steps, the test costs more than it saves)
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
@@ -983,7 +983,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           wmul = to;
           wmax = __int_as_float((127 + e) << 23);
           wback = __int_as_float((127 - 7 + e) << 23);
-          if (step != begin)
+          if (!CLUSTER || step != begin)
 #pragma unroll
             for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
         }
