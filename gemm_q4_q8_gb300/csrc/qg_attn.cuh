@@ -3,13 +3,16 @@
 // (qg_attn_64.cu ...); qg_attn.cu picks one.
 //
 // Mathematics. For a row (a query of one column and head) with scores s_j over
-// the tokens it sees, y = sum_j 2^(s_j - z) V_j / sum_j 2^(s_j - z) for any z,
-// scores in units of log 2. A run of tokens is summed with a reference z of its
-// own; two runs are joined by scaling each with 2^(z_run - z_both). So the tokens
+// the tokens it sees, y = sum_j 2^(m (s_j - z)) V_j / sum_j 2^(m (s_j - z)) for any
+// z, with m = scale log2 e. A run of tokens is summed with a reference z of its
+// own; two runs are joined by scaling each with 2^(m (z_run - z_both)). So the tokens
 // may be cut into runs anywhere, and every byte of the cache is read once. z need
-// not be the maximum: it moves up to it only when a score passes z by more than 8
+// not be the maximum: it moves up to it only when a score passes z by more than 8 / m
 // (weights then stay below 2^8, in the middle of f16), which is rare after the
-// first tokens, so most steps have no maximum to find and nothing to rescale.
+// first tokens, so most steps have no maximum to find and nothing to rescale. z is
+// a score as it came out of the products, so its own weight is 1 exactly however
+// large the scores are (m z, rounded, is off by whole powers of two from scores of
+// 2^24 on).
 //
 // Work. The rows of one kv head (all its query heads, all columns; 8 NT to a
 // tile) share its keys and values. An item is a (sequence, kv head, row tile);
@@ -151,7 +154,8 @@ struct AttnDev {
   AttnWs ws;
   int group;    // query heads of a kv head
   int tiles;    // row tiles of a kv head
-  float scale;  // |scale| log2 e; 1 for a scale of 0
+  float mul;    // |scale| log2 e, of a raw score (1 for a scale of 0; Q8_0: of one in units of 2^-24)
+  float slack;  // AT_SLACK / mul
   __device__ __forceinline__ int head_of(int item) const { return tiles == 1 ? item : item / tiles; }
   uint32_t q_and, q_xor;  // and its sign, applied to the queries
 };
@@ -661,20 +665,19 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     float o[NB][NT][2][4];
 #pragma unroll
     for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] = 0.f;
-    // of rows 2t, 2t + 1: the reference z, as -z (0 while there is none) and as the raw score above which it
+    // of rows 2t, 2t + 1: the reference z, a raw score (0 while there is none), and the score above which it
     // moves (-inf while there is none); the sum of this lane's tokens' weights
-    const float mul = TYPE == QG_F16 ? p.scale : p.scale * 16777216.f;  // Q8_0: u was u 2^-24
-    const float inv_mul = 1.f / mul;
-    float zneg[NT][2], limit[NT][2], l[NT][2];
+    const float2 mul = make_float2(p.mul, p.mul);
+    float z[NT][2], limit[NT][2], l[NT][2];
 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
         limit[nt][c] = -INFINITY;
-        zneg[nt][c] = l[nt][c] = 0.f;
+        z[nt][c] = l[nt][c] = 0.f;
       }
-    auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : -zneg[nt][c]; };
+    auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : z[nt][c]; };
     // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
     // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
@@ -829,13 +832,13 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             float x = fmaxf(s[nt][c], s[nt][2 + c]);
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
             x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16)) * mul;
-            const float z = ref(nt, c);
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+            const float was = ref(nt, c);
             f[c] = 1.f;
-            if (x > z) {
-              f[c] = ex2(z - x);
-              zneg[nt][c] = -x;
-              limit[nt][c] = (x + AT_SLACK) * inv_mul;
+            if (x > was) {
+              f[c] = ex2((was - x) * p.mul);
+              z[nt][c] = x;
+              limit[nt][c] = __fadd_rd(x, p.slack);  // (not a step above: a step may be many times the slack)
               l[nt][c] *= f[c];
             }
           }
@@ -854,11 +857,15 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          s[nt][c] = ex2(fmaf(s[nt][c], mul, zneg[nt][c]));
-          s[nt][2 + c] = ex2(fmaf(s[nt][2 + c], mul, zneg[nt][c]));
-          l[nt][c] += s[nt][c] + s[nt][2 + c];
+        for (int i = 0; i < 4; i += 2) {
+          const float2 x = mul2(sub2(make_float2(s[nt][i], s[nt][i + 1]), make_float2(z[nt][0], z[nt][1])), mul);
+          s[nt][i] = ex2(x.x);
+          s[nt][i + 1] = ex2(x.y);
         }
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int c = 0; c < 2; ++c) l[nt][c] += s[nt][c] + s[nt][2 + c];
 
       // ---- weights times values
       if constexpr (C::SPLIT) arrived(bar_at + 8);
@@ -1047,7 +1054,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
         float x = s_z[row];
 #pragma unroll
         for (int w = 1; w < AT_WARPS; ++w) x = fmaxf(x, s_z[w * ROWS + row]);
-        f[nt][c] = limit[nt][c] == -INFINITY ? 0.f : ex2(-zneg[nt][c] - x) * wback;
+        f[nt][c] = limit[nt][c] == -INFINITY ? 0.f : ex2((z[nt][c] - x) * p.mul) * wback;
       }
     if (tid < ROWS) {
       float top = s_z[tid], sum = 0.f;
@@ -1056,7 +1063,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
       for (int w = 0; w < AT_WARPS; ++w) {
         const float x = s_z[w * ROWS + tid];
-        sum += x == -INFINITY ? s_l[w * ROWS + tid] : s_l[w * ROWS + tid] * ex2(x - top);
+        sum += x == -INFINITY ? s_l[w * ROWS + tid] : s_l[w * ROWS + tid] * ex2((x - top) * p.mul);
       }
       s_top[tid] = top;
       s_sum[tid] = sum;
@@ -1166,7 +1173,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       float sum = 0.f, y0 = 0.f, y1 = 0.f;
 #pragma unroll
       for (int j = 0; j < AT_CLUSTER; ++j) {
-        const float w = z[j] == -INFINITY ? 0.f : ex2(z[j] - top);
+        const float w = z[j] == -INFINITY ? 0.f : ex2((z[j] - top) * p.mul);
         sum += z[j] == -INFINITY ? l[j] : l[j] * w;
         if (w != 0.f) {
           y0 = fmaf(v[j].x, w, y0);
@@ -1259,14 +1266,14 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kern
     float z = top;
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) z = fmaxf(z, zl[j].x);
-    const float f = top == -INFINITY ? 0.f : ex2(top - z);
+    const float f = top == -INFINITY ? 0.f : ex2((top - z) * p.mul);
     sum = top == -INFINITY ? sum : sum * f;  // (a part that has seen nothing but NaN has a sum of its own)
 #pragma unroll
     for (int k = 0; k < V; ++k) y[k] *= f;
     top = z;
 #pragma unroll
     for (int j = 0; j < BATCH; ++j) {
-      const float w = zl[j].x == -INFINITY ? 0.f : ex2(zl[j].x - top);
+      const float w = zl[j].x == -INFINITY ? 0.f : ex2((zl[j].x - top) * p.mul);
       sum += zl[j].x == -INFINITY ? zl[j].y : zl[j].y * w;
       if (w != 0.f)
 #pragma unroll
@@ -1285,7 +1292,7 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kern
 #pragma unroll
     for (int i = 0; i < WARPS; ++i) {
       const float2 t = s_zl[i];
-      w[i] = t.x == -INFINITY ? 0.f : ex2(t.x - z);
+      w[i] = t.x == -INFINITY ? 0.f : ex2((t.x - z) * p.mul);
       l += t.x == -INFINITY ? t.y : t.y * w[i];
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -1319,7 +1326,9 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   const int all = p.group * a.ncols;
   p.tiles = (all + C::ROWS - 1) / C::ROWS;
   // scores are compared before they are scaled, so the scale's sign goes to the queries
-  p.scale = a.scale == 0.f ? 1.f : (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+  p.mul = a.scale == 0.f ? 1.f : (float)(std::fabs((double)a.scale) * 1.4426950408889634);
+  if (TYPE == QG_Q8_0) p.mul *= 16777216.f;
+  p.slack = (float)(AT_SLACK / (double)p.mul);
   p.q_and = a.scale == 0.f ? 0u : 0xffffffffu;
   p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;
   const int n_items = a.c.n_seq * a.c.n_kv_heads * p.tiles;
