@@ -154,7 +154,7 @@ struct AttnDev {
   AttnWs ws;
   int group;    // query heads of a kv head
   int tiles;    // row tiles of a kv head
-  float mul;    // |scale| log2 e, of a raw score (1 for a scale of 0; Q8_0: of one in units of 2^-24)
+  float mul;    // |scale| log2 e, for raw scores (Q8_0: in units of 2^24); 1 for a scale of 0
   float slack;  // AT_SLACK / mul
   __device__ __forceinline__ int head_of(int item) const { return tiles == 1 ? item : item / tiles; }
   uint32_t q_and, q_xor;  // and its sign, applied to the queries
@@ -1326,8 +1326,11 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   const int all = p.group * a.ncols;
   p.tiles = (all + C::ROWS - 1) / C::ROWS;
   // scores are compared before they are scaled, so the scale's sign goes to the queries
-  p.mul = a.scale == 0.f ? 1.f : (float)(std::fabs((double)a.scale) * 1.4426950408889634);
-  if (TYPE == QG_Q8_0) p.mul *= 16777216.f;
+  // Kept within 2^+-100, beyond which the weights no longer depend on it: raw scores of finite queries and keys are 0 or at
+  // least 2^-72 apart (products of 2^-24 steps, and the scale's for Q8_0) and below 2^48, so that at 2^100 one step takes a
+  // weight to 0 and at 2^-100 all weigh 1.
+  const double mul = std::fabs((double)a.scale) * 1.4426950408889634 * (TYPE == QG_Q8_0 ? 16777216. : 1.);
+  p.mul = a.scale == 0.f ? 1.f : (float)std::fmin(std::fmax(mul, std::ldexp(1., -100)), std::ldexp(1., 100));
   p.slack = (float)(AT_SLACK / (double)p.mul);
   p.q_and = a.scale == 0.f ? 0u : 0xffffffffu;
   p.q_xor = a.scale < 0.f ? 0x80008000u : 0u;

@@ -1,5 +1,5 @@
 """Softmax weights of attention where a 16-bit or 32-bit exponent ends: scores of any size that finite f16 queries and keys
-can give."""
+can give, and every finite scale."""
 import numpy as np
 import pytest
 
@@ -62,3 +62,26 @@ def test_scores_of_any_size(qtype, heads, d, n, wide, a, b, order):
     c.upload()
     q = np.tile(a * sign, (heads, 1)).astype(np.float16)
     check_tops(c, vs, q, n, 1, d ** -0.5, f"{order} {a} x {b}")
+
+
+@pytest.mark.parametrize("qtype", [F16, Q8])
+@pytest.mark.parametrize("heads,d,wide", [(3, 64, 0), (12, 256, 0), (8, 128, 300), (33, 64, 300)])
+@pytest.mark.parametrize("scale", [1e20, 1e30, 3e31, -1e34, 2.5e38, 3.4e38, -3.4e38])
+def test_scale_up_to_the_end_of_f32(qtype, heads, d, wide, scale):
+    """Every finite scale has an answer: one token takes all the weight."""
+    n, kv = 70, heads // 4 or 1
+    c, _, vs = filled(qtype, kv, d, 16, [n], seed=17, extra_pages=wide)
+    q = rng(32, d).standard_normal((heads // kv * kv, d)).astype(np.float16)
+    check_tops(c, vs, q, n, kv, scale, f"scale {scale}")
+
+
+@pytest.mark.parametrize("qtype", [F16, Q8])
+@pytest.mark.parametrize("heads,d,wide", [(3, 64, 0), (12, 256, 300)])
+@pytest.mark.parametrize("scale", [1e-37, -1e-40, 1e-45])
+def test_scale_down_to_subnormals(qtype, heads, d, wide, scale):
+    c, ks, vs = filled(qtype, 1, d, 16, [70], 19, extra_pages=wide)
+    q = rng(33, heads).standard_normal((1, 1, heads, d)).astype(np.float16)
+    y, err = attend(c, q, [70], scale=scale)
+    want, bound = ref.attention(q, ks, vs, [70], 1, 0, scale)
+    assert err == 0
+    assert_within(y, want, bound, f"scale {scale}")
