@@ -8,7 +8,7 @@
 // own; two runs are joined by scaling each with 2^(m (z_run - z_both)). So the tokens
 // may be cut into runs anywhere, and every byte of the cache is read once. z need
 // not be the maximum: it moves up to it only when a score passes z by more than 8 / m
-// (weights then stay below 2^8, in the middle of f16), which is rare after the
+// (weights then stay below 2^8; times 2^7 in f16, at_lift), which is rare after the
 // first tokens, so most steps have no maximum to find and nothing to rescale. z is
 // a score as it came out of the products, so its own weight is 1 exactly however
 // large the scores are (m z, rounded, is off by whole powers of two from scores of
@@ -104,6 +104,10 @@ constexpr int AT_CLUSTER = 16;  // CTAs of a cluster, at most
 // 2,000) is gone at four (4,000 tokens: 8.6 us against 8.5; f16, 8 heads of 128: 9.45 against 9.4).
 constexpr int AT_CLUSTER_UNITS = 3;
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
+// f16: every weight is 2^7 times as large, in numerators and sums alike. The largest then lies between 2^7 and 2^15, and what
+// rounding to f16 takes from small ones (up to 2^-25 below its normals) is 2^-32 of it: a first token far above 30,000 others,
+// whose sum the answer is, else cost those of its warp a quarter of their weight. (Q8_0: wmul below does this.)
+constexpr float at_lift(int type) { return type == QG_F16 ? 7.f : 0.f; }
 
 template <int TYPE, int D, int NT>
 struct AttnCfg {
@@ -858,7 +862,8 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
-          const float2 x = mul2(sub2(make_float2(s[nt][i], s[nt][i + 1]), make_float2(z[nt][0], z[nt][1])), mul);
+          const float2 d = sub2(make_float2(s[nt][i], s[nt][i + 1]), make_float2(z[nt][0], z[nt][1]));
+          const float2 x = TYPE == QG_F16 ? fma2(d, mul, make_float2(at_lift(TYPE), at_lift(TYPE))) : mul2(d, mul);
           s[nt][i] = ex2(x.x);
           s[nt][i + 1] = ex2(x.y);
         }

@@ -1,11 +1,12 @@
 """Softmax weights of attention where a 16-bit or 32-bit exponent ends: scores of any size that finite f16 queries and keys
-can give, and every finite scale."""
+can give, every finite scale, and sums of weights far below the largest."""
 import numpy as np
 import pytest
 
 torch = pytest.importorskip("torch")
 
 import attn_ref as ref  # noqa: E402
+import gemm_q4_q8_gb300 as qg  # noqa: E402
 from test_parity_attn import F16, Q8, _lib, assert_within, attend, filled, rng  # noqa: E402, F401
 
 pytestmark = pytest.mark.gpu
@@ -85,3 +86,43 @@ def test_scale_down_to_subnormals(qtype, heads, d, wide, scale):
     want, bound = ref.attention(q, ks, vs, [70], 1, 0, scale)
     assert err == 0
     assert_within(y, want, bound, f"scale {scale}")
+
+
+@pytest.mark.parametrize("qtype,heads,d,lift", [(F16, 1, 64, 7), (F16, 16, 128, 7), (F16, 32, 256, 7), (Q8, 1, 64, 5),
+                                                (Q8, 16, 256, 5)])
+@pytest.mark.parametrize("below", [20.5, 23.5, 24.40625, 25.125])
+def test_many_tokens_far_below_the_first(qtype, heads, d, lift, below):
+    """A first token that takes nearly all the weight, with a value of zero, before 30,000 tokens that weigh about 2^-below of it
+    each: what they add up to is the answer. As many sequences as a call takes, all over the same pages, so that a warp has the
+    first token and many of the others in one run. Scores are key element 0, in powers of two (scale = log 2).
+
+    A weight in f16 has half a step of 2^-25 below the normals, and the largest is at least 2^lift (Q8_0: times the block's
+    scale, which comes with 127 times it), so each weight is off by 2^-11 of itself and by 2^-(25 + lift) of the
+    largest. Its exponent passes three f32 roundings of numbers up to 26 (as a factor: 3 x 26 half steps), exp2 and the sums as
+    in attn_ref.attention: 16 half steps and those of at most 4,160 terms."""
+    n, ps, n_seq = 30001, 64, 1024
+    pages = -(-n // ps)
+    g = rng(34, d, int(below * 32))
+    k, v = np.zeros((n, 1, d), np.float32), np.abs(1 + 0.2 * g.standard_normal((n, 1, d))).astype(np.float32)
+    k[1:, 0, 0] = -below + g.integers(-16, 17, n - 1) / 64
+    v[0] = 0
+    pool = torch.zeros(pages * qg.qkv_page_bytes(qtype, 1, d, ps), dtype=torch.uint8, device="cuda")
+    table = torch.randperm(pages, device="cuda").to(torch.int32).view(1, pages)
+    one = qg.qkv_cache(qtype, pool, table, 1, d, ps)
+    pos = torch.arange(n, dtype=torch.int32, device="cuda")
+    qg.qkv_append(one, torch.from_numpy(k).cuda(), torch.from_numpy(v).cuda(), pos)
+    kr, vr = (torch.empty((n, 1, d), dtype=torch.float32, device="cuda") for _ in range(2))
+    qg.qkv_read(one, pos, kr, vr)
+    c = qg.qkv_cache(qtype, pool, table.repeat(n_seq, 1), 1, d, ps)
+    q = torch.zeros((n_seq, 1, heads, d), dtype=torch.float16, device="cuda")
+    q[..., 0] = 1
+    y = torch.empty_like(q)
+    ws = torch.empty(qg.qattn_workspace_bytes(c, heads, 1), dtype=torch.uint8, device="cuda")
+    qg.qattn_paged(c, q, torch.full((n_seq,), n, dtype=torch.int32, device="cuda"), y, ws, scale=float(np.log(2)))
+    w, vr = torch.exp2(kr[:, 0, 0].double()), vr[:, 0].double()
+    want = w @ vr / w.sum()
+    rel = (16 + 2 * 3 * 26 + 2 * 4160) * ref.SINGLE + ref.HALF
+    least = 2.0 ** -(25 + lift) * (vr.sum(0) if qtype == F16 else n * vr.max())
+    bound = rel * want + least / w.sum() + ref.HALF * want + ref.SUB
+    off = (y.double() - want).abs()
+    assert (off <= bound).all(), float((off / want).max())
