@@ -404,7 +404,8 @@ qg_status qrope_plan(qg_rope* plan, int rot_dim, int interleaved, double base, d
       theta = theta * keep + theta / factor * (1 - keep);
     }
     double turns = theta / pi2;
-    if (!std::isfinite(turns)) return QG_ERR_SHAPE;
+    // its rounding errors (a few 2^-53 of it) would exceed those of the f32 angle, 2^-26 turns
+    if (!(turns < 67108864.0)) return QG_ERR_SHAPE;
     turns -= std::floor(turns);  // whole turns do nothing
     if (turns >= 1.0) turns = 0.0;
     p.step[i] = (uint64_t)std::ldexp(turns, 64);

@@ -10,8 +10,9 @@
 // the sines and cosines of its eight elements over all rows.
 //
 // Angles: a pair's frequency is a 64-bit fixed-point fraction of a turn per
-// position. Frequency times position modulo 2^64 is then the exact fraction of
-// a turn (no large f32 angle, no f64), whose top 32 bits go to sincospif.
+// position. Frequency times position modulo 2^64 is then the fraction of a turn
+// without rounding (no large f32 angle, no f64 here), whose top 32 bits go to
+// sincospif.
 //
 // Q8_0: the 32 elements of a block are on four neighbouring lanes, so the
 // block's largest magnitude is two shuffles away.
