@@ -282,7 +282,9 @@ def _dtypes():
     """torch's dtypes that the calls below take (torch is imported on first use)."""
     global _ELEM, _INT32, _FLOAT16
     import torch
-    _ELEM, _INT32, _FLOAT16 = {torch.float32: QG_F32, torch.float16: QG_F16}, torch.int32, torch.float16
+    _FLOAT16 = torch.float16  # in this order: a thread that finds _ELEM or _INT32 set uses what stands before it, too
+    _INT32 = torch.int32
+    _ELEM = {torch.float32: QG_F32, torch.float16: QG_F16}
 
 
 def _elem(t, name):

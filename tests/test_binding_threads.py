@@ -63,3 +63,27 @@ def test_current_stream(monkeypatch):
         monkeypatch.setattr(qg, n, None)
     assert interrupted(qg._stream.__code__, lambda: qg._stream(None), other) > 10
     assert qg._stream(None) == 1003
+
+
+def test_element_types(monkeypatch):
+    names = ("_ELEM", "_INT32", "_FLOAT16")
+    for n in names:
+        monkeypatch.setattr(qg, n, None)
+    table, pool = torch.zeros((1, 1), dtype=torch.int32), torch.zeros(qg.qkv_page_bytes(8, 2, 64, 16), dtype=torch.uint8)
+    cache = qg.QGKVCache(pool.data_ptr(), table.data_ptr(), 8, 2, 64, 16, 1, 1, 1)
+    k, pos = torch.zeros(0, 2, 64), torch.zeros(0, dtype=torch.int32)
+    q, q_out = torch.zeros(0, 4, 64), torch.zeros(0, 4, 64, dtype=torch.float16)
+    one = torch.zeros(1, 1, 4, 64, dtype=torch.float16)
+
+    def calls():  # none of them gets as far as a device: no tokens, no workspace
+        was = {n: getattr(qg, n) for n in names}
+        qg.qkv_append(cache, k, k, pos, q=q, q_out=q_out, stream=0)
+        for n, v in was.items():
+            setattr(qg, n, v)
+        with pytest.raises(qg.QGError) as e:
+            qg.qattn_paged(cache, one, torch.zeros(1, dtype=torch.int32), torch.zeros_like(one), pool[:0], stream=0)
+        assert e.value.status == qg.QG_ERR_WORKSPACE
+        for n, v in was.items():
+            setattr(qg, n, v)
+    assert interrupted(qg._dtypes.__code__, lambda: qg._elem(k, "k"), calls) > 10
+    calls()
