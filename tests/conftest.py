@@ -25,3 +25,13 @@ def gpu_available() -> bool:
         return torch.cuda.is_available()
     except Exception:
         return False
+
+
+#: host-side tests that end in calls whose arguments are all right and whose addresses are made up: QG_ERR_CUDA where there is
+#: no GPU, a kernel on addresses of nothing where there is one
+MADE_UP_ADDRESSES = {"test_rope_refusals", "test_append_refusals", "test_read_refusals", "test_attention_refusals"}
+
+
+def pytest_runtest_setup(item):
+    if item.path.name == "test_attn_abi.py" and item.name in MADE_UP_ADDRESSES and gpu_available():
+        pytest.skip("calls with made-up addresses: not where there is a GPU")
