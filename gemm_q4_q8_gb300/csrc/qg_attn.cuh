@@ -73,6 +73,7 @@
 #include <cmath>
 
 #include "qg_async.cuh"
+#include "qg_attn.h"
 #include "qg_common.cuh"
 #include "qg_internal.h"
 #include "qg_kv.cuh"
@@ -85,20 +86,8 @@ static __device__ int32_t g_attn_error;
 
 namespace {
 
-constexpr int AT_WARPS = 4;
 constexpr int AT_THREADS = AT_WARPS * 32;
-// Warps that share a record: 32 rows of heads of 256 are split between two, 128 dimensions each, which add their scores
-// up; each then has the registers of a warp on heads of 128. (16 sequences of 8,191 f16 tokens, two kv heads, 32 rows:
-// 68 us, against 90 for two tiles of 16 rows that read everything twice. For fewer rows, and for Q8_0, a warp on its own
-// is faster: f16, 8 rows 47 us against 50, 16 rows 51 against 56; Q8_0, 16 rows 36 against 42, 32 rows 56 as two tiles
-// of 16 against 65 or, as one, 68.)
-__host__ __device__ constexpr int at_team(int d, int nt) { return d == 256 && nt == 4 ? 2 : 1; }
-// Tokens of a unit: a record of 16 for every team of the CTA.
-__host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_team(d, nt) * KV_GROUP; }
 constexpr int AT_SMS = 152;
-// An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
-// the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64).
-constexpr int at_pad(int nt) { return nt == 1 ? 2 : 4; }
 constexpr int AT_CLUSTER = 16;  // CTAs of a cluster, at most
 // Units of a CTA of a cluster, at most: what its join saves (1.9 us of 8.4 at 1,000 tokens, two Q8_0 heads of 256; 0.7 of 7.7 at
 // 2,000) is gone at four (4,000 tokens: 8.6 us against 8.5; f16, 8 heads of 128: 9.45 against 9.4).
