@@ -22,8 +22,9 @@
 // grid that fills the machine once, so a batch of ragged lengths and one very long
 // sequence load every SM alike. A CTA that covers an item whole writes y; where an item is
 // cut, each CTA writes its sum, reference and weight to the workspace, and a
-// second kernel joins them in CTA order. The cuts depend on lens and the shape
-// alone, and so do the results. (Joining in the CTA that finishes last needs no
+// second kernel joins them in CTA order. The cuts, and so the last bits of the
+// results, depend on lens, the window, the shape and the cache's type; and on the
+// room of the page table where that decides on the form below. (Joining in the CTA that finishes last needs no
 // second kernel but a first one that clears its counters, and has one CTA's loads
 // to work with: 1,000 tokens of two heads of 256 took 14.3 us so, 10.7 with the
 // second kernel.) Where the page table has room for little, each item is a cluster's
@@ -56,13 +57,19 @@
 // to f16 (so V itself is never rounded); a power of two that follows the largest
 // scale seen keeps that product in the normal range of f16.
 //
-// Bound. One tile of 8 rows: by memory, at 6.1 TB/s in f16 (131,071 tokens of 8 kv
+// Weights are rounded to f16 because the matrix product with the values takes both
+// factors in one type, and values are f16 (or integers that f16 holds): half a step,
+// 2^-11 of a weight, or 2^-32 of its run's largest (Q8_0, times the largest scale: 2^-30). Their sum is of the unrounded ones. Scores,
+// references, sums and the join are f32.
+//
+// Bound (times of calls replayed in a graph; from Python 1 to 2 us more). One tile of
+// 8 rows: by memory, at 6.1 TB/s in f16 (131,071 tokens of 8 kv
 // heads of 128 in 88 us; the bytes alone take 79 at the rate of a large copy), and
 // nearly so in Q8_0 (64 ragged sequences, 279 MB, in 50 us, issue slots half
 // used). More rows: by the latency of the instructions between two matrix
 // products, with the 8 to 16 warps that the accumulators leave room for (Q8_0, 32 rows of heads
 // of 256: 800 instructions a record and tile of 16 rows, issue slots 38% and
-// tensor pipe 24% used, 37 us for 82 MB). One short sequence: by the chain of
+// tensor pipe 25% used, 38 us for 82 MB). One short sequence: by the chain of
 // dependent loads length and page, record, and by 1,500 to 2,000 instructions a warp
 // that run once (1,000 Q8_0 tokens of two heads of 256: 6.4 us; 8.4 with runs and the
 // second kernel).
@@ -89,7 +96,9 @@ namespace {
 constexpr int AT_THREADS = AT_WARPS * 32;
 constexpr int AT_SMS = 152;
 constexpr int AT_CLUSTER = 16;  // CTAs of a cluster, at most
-// Units of a CTA of a cluster, at most: what its join saves (1.9 us of 8.4 at 1,000 tokens, two Q8_0 heads of 256; 0.7 of 7.7 at
+// Units of a CTA of a cluster, at most, of the room that the page table has for a sequence (the lengths are not known on the
+// host): a table for 131,072 tokens never gets clusters, and 1,000 Q8_0 tokens of two heads of 256 take 8.3 us with it
+// and 6.4 with one for 1,008 (f16, 8 heads of 128: 7.2 and 6.1). The limit: what the join saves (1.9 us of 8.4 at 1,000 tokens, two Q8_0 heads of 256; 0.7 of 7.7 at
 // 2,000) is gone at four (4,000 tokens: 8.6 us against 8.5; f16, 8 heads of 128: 9.45 against 9.4).
 constexpr int AT_CLUSTER_UNITS = 3;
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
@@ -115,7 +124,9 @@ struct AttnCfg {
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
   static constexpr size_t qbuf = (size_t)ROWS * QPITCH + (QSMEM && TYPE == QG_Q8_0 ? (size_t)(D / 32) * ROWS * 8 : 0);
   // Stages of a team's ring with n CTAs on an SM (227 KB, with 1 KB of the system's and 600 bytes for up to
-  // 72 sequences a CTA).
+  // 72 sequences a CTA). Many more sequences than that may not leave room for as many CTAs, and the grid is then more than
+  // one wave: 1,000 f16 tokens a sequence, 16 rows of heads of 64, take 33.0 us for 450 sequences and 42.5 for 460;
+  // 8 rows of heads of 128, 46.5 for 460 and 56.8 for 480.
   static constexpr int fit(int n) {
     return (int)(((size_t)(227 * 1024) / n - 1024 - 600 - obuf - stats - qbuf - 256) / ((size_t)TEAMS * STAGE));
   }

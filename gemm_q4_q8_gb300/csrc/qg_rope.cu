@@ -47,7 +47,7 @@ enum Layout {
   PLAIN,   // no rotation
   PAIRS,   // interleaved, rot_dim a multiple of 8: partners within the lane
   HALVES,  // half layout, rot_dim a multiple of 16: partners in one other aligned group of eight
-  ANY      // everything else, element by element
+  ANY      // everything else, element by element (8,191 x 40 x 128, 100 of them turned: 65 to 72 us instead of 40)
 };
 Layout layout_of(const qg_rope& p) {
   return p.interleaved ? (p.rot_dim % 8 ? ANY : PAIRS) : (p.rot_dim % 16 ? ANY : HALVES);

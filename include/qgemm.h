@@ -422,10 +422,12 @@ qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *p
  * Tokens that a row does not see (padding of the last page, later columns,
  * outside the window) have no effect on it, whatever their bytes hold.
  * Scores, softmax sums and the weighted sum are f32; a weight (times the
- * block's scale for Q8_0) is rounded to f16 before it meets its value, and y
- * is rounded to f16 once. Results are the same from run to run; the order of
- * the sums depends on lens, so a column of a wider call need not equal the
- * one-column call bit for bit.
+ * block's scale for Q8_0) is rounded to f16 before it meets its value: by at
+ * most 2^-11 of itself, or 2^-30 of the largest weight (times the largest
+ * scale). y is rounded to f16 once. Results are the same from run to run. The
+ * order of the sums depends on lens, window and the sizes, max_pages among
+ * them: a column of a wider call need not equal the one-column call bit for
+ * bit, nor a call over a wider page table the same call over a narrow one.
  * ------------------------------------------------------------------------- */
 #define QG_ATTN_MAX_COLS 16
 #define QG_ATTN_MAX_GROUP 64
