@@ -15,6 +15,7 @@ import os
 QG_F32 = 0
 QG_F16 = 1
 Q4_0 = 2
+Q4_1 = 3
 Q8_0 = 8
 
 _HERE = os.path.dirname(os.path.abspath(__file__))

@@ -163,7 +163,7 @@ bool plan_ok(const qg_rope* p) {
   return p->rot_dim >= 2 && p->rot_dim <= QG_ROPE_MAX_DIM && (p->rot_dim & 1) == 0;
 }
 qg_status kv_shape(int type, int n_kv_heads, int head_dim, int page_size) {
-  if (type != QG_F16 && type != QG_Q8_0) return QG_ERR_TYPE;
+  if (type != QG_F16 && type != QG_Q8_0 && type != QG_Q4_1) return QG_ERR_TYPE;
   if (n_kv_heads < 1 || n_kv_heads > 256 || (head_dim != 64 && head_dim != 128 && head_dim != 256) ||
       page_size < 16 || page_size > 256 || (page_size & (page_size - 1)))
     return QG_ERR_SHAPE;

@@ -7,14 +7,10 @@ namespace qg {
 namespace {
 
 // Row tiles of 8 that a CTA handles together: as few as hold the rows of a kv
-// head, at most as many as leave the accumulator (8 NT x head_dim over a warp; two
-// warps for 32 rows of 256) 128 registers a thread. Q8_0 needs more registers
-// beside it and takes at most half as many (64 rows of heads of 64, 16 sequences
-// of 8,191 tokens: 121 us with eight tiles, 102 with two times four, f16 85 and
-// 102; 32 rows of heads of 128, Q8_0: 58 either way). More rows are further items,
-// which read the keys and values again (from L2, mostly).
+// head, up to at_most. More rows are further items, which read the keys and values
+// again (from L2, mostly).
 int tiles_of(int type, int rows, int head_dim) {
-  const int most = (head_dim == 64 ? 8 : 4) / (type == QG_F16 ? 1 : 2);
+  const int most = at_most(type, head_dim);
   int nt = 1;
   while (nt < most && nt * 8 < rows) nt *= 2;
   return nt;
@@ -42,7 +38,7 @@ bool attn_size_ok(const qg_kvcache& c, int n_heads, int ncols) {
   return units * c.n_seq * c.n_kv_heads * tiles < ((int64_t)1 << 31);
 }
 
-// (the larger of the two types': the call does not name one)
+// (the largest of the types', of which Q8_0 and Q4_1 have the same tiles: the call does not name one)
 size_t attn_ws_bytes(int, int n_heads, int n_kv_heads, int head_dim, int ncols) {
   const int rows = n_heads / n_kv_heads * ncols;
   const size_t a = ws_of(QG_F16, rows, head_dim), b = ws_of(QG_Q8_0, rows, head_dim);

@@ -105,7 +105,7 @@ constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this
 // f16: every weight is 2^7 times as large, in numerators and sums alike. The largest then lies between 2^7 and 2^15, and what
 // rounding to f16 takes from small ones (up to 2^-25 below its normals) is 2^-32 of it: a first token far above 30,000 others,
 // whose sum the answer is, else cost those of its warp a quarter of their weight. (Q8_0: wmul below does this.)
-constexpr float at_lift(int type) { return type == QG_F16 ? 7.f : 0.f; }
+constexpr float at_lift(int type) { return type == QG_Q8_0 ? 0.f : 7.f; }
 
 template <int TYPE, int D, int NT>
 struct AttnCfg {
@@ -118,7 +118,7 @@ struct AttnCfg {
   static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
   // dimensions joined at a time (32 also where 64 would leave one stage less)
   static constexpr int OD = NT > 2 || (NT == 1 && RECORD == 8192) ? 32 : 64;
-  static constexpr int OPITCH = OD + 4;         // floats: no bank conflicts
+  static constexpr int OPITCH = TYPE == QG_Q4_1 ? OD : OD + 4;  // floats: no bank conflicts (Q4_1: by at_swap)
   static constexpr size_t obuf = (size_t)AT_WARPS * ROWS * OPITCH * 4;
   static_assert(TEAM == 1 || obuf >= (size_t)2 * AT_WARPS * NT * 512, "a team's scores pass through the join buffer");
   static constexpr size_t stats = (size_t)2 * (2 * AT_WARPS + 2) * ROWS * 4;  // by parity: z, sums; row's z, sum
@@ -139,6 +139,7 @@ struct AttnCfg {
   // With one stage its halves come and go on their own: keys while values are in use, and the other way round.
   static constexpr bool SPLIT = STAGES == 1;
   static_assert(STAGES >= 1 && (TEAM == 1 || !SPLIT), "room for the records in use");
+  static_assert(TYPE != QG_Q4_1 || (TEAM == 1 && !SPLIT), "4 bits: a warp on its own, whole records");
   static_assert(NB % 2 == 0, "blocks are looked through in pairs");
   static constexpr int BARS = SPLIT ? 2 : STAGES;
   static constexpr size_t ring = (size_t)TEAMS * STAGES * STAGE;
@@ -213,6 +214,31 @@ __device__ __forceinline__ void ldsm_bytes_trans(uint32_t at, uint32_t (&r)[4]) 
   asm volatile("ldmatrix.sync.aligned.m16n16.x2.trans.shared.b8 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                : "r"(at));
+}
+// Exclusive or with the place of a row's dimension in shared memory, by row: Q4_1's rows of a quad then differ in their bank.
+template <int TYPE>
+__device__ __forceinline__ int at_swap(int row) {
+  return TYPE == QG_Q4_1 ? ((row & 2) << 1) | ((row & 4) << 2) : 0;
+}
+__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
+  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&d);
+}
+// Q4_1: four f16 pairs of a fragment out of two words' low or high quants (bits MASK), as subnormals.
+template <uint32_t MASK>
+__device__ __forceinline__ void nibbles(uint32_t x, uint32_t y, uint32_t (&a)[4]) {
+  a[0] = x & MASK;
+  a[1] = y & MASK;
+  a[2] = (x >> 8) & MASK;
+  a[3] = (y >> 8) & MASK;
+}
+constexpr uint32_t NIB_LO = 0x000F000Fu, NIB_HI = 0x00F000F0u;
+// D = A B of 8 columns of A.
+__device__ __forceinline__ void mma1688(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t b) {
+  const float z = 0.f;
+  asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5}, {%6}, {%7, %7, %7, %7};"
+      : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+      : "r"(a0), "r"(a1), "r"(b), "f"(z));
 }
 // Transpose of an 8 x 8 matrix of f16 held by a warp, two elements of a row a lane.
 __device__ __forceinline__ uint32_t transpose8(uint32_t x) {
@@ -473,7 +499,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   uint8_t* const ring = s_ring + (size_t)team * C::STAGES * C::STAGE;
   const uint32_t ring_at = smem_u32(ring), bar_at = smem_u32(s_bar + team * C::BARS);
   // In a half record: where this warp's blocks are, and (Q8_0) from there their scales.
-  constexpr int BLOCKS = NB * 32 * KV_GROUP * (TYPE == QG_F16 ? 2 : 1);
+  constexpr int BLOCKS = NB * 32 * KV_GROUP * (TYPE == QG_F16 ? 4 : TYPE == QG_Q8_0 ? 2 : 1) / 2;
   const int own = share * BLOCKS, scales = TEAM * BLOCKS - share * (BLOCKS - NB * 32);
   // Page numbers: lane i looks up step base + i. Raw until the batch is entered,
   // so that the load has the whole batch before to arrive.
@@ -561,11 +587,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     __syncwarp();
   };
 
-  // Which token of the record position i of the 16-wide side is. f16: token i. Q8_0: i/2 (i even) or
+  // Which token of the record position i of the 16-wide side is. f16, Q4_1: token i. Q8_0: i/2 (i even) or
   // 4 + (i/2 + 2) mod 4 (i odd), and 8 more for i >= 8: the rows of 32 bytes that the lanes of a shared-memory phase
   // read then differ modulo 4 (no bank conflict), and a lane's two tokens, 8 apart, have their scales in one word.
   auto token_of = [](int i) {
-    return TYPE == QG_F16 ? i : (i & 8) + ((i & 1) ? 4 + ((((i & 7) >> 1) + 2) & 3) : (i & 7) >> 1);
+    return TYPE != QG_Q8_0 ? i : (i & 8) + ((i & 1) ? 4 + ((((i & 7) >> 1) + 2) & 3) : (i & 7) >> 1);
   };
   const int tok_a = token_of(g);  // this lane's tokens as rows of the scores: tok_a and tok_a + 8
   const uint32_t scale_at = (tok_a & 3) * 8, scale_sel = (tok_a & 4) ? 0x7632u : 0x5410u;
@@ -573,6 +599,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   uint32_t v_at;
   if constexpr (TYPE == QG_F16) {
     v_at = ((lane & 7) + ((lane >> 4) & 1) * 8) * 64 + ((lane >> 3) & 1) * 16;
+  } else if constexpr (TYPE == QG_Q4_1) {
+    // as below, but bytes 0 and 2 are tokens 2t, 2t+1 and bytes 1 and 3 tokens 2t+8, 2t+9, as nibbles() pairs them; the two
+    // matrices are two blocks
+    const int j = lane & 15;
+    v_at = (2 * (j >> 2) + ((j >> 1) & 1) + 8 * (j & 1)) * 16 + (lane >> 4) * 256;
   } else {
     // row j of the byte matrix goes to byte j mod 4 of lane j / 4: positions 2t, 2t+1, 2t+8, 2t+9
     const int j = lane & 15, i = 2 * (j >> 2) + (j & 1) + 4 * (j & 2);
@@ -580,7 +611,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
   }
 
   // CLUSTER: place of (row, dimension) among a warp's sums; the exclusive or keeps a quad's rows on different banks
-  auto in_sums = [](int row, int dim) { return row * D + (dim ^ ((row & 6) << 2)); };
+  auto in_sums = [](int row, int dim) { return row * D + (dim ^ (TYPE == QG_Q4_1 ? at_swap<TYPE>(row) : (row & 6) << 2)); };
+  // of a block: the dimension of accumulator 4 blk + e of this lane
+  auto dim_of = [&](int e) {
+    return TYPE == QG_Q4_1 ? 16 * (e & 1) + 4 * (e >> 1) + 8 * (g >> 2) + ((g & 1) << 1) + ((g >> 1) & 1) : 8 * e + g;
+  };
 
   // --------------------------------------------------------------- items
   int turn = 0;  // of the statistics' two buffers
@@ -615,18 +650,23 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     // Q: the B fragments of a block and row tile, dimensions 8t .. 8t+7 of row g; and, for
     // Q8_0, -128 2^-24 sum of the block's queries of rows 2t and 2t + 1.
     uint32_t qf[C::QSMEM ? 1 : NB][C::QSMEM ? 1 : NT][4];
-    float qc[C::QSMEM || TYPE == QG_F16 ? 1 : NB][C::QSMEM || TYPE == QG_F16 ? 1 : NT][4];  // (each twice, as the mma's C)
+    float qc[C::QSMEM || TYPE != QG_Q8_0 ? 1 : NB][C::QSMEM || TYPE != QG_Q8_0 ? 1 : NT][4];  // (each twice, as the mma's C)
+    // Q4_1: the sums of the blocks' queries as two f16 each (what the first one's rounding leaves is the second), times a power
+    // of two by row, as the B fragment of the product with the blocks' m; and that power's inverse of rows 2t, 2t + 1.
+    uint32_t qm[NT][D == 256 ? 2 : 1];
+    float2 qback[NT];
     const uint32_t q_at = smem_u32(s_q) + g * C::QPITCH + 16 * t + share * (NB * 64);  // this lane's, of the warp's first block
     auto load_q = [&](int blk, int nt, uint32_t (&q)[4]) {
       lds128(q_at + nt * 8 * C::QPITCH + blk * 64, q[0], q[1], q[2], q[3]);
     };
-    auto sum_q = [&](const uint32_t (&q)[4]) {  // of row g
+    auto sum_of = [&](const uint32_t (&q)[4]) {  // of row g
       float s = ((lo_f32(q[0]) + hi_f32(q[0])) + (lo_f32(q[1]) + hi_f32(q[1]))) +
                 ((lo_f32(q[2]) + hi_f32(q[2])) + (lo_f32(q[3]) + hi_f32(q[3])));
       s += __shfl_xor_sync(0xffffffffu, s, 1);
       s += __shfl_xor_sync(0xffffffffu, s, 2);
-      return s * -7.62939453125e-06f;  // -128 * 2^-24
+      return s;
     };
+    auto sum_q = [&](const uint32_t (&q)[4]) { return sum_of(q) * -7.62939453125e-06f; };  // -128 * 2^-24
     float* const s_qsum = reinterpret_cast<float*>(s_q + ROWS * C::QPITCH);  // [block][tile][t][4]
     copies_done();
     if (p.q_and != 0xffffffffu || p.q_xor) {  // a scale that is not positive: each thread on what it copied
@@ -660,6 +700,42 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           }
         }
     }
+    if constexpr (TYPE == QG_Q4_1) {
+      // lane t has blocks 2 pair, 2 pair + 1, and of them the first f16 (which = 0), the second (1) or neither
+      const int pair = t % (NB / 2), which = NB == 8 ? 0 : t / (NB / 2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float s0 = 0.f, s1 = 0.f, most = 0.f;
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          float s;
+          if constexpr (C::QSMEM) {
+            uint32_t q[4];
+            load_q(blk, nt, q);
+            s = sum_of(q);
+          } else {
+            s = sum_of(qf[blk][nt]);
+          }
+          most = fmaxf(most, fabsf(s));
+          if (blk == 2 * pair) s0 = s;
+          if (blk == 2 * pair + 1) s1 = s;
+        }
+        // most, times 2^-up, lies between 2^13 and 2^14 (most is 0 or between 2^-24 and 2^21; infinite or NaN queries leave NaN)
+        const int up = most > 0.f ? min(((__float_as_int(most) >> 23) & 0xff) - 127, 40) - 13 : 0;
+        const float to = __int_as_float((127 - up) << 23);
+        s0 *= to;
+        s1 *= to;
+        const uint32_t hi = pack_f16(s0, s1), lo = pack_f16(s0 - lo_f32(hi), s1 - hi_f32(hi));
+        if constexpr (D == 256) {
+          qm[nt][0] = hi;
+          qm[nt][1] = lo;
+        } else {
+          qm[nt][0] = which == 0 ? hi : which == 1 ? lo : 0u;
+        }
+        const float back = __int_as_float((127 + up - 24) << 23);  // (scores are in units of 2^24)
+        qback[nt] = make_float2(__shfl_sync(0xffffffffu, back, 8 * t), __shfl_sync(0xffffffffu, back, 8 * t + 4));
+      }
+    }
     if (!C::QSMEM && step + todo < steps) {
       __syncthreads();  // the buffer is in all warps' registers
       stage_q(at);
@@ -683,8 +759,14 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       }
     auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : z[nt][c]; };
     // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
-    // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul.
+    // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul. Q4_1: wback = 2^e,
+    // and the products of weights and d are brought below 2^15 by 2^-e in two factors: the d by wm_d, the weights by wm_w
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
+    uint32_t wm_d = 0x3C003C00u, wm_w = 0x3C003C00u;
+    // Q4_1: om[nt][c] of block g (c < 2): sum of weights times m, of row 8 nt + 2t + c
+    float om[TYPE == QG_Q4_1 ? NT : 1][4];
+#pragma unroll
+    for (int nt = 0; nt < (TYPE == QG_Q4_1 ? NT : 1); ++nt) om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
 
     const int begin = step;
     for (const int end = step + todo; step < end; ++step) {
@@ -725,13 +807,49 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 
       // ---- scores: s[nt][c] of token tok_a + 8 (c/2), row 8 nt + 2t + c%2
       float s[NT][4];
+      uint32_t kd[TYPE == QG_Q4_1 ? 2 : 1][TYPE == QG_Q4_1 ? NB / 2 : 1];  // Q4_1: the d of tokens tok_a, tok_a + 8
+      if constexpr (TYPE == QG_Q4_1) {
+        const uint32_t d_at = kb + scales + tok_a * (2 * NB), m_at = d_at + D + 4 * (t % (NB / 2));
 #pragma unroll
-      for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] = 0.f;
+        for (int i = 0; i < 2; ++i) {
+          if constexpr (NB == 2) kd[i][0] = lds32(d_at + i * 8 * 2 * NB);
+          if constexpr (NB == 4) lds64(d_at + i * 8 * 2 * NB, kd[i][0], kd[i][1]);
+          if constexpr (NB == 8) lds128(d_at + i * 8 * 2 * NB, kd[i][0], kd[i][1], kd[i][2], kd[i][3]);
+        }
+        const uint32_t m0 = lds32(m_at), m1 = lds32(m_at + 8 * 2 * NB);
+        const uint32_t am[4] = {m0, m1, m0, m1};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          float part[4];
+          if constexpr (NB == 8)
+            mma16816(part, am, qm[nt][0], qm[nt][1]);
+          else
+            mma1688(part, m0, m1, qm[nt][0]);
+          const float2 lo = mul2(make_float2(part[0], part[1]), qback[nt]), hi = mul2(make_float2(part[2], part[3]), qback[nt]);
+          s[nt][0] = lo.x;
+          s[nt][1] = lo.y;
+          s[nt][2] = hi.x;
+          s[nt][3] = hi.y;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NT * 4; ++i) s[i >> 2][i & 3] = 0.f;
+      }
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk) {
         uint32_t a0[4], a1[4];
         float e0 = 0.f, e1 = 0.f;
-        if constexpr (TYPE == QG_F16) {
+        if constexpr (TYPE == QG_Q4_1) {
+          const uint32_t at = kb + blk * 256 + tok_a * 16 + t * 4;
+          const uint32_t x = lds32(at), y = lds32(at + 128);
+          nibbles<NIB_LO>(x, y, a0);
+          if constexpr (NT == 1)
+            nibbles<NIB_HI>(x, y, a1);  // 16 times their values
+          else
+            nibbles<NIB_LO>(x >> 4, y >> 4, a1);
+          e0 = blk & 1 ? hi_f32(kd[0][blk / 2]) : lo_f32(kd[0][blk / 2]);
+          e1 = blk & 1 ? hi_f32(kd[1][blk / 2]) : lo_f32(kd[1][blk / 2]);
+        } else if constexpr (TYPE == QG_F16) {
           const uint32_t at = kb + blk * 1024 + tok_a * 64 + t * 16;
           lds128(at, a0[0], a0[2], a1[0], a1[2]);
           lds128(at + 512, a0[1], a0[3], a1[1], a1[3]);
@@ -767,15 +885,29 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             mma16816_acc(s[nt], a1, q[2], q[3]);
           } else {
             float part[4], c[4];
-            if constexpr (C::QSMEM) {
+            if constexpr (TYPE == QG_Q4_1) {
+              mma16816(part, a0, q[0], q[1]);
+            } else if constexpr (C::QSMEM) {
               const float4 x = *reinterpret_cast<const float4*>(s_qsum + ((share * NB + blk) * NT + nt) * 16 + 4 * t);
               c[0] = x.x; c[1] = x.y; c[2] = x.z; c[3] = x.w;
             } else {
 #pragma unroll
               for (int i = 0; i < 4; ++i) c[i] = qc[blk][nt][i];
             }
-            mma16816_from(part, a0, q[0], q[1], c);
-            mma16816_acc(part, a1, q[2], q[3]);
+            if constexpr (TYPE == QG_Q8_0) mma16816_from(part, a0, q[0], q[1], c);
+            if constexpr (TYPE == QG_Q4_1 && NT == 1) {  // (two more instructions a row tile, three less a block than the shift)
+              float high[4];
+              mma16816(high, a1, q[2], q[3]);
+              const float2 k = make_float2(0.0625f, 0.0625f);
+              const float2 lo = fma2(make_float2(high[0], high[1]), k, make_float2(part[0], part[1]));
+              const float2 hi = fma2(make_float2(high[2], high[3]), k, make_float2(part[2], part[3]));
+              part[0] = lo.x;
+              part[1] = lo.y;
+              part[2] = hi.x;
+              part[3] = hi.y;
+            } else {
+              mma16816_acc(part, a1, q[2], q[3]);
+            }
             const float2 lo = fma2(make_float2(part[0], part[1]), make_float2(e0, e0), make_float2(s[nt][0], s[nt][1]));
             const float2 hi = fma2(make_float2(part[2], part[3]), make_float2(e1, e1), make_float2(s[nt][2], s[nt][3]));
             s[nt][0] = lo.x;
@@ -863,7 +995,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 #pragma unroll
         for (int i = 0; i < 4; i += 2) {
           const float2 d = sub2(make_float2(s[nt][i], s[nt][i + 1]), make_float2(z[nt][0], z[nt][1]));
-          const float2 x = TYPE == QG_F16 ? fma2(d, mul, make_float2(at_lift(TYPE), at_lift(TYPE))) : mul2(d, mul);
+          const float2 x = TYPE != QG_Q8_0 ? fma2(d, mul, make_float2(at_lift(TYPE), at_lift(TYPE))) : mul2(d, mul);
           s[nt][i] = ex2(x.x);
           s[nt][i + 1] = ex2(x.y);
         }
@@ -937,6 +1069,115 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           for (int nt = 0; nt < NT; ++nt) {
             mma16816_acc(o[blk][nt][0], v0, w0[nt], w1[nt]);
             mma16816_acc(o[blk][nt][1], v1, w0[nt], w1[nt]);
+          }
+        }
+      } else if constexpr (TYPE == QG_Q4_1) {
+        if (__builtin_expect(masked, 0)) {
+          // As for Q8_0, for d and m alike: those of tokens that no row sees are cleared, and one that is not finite, of a token
+          // that some rows do not see, is taken out and given to the rows that see it.
+          uint16_t* sc = reinterpret_cast<uint16_t*>(vp + scales);
+#pragma unroll
+          for (int two = 0; two < 2 * NB; two += 2) {  // the 16 of each by a half of the warp; from NB on they are m
+            uint16_t& x = sc[two * KV_GROUP + lane];
+            const uint16_t was = x;
+            const int tk = tok + kv_value_token(lane & 15);
+            const bool seen = tk < sp.hi && tk >= sp.lo;
+            const bool bad = seen && (was & 0x7C00) == 0x7C00;
+            if (!seen || bad) x = 0;
+            const uint32_t both = __ballot_sync(0xffffffffu, bad);
+            if (__builtin_expect(both == 0, 1)) continue;
+            const bool is_m = two >= NB;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const int blk = (two + h) % NB;
+              uint32_t odd = h == 0 ? both & 0xffffu : both >> 16;
+              while (odd) {
+                const int j = __ffs(odd) - 1, tj = tok + kv_value_token(j);
+                odd &= odd - 1;
+                const float its = __half2float(__ushort_as_half((uint16_t)__shfl_sync(0xffffffffu, (uint32_t)was, 16 * h + j)));
+                const float what = is_m ? its : __int_as_float(0x7fffffff);
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                  for (int c = 0; c < 2; ++c) {
+                    int lo, hi;
+                    row_sees(nt * 8 + 2 * t + c, lo, hi);
+                    const float add = tj <= hi && tj > lo ? what : 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[blk][nt][e >> 1][2 * (e & 1) + c] += add;
+                  }
+              }
+            }
+          }
+          __syncwarp();
+        }
+        uint32_t w0[NT], w1[NT];
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          w0[nt] = transpose8(pack_f16(s[nt][0], s[nt][1]));
+          w1[nt] = transpose8(pack_f16(s[nt][2], s[nt][3]));
+        }
+        {  // weights times m: the blocks on the wide side
+          uint32_t am[4] = {0u, 0u, 0u, 0u};
+          lds64(vb + scales + D + (g & (NB - 1)) * 32 + t * 8, am[0], am[2]);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816_acc(om[nt], am, w0[nt], w1[nt]);
+        }
+        uint32_t d[NB][2];  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+        __half2 big = __float2half2_rn(0.f);
+#pragma unroll
+        for (int blk = 0; blk < NB; ++blk) {
+          lds64(vb + scales + blk * 32 + t * 8, d[blk][0], d[blk][1]);
+          big = __hmax2(big, __hmax2(*reinterpret_cast<__half2*>(&d[blk][0]), *reinterpret_cast<__half2*>(&d[blk][1])));
+        }
+        float dmax = fmaxf(__low2float(big), __high2float(big));
+        if (__builtin_expect(__any_sync(0xffffffffu, dmax > wmax), 0)) {
+          dmax = wmax;  // again without infinities, which would cost the others their bits
+#pragma unroll
+          for (int i = 0; i < 2 * NB; ++i) {
+            const float x = lo_f32(d[i / 2][i % 2]), y = hi_f32(d[i / 2][i % 2]);
+            if (x <= 65504.f) dmax = fmaxf(dmax, x);
+            if (y <= 65504.f) dmax = fmaxf(dmax, y);
+          }
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 1));
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 2));
+          if (dmax > wmax) {
+            // as below. Small scales are made larger, which takes no bit off them (by 2^15 at most: at 2^-24 and a weight of 2^7 the
+            // product is 2^-2). Large ones, next to which ordinary ones would lose theirs, are made smaller by half of what has to be
+            // taken off, the weights by the other half (both have bits to spare: 60,000 in one token and 0.1 in the others)
+            const int e = max(((__float_as_int(dmax) >> 23) & 0xff) - 127 + 2, -15), by_w = e > 0 ? e / 2 : 0;
+            const float f = __int_as_float((127 - e) << 23) * wback;  // (at the first move there is nothing to scale yet)
+            wmax = wback = __int_as_float((127 + e) << 23);
+            const float to_d = __int_as_float((127 + by_w - e) << 23), to_w = __int_as_float((127 - by_w) << 23);
+            wm_d = pack_f16(to_d, to_d);
+            wm_w = pack_f16(to_w, to_w);
+            if (!CLUSTER || step != begin)
+#pragma unroll
+              for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
+          }
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          w0[nt] = hmul2_u(w0[nt], wm_w);
+          w1[nt] = hmul2_u(w1[nt], wm_w);
+        }
+#pragma unroll
+        for (int two = 0; two < NB; two += 2) {
+          uint32_t v[4];  // of four tokens: bytes g, g + 8 of a block, and of the next one
+          ldsm_bytes_trans(vb + two * 256 + v_at, v);
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const int blk = two + h;
+            uint32_t v0[4], v1[4];
+            nibbles<NIB_LO>(v[2 * h], v[2 * h + 1], v0);
+            nibbles<NIB_HI>(v[2 * h], v[2 * h + 1], v1);  // 16 times their values: taken off at the item's end
+            const uint32_t n0 = hmul2_u(d[blk][0], wm_d), n1 = hmul2_u(d[blk][1], wm_d);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+              const uint32_t b0 = hmul2_u(w0[nt], n0), b1 = hmul2_u(w1[nt], n1);
+              mma16816_acc(o[blk][nt][0], v0, b0, b1);
+              mma16816_acc(o[blk][nt][1], v1, b0, b1);
+            }
           }
         }
       } else {
@@ -1028,6 +1269,23 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       next();
     }
 
+    if constexpr (TYPE == QG_Q4_1) {  // quants came as multiples of 2^-24 and 2^-20; and the blocks' m join
+      const float back[2] = {wback * 16777216.f, wback * 1048576.f};
+#pragma unroll
+      for (int blk = 0; blk < NB; ++blk)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const float m = __shfl_sync(0xffffffffu, om[nt][c], 4 * blk + t);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              float& x = o[blk][nt][e >> 1][2 * (e & 1) + c];
+              x = fmaf(x, back[e >> 1], m);
+            }
+          }
+      wback = 1.f;
+    }
     // ------------------------------------------------ the four warps' sums
     const size_t part = (size_t)cta * 2 + (starts ? 1 : 0);
     float* const s_z = s_stat + turn * (2 * AT_WARPS + 2) * ROWS;  // [warp][row]
@@ -1078,7 +1336,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       float* const s_all = reinterpret_cast<float*>(s_ring);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        float* const to = s_all + warp * (ROWS * D) + in_sums(2 * t, 8 * e + g);
+        float* const to = s_all + warp * (ROWS * D) + in_sums(2 * t, dim_of(e));
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk)
 #pragma unroll
@@ -1110,7 +1368,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             for (int c = 0; c < 2; ++c)
 #pragma unroll
               for (int e = 0; e < 4; ++e)
-                s_o[(warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + 8 * e + g] =
+                s_o[(warp * ROWS + nt * 8 + 2 * t + c) * C::OPITCH + hb * 32 + (dim_of(e) ^ at_swap<TYPE>(2 * t))] =
                     f[nt][c] == 0.f ? 0.f : o[blk][nt][e >> 1][2 * (e & 1) + c] * f[nt][c];
         }
         __syncthreads();
@@ -1120,10 +1378,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           const int i = tid + k * AT_THREADS, of = i / (ROWS * QUADS), row = i / QUADS % ROWS, dim = (i % QUADS) * 4;
           const int r = tile * ROWS + row;
           if (of >= TEAM || r >= rows) continue;
-          float4 y = *reinterpret_cast<const float4*>(s_o + (of * ROWS + row) * C::OPITCH + dim);
+          float4 y = *reinterpret_cast<const float4*>(s_o + (of * ROWS + row) * C::OPITCH + (dim ^ at_swap<TYPE>(row)));
 #pragma unroll
           for (int w = TEAM; w < AT_WARPS; w += TEAM) {
-            const float4 x = *reinterpret_cast<const float4*>(s_o + ((of + w) * ROWS + row) * C::OPITCH + dim);
+            const float4 x = *reinterpret_cast<const float4*>(s_o + ((of + w) * ROWS + row) * C::OPITCH + (dim ^ at_swap<TYPE>(row)));
             y.x += x.x; y.y += x.y; y.z += x.z; y.w += x.w;
           }
           const int at = of * (NB * 32) + pass * C::OD + dim;
@@ -1316,9 +1574,15 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kern
 }
 
 template <int D, int NT>
+constexpr int attn_grid_q4() {
+  if constexpr (NT <= at_most(QG_Q4_1, D)) return AttnCfg<QG_Q4_1, D, NT>::GRID;
+  return 0;
+}
+// (the largest of the types': the workspace's size does not depend on it)
+template <int D, int NT>
 constexpr size_t attn_ws_of() {
-  constexpr int grid = AttnCfg<QG_Q8_0, D, NT>::GRID;
-  static_assert(grid >= AttnCfg<QG_F16, D, NT>::GRID, "the workspace's size does not depend on the type");
+  constexpr int of_q8 = AttnCfg<QG_Q8_0, D, NT>::GRID, of_q4 = attn_grid_q4<D, NT>(), grid = of_q8 > of_q4 ? of_q8 : of_q4;
+  static_assert(grid >= AttnCfg<QG_F16, D, NT>::GRID, "room for f16, too");
   return (size_t)grid * ((size_t)2 * 8 * NT * (8 + D * 4));
 }
 
@@ -1334,7 +1598,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   // Kept within 2^+-100, beyond which the weights no longer depend on it: raw scores of finite queries and keys are 0 or at
   // least 2^-72 apart (products of 2^-24 steps, and the scale's for Q8_0) and below 2^48, so that at 2^100 one step takes a
   // weight to 0 and at 2^-100 all weigh 1.
-  const double mul = std::fabs((double)a.scale) * 1.4426950408889634 * (TYPE == QG_Q8_0 ? 16777216. : 1.);
+  const double mul = std::fabs((double)a.scale) * 1.4426950408889634 * (TYPE == QG_F16 ? 1. : 16777216.);
   p.mul = a.scale == 0.f ? 1.f : (float)std::fmin(std::fmax(mul, std::ldexp(1., -100)), std::ldexp(1., 100));
   p.slack = (float)(AT_SLACK / (double)p.mul);
   p.q_and = a.scale == 0.f ? 0u : 0xffffffffu;

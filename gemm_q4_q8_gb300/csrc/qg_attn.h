@@ -1,6 +1,5 @@
 // qg_attn.h -- the attention's launchers by head size, between its translation
-// units. nt: row tiles of 8 that a CTA handles together, a power of two: up to 8 at
-// heads of 64 and 4 above, half of that for Q8_0.
+// units. nt: row tiles of 8 that a CTA handles together, a power of two, up to at_most.
 #pragma once
 #include "qg_internal.h"
 #include "qg_kv.cuh"
@@ -8,6 +7,11 @@
 namespace qg {
 
 constexpr int AT_WARPS = 4;
+// Row tiles of a CTA, at most: as many as leave the accumulator (8 nt x head_dim over a warp; two warps for 32 rows of 256)
+// 128 registers a thread. The quantised types need more registers beside it and take at most half as many (Q8_0, 64 rows of
+// heads of 64, 16 sequences of 8,191 tokens: 121 us with eight tiles, 102 with two times four, f16 85 and 102; 32 rows of heads
+// of 128: 58 either way).
+__host__ __device__ constexpr int at_most(int type, int d) { return (d == 64 ? 8 : 4) / (type == QG_F16 ? 1 : 2); }
 // Warps that share a record: 32 rows of heads of 256 are split between two, 128 dimensions each, which add their scores
 // up; each then has the registers of a warp on heads of 128. (16 sequences of 8,191 f16 tokens, two kv heads, 32 rows:
 // 68 us, against 90 for two tiles of 16 rows that read everything twice. For fewer rows, and for Q8_0, a warp on its own

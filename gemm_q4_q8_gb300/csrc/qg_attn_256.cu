@@ -4,12 +4,21 @@
 
 namespace qg {
 
+template <int NT>
+static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
+  if (a.c.type == QG_F16) return attn_typed<QG_F16, 256, NT>(a, s);
+  if constexpr (NT <= at_most(QG_Q8_0, 256)) {
+    if (a.c.type == QG_Q8_0) return attn_typed<QG_Q8_0, 256, NT>(a, s);
+    if (a.c.type == QG_Q4_1) return attn_typed<QG_Q4_1, 256, NT>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 cudaError_t attn_launch_256(const AttnArgs& a, int nt, cudaStream_t s) {
-  const bool f16 = a.c.type == QG_F16;
   switch (nt) {
-    case 1: return f16 ? attn_typed<QG_F16, 256, 1>(a, s) : attn_typed<QG_Q8_0, 256, 1>(a, s);
-    case 2: return f16 ? attn_typed<QG_F16, 256, 2>(a, s) : attn_typed<QG_Q8_0, 256, 2>(a, s);
-    case 4: return f16 ? attn_typed<QG_F16, 256, 4>(a, s) : cudaErrorInvalidValue;
+    case 1: return launch_tiles<1>(a, s);
+    case 2: return launch_tiles<2>(a, s);
+    case 4: return launch_tiles<4>(a, s);
   }
   return cudaErrorInvalidValue;
 }

@@ -4,13 +4,22 @@
 
 namespace qg {
 
+template <int NT>
+static cudaError_t launch_tiles(const AttnArgs& a, cudaStream_t s) {
+  if (a.c.type == QG_F16) return attn_typed<QG_F16, 64, NT>(a, s);
+  if constexpr (NT <= at_most(QG_Q8_0, 64)) {
+    if (a.c.type == QG_Q8_0) return attn_typed<QG_Q8_0, 64, NT>(a, s);
+    if (a.c.type == QG_Q4_1) return attn_typed<QG_Q4_1, 64, NT>(a, s);
+  }
+  return cudaErrorInvalidValue;
+}
+
 cudaError_t attn_launch_64(const AttnArgs& a, int nt, cudaStream_t s) {
-  const bool f16 = a.c.type == QG_F16;
   switch (nt) {
-    case 1: return f16 ? attn_typed<QG_F16, 64, 1>(a, s) : attn_typed<QG_Q8_0, 64, 1>(a, s);
-    case 2: return f16 ? attn_typed<QG_F16, 64, 2>(a, s) : attn_typed<QG_Q8_0, 64, 2>(a, s);
-    case 4: return f16 ? attn_typed<QG_F16, 64, 4>(a, s) : attn_typed<QG_Q8_0, 64, 4>(a, s);
-    case 8: return f16 ? attn_typed<QG_F16, 64, 8>(a, s) : cudaErrorInvalidValue;
+    case 1: return launch_tiles<1>(a, s);
+    case 2: return launch_tiles<2>(a, s);
+    case 4: return launch_tiles<4>(a, s);
+    case 8: return launch_tiles<8>(a, s);
   }
   return cudaErrorInvalidValue;
 }

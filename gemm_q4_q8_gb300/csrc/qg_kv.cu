@@ -1,7 +1,8 @@
 // qg_kv.cu -- the paged key/value cache read back (qkv_read): a warp owns a
 // token, eight consecutive elements a lane as in qg_rope.cu, and walks over the
 // key rows, then the value rows. A Q8_0 element is (quant - 128) * scale, exact
-// in f32 (an 8-bit integer times an 11-bit significand), rounded once for f16.
+// in f32 (an 8-bit integer times an 11-bit significand), rounded once for f16. A Q4_1
+// element is quant * d + m, rounded once.
 //
 // Bound by memory: 2 (f16) or 17/16 (Q8_0) bytes read an element, 2 or 4 written.
 // 32,767 f16 tokens of 8 heads of 128 (268 MB moved): 44.5 us, 6.0 TB/s.
@@ -65,7 +66,7 @@ __global__ void __launch_bounds__(RD_THREADS)
   }
   // this lane's eight elements of a half record, and their scale
   const int i = pos & (KV_GROUP - 1), blk = d0 >> 5;
-  const int at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 2 : 1);
+  const int at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 4 : TYPE == QG_Q8_0 ? 2 : 1) / 2;
   const int scale_at = KV_GROUP * d + (blk * KV_GROUP + kv_scale_place(i)) * 2;
   const int kv = c.n_kv_heads, kg = (kv + at_once - 1) / at_once;  // row groups: keys, then values
   TO* const ko = k_out ? k_out + tok * kv * d + d0 : nullptr;
@@ -81,12 +82,17 @@ __global__ void __launch_bounds__(RD_THREADS)
       const int r = (is_v ? m - kg : m) * at_once + first;
       TO* const out = is_v ? vo : ko;
       to[j] = m < 2 * kg && r < kv && out ? out + r * d : nullptr;
-      q[j] = TYPE == QG_F16 ? make_uint4(0, 0, 0, 0) : make_uint4(0x80808080u, 0x80808080u, 0, 0);
+      q[j] = TYPE == QG_Q8_0 ? make_uint4(0x80808080u, 0x80808080u, 0, 0) : make_uint4(0, 0, 0, 0);
       sc[j] = 0;
       if (place && to[j]) {
         const uint8_t* half = place + (size_t)((uint32_t)r * (uint32_t)head_bytes + (is_v ? kv_half_bytes(TYPE, d) : 0));
         if constexpr (TYPE == QG_F16) {
           q[j] = *reinterpret_cast<const uint4*>(half + at);
+        } else if constexpr (TYPE == QG_Q4_1) {
+          const uint8_t* const d_at = half + 8 * d + 2 * kv_q4_place(is_v, d, blk, i);
+          q[j].x = *reinterpret_cast<const uint32_t*>(half + at);
+          sc[j] = *reinterpret_cast<const uint16_t*>(d_at);
+          q[j].y = *reinterpret_cast<const uint16_t*>(d_at + d);
         } else {
           const uint2 x = *reinterpret_cast<const uint2*>(half + at);
           q[j].x = x.x;
@@ -113,6 +119,32 @@ __global__ void __launch_bounds__(RD_THREADS)
           w[h] = *reinterpret_cast<const uint32_t*>(&v);
         }
         *reinterpret_cast<uint4*>(to[j]) = make_uint4(w[0], w[1], w[2], w[3]);
+        continue;
+      }
+      if constexpr (TYPE == QG_Q4_1) {
+        // pairs of quants as f16 1024 + q, less 1024; quant * d + m has one rounding
+        __half2 h[4];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const uint32_t u = ((k & 2 ? q[j].x >> 4 : q[j].x) >> (k & 1 ? 8 : 0) & 0x000F000Fu) | 0x64006400u;
+          h[k] = __hsub2(*reinterpret_cast<const __half2*>(&u), __half2half2(__ushort_as_half(0x6400)));
+        }
+        if constexpr (sizeof(TO) == 2) {
+          const __half2 s = __half2half2(__ushort_as_half(sc[j])), m = __half2half2(__ushort_as_half((uint16_t)q[j].y));
+#pragma unroll
+          for (int k = 0; k < 4; ++k) h[k] = __hfma2(h[k], s, m);
+          *reinterpret_cast<uint4*>(to[j]) = *reinterpret_cast<const uint4*>(h);
+        } else {
+          const float s = h2f(sc[j]), m = h2f((uint16_t)q[j].y);
+          float y[8];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const float2 f = __half22float2(h[k]);
+            y[2 * k] = fmaf(f.x, s, m);
+            y[2 * k + 1] = fmaf(f.y, s, m);
+          }
+          write8(to[j], y);
+        }
         continue;
       }
       float y[8];
@@ -157,6 +189,9 @@ cudaError_t kv_read_launch(const qg_kvcache& c, const int32_t* seq, const int32_
   if (c.type == QG_F16)
     return yt == QG_F32 ? read_typed<QG_F16, float>(c, seq, pos, ntok, k_out, v_out, err, s)
                         : read_typed<QG_F16, __half>(c, seq, pos, ntok, k_out, v_out, err, s);
+  if (c.type == QG_Q4_1)
+    return yt == QG_F32 ? read_typed<QG_Q4_1, float>(c, seq, pos, ntok, k_out, v_out, err, s)
+                        : read_typed<QG_Q4_1, __half>(c, seq, pos, ntok, k_out, v_out, err, s);
   return yt == QG_F32 ? read_typed<QG_Q8_0, float>(c, seq, pos, ntok, k_out, v_out, err, s)
                       : read_typed<QG_Q8_0, __half>(c, seq, pos, ntok, k_out, v_out, err, s);
 }

@@ -15,7 +15,8 @@
 // sincospif.
 //
 // Q8_0: the 32 elements of a block are on four neighbouring lanes, so the
-// block's largest magnitude is two shuffles away.
+// block's largest magnitude is two shuffles away. Q4_1: so are its smallest and
+// largest element, and a lane's eight are one word.
 //
 // Bound by memory: 4 bytes read and 2 (f16) or 17/16 (Q8_0) written an element.
 // qrope, 8,191 tokens of 40 heads of 128, f32 to f16: 40.1 us, 6.3 TB/s. qkv_append,
@@ -110,6 +111,12 @@ __device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
 __device__ __forceinline__ float max_nan(float a, float b) {
   float d;
   asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
+__device__ __forceinline__ float min_nan(float a, float b) {
+  float d;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
   return d;
 }
 
@@ -351,12 +358,80 @@ struct AppendParams {
 template <int TYPE>
 struct Spot {
   int at, scale_at;  // bytes; scale_at < 0: another lane writes it
-  __device__ __forceinline__ Spot(int d0, int d, int i) {
+  __device__ __forceinline__ Spot(int d0, int d, int i, bool is_v) {
     const int blk = d0 >> 5;
-    at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 2 : 1);
-    scale_at = (d0 & 31) == 0 ? KV_GROUP * d + 2 * (blk * KV_GROUP + kv_scale_place(i)) : -1;
+    at = (blk * (KV_GROUP * 32) + i * 32 + (d0 & 31)) * (TYPE == QG_F16 ? 4 : TYPE == QG_Q8_0 ? 2 : 1) / 2;
+    scale_at = d0 & 31 ? -1
+               : TYPE == QG_Q4_1 ? 8 * d + 2 * kv_q4_place(is_v, d, blk, i)
+                                 : KV_GROUP * d + 2 * (blk * KV_GROUP + kv_scale_place(i));
   }
 };
+
+// Q4_1. m is the largest f16 not above the block's smallest element, d the smallest f16 h with 15 h >= r, r = largest - m
+// (f32): as for Q8_0, r times a little more than 1/15, rounded up, is h or the f16 behind it, and 15 h is exact. The quant
+// is the integer nearest to (x - m) / d, two f32 operations; by an approximate reciprocal it is off by less than 15 * 1.5
+// 2^-23 = 2.7e-6, and only next to a half is the division needed.
+__device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot, int d, const float (&y)[8]) {
+  float lo = y[0], hi = y[0];  // an infinity or a NaN stays one
+#pragma unroll
+  for (int e = 1; e < 8; ++e) {
+    lo = min_nan(lo, y[e]);
+    hi = max_nan(hi, y[e]);
+  }
+#pragma unroll
+  for (int x = 1; x <= 2; ++x) {
+    lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, x));
+    hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, x));
+  }
+  const bool bad = !(fabsf(lo) <= 3.402823466e38f) || !(fabsf(hi) <= 3.402823466e38f);
+  uint32_t m_bits = __half_as_ushort(__float2half_rd(lo));
+  bool clamp = m_bits == 0xFC00;
+  if (clamp) m_bits = 0xFBFF;
+  const float m = __half2float(__ushort_as_half((uint16_t)m_bits)), r = fmaxf(hi - m, 0.f);  // (below 0 where m is -65504 and x far below)
+  uint32_t bits = __half_as_ushort(__float2half_ru(r * 0x1.111112p-4f));
+  if (bits == 0 && r > 0.f) bits = 1;
+  if (bits && 15.f * __half2float(__ushort_as_half((uint16_t)(bits - 1))) >= r) --bits;
+  if (bits > 0x7BFF) {
+    bits = 0x7BFF;
+    clamp = true;
+  }
+  uint32_t w = 0;
+  if (!bad && bits != 0) {
+    const float ds = __half2float(__ushort_as_half((uint16_t)bits)), magic = 12582912.f;
+    float inv;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ds));
+    float b[8], off = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; e += 2) {
+      const float2 q = mul2(sub2(make_float2(y[e], y[e + 1]), make_float2(m, m)), make_float2(inv, inv));
+      const float2 n = sub2(q, make_float2(-magic, -magic));
+      const float2 x = sub2(q, sub2(n, make_float2(magic, magic)));
+      off = fmaxf(off, fmaxf(fabsf(x.x), fabsf(x.y)));
+      b[e] = n.x;
+      b[e + 1] = n.y;
+    }
+    if (off > 0.49999f || clamp)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) b[e] = fminf(fmaxf(__fdiv_rn(y[e] - m, ds), 0.f), 15.f) + magic;
+    uint32_t n[2];
+#pragma unroll
+    for (int h = 0; h < 2; ++h)  // bytes: elements 0, 2, 1, 3 of each four
+      n[h] = __byte_perm(__byte_perm(__float_as_uint(b[4 * h]), __float_as_uint(b[4 * h + 2]), 0x0040),
+                         __byte_perm(__float_as_uint(b[4 * h + 1]), __float_as_uint(b[4 * h + 3]), 0x0040), 0x5410);
+    w = n[0] | n[1] << 4;
+  }
+  if (bad) {
+    bits = 0x7FFF;
+    m_bits = 0;
+  }
+  if (half) {
+    *reinterpret_cast<uint32_t*>(half + spot.at) = w;
+    if (spot.scale_at >= 0) {
+      *reinterpret_cast<uint16_t*>(half + spot.scale_at) = (uint16_t)bits;
+      *reinterpret_cast<uint16_t*>(half + spot.scale_at + d) = (uint16_t)m_bits;
+    }
+  }
+}
 
 // Eight elements of a row into its half record (NULL: nowhere; the lanes of a block call together).
 //
@@ -367,8 +442,10 @@ struct Spot {
 // (With two IEEE divisions a block, a clamp and a test an element, key and value rows took most of the kernel's issue
 // slots: a prompt of 16,382 tokens, appended and read back, 142 us instead of 135.)
 template <int TYPE>
-__device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, float (&y)[8]) {
-  if constexpr (TYPE == QG_F16) {
+__device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, int d, float (&y)[8]) {
+  if constexpr (TYPE == QG_Q4_1) {
+    put8_q4(half, spot, d, y);
+  } else if constexpr (TYPE == QG_F16) {
     if (half) store8(reinterpret_cast<__half*>(half + spot.at), y);
   } else {
     float top = fabsf(y[0]);  // an infinity or a NaN stays one
@@ -473,7 +550,7 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     }
   }
   const Turn<LAYOUT> t(plan, my_sc, d0);
-  const Spot<TYPE> spot(d0, d, in_group);
+  const Spot<TYPE> spot(d0, d, in_group, false);
   const uint32_t head_bytes = groups * rec;
   const int kv = a.c.n_kv_heads;
   const T* const kr = a.k + tok * a.ks;
@@ -484,14 +561,15 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
       load8(kr + r * d + d0, x);
       t.apply(plan, kr + r * d, d0, x, y);
     }
-    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes : nullptr, spot, y);
+    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes : nullptr, spot, d, y);
   }
+  const Spot<TYPE> v_spot(d0, d, in_group, true);
   const T* const vr = a.v + tok * a.vs + d0;
   for (n -= kg; n < kg; n += all_parts) {
     const int r = n * at_once + first;
     float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (r < kv) load8(vr + r * d, y);
-    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes + kv_half_bytes(TYPE, d) : nullptr, spot, y);
+    put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes + kv_half_bytes(TYPE, d) : nullptr, v_spot, d, y);
   }
 }
 
@@ -549,6 +627,8 @@ cudaError_t rope_launch(const qg_rope& plan, int xt, const void* x, int64_t xs, 
 }
 
 cudaError_t kv_append_launch(const KvAppendArgs& a, cudaStream_t s) {
+  if (a.c.type == QG_Q4_1)
+    return a.xt == QG_F32 ? append_typed<float, QG_Q4_1>(a, s) : append_typed<__half, QG_Q4_1>(a, s);
   if (a.xt == QG_F32)
     return a.c.type == QG_F16 ? append_typed<float, QG_F16>(a, s) : append_typed<float, QG_Q8_0>(a, s);
   return a.c.type == QG_F16 ? append_typed<__half, QG_F16>(a, s) : append_typed<__half, QG_Q8_0>(a, s);

@@ -80,8 +80,8 @@ typedef enum {
 } qg_status;
 
 /* GGUF type ids. Weights are Q4_0 or Q8_0; F32 and F16 are element types of the
- * rotary and cache calls, F16 and Q8_0 the types of a key/value cache. */
-typedef enum { QG_F32 = 0, QG_F16 = 1, QG_Q4_0 = 2, QG_Q8_0 = 8 } qg_type;
+ * rotary and cache calls, F16, Q8_0 and Q4_1 the types of a key/value cache. */
+typedef enum { QG_F32 = 0, QG_F16 = 1, QG_Q4_0 = 2, QG_Q4_1 = 3, QG_Q8_0 = 8 } qg_type;
 
 /* Static, NUL-terminated description of a status code. */
 const char *qg_status_str(qg_status s);
@@ -319,7 +319,7 @@ qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride
 
 /* ---------------------------------------------------------------------------
  * Paged key/value cache ("Architecture", section "Memory and caching": the KV
- * cache is f16 or int8). A pool of pages of page_size tokens; a page holds the
+ * cache is f16 or int8; here 4 bits, too). A pool of pages of page_size tokens; a page holds the
  * keys and values of all n_kv_heads heads of one layer. page_table[s][j] is the
  * pool index of the page with tokens j * page_size ... of sequence s.
  *
@@ -330,11 +330,21 @@ qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride
  *   QG_Q8_0 half: [D/32][16 tokens][32] quants, stored as q + 128 (unsigned),
  *           then f16 scales [D/32][16], token i of the group at place
  *           4 * (i mod 4) + i / 4                               (17 D bytes)
+ *   QG_Q4_1 half: [D/32][16 tokens][16] bytes of quants: byte 4 w + b of a block
+ *           holds element 8 w + {0, 2, 1, 3}[b] in its low 4 bits and the element 4
+ *           behind that in its high ones; then f16 d, then f16 m, 16 D/32 each: of
+ *           keys [16 tokens][D/32], of values [D/32][16], token i of the group at
+ *           place 4 * (i mod 8 / 2) + i mod 2 + 2 * (i / 8)     (10 D bytes)
  * Q8_0 blocks (32 elements of one token's head, value q * d): d is
  * max |x| / 127 rounded up to f16 (at most 65504), q the integer nearest to
  * x / d (ties to even, within +-127). A block with a NaN or an infinity gets
  * d = NaN, so that it is not silently lost.
- *   type       : QG_F16 or QG_Q8_0 (QG_ERR_TYPE)
+ * Q4_1 blocks (the same 32 elements, value q * d + m): m is the largest f16 not
+ * above min x (at least -65504), d the smallest f16 >= 0 with 15 d >= max x - m (at
+ * most 65504; the difference in f32), q the integer nearest to (x - m) / d (f32
+ * operations, ties to even, within 0..15; 0 where d is 0). A block with a NaN or an
+ * infinity gets d = NaN.
+ *   type       : QG_F16, QG_Q8_0 or QG_Q4_1 (QG_ERR_TYPE)
  *   n_kv_heads : 1..256; head_dim: 64, 128 or 256; page_size: 16, 32, 64, 128
  *                or 256; n_pages >= 1; n_seq: 1..1024; max_pages >= 1, with
  *                max_pages * page_size < 2^31 (QG_ERR_SHAPE)
@@ -391,7 +401,7 @@ qg_status qkv_append(const qg_kvcache *cache, const qg_rope *rope, qg_type xt, c
                      const int32_t *pos, int ntok, int32_t *err_flag, cudaStream_t stream);
 
 /* Read tokens back: k_out, v_out [ntok][n_kv_heads][head_dim] of type yt
- * (QG_F16 or QG_F32; f16 rounds q * d once). Keys come as stored (rotated).
+ * (QG_F16 or QG_F32; f16 rounds q * d once, both round q * d + m once). Keys come as stored (rotated).
  * seq, pos as in qkv_append; padding and skipped tokens give zeros. k_out and
  * v_out may each be NULL (not wanted), 16-byte aligned. */
 qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *pos, int ntok,
@@ -424,7 +434,8 @@ qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *p
  * Scores, softmax sums and the weighted sum are f32; a weight (times the
  * block's scale for Q8_0) is rounded to f16 before it meets its value: by at
  * most 2^-11 of itself, or 2^-30 of the largest weight (times the largest
- * scale). y is rounded to f16 once. Results are the same from run to run. The
+ * scale). For Q4_1 it is rounded before it meets the block's m, and again when it
+ * has been multiplied by the block's d. y is rounded to f16 once. Results are the same from run to run. The
  * order of the sums depends on lens, window and the sizes, max_pages among
  * them: a column of a wider call need not equal the one-column call bit for
  * bit, nor a call over a wider page table the same call over a narrow one.
