@@ -23,7 +23,8 @@ LIB_PATH = os.path.join(_HERE, "libqgemm.so")
 
 EXPORTS = ("qg_status_str", "qgemv_q4_0", "qgemv_q8_0", "qgemm_cols", "qffn_gate_up_silu",
            "qmoe_workspace_bytes", "qmoe_experts", "qmoe_experts_noalloc", "qrepack",
-           "qargmax_f32", "qtopk_f32", "qmoe_router", "qrope_plan", "qrope",
+           "qargmax_f32", "qtopk_f32", "qmoe_router", "qroute_plan", "qmoe_route", "qmoe_router_planned",
+           "qembed", "qrms_norm", "qrope_plan", "qrope",
            "qkv_page_bytes", "qkv_append", "qkv_read", "qattn_workspace_bytes", "qattn_paged",
            "qg_kernel_launches", "qg_device_error",
            "qg_wait_selftest", "qg_last_cuda_error", "qg_last_cuda_error_string")
@@ -56,6 +57,12 @@ class QGRope(C.Structure):
                 ("reserved", C.c_int32), ("step", C.c_uint64 * 128)]
 
 
+class QGRoute(C.Structure):
+    """A routing plan (host memory), filled by qroute_plan."""
+    _fields_ = [("score", C.c_int32), ("n_group", C.c_int32), ("top_group", C.c_int32), ("group_top", C.c_int32),
+                ("renorm", C.c_int32), ("scale", C.c_float)]
+
+
 class QGKVCache(C.Structure):
     """A paged key/value cache: device pointers and sizes (made by qkv_cache)."""
     _fields_ = [("pool", C.c_void_p), ("page_table", C.c_void_p), ("type", C.c_int32),
@@ -65,6 +72,10 @@ class QGKVCache(C.Structure):
 
 # bits of the cache calls' error flag (include/qgemm.h)
 QG_KV_BAD_SEQ, QG_KV_BAD_POS, QG_KV_BAD_PAGE = 1, 2, 4
+# and of qembed's
+QG_EMBED_BAD_ID = 1
+# scores of a routing plan
+QG_SCORE_SOFTMAX, QG_SCORE_SIGMOID = 0, 1
 
 _lib = None
 
@@ -98,6 +109,12 @@ def load(path: str | None = None):
     L.qmoe_router.argtypes = [vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
     i64, f64 = C.c_int64, C.c_double
     rope, cache = C.POINTER(QGRope), C.POINTER(QGKVCache)
+    route = C.POINTER(QGRoute)
+    L.qroute_plan.argtypes = [route, i32, i32, i32, i32, i32, f64]
+    L.qmoe_route.argtypes = [route, vp, i64, vp, i32, i32, i32, vp, vp, vp]
+    L.qmoe_router_planned.argtypes = [route, vp, vp, vp, i32, i32, i32, i32, vp, vp, vp, vp]
+    L.qembed.argtypes = [i32, vp, vp, i32, i32, vp, i32, C.c_float, i32, vp, i64, vp, vp]
+    L.qrms_norm.argtypes = [i32, vp, i64, vp, i64, vp, i64, vp, C.c_float, C.c_float, i32, i32, i32, i32, vp, i64, vp, vp]
     L.qrope_plan.argtypes = [rope, i32, i32, f64, f64, i32, f64, f64, f64]
     L.qrope.argtypes = [rope, i32, vp, i64, vp, i32, i32, i32, i32, vp, i64, vp]
     L.qkv_page_bytes.argtypes = [i32, i32, i32, i32]
@@ -328,6 +345,124 @@ def _int32s(t, name, n):
 
 def _flag(t):
     return None if t is None else _int32s(t, "err_flag", 1)
+
+
+_SCORES = {"softmax": QG_SCORE_SOFTMAX, "sigmoid": QG_SCORE_SIGMOID}
+
+
+def qroute_plan(score="softmax", n_group=1, top_group=1, group_top=1, renorm=True, scale=1.0) -> QGRoute:
+    """A routing plan: softmax or sigmoid scores, the experts in n_group groups of which the top_group with the
+    largest sums of their group_top (1 or 2) best stay, weights renormalised over the chosen and scaled. Host
+    memory; keep it and pass it to any number of calls."""
+    if score not in _SCORES:
+        raise ValueError(f"score: 'softmax' or 'sigmoid' expected, got {score!r}")
+    plan = QGRoute()
+    _check("qroute_plan", load().qroute_plan(C.byref(plan), _SCORES[score], n_group, top_group, group_top, int(renorm),
+                                             scale))
+    return plan
+
+
+def _floats(t, name, n):
+    """Address of n contiguous float32, None for None."""
+    if t is None:
+        return None
+    if _ELEM is None:
+        _dtypes()
+    if _ELEM.get(t.dtype) != QG_F32 or t.numel() != n or not t.is_contiguous():
+        raise ValueError(f"{name}: {n} contiguous float32 expected, got {t.dtype} {tuple(t.shape)}")
+    return t.data_ptr()
+
+
+def qmoe_route(plan, logits, topk, ids_out, rw_out, bias=None, stream=None):
+    """Experts of each row of f32 logits [ntok, n_expert] (any row stride) by a plan, with an f32 bias [n_expert]
+    added to the scores for the choice: ids_out int32, rw_out f32 [ntok, topk]."""
+    if _ELEM is None:
+        _dtypes()
+    ntok, e = logits.shape
+    if _ELEM.get(logits.dtype) != QG_F32 or (e > 1 and logits.stride(1) != 1):
+        raise ValueError(f"logits: float32 rows expected, got {logits.dtype} with strides {logits.stride()}")
+    n = ntok * topk
+    st = (_lib or load()).qmoe_route(plan, logits.data_ptr(), logits.stride(0), _floats(bias, "bias", e), ntok, e, topk,
+                                     _int32s(ids_out, "ids_out", n), _floats(rw_out, "rw_out", n), _stream(stream))
+    if st:
+        _check("qmoe_route", st)
+
+
+def qmoe_router_planned(plan, w_router, x, topk, ids_out, rw_out, bias=None, logits_out=None, stream=None):
+    """qmoe_router by a plan: w_router f32 [n_expert, hidden], x f16 [ncols, hidden] (1..16 columns) -> ids_out
+    int32, rw_out f32 [ncols, topk], logits_out None or f32 [ncols, n_expert]."""
+    e, hidden = w_router.shape
+    ncols = x.shape[0]
+    wr = _floats(w_router, "w_router", e * hidden)  # (sets the dtypes up)
+    n = ncols * topk
+    st = (_lib or load()).qmoe_router_planned(plan, wr, _dense(x, "x", _FLOAT16, (ncols, hidden)), _floats(bias, "bias", e),
+                                              e, hidden, ncols, topk, _floats(logits_out, "logits_out", ncols * e),
+                                              _int32s(ids_out, "ids_out", n), _floats(rw_out, "rw_out", n),
+                                              _stream(stream))
+    if st:
+        _check("qmoe_router_planned", st)
+
+
+def qembed(qtype, q, scl, ids, y, scale=1.0, err_flag=None, stream=None):
+    """y[t] = scale * W[ids[t]]: W Q4_0 or Q8_0 (q, scl as in qgemv_*) or QG_F16 (q f16 [rows, k], scl None), ids
+    int32 [ntok], y f32 or f16 [ntok, k] (any row stride)."""
+    if _ELEM is None:
+        _dtypes()
+    rows, k = q.shape
+    if qtype == Q4_0:
+        k *= 2
+    nbytes = rows * k // 2 if qtype == Q4_0 else rows * k * (2 if qtype == QG_F16 else 1)
+    if not q.is_contiguous() or q.nbytes != nbytes or (qtype == QG_F16 and q.dtype != _FLOAT16):
+        raise ValueError(f"q: contiguous rows of type {qtype} expected, got {q.dtype} {tuple(q.shape)}")
+    if scl is not None and (not scl.is_contiguous() or scl.nbytes != rows * (k // 32) * 2):
+        raise ValueError(f"scl: {rows} x {k // 32} contiguous f16 bits expected, got {scl.dtype} {tuple(scl.shape)}")
+    ntok = ids.numel()
+    kind = _elem(y, "y")
+    if y.shape != (ntok, k) or (k > 1 and y.stride(1) != 1):
+        raise ValueError(f"y: {ntok} rows of {k} expected, got {tuple(y.shape)} with strides {y.stride()}")
+    st = (_lib or load()).qembed(int(qtype), q.data_ptr(), _ptr(scl), rows, k, _int32s(ids, "ids", ntok), ntok, scale, kind,
+                                 y.data_ptr(), y.stride(0), _flag(err_flag), _stream(stream))
+    if st:
+        _check("qembed", st)
+
+
+def _vectors(t, shape, name):
+    """Token stride of a tensor [ntok, n] or [ntok, heads, n] whose vectors of a token are neighbours."""
+    if len(shape) == 3:
+        return _rows(t, shape, name)
+    if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name}: rows of shape {tuple(shape)} expected, got {tuple(t.shape)} with strides {t.stride()}")
+    return t.stride(0)
+
+
+def qrms_norm(x, w, y, eps=1e-6, add=None, sum_out=None, w_add=0.0, y_scl=None, stream=None):
+    """Root-mean-square norm of x [ntok, n] or [ntok, heads, n] (f32 or f16, any token stride), plus add (as x; the
+    sum goes to sum_out, which may be x or add), times w + w_add (w f32 [n] or None). y f32 or f16 as x (it may be
+    x), or with y_scl Q8_0 rows: y int8 and y_scl f16 [ntok(, heads), n / 32], contiguous."""
+    if _ELEM is None:
+        _dtypes()
+    shape, kind = x.shape, _elem(x, "x")
+    if len(shape) not in (2, 3):
+        raise ValueError(f"x: [ntok, n] or [ntok, heads, n] expected, got {tuple(shape)}")
+    ntok, n = shape[0], shape[-1]
+    heads = shape[1] if len(shape) == 3 else 1
+    for t, name in ((add, "add"), (sum_out, "sum_out")):
+        if t is not None and t.dtype != x.dtype:
+            raise ValueError(f"{name}: {x.dtype} expected, as x, got {t.dtype}")
+    if y_scl is None:
+        yt, ys = _elem(y, "y"), _vectors(y, shape, "y")
+    else:
+        yt, ys = Q8_0, 0
+        if y.shape != shape or y.element_size() != 1 or not y.is_contiguous():
+            raise ValueError(f"y: contiguous int8 {tuple(shape)} expected, got {y.dtype} {tuple(y.shape)}")
+        if y_scl.element_size() != 2 or y_scl.numel() != ntok * heads * (n // 32) or not y_scl.is_contiguous():
+            raise ValueError(f"y_scl: {ntok * heads} x {n // 32} contiguous f16 expected, got {y_scl.dtype} {tuple(y_scl.shape)}")
+    st = (_lib or load()).qrms_norm(kind, x.data_ptr(), _vectors(x, shape, "x"), _ptr(add),
+                                    0 if add is None else _vectors(add, shape, "add"), _ptr(sum_out),
+                                    0 if sum_out is None else _vectors(sum_out, shape, "sum_out"), _floats(w, "w", n), w_add,
+                                    eps, ntok, heads, n, yt, y.data_ptr(), ys, _ptr(y_scl), _stream(stream))
+    if st:
+        _check("qrms_norm", st)
 
 
 def qrope_plan(rot_dim, base=10000.0, interleaved=False, factor=1.0, orig_ctx=0, low_turns=1.0,

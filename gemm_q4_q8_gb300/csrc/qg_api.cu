@@ -6,6 +6,7 @@
 
 #include <atomic>
 #include <cmath>
+#include <initializer_list>
 #include <map>
 #include <mutex>
 #include <tuple>
@@ -158,6 +159,14 @@ bool rows_ok(int ntok, int64_t row, int64_t stride) {
 }
 size_t rows_bytes(int ntok, int64_t row, int64_t stride, int t) {
   return ((size_t)(ntok - 1) * (ntok > 1 ? stride : 0) + row) * (t == QG_F32 ? 4 : 2);
+}
+struct Range { const void* p; size_t n; };
+// Whether one of a routing's two outputs, of n bytes each, overlaps the other or an input that is there.
+bool routing_overlaps(const void* ids, const void* rw, size_t n, std::initializer_list<Range> in) {
+  if (overlaps(ids, n, rw, n)) return true;
+  for (const Range& i : in)
+    if (i.p && i.n && (overlaps(ids, n, i.p, i.n) || overlaps(rw, n, i.p, i.n))) return true;
+  return false;
 }
 bool plan_ok(const qg_rope* p) {
   return p->rot_dim >= 2 && p->rot_dim <= QG_ROPE_MAX_DIM && (p->rot_dim & 1) == 0;
@@ -346,6 +355,141 @@ qg_status qmoe_router(const float* w_router, const uint16_t* x, int n_expert, in
                                      ids_out, rw_out, stream));
 }
 
+qg_status qroute_plan(qg_route* plan, int score, int n_group, int top_group, int group_top,
+                      int renorm, double scale) {
+  if (!plan) return QG_ERR_NULL;
+  qg_route r{};
+  r.score = score;
+  r.n_group = n_group;
+  r.top_group = top_group;
+  r.group_top = group_top;
+  r.renorm = renorm != 0;
+  r.scale = (float)scale;
+  if (!qg::route_plan_ok(r)) return QG_ERR_SHAPE;
+  *plan = r;
+  return QG_OK;
+}
+
+qg_status qmoe_route(const qg_route* plan, const float* logits, int64_t stride, const float* bias,
+                     int ntok, int n_expert, int topk, int32_t* ids_out, float* rw_out,
+                     cudaStream_t stream) {
+  if (!plan) return QG_ERR_NULL;
+  if (!qg::route_plan_ok(*plan) || !qg::route_shape_ok(*plan, n_expert, topk) || ntok < 0 ||
+      !rows_ok(ntok, n_expert, stride))
+    return QG_ERR_SHAPE;
+  if (ntok == 0) return QG_OK;
+  if (!logits || !ids_out || !rw_out) return QG_ERR_NULL;
+  if (!aligned(logits, 4) || !aligned(bias, 4) || !aligned(ids_out, 4) || !aligned(rw_out, 4)) return QG_ERR_ALIGN;
+  const size_t in = rows_bytes(ntok, n_expert, stride, QG_F32), out = (size_t)ntok * topk * 4;
+  if (routing_overlaps(ids_out, rw_out, out, {{logits, in}, {bias, (size_t)n_expert * 4}})) return QG_ERR_ALIAS;
+  qg_status st = check_device();
+  if (st != QG_OK) return st;
+  return from_cuda(qg::route_launch(*plan, logits, stride, bias, ntok, n_expert, topk, ids_out, rw_out, stream));
+}
+
+qg_status qmoe_router_planned(const qg_route* plan, const float* w_router, const uint16_t* x,
+                              const float* bias, int n_expert, int hidden, int ncols, int topk,
+                              float* logits_out, int32_t* ids_out, float* rw_out,
+                              cudaStream_t stream) {
+  if (!plan) return QG_ERR_NULL;
+  if (!qg::route_plan_ok(*plan) || !qg::router_shape_ok(n_expert, hidden, ncols, topk) ||
+      !qg::route_shape_ok(*plan, n_expert, topk))
+    return QG_ERR_SHAPE;
+  if (!w_router || !x || !ids_out || !rw_out) return QG_ERR_NULL;
+  if (!aligned(w_router, 16) || !aligned(x, 2) || !aligned(bias, 4) || !aligned(ids_out, 4) || !aligned(rw_out, 4) ||
+      !aligned(logits_out, 4))
+    return QG_ERR_ALIGN;
+  const size_t out = (size_t)ncols * topk * 4, nl = logits_out ? (size_t)ncols * n_expert * 4 : 0;
+  const Range w{w_router, (size_t)n_expert * hidden * 4}, xs{x, (size_t)ncols * hidden * 2}, b{bias, (size_t)n_expert * 4};
+  if (routing_overlaps(ids_out, rw_out, out, {w, xs, b, {logits_out, nl}})) return QG_ERR_ALIAS;
+  for (const Range& i : {w, xs, b})
+    if (logits_out && i.p && overlaps(logits_out, nl, i.p, i.n)) return QG_ERR_ALIAS;
+  qg_status st = check_device();
+  if (st != QG_OK) return st;
+  return from_cuda(qg::router_planned_launch(*plan, w_router, x, bias, n_expert, hidden, ncols, topk, logits_out, ids_out,
+                                             rw_out, stream));
+}
+
+qg_status qembed(qg_type t, const void* q, const uint16_t* scl, int rows, int k, const int32_t* ids,
+                 int ntok, float scale, qg_type yt, void* y, int64_t y_stride, int32_t* err_flag,
+                 cudaStream_t stream) {
+  if ((!valid_type((int)t) && t != QG_F16) || !float_type((int)yt)) return QG_ERR_TYPE;
+  if (rows < 1 || k <= 0 || (k % 32) || ntok < 0 || !std::isfinite(scale) || !rows_ok(ntok, k, y_stride)) return QG_ERR_SHAPE;
+  if (ntok == 0) return QG_OK;
+  if (!q || (t != QG_F16 && !scl) || !ids || !y) return QG_ERR_NULL;
+  if (!aligned(q, 16) || !aligned(scl, 16) || !aligned(y, 16) || !aligned(ids, 4) || !aligned(err_flag, 4) ||
+      (ntok > 1 && y_stride % 8))
+    return QG_ERR_ALIGN;
+  const size_t nq = (size_t)rows * k * (t == QG_F16 ? 4 : t == QG_Q8_0 ? 2 : 1) / 2, ny = rows_bytes(ntok, k, y_stride, (int)yt);
+  const Range in[] = {{q, nq}, {t == QG_F16 ? nullptr : scl, (size_t)rows * (k / 32) * 2}, {ids, (size_t)ntok * 4}};
+  for (const Range& i : in)
+    if (i.p && overlaps(y, ny, i.p, i.n)) return QG_ERR_ALIAS;
+  qg_status st = check_device();
+  if (st != QG_OK) return st;
+  qg::EmbedArgs a{};
+  a.qt = (int)t; a.yt = (int)yt;
+  a.q = q; a.scl = scl;
+  a.rows = rows; a.k = k;
+  a.ids = ids; a.ntok = ntok;
+  a.scale = scale;
+  a.y = y; a.ys = y_stride;
+  a.err = err_flag;
+  return from_cuda(qg::embed_launch(a, stream));
+}
+
+qg_status qrms_norm(qg_type xt, const void* x, int64_t x_stride, const void* add, int64_t add_stride,
+                    void* sum, int64_t sum_stride, const float* w, float w_add, float eps, int ntok,
+                    int n_heads, int n, qg_type yt, void* y, int64_t y_stride, uint16_t* y_scl,
+                    cudaStream_t stream) {
+  const bool q8 = yt == QG_Q8_0;
+  if (!float_type((int)xt) || (!float_type((int)yt) && !q8)) return QG_ERR_TYPE;
+  if (ntok < 0 || n_heads < 1 || n < 1 || n > QG_NORM_MAX || (q8 && n % 32) || !std::isfinite(w_add) || !std::isfinite(eps) ||
+      eps < 0.f || (int64_t)ntok * n_heads >= ((int64_t)1 << 31))
+    return QG_ERR_SHAPE;
+  if (ntok == 0) return QG_OK;
+  const int64_t row = (int64_t)n_heads * n;
+  if (!rows_ok(ntok, row, x_stride) || (add && !rows_ok(ntok, row, add_stride)) || (sum && !rows_ok(ntok, row, sum_stride)) ||
+      (!q8 && !rows_ok(ntok, row, y_stride)))
+    return QG_ERR_SHAPE;
+  if (!x || !y || (q8 && !y_scl)) return QG_ERR_NULL;
+  const uintptr_t el = xt == QG_F32 ? 4 : 2, yl = q8 ? 16 : yt == QG_F32 ? 4 : 2;
+  if (!aligned(x, el) || !aligned(add, el) || !aligned(sum, el) || !aligned(w, 4) || !aligned(y, yl) || (q8 && !aligned(y_scl, 16)))
+    return QG_ERR_ALIGN;
+  // (a stride that is not used is taken for a whole number of 16 bytes)
+  auto wide = [&](const void* p, int64_t stride) { return !p || (aligned(p, 16) && (ntok == 1 || stride % 8 == 0)); };
+  const bool vec = n % 8 == 0 && wide(x, x_stride) && wide(add, add_stride) && wide(sum, sum_stride) && (q8 || wide(y, y_stride)) &&
+                   aligned(w, 16);
+  if (q8 && !vec) return QG_ERR_ALIGN;
+  struct Rows { const void* p; size_t n; int64_t stride; int t; };
+  auto rows_of = [&](const void* p, int64_t stride, int t) {
+    return Rows{p, p ? rows_bytes(ntok, row, stride, t) : 0, ntok == 1 ? row : stride, t};
+  };
+  const Rows in[] = {rows_of(x, x_stride, (int)xt), rows_of(add, add_stride, (int)xt)};
+  const Rows s = rows_of(sum, sum_stride, (int)xt);
+  const Rows o = q8 ? Rows{y, (size_t)ntok * row, -1, (int)yt} : rows_of(y, y_stride, (int)yt);
+  const Range scales{q8 ? y_scl : nullptr, q8 ? (size_t)ntok * row / 16 : 0}, ws{w, (size_t)n * 4};
+  auto clash = [&](const Rows& out, const Rows& a) {
+    return out.p && a.p && overlaps(out.p, out.n, a.p, a.n) && !(out.p == a.p && out.stride == a.stride && out.t == a.t);
+  };
+  for (const Rows& i : in)
+    if (clash(s, i) || clash(o, i) || (scales.p && i.p && overlaps(scales.p, scales.n, i.p, i.n))) return QG_ERR_ALIAS;
+  if (s.p && overlaps(s.p, s.n, o.p, o.n)) return QG_ERR_ALIAS;
+  if (scales.p && (overlaps(scales.p, scales.n, o.p, o.n) || (s.p && overlaps(scales.p, scales.n, s.p, s.n)))) return QG_ERR_ALIAS;
+  if (w && (overlaps(w, ws.n, o.p, o.n) || (s.p && overlaps(w, ws.n, s.p, s.n)) || (scales.p && overlaps(w, ws.n, scales.p, scales.n))))
+    return QG_ERR_ALIAS;
+  qg_status st = check_device();
+  if (st != QG_OK) return st;
+  qg::NormArgs a{};
+  a.xt = (int)xt; a.yt = (int)yt;
+  a.x = x; a.add = add; a.sum = sum;
+  a.w = w; a.y = y; a.scl = y_scl;
+  a.xs = x_stride; a.as = add_stride; a.ss = sum_stride; a.ys = y_stride;
+  a.w_add = w_add; a.eps = eps;
+  a.ntok = ntok; a.heads = n_heads; a.n = n;
+  a.vec = vec;
+  return from_cuda(qg::norm_launch(a, stream));
+}
+
 qg_status qargmax_f32(const float* x, int n, int ncols, int32_t* idx_out, float* val_out,
                       cudaStream_t stream) {
   if (n < 1 || ncols < 1 || ncols > 64) return QG_ERR_SHAPE;
@@ -463,7 +607,6 @@ qg_status qkv_append(const qg_kvcache* cache, const qg_rope* rope, qg_type xt, c
       (ntok > 1 && (k_stride % 8 || v_stride % 8 || (q && q_stride % 8))))
     return QG_ERR_ALIGN;
   // what is written (q_out, the pool) must not be read: queries, keys, values, positions, table
-  struct Range { const void* p; size_t n; };
   const Range in[] = {{k, rows_bytes(ntok, row, k_stride, (int)xt)},
                       {v, rows_bytes(ntok, row, v_stride, (int)xt)},
                       {q, q ? rows_bytes(ntok, qrow, q_stride, (int)xt) : 0},
@@ -537,7 +680,6 @@ qg_status qattn_paged(const qg_kvcache* cache, const uint16_t* q, int n_heads, i
   const size_t pool = (size_t)cache->n_pages *
                       qg::kv_page_bytes(cache->type, cache->n_kv_heads, cache->head_dim, cache->page_size);
   const size_t nl = (size_t)cache->n_seq * 4, table = nl * cache->max_pages;
-  struct Range { const void* p; size_t n; };
   const Range in[] = {{q, nq}, {lens, nl}, {cache->pool, pool}, {cache->page_table, table}};
   if (overlaps(ws, need, y, nq)) return QG_ERR_ALIAS;
   for (const Range& r : in)

@@ -142,6 +142,42 @@ bool router_shape_ok(int E, int hidden, int ncols, int topk);
 cudaError_t router_launch(const float* w, const uint16_t* x, int E, int hidden, int ncols,
                           int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s);
 
+// Routing from logits (qg_route.cu), and the router with it in one launch (qg_router.cu).
+bool route_plan_ok(const qg_route& r);
+bool route_shape_ok(const qg_route& r, int E, int topk);  // of a plan that is ok
+cudaError_t route_launch(const qg_route& r, const float* logits, int64_t stride, const float* bias, int ntok, int E, int topk,
+                         int32_t* ids, float* rw, cudaStream_t s);
+cudaError_t router_planned_launch(const qg_route& r, const float* w, const uint16_t* x, const float* bias, int E, int hidden,
+                                  int ncols, int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s);
+
+// Root-mean-square norm (qg_norm.cu) and embedding lookup (qg_embed.cu). Arguments are those of the C calls, checked.
+struct NormArgs {
+  int xt, yt;
+  const void *x, *add;
+  void* sum;
+  const float* w;
+  void* y;
+  uint16_t* scl;
+  int64_t xs, as, ss, ys;
+  float w_add, eps;
+  int ntok, heads, n;
+  bool vec;  // every row begins at a multiple of 16 bytes
+};
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t s);
+struct EmbedArgs {
+  int qt, yt;
+  const void* q;
+  const uint16_t* scl;
+  int rows, k;
+  const int32_t* ids;
+  int ntok;
+  float scale;
+  void* y;
+  int64_t ys;
+  int32_t* err;
+};
+cudaError_t embed_launch(const EmbedArgs& a, cudaStream_t s);
+
 // Rotary positions (qg_rope.cu). Arguments are those of the C calls, checked.
 cudaError_t rope_launch(const qg_rope& plan, int xt, const void* x, int64_t xs, const int32_t* pos,
                         int ntok, int n_heads, int head_dim, int yt, void* y, int64_t ys,

@@ -1,0 +1,227 @@
+// qg_norm.cu -- root-mean-square norm of rows with the residual's addition (qrms_norm), to f32, f16 or Q8_0 rows.
+//
+// s = x + add (rounded to x's type where that is f16: the sum that is stored is the one that is normed),
+// y = s (w + w_add) / sqrt(mean s^2 + eps). A row stays in registers: its elements are read once, their squares summed in f32,
+// and normed where they are. Rows of up to 1,024 elements are a warp's (or 8 or 16 lanes' of one), longer ones a block's.
+//
+// Squares that leave the range of f32 (elements beyond 10^18, or all below 10^-17 with an eps as small) are summed again in
+// 64 bits: a row that needs it shows by its sum.
+//
+// Bound by memory.
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "qg_blocks.cuh"
+#include "qg_common.cuh"
+#include "qg_internal.h"
+
+namespace qg {
+
+namespace {
+
+constexpr int NM_WARP_THREADS = 128;
+
+template <class TI>
+struct NormParams {
+  const TI *x, *add;
+  TI* sum;
+  const float* w;
+  void* y;
+  uint16_t* scl;
+  int64_t xs, as, ss, ys;
+  float w_add, eps;
+  int heads, n;
+  int64_t rows;
+};
+
+template <class T>
+__device__ __forceinline__ float round_to(float v);
+template <>
+__device__ __forceinline__ float round_to<float>(float v) { return v; }
+template <>
+__device__ __forceinline__ float round_to<__half>(float v) { return __half2float(__float2half_rn(v)); }
+__device__ __forceinline__ float as_f32(float v) { return v; }
+__device__ __forceinline__ float as_f32(__half v) { return __half2float(v); }
+__device__ __forceinline__ void put(float* p, float v) { *p = v; }
+__device__ __forceinline__ void put(__half* p, float v) { *p = __float2half_rn(v); }
+
+// Sum over the group of a row: `lanes` lanes of a warp, or (BLOCK) all warps, in one order for everybody.
+template <bool BLOCK, class A>
+__device__ __forceinline__ A row_sum(A v, int lanes, A* part) {
+  for (int off = BLOCK ? 16 : lanes >> 1; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if constexpr (BLOCK) {
+    if ((threadIdx.x & 31) == 0) part[threadIdx.x >> 5] = v;
+    __syncthreads();
+    v = 0;
+    for (int i = 0; i < (int)(blockDim.x >> 5); ++i) v += part[i];
+  }
+  return v;
+}
+
+// YT: the type of y. VEC: rows in groups of eight elements, 16-byte aligned. U: such groups of a thread.
+template <class TI, int YT, bool VEC, int U, bool BLOCK>
+__global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(const __grid_constant__ NormParams<TI> p, int lanes) {
+  __shared__ float part[BLOCK ? 32 : 1];
+  __shared__ double part64[BLOCK ? 32 : 1];
+  pdl_trigger();
+  pdl_wait();
+  const int width = BLOCK ? blockDim.x : lanes;
+  const int t = BLOCK ? threadIdx.x : threadIdx.x & (lanes - 1);
+  const int64_t row = BLOCK ? blockIdx.x : (int64_t)blockIdx.x * (NM_WARP_THREADS / lanes) + threadIdx.x / lanes;
+  const bool live = BLOCK || row < p.rows;
+  const int64_t tok = live ? row / p.heads : 0, head = live ? row - tok * p.heads : 0;
+  const TI* const x = p.x + tok * p.xs + head * p.n;
+  const TI* const add = p.add ? p.add + tok * p.as + head * p.n : nullptr;
+  TI* const sum = p.sum ? p.sum + tok * p.ss + head * p.n : nullptr;
+  // element e of the thread's group c; ok: is it one
+  auto at = [&](int c, int e) { return VEC ? (c * width + t) * 8 + e : (c * 8 + e) * width + t; };
+  auto ok = [&](int i) { return live && i < p.n; };
+
+  float v[U][8];
+#pragma unroll
+  for (int c = 0; c < U; ++c) {
+    if constexpr (VEC) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = 0.f;
+      if (ok(at(c, 0))) load8(x + at(c, 0), v[c]);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = ok(at(c, e)) ? as_f32(x[at(c, e)]) : 0.f;
+    }
+  }
+  if (add) {
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+      float a[8];
+      if constexpr (VEC) {
+        if (!ok(at(c, 0))) continue;
+        load8(add + at(c, 0), a);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) a[e] = ok(at(c, e)) ? as_f32(add[at(c, e)]) : 0.f;
+      }
+#pragma unroll
+      for (int e = 0; e < 8; ++e) v[c][e] = round_to<TI>(v[c][e] + a[e]);
+    }
+  }
+  if (sum) {
+#pragma unroll
+    for (int c = 0; c < U; ++c) {
+      if constexpr (VEC) {
+        if (ok(at(c, 0))) store8(sum + at(c, 0), v[c]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (ok(at(c, e))) put(sum + at(c, e), v[c][e]);
+      }
+    }
+  }
+  float ss = 0.f;
+#pragma unroll
+  for (int c = 0; c < U; ++c)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) ss = fmaf(v[c][e], v[c][e], ss);
+  ss = row_sum<BLOCK>(ss, lanes, part);
+  const float mean = ss / (float)p.n + p.eps;
+  float r = 1.f / sqrtf(mean);
+  const bool wide = live && !(ss <= 0x1p120f && mean >= 0x1p-100f);  // (NaN, too)
+  if (__builtin_expect(BLOCK ? wide : __any_sync(0xffffffffu, wide), 0)) {
+    double s = 0;
+#pragma unroll
+    for (int c = 0; c < U; ++c)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s = fma((double)v[c][e], (double)v[c][e], s);
+    s = 1. / sqrt(row_sum<BLOCK>(s, lanes, part64) / p.n + (double)p.eps);
+    // an element times s is at most sqrt n; s alone may leave the range of f32
+    if (wide) {
+#pragma unroll
+      for (int c = 0; c < U; ++c)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) v[c][e] = (float)(v[c][e] * s);
+      r = 1.f;
+    }
+  }
+#pragma unroll
+  for (int c = 0; c < U; ++c) {
+    float y[8];
+    if constexpr (VEC) {
+      const int i = at(c, 0);
+      float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+      if (p.w && ok(i)) load8(p.w + i, g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) y[e] = v[c][e] * r * (g[e] + p.w_add);
+      if constexpr (YT == QG_Q8_0) {
+        uint32_t q[2];
+        const uint32_t bits = q8_block(y, q);
+        // stored order: of each 16 bytes the two halves byte by byte, a half a lane
+        const bool second = t & 1;
+        const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? q[0] : q[1], 1);
+        const uint32_t a = second ? got : q[0], b = second ? q[1] : got;
+        if (ok(i)) {
+          reinterpret_cast<uint2*>(static_cast<int8_t*>(p.y) + row * p.n)[i >> 3] =
+              make_uint2(__byte_perm(a, b, 0x5140) ^ 0x80808080u, __byte_perm(a, b, 0x7362) ^ 0x80808080u);
+          if ((t & 3) == 0) p.scl[row * (p.n >> 5) + (i >> 5)] = (uint16_t)bits;
+        }
+      } else if (ok(i)) {
+        if constexpr (YT == QG_F16) store8(static_cast<__half*>(p.y) + tok * p.ys + head * p.n + i, y);
+        if constexpr (YT == QG_F32) store8(static_cast<float*>(p.y) + tok * p.ys + head * p.n + i, y);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = at(c, e);
+        if (!ok(i)) continue;
+        const float o = v[c][e] * r * ((p.w ? p.w[i] : 1.f) + p.w_add);
+        if constexpr (YT == QG_F16) put(static_cast<__half*>(p.y) + tok * p.ys + head * p.n + i, o);
+        if constexpr (YT == QG_F32) put(static_cast<float*>(p.y) + tok * p.ys + head * p.n + i, o);
+      }
+    }
+  }
+}
+
+template <class TI, int YT, bool VEC, int U>
+cudaError_t norm_u(const NormParams<TI>& p, cudaStream_t s) {
+  const int eights = (p.n + 7) / 8, need = (eights + U - 1) / U;
+  if (need <= 32) {
+    int lanes = 4;
+    while (lanes < need) lanes *= 2;
+    const int per = NM_WARP_THREADS / lanes;
+    return launch_pdl(norm_kernel<TI, YT, VEC, U, false>, dim3((unsigned)((p.rows + per - 1) / per)), dim3(NM_WARP_THREADS), 0, s, 0,
+                      LC_L1, p, lanes);
+  }
+  return launch_pdl(norm_kernel<TI, YT, VEC, U, true>, dim3((unsigned)p.rows), dim3((need + 31) / 32 * 32), 0, s, 0, LC_L1, p, 0);
+}
+
+template <class TI, int YT, bool VEC>
+cudaError_t norm_vec(const NormParams<TI>& p, cudaStream_t s) {
+  const int eights = (p.n + 7) / 8;
+  if (eights <= 32 || (eights <= 1024 && p.rows <= 152)) return norm_u<TI, YT, VEC, 1>(p, s);
+  if (eights <= 1024) return norm_u<TI, YT, VEC, 2>(p, s);
+  return norm_u<TI, YT, VEC, 4>(p, s);
+}
+
+template <class TI>
+cudaError_t norm_typed(const NormArgs& a, cudaStream_t s) {
+  NormParams<TI> p;
+  p.x = static_cast<const TI*>(a.x);
+  p.add = static_cast<const TI*>(a.add);
+  p.sum = static_cast<TI*>(a.sum);
+  p.w = a.w;
+  p.y = a.y;
+  p.scl = a.scl;
+  p.xs = a.xs; p.as = a.as; p.ss = a.ss; p.ys = a.ys;
+  p.w_add = a.w_add; p.eps = a.eps;
+  p.heads = a.heads; p.n = a.n;
+  p.rows = (int64_t)a.ntok * a.heads;
+  if (a.yt == QG_Q8_0) return norm_vec<TI, QG_Q8_0, true>(p, s);
+  if (a.vec) return a.yt == QG_F16 ? norm_vec<TI, QG_F16, true>(p, s) : norm_vec<TI, QG_F32, true>(p, s);
+  return a.yt == QG_F16 ? norm_vec<TI, QG_F16, false>(p, s) : norm_vec<TI, QG_F32, false>(p, s);
+}
+
+}  // namespace
+
+cudaError_t norm_launch(const NormArgs& a, cudaStream_t s) {
+  return a.xt == QG_F32 ? norm_typed<float>(a, s) : norm_typed<__half>(a, s);
+}
+
+}  // namespace qg

@@ -25,6 +25,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "qg_blocks.cuh"
 #include "qg_common.cuh"
 #include "qg_internal.h"
 #include "qg_kv.cuh"
@@ -61,22 +62,6 @@ __device__ __forceinline__ float elem<float>(const float* p) { return *p; }
 template <>
 __device__ __forceinline__ float elem<__half>(const __half* p) { return __half2float(*p); }
 
-// Eight consecutive elements, 16-byte aligned.
-__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
-  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
-}
-__device__ __forceinline__ void load8(const __half* p, float (&v)[8]) {
-  const uint4 w = *reinterpret_cast<const uint4*>(p);
-  const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
-    v[2 * i] = f.x;
-    v[2 * i + 1] = f.y;
-  }
-}
 // Four consecutive elements, aligned to four.
 __device__ __forceinline__ void load4(const float* p, float (&v)[4]) {
   const float4 a = *reinterpret_cast<const float4*>(p);
@@ -88,38 +73,12 @@ __device__ __forceinline__ void load4(const __half* p, float (&v)[4]) {
   const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&w.y));
   v[0] = a.x; v[1] = a.y; v[2] = b.x; v[3] = b.y;
 }
-__device__ __forceinline__ uint32_t pack2(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
-  return *reinterpret_cast<const uint32_t*>(&h);
-}
-__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
-}
 __device__ __forceinline__ void store4(float* p, const float* v) {
   *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
 }
 __device__ __forceinline__ void store4(__half* p, const float* v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
 }
-__device__ __forceinline__ void store8(__half* p, const float (&v)[8]) {
-  *reinterpret_cast<uint4*>(p) =
-      make_uint4(pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7]));
-}
-
-// The larger of two magnitudes; a NaN if either is one.
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float d;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
-__device__ __forceinline__ float min_nan(float a, float b) {
-  float d;
-  asm("min.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-  return d;
-}
-
 // Sines and cosines (times mscale) of the block's tokens: sc[token][pair].
 __device__ __forceinline__ void make_turns(const qg_rope& plan, float2* sc, const int32_t* pos, int64_t tok0,
                                            int tokens, int64_t ntok) {
@@ -434,13 +393,6 @@ __device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot
 }
 
 // Eight elements of a row into its half record (NULL: nowhere; the lanes of a block call together).
-//
-// Q8_0. The scale is the smallest f16 h with 127 h >= the block's largest magnitude. The product with R, a little
-// above 1/127, rounded up is that h or the f16 behind it, and 127 h is exact in f32 (18 bits), so one comparison
-// decides. x / h by an approximate reciprocal is off by at most 127 (2^-23 + 2^-24) < 2.3e-5; only next to a half is the
-// division needed to know the nearest integer q. 1.5 2^23 + 128 + q has q + 128 as its low byte.
-// (With two IEEE divisions a block, a clamp and a test an element, key and value rows took most of the kernel's issue
-// slots: a prompt of 16,382 tokens, appended and read back, 142 us instead of 135.)
 template <int TYPE>
 __device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, int d, float (&y)[8]) {
   if constexpr (TYPE == QG_Q4_1) {
@@ -448,40 +400,8 @@ __device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, int 
   } else if constexpr (TYPE == QG_F16) {
     if (half) store8(reinterpret_cast<__half*>(half + spot.at), y);
   } else {
-    float top = fabsf(y[0]);  // an infinity or a NaN stays one
-#pragma unroll
-    for (int e = 1; e < 8; ++e) top = max_nan(top, fabsf(y[e]));
-    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 1));
-    top = max_nan(top, __shfl_xor_sync(0xffffffffu, top, 2));
-    constexpr float R = 0x1.02040cp-7f;
-    uint32_t bits = __half_as_ushort(__float2half_ru(top * R));
-    if (127.f * __half2float(__ushort_as_half(bits - 1)) >= top) --bits;  // (false for 0 - 1, a NaN)
-    const bool bad = !(top <= 3.402823466e38f), high = bits > 0x7BFF;
-    if (high) bits = 0x7BFF;
-    if (bad) bits = 0x7FFF;
-    uint32_t w[2] = {0x80808080u, 0x80808080u};
-    if (!bad && bits != 0) {
-      const float ds = __half2float(__ushort_as_half(bits)), magic = 12582912.f + 128.f;
-      float inv;
-      asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ds));
-      float b[8], off = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 q = mul2(make_float2(y[e], y[e + 1]), make_float2(inv, inv));
-        const float2 m = sub2(q, make_float2(-magic, -magic));
-        const float2 r = sub2(q, sub2(m, make_float2(magic, magic)));
-        off = fmaxf(off, fmaxf(fabsf(r.x), fabsf(r.y)));
-        b[e] = m.x;
-        b[e + 1] = m.y;
-      }
-      if (off > 0.49996f || high)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) b[e] = fminf(fmaxf(__fdiv_rn(y[e], ds), -127.f), 127.f) + magic;
-#pragma unroll
-      for (int h = 0; h < 2; ++h)
-        w[h] = __byte_perm(__byte_perm(__float_as_uint(b[4 * h]), __float_as_uint(b[4 * h + 1]), 0x0040),
-                           __byte_perm(__float_as_uint(b[4 * h + 2]), __float_as_uint(b[4 * h + 3]), 0x0040), 0x5410);
-    }
+    uint32_t w[2];
+    const uint32_t bits = q8_block(y, w);
     if (half) {
       *reinterpret_cast<uint2*>(half + spot.at) = make_uint2(w[0], w[1]);
       if (spot.scale_at >= 0) *reinterpret_cast<uint16_t*>(half + spot.scale_at) = (uint16_t)bits;
@@ -563,7 +483,7 @@ __global__ void __launch_bounds__(ROW_THREADS, APPEND_BLOCKS)
     }
     put8<TYPE>(place && r < kv ? place + (size_t)r * head_bytes : nullptr, spot, d, y);
   }
-  const Spot<TYPE> v_spot(d0, d, in_group, true);
+  const Spot<TYPE> v_spot = TYPE == QG_Q4_1 ? Spot<TYPE>(d0, d, in_group, true) : spot;
   const T* const vr = a.v + tok * a.vs + d0;
   for (n -= kg; n < kg; n += all_parts) {
     const int r = n * at_once + first;

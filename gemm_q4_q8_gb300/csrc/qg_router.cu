@@ -23,11 +23,15 @@
 // A threshold T (the k-th largest of 32 segment maxima) leaves only the keys
 // that can be in the top k; each of those is ranked by counting the candidates
 // that beat it, and since keys are distinct the experts of rank < k land in
-// distinct slots. One warp then normalises their exponentials.
+// distinct slots. One warp then normalises their exponentials. With a plan
+// (qmoe_router_planned) a warp of CTA c routes column c instead (qg_route.cuh).
 #include <cuda_runtime.h>
+
+#include <type_traits>
 
 #include "qg_common.cuh"
 #include "qg_internal.h"
+#include "qg_route.cuh"
 
 namespace qg {
 
@@ -107,12 +111,20 @@ __device__ __forceinline__ void rt_row(const float* __restrict__ wr, const __hal
   }
 }
 
-template <int NC, bool XS, bool VEC>
+struct NoPlan {};
+struct Plan {
+  qg_route r;
+  const float* bias;
+};
+
+template <int NC, bool XS, bool VEC, class PLAN>
 __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restrict__ w,
                                                             const __half* __restrict__ x, int E,
                                                             int hidden, int ncols, int topk,
                                                             float* logits_out, int32_t* ids_out,
-                                                            float* rw_out) {
+                                                            float* rw_out, const __grid_constant__ PLAN plan) {
+  constexpr bool PLANNED = std::is_same<PLAN, Plan>::value;
+  __shared__ double s_c[PLANNED ? RT_MAXE : 1];
   __shared__ float s_lg[RT_MAXE];              // column `rank`: every expert's logit
   __shared__ uint64_t s_key[RT_MAXE];          // candidates (unordered)
   __shared__ uint64_t s_seg[32];
@@ -169,6 +181,11 @@ __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restr
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
   if ((int)rank >= ncols) return;
   const int c = (int)rank;
+  if constexpr (PLANNED) {
+    if (warp == 0)
+      route_token(plan.r, s_lg, plan.bias, E, topk, s_c, ids_out + (size_t)c * topk, rw_out + (size_t)c * topk);
+    return;
+  }
   // Pruning: T = the k-th largest of 32 segment maxima (16 threads, up to 2
   // keys each, per segment). At least k keys are >= T, so every top-k key is
   // >= T, and a candidate's rank among all keys equals its rank among the
@@ -237,19 +254,20 @@ __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restr
   }
 }
 
-template <int NC, bool XS, bool VEC>
+template <int NC, bool XS, bool VEC, class PLAN>
 static cudaError_t router_go(size_t smem, const float* w, const __half* x, int E, int hidden,
                              int ncols, int topk, float* logits, int32_t* ids, float* rw,
-                             cudaStream_t s) {
-  auto kern = router_kernel<NC, XS, VEC>;
+                             cudaStream_t s, const PLAN& plan) {
+  auto kern = router_kernel<NC, XS, VEC, PLAN>;
   const cudaError_t e = prepare_kernel(reinterpret_cast<const void*>(kern), smem, true);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3(RT_CLUSTER), dim3(RT_THREADS), smem, s, RT_CLUSTER, LC_L1, w, x, E,
-                    hidden, ncols, topk, logits, ids, rw);
+                    hidden, ncols, topk, logits, ids, rw, plan);
 }
 
-cudaError_t router_launch(const float* w, const uint16_t* x, int E, int hidden, int ncols,
-                          int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s) {
+template <class PLAN>
+static cudaError_t router_any(const float* w, const uint16_t* x, int E, int hidden, int ncols,
+                              int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s, const PLAN& plan) {
   const __half* xh = reinterpret_cast<const __half*>(x);
   const bool vec = (hidden % 4) == 0 && (reinterpret_cast<uintptr_t>(x) & 7) == 0;
   const size_t s_x = (size_t)ncols * hidden * (vec ? 4 : 2);
@@ -260,15 +278,24 @@ cudaError_t router_launch(const float* w, const uint16_t* x, int E, int hidden, 
   // whatever the number of columns (the lane -> k order differs between the
   // float4 and scalar sweeps).
   if (xs && vec) {
-    if (ncols == 1) return router_go<1, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-    if (ncols <= 2) return router_go<2, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-    if (ncols <= 4) return router_go<4, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-    if (ncols <= 8) return router_go<8, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-    return router_go<16, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
+    if (ncols == 1) return router_go<1, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+    if (ncols <= 2) return router_go<2, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+    if (ncols <= 4) return router_go<4, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+    if (ncols <= 8) return router_go<8, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+    return router_go<16, true, true>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
   }
-  if (xs) return router_go<RT_MAXC, true, false>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-  if (vec) return router_go<RT_MAXC, false, true>(0, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
-  return router_go<RT_MAXC, false, false>(0, w, xh, E, hidden, ncols, topk, logits, ids, rw, s);
+  if (xs) return router_go<RT_MAXC, true, false>(s_x, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+  if (vec) return router_go<RT_MAXC, false, true>(0, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+  return router_go<RT_MAXC, false, false>(0, w, xh, E, hidden, ncols, topk, logits, ids, rw, s, plan);
+}
+
+cudaError_t router_launch(const float* w, const uint16_t* x, int E, int hidden, int ncols,
+                          int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s) {
+  return router_any(w, x, E, hidden, ncols, topk, logits, ids, rw, s, NoPlan{});
+}
+cudaError_t router_planned_launch(const qg_route& r, const float* w, const uint16_t* x, const float* bias, int E, int hidden,
+                                  int ncols, int topk, float* logits, int32_t* ids, float* rw, cudaStream_t s) {
+  return router_any(w, x, E, hidden, ncols, topk, logits, ids, rw, s, Plan{r, bias});
 }
 
 bool router_shape_ok(int E, int hidden, int ncols, int topk) {

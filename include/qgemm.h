@@ -241,6 +241,103 @@ qg_status qmoe_router(const float *w_router, const uint16_t *x, int n_expert, in
                       cudaStream_t stream);
 
 /* ---------------------------------------------------------------------------
+ * Routing by a plan: scores, a bias for balance, groups of experts. A plan is host
+ * memory, filled by qroute_plan and read during a call. For each token, over its
+ * logits l_e of n_expert experts:
+ *   p_e = softmax(l)_e (QG_SCORE_SOFTMAX) or 1 / (1 + exp(-l_e)) (QG_SCORE_SIGMOID);
+ *   c_e = p_e + bias_e (bias NULL: p_e);
+ *   the experts form n_group groups of n_expert / n_group neighbours, each worth the
+ *   sum of its group_top (1 or 2) largest c_e; those of the top_group groups worth most
+ *   stay in the choice (lowest group on ties; top_group == n_group: all of them);
+ *   ids: the topk experts of largest c_e, in that order, lowest id on ties;
+ *   rw: their p_e (without the bias), divided by their sum if renorm (0 where that is
+ *   0), times scale.
+ * The choice is that of 64-bit arithmetic on the f32 logits and bias; without a bias
+ * the experts' order is that of the logits. rw is within 2^-19 of its value. A NaN
+ * logit ranks behind every number and is left out of the softmax's sum (where it is
+ * chosen all the same, its weight is NaN); infinite logits count as alike.
+ *   n_group: 1..32; top_group: 1..n_group; scale finite (QG_ERR_SHAPE)
+ *   topk: 1..32; n_expert: 1..1024, a multiple of n_group; topk <= top_group *
+ *   n_expert / n_group, and where top_group < n_group, group_top <= n_expert / n_group
+ * ------------------------------------------------------------------------- */
+typedef enum { QG_SCORE_SOFTMAX = 0, QG_SCORE_SIGMOID = 1 } qg_score;
+
+typedef struct qg_route {
+  int32_t score; /* qg_score */
+  int32_t n_group, top_group, group_top;
+  int32_t renorm;
+  float scale;
+} qg_route;
+
+qg_status qroute_plan(qg_route *plan, int score, int n_group, int top_group, int group_top,
+                      int renorm, double scale);
+
+/* From logits: f32 [ntok] tokens of n_expert neighbouring values, token t at logits +
+ * t * stride (stride >= n_expert; ignored when ntok <= 1); bias: NULL or f32 [n_expert];
+ * ids_out int32, rw_out f32 [ntok][topk]. All 4-byte aligned; an output must not overlap
+ * anything else (QG_ERR_ALIAS). ntok == 0 launches nothing. */
+qg_status qmoe_route(const qg_route *plan, const float *logits, int64_t stride,
+                     const float *bias, int ntok, int n_expert, int topk, int32_t *ids_out,
+                     float *rw_out, cudaStream_t stream);
+
+/* qmoe_router by a plan: the logits of 1..16 columns and their routing in one launch.
+ * Arguments as qmoe_router, with the plan and the bias; logits_out may be NULL. */
+qg_status qmoe_router_planned(const qg_route *plan, const float *w_router, const uint16_t *x,
+                              const float *bias, int n_expert, int hidden, int ncols, int topk,
+                              float *logits_out, int32_t *ids_out, float *rw_out,
+                              cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Embedding lookup: y[t] = scale * W[ids[t]] for ntok tokens, W a matrix in the layout
+ * above (the LM head's, where the two are tied).
+ *   t     : QG_Q4_0 or QG_Q8_0 (q, scl: the matrix's arrays), or QG_F16 (q: f16
+ *           [rows][k], scl NULL); k a multiple of 32, rows >= 1
+ *   ids   : device int32 [ntok]. One outside [0, rows) gives a row of zeros and ORs
+ *           QG_EMBED_BAD_ID into *err_flag (device int32 or NULL, never cleared)
+ *   scale : finite; a weight times scale is rounded to f32, then to yt
+ *   y     : yt (QG_F32 or QG_F16), token t's k elements at y + t * y_stride
+ * q, scl, y 16-byte aligned, y_stride a multiple of 8 elements and >= k (ignored when
+ * ntok <= 1); y must not overlap the inputs (QG_ERR_ALIAS).
+ * ------------------------------------------------------------------------- */
+#define QG_EMBED_BAD_ID 1
+
+qg_status qembed(qg_type t, const void *q, const uint16_t *scl, int rows, int k,
+                 const int32_t *ids, int ntok, float scale, qg_type yt, void *y,
+                 int64_t y_stride, int32_t *err_flag, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * Root-mean-square norm of n_heads vectors of n elements for each of ntok tokens (a
+ * hidden state: one; queries or keys: one a head), with the residual's addition:
+ *   s = x + add (add NULL: x), f32, rounded once where xt is QG_F16;
+ *   y = s * (w + w_add) / sqrt(mean(s^2) + eps)
+ *   x    : xt (QG_F32 or QG_F16), token t's vectors at x + t * x_stride elements,
+ *          n_heads * n neighbouring elements
+ *   add  : NULL or of type xt, at add + t * add_stride
+ *   sum  : NULL or of type xt, at sum + t * sum_stride: s, written
+ *   w    : f32 [n], or NULL (1); w_add: 0, or 1 for weights that are kept less 1
+ *   eps  : >= 0, finite (0 with a vector of zeros gives NaN)
+ *   y    : yt QG_F32 or QG_F16: at y + t * y_stride; or
+ *          QG_Q8_0: rows of a Q8_0 matrix in the layout above, int8 [ntok * n_heads][n],
+ *          with the scales in y_scl, [ntok * n_heads][n / 32] (qgemv_q8_0 scores them,
+ *          qembed reads them back); blocks as in the cache. y_stride is not used.
+ *   n    : 1..32768, for QG_Q8_0 a multiple of 32; n_heads >= 1; strides >= n_heads * n
+ *          (ignored when ntok <= 1)
+ * Sums are f32 (64 bits where the squares leave its range); a vector's result depends on
+ * nothing but the vector, n, the alignment and whether there are more than 152 vectors.
+ * Each pointer aligned to its elements; for QG_Q8_0 all 16-byte aligned and the strides
+ * multiples of 8 elements (QG_ERR_ALIGN). Rows that begin at multiples of 16 bytes, with
+ * w so aligned, too, are read and written in wide accesses.
+ * sum may be x or add, and y may be x or add where it has their type and sum is
+ * elsewhere or NULL, each with the same stride; any other overlap is QG_ERR_ALIAS.
+ * ------------------------------------------------------------------------- */
+#define QG_NORM_MAX 32768
+
+qg_status qrms_norm(qg_type xt, const void *x, int64_t x_stride, const void *add,
+                    int64_t add_stride, void *sum, int64_t sum_stride, const float *w,
+                    float w_add, float eps, int ntok, int n_heads, int n, qg_type yt, void *y,
+                    int64_t y_stride, uint16_t *y_scl, cudaStream_t stream);
+
+/* ---------------------------------------------------------------------------
  * Sampling over f32 logits ("Engine and kernels", section "Kernel families":
  * greedy argmax and top-k on the GPU, so a token reads back a few bytes instead
  * of the logits; section "Fewer passes": lowest-index tie-breaking).
