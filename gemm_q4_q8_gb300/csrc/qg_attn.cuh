@@ -978,6 +978,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
               l[nt][c] *= f[c];
             }
           }
+          if constexpr (TYPE == QG_Q4_1) {
+            om[nt][0] *= f[0];
+            om[nt][1] *= f[1];
+          }
           if (CLUSTER && step == begin) continue;  // nothing is there yet (with more steps, the test costs more than it saves)
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk)

@@ -325,9 +325,32 @@ def test_attention_many_rows(heads, ncols, d):
     check(1, heads, d, 64, [200, 90], ncols, seed=heads)
 
 
-def test_attention_large_scores():
+@pytest.mark.parametrize("wide", [0, 2000])
+def test_attention_large_scores(wide):
     """Scores of several hundred: one token takes nearly all the weight."""
-    check(2, 8, 128, 32, [500, 77], 2, seed=5, size=100.0)
+    check(2, 8, 128, 32, [500, 77], 2, seed=5, size=100.0, extra_pages=wide)
+
+
+@pytest.mark.parametrize("wide", [0, 3000])
+@pytest.mark.parametrize("step", [0.02, 0.3, -0.3, 3.0])
+@pytest.mark.parametrize("d,heads,ncols", [(64, 8, 1), (128, 5, 1), (128, 8, 2), (256, 16, 1), (64, 32, 1)])
+def test_attention_rising_scores(d, heads, ncols, step, wide):
+    """Scores that rise (or fall) from token to token: the running reference moves again and again, and every sum with it, the
+    blocks' m among them."""
+    n, lens = 700, [700, 33]
+    c, ks, vs = filled(1, d, 16, lens, 17, extra_pages=wide)
+    g = rng(18, d)
+    for s, n in enumerate(lens):
+        for j in range(n):
+            k = g.standard_normal(d) * 0.1 + step * j * d ** -0.5
+            v = g.standard_normal(d) + 1.5
+            c.put(s, j, 0, k.astype(np.float32), v.astype(np.float32))
+            ks[s][:, j, 0], vs[s][:, j, 0] = c.get(s, j, 0)
+    c.upload()
+    q = (1 + 0.1 * g.standard_normal((2, ncols, heads, d))).astype(np.float16)
+    y, _ = attend(c, q, lens, scale=1.0)
+    want, bound = ref.attention(q, ks, vs, lens, ncols, 0, 1.0)
+    assert_within(y, want, bound, f"step {step}")
 
 
 @pytest.mark.parametrize("size", [1e-4, 1e-2, 1.0, 100.0, 1000.0])
