@@ -220,8 +220,8 @@ template <int TYPE>
 __device__ __forceinline__ int at_swap(int row) {
   return TYPE == QG_Q4_1 ? ((row & 2) << 1) | ((row & 4) << 2) : 0;
 }
-__device__ __forceinline__ uint32_t hmul2_u(uint32_t a, uint32_t b) {
-  const __half2 d = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+__device__ __forceinline__ uint32_t hfma2_u(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 d = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b), *reinterpret_cast<const __half2*>(&c));
   return *reinterpret_cast<const uint32_t*>(&d);
 }
 // Q4_1: four f16 pairs of a fragment out of two words' low or high quants (bits MASK), as subnormals.
@@ -759,11 +759,10 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       }
     auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : z[nt][c]; };
     // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
-    // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul. Q4_1: wback = 2^e,
-    // and the products of weights and d are brought below 2^15 by 2^-e in two factors: the d by wm_d, the weights by wm_w
+    // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul. Q4_1: the same with
+    // 2^-e, weights being 2^7 times as large from the start.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
-    uint32_t wm_d = 0x3C003C00u, wm_w = 0x3C003C00u;
-    // Q4_1: om[nt][c] of block g (c < 2): sum of weights times m, of row 8 nt + 2t + c
+    // Q4_1: om[nt][c] of block g (c < 2): sum of weights times m + 8 d, of row 8 nt + 2t + c
     float om[TYPE == QG_Q4_1 ? NT : 1][4];
 #pragma unroll
     for (int nt = 0; nt < (TYPE == QG_Q4_1 ? NT : 1); ++nt) om[nt][0] = om[nt][1] = om[nt][2] = om[nt][3] = 0.f;
@@ -1121,50 +1120,50 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           w0[nt] = transpose8(pack_f16(s[nt][0], s[nt][1]));
           w1[nt] = transpose8(pack_f16(s[nt][2], s[nt][3]));
         }
-        {  // weights times m: the blocks on the wide side
-          uint32_t am[4] = {0u, 0u, 0u, 0u};
+        {  // weights times m + 8 d: the blocks on the wide side
+          uint32_t am[4] = {0u, 0u, 0u, 0u}, d0, d1;
+          lds64(vb + scales + (g & (NB - 1)) * 32 + t * 8, d0, d1);
           lds64(vb + scales + D + (g & (NB - 1)) * 32 + t * 8, am[0], am[2]);
+          am[0] = hfma2_u(d0, 0x48004800u, am[0]);
+          am[2] = hfma2_u(d1, 0x48004800u, am[2]);
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma16816_acc(om[nt], am, w0[nt], w1[nt]);
         }
-        uint32_t d[NB][2];  // of tokens 2t, 2t + 1 and of 2t + 8, 2t + 9
+        uint32_t d[NB];  // of tokens g, g + 8
         __half2 big = __float2half2_rn(0.f);
 #pragma unroll
         for (int blk = 0; blk < NB; ++blk) {
-          lds64(vb + scales + blk * 32 + t * 8, d[blk][0], d[blk][1]);
-          big = __hmax2(big, __hmax2(*reinterpret_cast<__half2*>(&d[blk][0]), *reinterpret_cast<__half2*>(&d[blk][1])));
+          uint32_t d0, d1;
+          lds64(vb + scales + blk * 32 + (g >> 1) * 8, d0, d1);
+          d[blk] = __byte_perm(d0, d1, g & 1 ? 0x7632u : 0x5410u);
+          big = __hmax2(big, *reinterpret_cast<__half2*>(&d[blk]));
         }
         float dmax = fmaxf(__low2float(big), __high2float(big));
         if (__builtin_expect(__any_sync(0xffffffffu, dmax > wmax), 0)) {
           dmax = wmax;  // again without infinities, which would cost the others their bits
 #pragma unroll
-          for (int i = 0; i < 2 * NB; ++i) {
-            const float x = lo_f32(d[i / 2][i % 2]), y = hi_f32(d[i / 2][i % 2]);
+          for (int blk = 0; blk < NB; ++blk) {
+            const float x = lo_f32(d[blk]), y = hi_f32(d[blk]);
             if (x <= 65504.f) dmax = fmaxf(dmax, x);
             if (y <= 65504.f) dmax = fmaxf(dmax, y);
           }
-          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 1));
-          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 2));
-          if (dmax > wmax) {
-            // as below. Small scales are made larger, which takes no bit off them (by 2^15 at most: at 2^-24 and a weight of 2^7 the
-            // product is 2^-2). Large ones, next to which ordinary ones would lose theirs, are made smaller by half of what has to be
-            // taken off, the weights by the other half (both have bits to spare: 60,000 in one token and 0.1 in the others)
-            const int e = max(((__float_as_int(dmax) >> 23) & 0xff) - 127 + 2, -15), by_w = e > 0 ? e / 2 : 0;
-            const float f = __int_as_float((127 - e) << 23) * wback;  // (at the first move there is nothing to scale yet)
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 4));
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 8));
+          dmax = fmaxf(dmax, __shfl_xor_sync(0xffffffffu, dmax, 16));
+          if (dmax > wmax) {  // as below
+            const int e = ((__float_as_int(dmax) >> 23) & 0xff) - 127 + 2;
+            const float to = __int_as_float((127 - e) << 23);
+            const float f = to * wback;  // at the first move there is nothing to scale yet
+            wmul = to;
             wmax = wback = __int_as_float((127 + e) << 23);
-            const float to_d = __int_as_float((127 + by_w - e) << 23), to_w = __int_as_float((127 - by_w) << 23);
-            wm_d = pack_f16(to_d, to_d);
-            wm_w = pack_f16(to_w, to_w);
             if (!CLUSTER || step != begin)
 #pragma unroll
               for (int i = 0; i < NB * NT * 8; ++i) (&o[0][0][0][0])[i] *= f;
           }
         }
+        float w[NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          w0[nt] = hmul2_u(w0[nt], wm_w);
-          w1[nt] = hmul2_u(w1[nt], wm_w);
-        }
+        for (int i = 0; i < NT * 4; ++i) w[i >> 2][i & 3] = s[i >> 2][i & 3] * wmul;
 #pragma unroll
         for (int two = 0; two < NB; two += 2) {
           uint32_t v[4];  // of four tokens: bytes g, g + 8 of a block, and of the next one
@@ -1175,10 +1174,21 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             uint32_t v0[4], v1[4];
             nibbles<NIB_LO>(v[2 * h], v[2 * h + 1], v0);
             nibbles<NIB_HI>(v[2 * h], v[2 * h + 1], v1);  // 16 times their values: taken off at the item's end
-            const uint32_t n0 = hmul2_u(d[blk][0], wm_d), n1 = hmul2_u(d[blk][1], wm_d);
+            // Less 8, exact: the sums of quants themselves would be many times what is left of them when m joins, and each product's
+            // rounding would weigh twice as much. (By two more products with -8 a block: 76.8 us instead of 73.8 for 262,143 tokens
+            // of 8 heads of 128, and 3.4e-4 instead of 2.6e-4 off 64 bits.)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              v0[i] = hsub2_u(v0[i], 0x00080008u);
+              v1[i] = hsub2_u(v1[i], 0x00800080u);
+            }
+            const float e0 = lo_f32(d[blk]), e1 = hi_f32(d[blk]);
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-              const uint32_t b0 = hmul2_u(w0[nt], n0), b1 = hmul2_u(w1[nt], n1);
+              const float2 lo = mul2(make_float2(w[nt][0], w[nt][1]), make_float2(e0, e0));
+              const float2 hi = mul2(make_float2(w[nt][2], w[nt][3]), make_float2(e1, e1));
+              const uint32_t b0 = transpose8(pack_f16(lo.x, lo.y));
+              const uint32_t b1 = transpose8(pack_f16(hi.x, hi.y));
               mma16816_acc(o[blk][nt][0], v0, b0, b1);
               mma16816_acc(o[blk][nt][1], v1, b0, b1);
             }
@@ -1273,7 +1283,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
       next();
     }
 
-    if constexpr (TYPE == QG_Q4_1) {  // quants came as multiples of 2^-24 and 2^-20; and the blocks' m join
+    if constexpr (TYPE == QG_Q4_1) {  // quants came as multiples of 2^-24 and 2^-20; and what is the blocks' joins
       const float back[2] = {wback * 16777216.f, wback * 1048576.f};
 #pragma unroll
       for (int blk = 0; blk < NB; ++blk)
