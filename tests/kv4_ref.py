@@ -78,33 +78,33 @@ def write_row(pool, d, off, i, is_v, row):
 
 
 def read_row(pool, d, off, i, is_v):
-    """(q d, m) of a token's row, f64 [D] each."""
-    qd, mm = np.empty(d), np.empty(d)
+    """(q d, m, d) of a token's row, f64 [D] each."""
+    qd, mm, dd = np.empty(d), np.empty(d), np.empty(d)
     for b in range(d // 32):
         at = off + b * 256 + i * 16
         q = (pool[at:at + 16][BYTES] >> SHIFTS) & 15
         at = off + scale_offset(d, i, b, is_v)
         s, m = (float(pool[at + k:at + k + 2].view(F16)[0]) for k in (0, d))
-        qd[32 * b:32 * b + 32], mm[32 * b:32 * b + 32] = q * s, m
-    return qd, mm
+        at = slice(32 * b, 32 * b + 32)
+        qd[at], mm[at], dd[at] = q * s, m, s
+    return qd, mm, dd
 
 
 def attention(q, ks, vs, lens, ncols, window, scale, dead=None):
-    """(y, bound) in f64 of q [seq, ncols, heads, D]. ks, vs: per sequence (q d, m), each [tokens, kv, D]. dead[s]: positions that
-    do not exist.
+    """(y, bound) in f64 of q [seq, ncols, heads, D]. ks, vs: per sequence (q d, m, d), each [tokens, kv, D]. dead[s]: positions
+    that do not exist.
 
     bound, with A = sum |Q| (q d + |m|) of a token: its score is an f32 sum of D products, with the blocks' sums of queries as two
     f16 each (2^-22 of them): (D + 8) half steps of f32 of the largest A, scaled; as in attn_ref.attention that is on the weight
-    and on the sum, with 16 half steps for the exponential. A weight is rounded to f16 before it meets m, once more after it has
-    met d: half a step of |m|, two of q d. Weights far below their run's largest are off by 2^-32 of it, a product with d by 2^-30
-    of the largest weight times the largest d. Where d of 1/4 and more occur, with 2^e at most 4 times the largest and h = e / 2
-    rounded down, weights are off by 2^(h - 32) of the largest before they meet d, and d by 2^(e - h - 25). f32 sums of n terms
-    add n half steps to numerator and sum; y is rounded once."""
+    and on the sum, with 16 half steps for the exponential. Values are taken as (q - 8) d + (m + 8 d): a weight times d is rounded
+    to f16, so is m + 8 d, and so is the weight that it meets: half a step of |q - 8| d and two of |m + 8 d|. Weights far below their
+    run's largest are off by 2^-32 of it, products with d by 2^-30 of the largest weight times the largest d (times |q - 8|). f32 sums of n
+    terms add n half steps to numerator and sum; y is rounded once."""
     n, _, heads, d = q.shape
     y = np.zeros(q.shape, np.float64)
     bound = np.zeros(q.shape, np.float64)
     for s in range(n):
-        (kq, km), (vq, vm) = ks[s], vs[s]
+        (kq, km, _), (vq, vm, vd) = ks[s], vs[s]
         g = heads // kq.shape[1]
         for c in range(ncols):
             p = lens[s] - ncols + c
@@ -115,7 +115,7 @@ def attention(q, ks, vs, lens, ncols, window, scale, dead=None):
             if not at:
                 continue
             for h in range(heads):
-                k1, k2, v1, v2 = (a[at, h // g] for a in (kq, km, vq, vm))
+                k1, k2, v1, v2, v3 = (a[at, h // g] for a in (kq, km, vq, vm, vd))
                 qq = q[s, c, h].astype(np.float64)
                 sc = (k1 + k2) @ qq * scale
                 mag = ((k1 + np.abs(k2)) @ np.abs(qq)).max() * abs(scale)
@@ -124,11 +124,7 @@ def attention(q, ks, vs, lens, ncols, window, scale, dead=None):
                 y[s, c, h] = w @ (v1 + v2)
                 e_score = (d + 8) * SINGLE * mag + 4 * SINGLE * np.abs(sc).max()
                 rel = 2 * e_score + 16 * SINGLE + 2 * len(at) * SINGLE
-                bound[s, c, h] = rel * (w @ (v1 + np.abs(v2))) + HALF * (w @ np.abs(v2)) + 2.01 * HALF * (w @ v1) + \
-                    HALF * np.abs(y[s, c, h]) + SUB + \
-                    w.max() * (2.0 ** -32 * np.abs(v2).sum(0) + len(at) * 2.0 ** -30 * v1.max())
-                most = vq[np.isfinite(vq)].max() / 14  # (a block's largest element has a quant of 14 at least)
-                if most >= 0.25:
-                    e = int(np.floor(np.log2(most))) + 2
-                    bound[s, c, h] += w.max() * 2.0 ** (e // 2 - 32) * v1.sum(0) + 15 * 2.0 ** (e - e // 2 - 25)
+                a, c8 = np.abs(v1 - 8 * v3), np.abs(v2 + 8 * v3)
+                bound[s, c, h] = rel * (w @ (a + c8)) + 1.01 * HALF * (w @ a) + 2.01 * HALF * (w @ c8) + HALF * np.abs(y[s, c, h]) + \
+                    SUB * (1 + w.sum()) + w.max() * (2.0 ** -32 * c8.sum(0) + 8 * len(at) * 2.0 ** -30 * np.nanmax(vd[np.isfinite(vd)]))
     return y, bound

@@ -28,8 +28,8 @@ def test_worked_bytes():
     assert pool[640 + 512:640 + 576].view(np.float16).reshape(2, 16)[:, 7].tolist() == [1, 1]
     assert pool[640 + 576:640 + 640].view(np.float16).reshape(2, 16)[:, 7].tolist() == [2, 2]
     for off, i, is_v, add in ((0, 3, False, 0), (640, 11, True, 2)):
-        qd, m = ref.read_row(pool, 64, off, i, is_v)
-        assert np.array_equal(qd, row) and (m == add).all()
+        qd, m, d = ref.read_row(pool, 64, off, i, is_v)
+        assert np.array_equal(qd, row) and (m == add).all() and (d == 1).all()
 
 
 def test_places_are_a_permutation():

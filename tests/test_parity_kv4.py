@@ -47,7 +47,7 @@ class Cache:
             ref.write_row(self.host, self.d, *self.where(seq, pos, head, is_v), is_v, row)
 
     def get(self, seq, pos, head):
-        """((q d, m) of the key, the same of the value)."""
+        """((q d, m, d) of the key, the same of the value)."""
         return [ref.read_row(self.host, self.d, *self.where(seq, pos, head, is_v), is_v) for is_v in (False, True)]
 
 
@@ -167,7 +167,7 @@ def test_append_rotated_with_queries(d, kv, heads, rot, inter):
     c.host = host(c.pool)
     for t in range(n):
         for h in range(kv):
-            (kq, km), (vq, vm) = c.get(t // each, pos[t], h)
+            (kq, km, _), (vq, vm, _) = c.get(t // each, pos[t], h)
             kw, ke = want[t, heads + h].reshape(-1, 32), err[t, heads + h].reshape(-1, 32)
             # half a step; a step is at most one f16 step above a 15th of the range, which m's rounding down widens by a step of m
             lo, span = kw.min(1), kw.max(1) - kw.min(1) + 2 * ke.max(1)
@@ -212,7 +212,7 @@ def test_read(d, kv, ps, out):
         for t in range(n):
             for h in range(kv):
                 if pos[t] >= 0:
-                    want[:, t, h] = [qd + m for qd, m in c.get(seq[t], pos[t], h)]  # (exact in f64: 4 + 11 bits and 11)
+                    want[:, t, h] = [qd + m for qd, m, _ in c.get(seq[t], pos[t], h)]  # (exact in f64: 4 + 11 bits and 11)
         want = want.astype({torch.float16: np.float16, torch.float32: np.float32}[out])
     for got, w in ((k, want[0]), (v, want[1])):
         np.testing.assert_array_equal(host(got), w)
@@ -257,7 +257,7 @@ def filled(kv, d, ps, lens, seed, fill=0xFF, extra_pages=0, shift=0.4):
     ks, vs = [], []
     for s, n in enumerate(lens):
         k, v = g.standard_normal((n, kv, d)) * 1.5 + shift, g.standard_normal((n, kv, d)) * 0.7 + 0.1
-        parts = np.empty((2, 2, n, kv, d))
+        parts = np.empty((2, 3, n, kv, d))
         for j in range(n):
             for h in range(kv):
                 c.put(s, j, h, k[j, h].astype(np.float32), v[j, h].astype(np.float32))
@@ -529,9 +529,9 @@ def test_attention_any_scale(scale, heads, d):
 def big_reference(c, q, lens, ncols, window=0):
     """(y, bound) by f64 torch on values read back from the cache, for long sequences.
 
-    With a the largest magnitude of a value's block, |m| <= a and q d <= 2 a and a step (q d + m reaches from the smallest to the
-    largest). The roundings of different tokens' weights are independent, at most h_j = 5 HALF a_j each (half a step of m, two of q d);
-    the sum of n such is within 6 sqrt(sum (w_j h_j)^2) but for one time in 10^7 (Hoeffding). f32 sums as in
+    With a the largest magnitude of a value's block, |m| <= a, 15 d is at most 2 a and a step (q d + m reaches from the smallest to the
+    largest), so |q - 8| d <= 8/15 of that and |m + 8 d| (the quant 8, between the smallest and the largest) <= a and a step, 1.2 a. The roundings of different tokens' weights are independent, at
+    most h_j = (1.1 + 2 * 1.2) HALF a_j each (attn_ref's and kv4_ref's terms); the sum of n such is within 6 sqrt(sum (w_j h_j)^2) but for one time in 10^7 (Hoeffding). f32 sums as in
     test_parity_attn.big_reference."""
     n, _, heads, d = q.shape
     kv = c.n_kv_heads
@@ -561,7 +561,7 @@ def big_reference(c, q, lens, ncols, window=0):
         w = w / w.sum(-1, keepdim=True)
         y = w @ v
         rel = (2 * ((d + 8) * mag + 4 * top.abs()) + 16 + 2 * min(L, 4160)) * ref.SINGLE
-        b = rel * (w @ (3.01 * va)) + 6 * ((w * w) @ (5.05 * ref.HALF * va).square()).sqrt() + ref.HALF * y.abs() + ref.SUB + \
+        b = rel * (w @ (3.01 * va)) + 6 * ((w * w) @ (3.6 * ref.HALF * va).square()).sqrt() + ref.HALF * y.abs() + ref.SUB + \
             w.amax(-1, keepdim=True) * L * 2.0 ** -28 * va.amax(1, keepdim=True)
         back = lambda t: t.view(kv, ncols, -1, d).permute(1, 0, 2, 3).reshape(ncols, heads, d)  # noqa: E731
         ys.append(back(y))
