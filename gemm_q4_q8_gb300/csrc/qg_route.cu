@@ -1,4 +1,5 @@
-// qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token (qg_route.cuh).
+// qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token at a time (qg_route.cuh), the next token's logits
+// on their way.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -12,16 +13,49 @@ namespace qg {
 namespace {
 
 constexpr int RO_WARPS = 4;
+constexpr int RO_BLOCKS = 152 * 12;  // with more tokens than warps of these, each takes several in turn
 
+// One lane's experts of a row.
+template <int NE>
+__device__ __forceinline__ void load_row(const float* row, int first, int mine, float (&v)[NE]) {
+#pragma unroll
+  for (int i = 0; i < NE; ++i) v[i] = i < mine ? row[first + i] : 0.f;
+}
+
+// NE: experts of a lane, at most; 0: all in 64 bits
+template <int NE>
 __global__ void __launch_bounds__(RO_WARPS * 32)
     route_kernel(const __grid_constant__ qg_route r, const float* logits, int64_t stride, const float* bias, int ntok, int E,
                  int topk, int32_t* ids, float* rw) {
   extern __shared__ double s_c[];
   pdl_trigger();
   pdl_wait();
-  const int64_t tok = (int64_t)blockIdx.x * RO_WARPS + (threadIdx.x >> 5);
-  if (tok >= ntok) return;
-  route_token(r, logits + tok * stride, bias, E, topk, s_c + (threadIdx.x >> 5) * E, ids + tok * topk, rw + tok * topk);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  double* const c = s_c + warp * E;
+  const int64_t step = (int64_t)gridDim.x * RO_WARPS;
+  int64_t tok = (int64_t)blockIdx.x * RO_WARPS + warp;
+  if constexpr (NE == 0) {
+    for (; tok < ntok; tok += step) route_exact(r, logits + tok * stride, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
+  } else {
+    __shared__ RouteSlot slots[RO_WARPS][RO_SLOTS];
+    const RouteDeal deal = route_deal(r, E);
+    const int group = lane / deal.lanes, from = (lane & (deal.lanes - 1)) * deal.per;
+    const int first = group * deal.size + from;
+    const int mine = first < E ? max(0, min(deal.per, deal.size - from)) : 0;
+    float b[NE], l[NE], next[NE];
+#pragma unroll
+    for (int i = 0; i < NE; ++i) b[i] = 0.f;
+    if (tok < ntok) load_row(logits + tok * stride, first, mine, next);
+    if (bias) load_row(bias, first, mine, b);
+    for (; tok < ntok; tok += step) {
+#pragma unroll
+      for (int i = 0; i < NE; ++i) l[i] = next[i];
+      if (tok + step < ntok) load_row(logits + (tok + step) * stride, first, mine, next);
+      if (!route_fast(r, deal, l, b, bias != nullptr, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
+        route_exact(r, logits + tok * stride, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
+      __syncwarp();  // the slots have been read
+    }
+  }
 }
 
 }  // namespace
@@ -38,7 +72,16 @@ bool route_shape_ok(const qg_route& r, int E, int topk) {
 
 cudaError_t route_launch(const qg_route& r, const float* logits, int64_t stride, const float* bias, int ntok, int E, int topk,
                          int32_t* ids, float* rw, cudaStream_t s) {
-  return launch_pdl(route_kernel, dim3((unsigned)((ntok + (int64_t)RO_WARPS - 1) / RO_WARPS)), dim3(RO_WARPS * 32),
+  const int per = route_deal(r, E).per;
+  const auto kern = per <= 1    ? route_kernel<1>
+                    : per <= 2  ? route_kernel<2>
+                    : per <= 4  ? route_kernel<4>
+                    : per <= 8  ? route_kernel<8>
+                    : per <= 16 ? route_kernel<16>
+                    : per <= 32 ? route_kernel<32>
+                                : route_kernel<0>;
+  const int64_t blocks = ((int64_t)ntok + RO_WARPS - 1) / RO_WARPS;
+  return launch_pdl(kern, dim3((unsigned)(blocks < RO_BLOCKS ? blocks : RO_BLOCKS)), dim3(RO_WARPS * 32),
                     (size_t)RO_WARPS * E * sizeof(double), s, 0, LC_L1, r, logits, stride, bias, ntok, E, topk, ids, rw);
 }
 

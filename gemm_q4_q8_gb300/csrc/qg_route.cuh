@@ -4,6 +4,14 @@
 // p_e = softmax or sigmoid of the logits, c_e = p_e + bias_e (p_e without a bias); the order is that of c, in 64 bits, and
 // without a bias that of the logits; lowest id on ties, NaN behind everything. With groups, a group's value is the sum of its
 // one or two largest c.
+//
+// Nearly always f32 decides: with a bound on the error of every c at hand, two that lie further apart than their bounds are in
+// the order that 64 bits find. So a token is routed in f32 (route_fast), and again in 64 bits (route_exact) where two of the
+// deciding ones are too near, where more than 64 experts may be among the k best, or where a logit or a bias is not finite.
+//
+// route_fast. The lanes of a warp are dealt to the groups, and a group's experts in runs to its lanes, in registers. The k-th
+// largest of the lanes' maxima is a bound below which no expert can be among the k best; what is above it, a few more than
+// k, goes to shared memory, one or two for each lane, which counts how many are ahead.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -13,6 +21,7 @@
 namespace qg {
 
 constexpr int RO_MAXE = 1024, RO_MAXK = 32, RO_MAXG = 32;
+constexpr int RO_SLOTS = 64;  // experts that may be among the k best: two a lane
 
 // A key whose order is that of the numbers, +0 and -0 alike; 1: NaN; 0: nothing there.
 __device__ __forceinline__ uint64_t ro_key(double v) {
@@ -35,7 +44,7 @@ __device__ __forceinline__ double ro_warp_sum(double v) {
 }
 
 // By a whole warp. c: shared, a double for each expert; done with when the call returns.
-__device__ __forceinline__ void route_token(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
+static __device__ __noinline__ void route_exact(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
                                             int32_t* ids, float* rw) {
   const int lane = threadIdx.x & 31;
   // softmax: the largest logit and the sum, NaN left out
@@ -118,6 +127,197 @@ __device__ __forceinline__ void route_token(const qg_route& r, const float* logi
     rw[lane] = (float)(w * (double)r.scale);
   }
   __syncwarp();
+}
+
+// How the experts are dealt to the lanes: a group's to `lanes` of them (a power of two), `per` neighbours each.
+struct RouteDeal {
+  int lanes, per, size;
+};
+__host__ __device__ inline RouteDeal route_deal(const qg_route& r, int E) {
+  RouteDeal d;
+  const int groups = r.top_group < r.n_group ? r.n_group : 1;
+  d.size = E / groups;
+  d.lanes = 32;
+  while (d.lanes * groups > 32) d.lanes /= 2;
+  d.per = (d.size + d.lanes - 1) / d.lanes;
+  return d;
+}
+
+__device__ __forceinline__ float ro_ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+__device__ __forceinline__ float ro_rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+// Order of finite f32 as unsigned numbers above 0.
+__device__ __forceinline__ uint32_t ro_key32(float v) {
+  const uint32_t b = __float_as_uint(v);
+  return b & 0x80000000u ? ~b : b | 0x80000000u;
+}
+__device__ __forceinline__ float ro_warp_sum(float v) {
+#pragma unroll
+  for (int off = 16; off >= 1; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  return v;
+}
+
+struct RouteSlot {
+  float c, off;  // an expert's c, and by how much it may be off
+  int id;
+  float l;
+};
+
+// l, bias: this lane's experts (0 where it has fewer than NE), `mine` of them from id `first`. False: not decided.
+template <int NE>
+__device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& deal, const float (&l)[NE], const float (&bias)[NE],
+                                           bool biased, int first, int mine, int topk, RouteSlot* slots, int32_t* ids, float* rw) {
+  const int lane = threadIdx.x & 31;
+  const bool grouped = r.top_group < r.n_group, soft = r.score == QG_SCORE_SOFTMAX;
+  bool odd = false;
+#pragma unroll
+  for (int i = 0; i < NE; ++i) odd |= !(fabsf(l[i]) < INFINITY) || !(fabsf(bias[i]) < INFINITY);
+  if (__any_sync(0xffffffffu, odd)) return false;
+  float top = 0.f, sum = 1.f;
+  if (soft && (biased || grouped || !r.renorm)) {
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i < mine) top = fmaxf(top, l[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+    float part[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i < mine) part[i & 3] += expf(l[i] - top);
+    sum = ro_warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+  } else if (soft) {  // only ratios are wanted
+    top = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i < mine) top = fmaxf(top, l[i]);
+#pragma unroll
+    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+  }
+  // c, and its error's bound. Sigmoid: the exponent is off by |l| 2^-23.4 (its factor and product), ex2, sum and reciprocal by less than
+  // 2^-21 together. Softmax: the exponent by |l - top| 2^-24, expf by 2^-22, and the sum by its additions, at most 15 2^-24, the same
+  // 2^-22 and the exponents' mean error, below 7 2^-24 (an entropy). The bounds are twice that and more.
+  float c[NE];
+  auto off_of = [&](float p, float l1, float c1) {
+    return fmaf(p, fmaf(fabsf(l1 - top), 0x1p-22f, soft ? 0x1p-18f : 0x1p-20f), fmaf(fabsf(c1), 0x1p-22f, 0x1p-120f));
+  };
+  auto p_of = [&](float l1) { return soft ? ro_ex2((l1 - top) * 1.44269504f) * ro_rcp(sum) : ro_rcp(1.f + ro_ex2(l1 * -1.44269504f)); };
+  if (biased || grouped) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) c[i] = p_of(l[i]) + bias[i];
+  }
+  bool open = true;
+  if (grouped) {
+    // the group's two largest, by its lanes
+    float v0 = -INFINITY, v1 = -INFINITY, worst = 0.f;
+#pragma unroll
+    for (int i = 0; i < NE; ++i)
+      if (i < mine) {
+        v1 = fmaxf(v1, fminf(v0, c[i]));
+        v0 = fmaxf(v0, c[i]);
+        worst = fmaxf(worst, off_of(c[i] - bias[i], l[i], c[i]));
+      }
+    for (int off = deal.lanes >> 1; off >= 1; off >>= 1) {
+      const float u0 = __shfl_xor_sync(0xffffffffu, v0, off), u1 = __shfl_xor_sync(0xffffffffu, v1, off);
+      worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, off));
+      v1 = fmaxf(fminf(v0, u0), fmaxf(v1, u1));
+      v0 = fmaxf(v0, u0);
+    }
+    const float worth = r.group_top == 2 ? v0 + v1 : v0;
+    const float off = fmaf(2.f, worst, fabsf(worth) * 0x1p-22f);
+    const int g = lane / deal.lanes;
+    int ahead = 0;
+    bool near = false;
+    for (int h = 0; h < r.n_group; ++h) {
+      const float its = __shfl_sync(0xffffffffu, worth, h * deal.lanes), its_off = __shfl_sync(0xffffffffu, off, h * deal.lanes);
+      ahead += its > worth;
+      near |= h != g && fabsf(its - worth) <= off + its_off;
+    }
+    if (__any_sync(0xffffffffu, near && g < r.n_group)) return false;
+    open = ahead < r.top_group;
+  }
+  if (!biased) {
+#pragma unroll
+    for (int i = 0; i < NE; ++i) c[i] = l[i];
+  }
+  if (!open) mine = 0;
+  auto its_off = [&](int i) { return biased ? off_of(c[i] - bias[i], l[i], c[i]) : 0.f; };
+  // the k-th largest of the lanes' maxima (of their lower bounds)
+  uint32_t key = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (i < mine) key = max(key, ro_key32(c[i] - its_off(i)));
+  uint32_t bound = 0;
+  for (int n = 0; n < topk; ++n) {
+    bound = __reduce_max_sync(0xffffffffu, key);
+    if (key == bound) key = 0;  // (with every lane that has it: the bound is then lower than need be)
+  }
+  uint32_t in = 0;
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (i < mine && ro_key32(c[i] + its_off(i)) >= bound) in |= 1u << i;
+  int at = __popc(in);
+  const int own = at;
+#pragma unroll
+  for (int off = 1; off < 32; off <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, at, off);
+    if (lane >= off) at += up;
+  }
+  const int n = __shfl_sync(0xffffffffu, at, 31);
+  if (n > RO_SLOTS) return false;
+  at -= own;
+#pragma unroll
+  for (int i = 0; i < NE; ++i)
+    if (in >> i & 1) slots[at++] = {c[i], its_off(i), first + i, l[i]};
+  __syncwarp();
+  RouteSlot me[2];
+  int rank[2] = {0, 0};
+  bool near = false;
+  float w[2] = {0.f, 0.f};
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    me[j] = {-INFINITY, 0.f, 0x7fffffff, 0.f};
+    if (j * 32 >= n) continue;
+    if (j * 32 + lane < n) me[j] = slots[j * 32 + lane];
+    bool close = false;
+    for (int m = 0; m < n; ++m) {
+      const RouteSlot it = slots[m];
+      rank[j] += it.c > me[j].c || (it.c == me[j].c && it.id < me[j].id);
+      close |= m != j * 32 + lane && fabsf(it.c - me[j].c) <= it.off + me[j].off;
+    }
+    if (j * 32 + lane >= n) rank[j] = topk;
+    if (rank[j] < topk) {
+      near |= close;
+      w[j] = soft ? expf(me[j].l - top) / sum : 1.f / (1.f + expf(-me[j].l));
+    }
+  }
+  if (__any_sync(0xffffffffu, biased && near)) return false;
+  if (n <= 32) rank[1] = topk;
+  if (r.renorm) {
+    const float all = ro_warp_sum(w[0] + w[1]);
+    if (all < 0x1p-100f) return false;  // (weights that f32 holds badly)
+    w[0] /= all;
+    w[1] /= all;
+  }
+  bool small = false;
+#pragma unroll
+  for (int j = 0; j < 2; ++j) small |= rank[j] < topk && w[j] < 0x1p-100f;
+  if (__any_sync(0xffffffffu, small)) return false;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (rank[j] < topk) {
+      ids[rank[j]] = me[j].id;
+      rw[rank[j]] = w[j] * r.scale;
+    }
+  __syncwarp();
+  return true;
 }
 
 }  // namespace qg

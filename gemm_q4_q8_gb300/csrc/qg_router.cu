@@ -117,6 +117,31 @@ struct Plan {
   const float* bias;
 };
 
+// By a warp, from logits in shared memory.
+template <int NE>
+__device__ __forceinline__ bool route_column_fast(const qg_route& r, const RouteDeal& deal, const float* logits, const float* bias, int E,
+                                                  int topk, RouteSlot* slots, int32_t* ids, float* rw) {
+  const int lane = threadIdx.x & 31, from = (lane & (deal.lanes - 1)) * deal.per, first = lane / deal.lanes * deal.size + from;
+  const int mine = first < E ? max(0, min(deal.per, deal.size - from)) : 0;
+  float b[NE], l[NE];
+#pragma unroll
+  for (int i = 0; i < NE; ++i) {
+    b[i] = bias && i < mine ? bias[first + i] : 0.f;
+    l[i] = i < mine ? logits[first + i] : 0.f;
+  }
+  return route_fast(r, deal, l, b, bias != nullptr, first, mine, topk, slots, ids, rw);
+}
+__device__ __forceinline__ void route_column(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
+                                             RouteSlot* slots, int32_t* ids, float* rw) {
+  const RouteDeal deal = route_deal(r, E);
+  bool done = false;
+  if (deal.per <= 8)
+    done = route_column_fast<8>(r, deal, logits, bias, E, topk, slots, ids, rw);
+  else if (deal.per <= 32)
+    done = route_column_fast<32>(r, deal, logits, bias, E, topk, slots, ids, rw);
+  if (!done) route_exact(r, logits, bias, E, topk, c, ids, rw);
+}
+
 template <int NC, bool XS, bool VEC, class PLAN>
 __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restrict__ w,
                                                             const __half* __restrict__ x, int E,
@@ -125,6 +150,7 @@ __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restr
                                                             float* rw_out, const __grid_constant__ PLAN plan) {
   constexpr bool PLANNED = std::is_same<PLAN, Plan>::value;
   __shared__ double s_c[PLANNED ? RT_MAXE : 1];
+  __shared__ RouteSlot s_slots[PLANNED ? RO_SLOTS : 1];
   __shared__ float s_lg[RT_MAXE];              // column `rank`: every expert's logit
   __shared__ uint64_t s_key[RT_MAXE];          // candidates (unordered)
   __shared__ uint64_t s_seg[32];
@@ -182,8 +208,7 @@ __global__ void __launch_bounds__(RT_THREADS) router_kernel(const float* __restr
   if ((int)rank >= ncols) return;
   const int c = (int)rank;
   if constexpr (PLANNED) {
-    if (warp == 0)
-      route_token(plan.r, s_lg, plan.bias, E, topk, s_c, ids_out + (size_t)c * topk, rw_out + (size_t)c * topk);
+    if (warp == 0) route_column(plan.r, s_lg, plan.bias, E, topk, s_c, s_slots, ids_out + (size_t)c * topk, rw_out + (size_t)c * topk);
     return;
   }
   // Pruning: T = the k-th largest of 32 segment maxima (16 threads, up to 2
