@@ -1,5 +1,4 @@
-// qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token at a time (qg_route.cuh), the next token's logits
-// on their way.
+// qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token (qg_route.cuh).
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -24,7 +23,7 @@ __device__ __forceinline__ void load_row(const float* row, int first, int mine, 
 
 // NE: experts of a lane, at most; 0: all in 64 bits
 template <int NE>
-__global__ void __launch_bounds__(RO_WARPS * 32)
+__global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? 8 : 1)
     route_kernel(const __grid_constant__ qg_route r, const float* logits, int64_t stride, const float* bias, int ntok, int E,
                  int topk, int32_t* ids, float* rw) {
   extern __shared__ double s_c[];
@@ -42,16 +41,13 @@ __global__ void __launch_bounds__(RO_WARPS * 32)
     const int group = lane / deal.lanes, from = (lane & (deal.lanes - 1)) * deal.per;
     const int first = group * deal.size + from;
     const int mine = first < E ? max(0, min(deal.per, deal.size - from)) : 0;
-    float b[NE], l[NE], next[NE];
+    float b[NE], l[NE];
 #pragma unroll
     for (int i = 0; i < NE; ++i) b[i] = 0.f;
-    if (tok < ntok) load_row(logits + tok * stride, first, mine, next);
     if (bias) load_row(bias, first, mine, b);
     for (; tok < ntok; tok += step) {
-#pragma unroll
-      for (int i = 0; i < NE; ++i) l[i] = next[i];
-      if (tok + step < ntok) load_row(logits + (tok + step) * stride, first, mine, next);
-      if (!route_fast(r, deal, l, b, bias != nullptr, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
+      load_row(logits + tok * stride, first, mine, l);
+      if (!route_fast(r, deal, l, b, bias, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
         route_exact(r, logits + tok * stride, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
       __syncwarp();  // the slots have been read
     }

@@ -6,8 +6,9 @@
 // one or two largest c.
 //
 // Nearly always f32 decides: with a bound on the error of every c at hand, two that lie further apart than their bounds are in
-// the order that 64 bits find. So a token is routed in f32 (route_fast), and again in 64 bits (route_exact) where two of the
-// deciding ones are too near, where more than 64 experts may be among the k best, or where a logit or a bias is not finite.
+// the order that 64 bits find. So a token is routed in f32 (route_fast); where two of the k best and their next, or two groups at
+// the border, are too near, these few are compared in 64 bits, and where more than 64 experts may be among the k best, a logit or a
+// bias is not finite, or a weight next to nothing, all of it is done again in 64 bits (route_exact).
 //
 // route_fast. The lanes of a warp are dealt to the groups, and a group's experts in runs to its lanes, in registers. The k-th
 // largest of the lanes' maxima is a bound below which no expert can be among the k best; what is above it, a few more than
@@ -22,6 +23,7 @@ namespace qg {
 
 constexpr int RO_MAXE = 1024, RO_MAXK = 32, RO_MAXG = 32;
 constexpr int RO_SLOTS = 64;  // experts that may be among the k best: two a lane
+constexpr int RO_NONE = 1 << 20;  // a rank behind all
 
 // A key whose order is that of the numbers, +0 and -0 alike; 1: NaN; 0: nothing there.
 __device__ __forceinline__ uint64_t ro_key(double v) {
@@ -165,96 +167,161 @@ __device__ __forceinline__ float ro_warp_sum(float v) {
 }
 
 struct RouteSlot {
-  float c, off;  // an expert's c, and by how much it may be off
+  union {
+    struct {
+      float c, off;  // an expert's c, and by how much it may be off
+    };
+    double exact;
+  };
   int id;
   float l;
 };
 
-// l, bias: this lane's experts (0 where it has fewer than NE), `mine` of them from id `first`. False: not decided.
+// Scores in 64 bits (softmax: over the sum), of finite logits.
+static __device__ __noinline__ double ro_score(bool soft, float l, float top) {
+  const double e = exp(soft ? (double)l - (double)top : -(double)l);
+  return soft ? e : 1. / (1. + e);
+}
 template <int NE>
-__device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& deal, const float (&l)[NE], const float (&bias)[NE],
-                                           bool biased, int first, int mine, int topk, RouteSlot* slots, int32_t* ids, float* rw) {
+__device__ __forceinline__ double ro_sum64(const float (&l)[NE], int mine, float top) {
+  double all = 0.;
+#pragma unroll 1
+  for (int i = 0; i < NE; ++i) {
+    float x = 0.f;
+#pragma unroll
+    for (int k = 0; k < NE; ++k) x = k == i ? l[k] : x;
+    const double e = ro_score(true, x, top);
+    if (i < mine) all += e;
+  }
+  return ro_warp_sum(all);
+}
+
+// l, b: this lane's experts (0 where it has fewer than NE), `mine` of them from id `first`; bias: all of them. False: not decided.
+template <int NE>
+__device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& deal, const float (&l)[NE], const float (&b)[NE],
+                                           const float* bias, int first, int mine, int topk, RouteSlot* slots, int32_t* ids, float* rw) {
   const int lane = threadIdx.x & 31;
   const bool grouped = r.top_group < r.n_group, soft = r.score == QG_SCORE_SOFTMAX;
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) odd |= !(fabsf(l[i]) < INFINITY) || !(fabsf(bias[i]) < INFINITY);
+  for (int i = 0; i < NE; ++i) odd |= !(fabsf(l[i]) < INFINITY) || !(fabsf(b[i]) < INFINITY);
   if (__any_sync(0xffffffffu, odd)) return false;
   float top = 0.f, sum = 1.f;
-  if (soft && (biased || grouped || !r.renorm)) {
+  if (soft) {
     top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (i < mine) top = fmaxf(top, l[i]);
+    const uint32_t k = __reduce_max_sync(0xffffffffu, top == -INFINITY ? 0u : ro_key32(top));
+    top = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+    if (bias || grouped || !r.renorm) {  // (else only ratios are wanted)
+      float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-    float part[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (i < mine) part[i & 3] += expf(l[i] - top);
-    sum = ro_warp_sum((part[0] + part[1]) + (part[2] + part[3]));
-  } else if (soft) {  // only ratios are wanted
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (i < mine) top = fmaxf(top, l[i]);
-#pragma unroll
-    for (int off = 16; off >= 1; off >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
+      for (int i = 0; i < NE; ++i)
+        if (i < mine) part[i & 3] += expf(l[i] - top);
+      sum = ro_warp_sum((part[0] + part[1]) + (part[2] + part[3]));
+    }
   }
-  // c, and its error's bound. Sigmoid: the exponent is off by |l| 2^-23.4 (its factor and product), ex2, sum and reciprocal by less than
-  // 2^-21 together. Softmax: the exponent by |l - top| 2^-24, expf by 2^-22, and the sum by its additions, at most 15 2^-24, the same
-  // 2^-22 and the exponents' mean error, below 7 2^-24 (an entropy). The bounds are twice that and more.
-  float c[NE];
-  auto off_of = [&](float p, float l1, float c1) {
-    return fmaf(p, fmaf(fabsf(l1 - top), 0x1p-22f, soft ? 0x1p-18f : 0x1p-20f), fmaf(fabsf(c1), 0x1p-22f, 0x1p-120f));
-  };
-  auto p_of = [&](float l1) { return soft ? ro_ex2((l1 - top) * 1.44269504f) * ro_rcp(sum) : ro_rcp(1.f + ro_ex2(l1 * -1.44269504f)); };
-  if (biased || grouped) {
+  // c, and a bound on the errors of the lane's. Sigmoid: the exponent is off by |l| 2^-23.4 (its factor and product), ex2, sum and
+  // reciprocal by less than 2^-21 together. Softmax: the exponent by |l - top| 2^-24, expf by 2^-22, and the sum by its additions, at
+  // most 15 2^-24, the same 2^-22 and the exponents' mean error, below 7 2^-24 (an entropy). The bounds are twice that and more.
+  float c[NE], off = 0.f;
+  if (bias || grouped) {
+    const float inv = ro_rcp(sum);
 #pragma unroll
-    for (int i = 0; i < NE; ++i) c[i] = p_of(l[i]) + bias[i];
+    for (int i = 0; i < NE; ++i) {
+      const float p = soft ? ro_ex2((l[i] - top) * 1.44269504f) * inv : ro_rcp(1.f + ro_ex2(l[i] * -1.44269504f));
+      c[i] = p + b[i];
+      if (i < mine) off = fmaxf(off, fmaf(p, fmaf(fabsf(l[i] - top), 0x1p-22f, soft ? 0x1p-18f : 0x1p-20f), fmaf(fabsf(c[i]), 0x1p-22f, 0x1p-120f)));
+    }
   }
   bool open = true;
   if (grouped) {
     // the group's two largest, by its lanes
-    float v0 = -INFINITY, v1 = -INFINITY, worst = 0.f;
+    float v0 = -INFINITY, v1 = -INFINITY;
 #pragma unroll
     for (int i = 0; i < NE; ++i)
       if (i < mine) {
         v1 = fmaxf(v1, fminf(v0, c[i]));
         v0 = fmaxf(v0, c[i]);
-        worst = fmaxf(worst, off_of(c[i] - bias[i], l[i], c[i]));
       }
-    for (int off = deal.lanes >> 1; off >= 1; off >>= 1) {
-      const float u0 = __shfl_xor_sync(0xffffffffu, v0, off), u1 = __shfl_xor_sync(0xffffffffu, v1, off);
-      worst = fmaxf(worst, __shfl_xor_sync(0xffffffffu, worst, off));
+    for (int x = deal.lanes >> 1; x >= 1; x >>= 1) {
+      const float u0 = __shfl_xor_sync(0xffffffffu, v0, x), u1 = __shfl_xor_sync(0xffffffffu, v1, x);
       v1 = fmaxf(fminf(v0, u0), fmaxf(v1, u1));
       v0 = fmaxf(v0, u0);
     }
     const float worth = r.group_top == 2 ? v0 + v1 : v0;
-    const float off = fmaf(2.f, worst, fabsf(worth) * 0x1p-22f);
-    const int g = lane / deal.lanes;
     int ahead = 0;
-    bool near = false;
-    for (int h = 0; h < r.n_group; ++h) {
-      const float its = __shfl_sync(0xffffffffu, worth, h * deal.lanes), its_off = __shfl_sync(0xffffffffu, off, h * deal.lanes);
-      ahead += its > worth;
-      near |= h != g && fabsf(its - worth) <= off + its_off;
-    }
-    if (__any_sync(0xffffffffu, near && g < r.n_group)) return false;
+    for (int h = 0; h < r.n_group; ++h) ahead += __shfl_sync(0xffffffffu, worth, h * deal.lanes) > worth;
     open = ahead < r.top_group;
+    // the least of those that stay and the most of the others: further apart than both may be off?
+    const bool there = lane < r.n_group * deal.lanes;
+    const uint32_t k = ro_key32(worth);
+    const uint32_t in = __reduce_min_sync(0xffffffffu, there && open ? k : 0xffffffffu);
+    const uint32_t out = __reduce_max_sync(0xffffffffu, there && !open ? k : 0u);
+    const uint32_t err = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(2.f, off, there ? fabsf(worth) * 0x1p-22f : 0.f)));
+    const int n_in = __popc(__ballot_sync(0xffffffffu, there && open));
+    auto value = [](uint32_t x) { return __uint_as_float(x & 0x80000000u ? x ^ 0x80000000u : ~x); };
+    const float reach = 2.f * __uint_as_float(err);
+    const float last = value(in), next = n_in > r.top_group * deal.lanes ? last : value(out);  // (groups equal at the border are all open)
+    if (last - next <= reach) {
+      // Above the next one by more than the errors: stays. Below the last one by more: does not. Those between in 64 bits, of each
+      // the experts that may be its largest.
+      const bool above = there && worth > next + reach, close = there && !above && worth >= last - reach;
+      const double all = soft ? ro_sum64<NE>(l, mine, top) : 1.;
+      double t0 = -INFINITY, t1 = -INFINITY;
+      uint32_t todo = 0;
+#pragma unroll
+      for (int i = 0; i < NE; ++i)
+        if (close && i < mine && c[i] + reach >= (r.group_top == 2 ? v1 : v0)) todo |= 1u << i;
+      while (__any_sync(0xffffffffu, todo)) {
+        const int k = __ffs(todo) - 1;
+        float x = 0.f, bx = 0.f;
+#pragma unroll
+        for (int i = 0; i < NE; ++i)
+          if (i == k) {
+            x = l[i];
+            bx = b[i];
+          }
+        if (todo) {
+          const double v = ro_score(soft, x, top) / all + (double)bx;
+          if (v > t0) {
+            t1 = t0;
+            t0 = v;
+          } else if (v > t1) {
+            t1 = v;
+          }
+        }
+        todo &= todo - 1;
+      }
+      for (int x = deal.lanes >> 1; x >= 1; x >>= 1) {
+        const double u0 = __shfl_xor_sync(0xffffffffu, t0, x), u1 = __shfl_xor_sync(0xffffffffu, t1, x);
+        t1 = t0 > u0 ? (u0 > t1 ? u0 : t1) : (t0 > u1 ? t0 : u1);
+        t0 = t0 > u0 ? t0 : u0;
+      }
+      const double exact = r.group_top == 2 ? t0 + t1 : t0;
+      const uint32_t all_close = __ballot_sync(0xffffffffu, close);
+      int left = r.top_group - __popc(__ballot_sync(0xffffffffu, above)) / deal.lanes;
+      const int g = lane / deal.lanes;
+      for (int h = 0; h < r.n_group; ++h) {
+        const double its = __shfl_sync(0xffffffffu, exact, h * deal.lanes);
+        if (all_close >> (h * deal.lanes) & 1) left -= its > exact || (its == exact && h < g);
+      }
+      open = above || (close && left > 0);
+    }
   }
-  if (!biased) {
+  if (!bias) {
+    off = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) c[i] = l[i];
   }
-  if (!open) mine = 0;
-  auto its_off = [&](int i) { return biased ? off_of(c[i] - bias[i], l[i], c[i]) : 0.f; };
+  const int here = open ? mine : 0;
   // the k-th largest of the lanes' maxima (of their lower bounds)
-  uint32_t key = 0;
+  float most = -INFINITY;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (i < mine) key = max(key, ro_key32(c[i] - its_off(i)));
-  uint32_t bound = 0;
+    if (i < here) most = fmaxf(most, c[i]);
+  uint32_t key = here > 0 ? ro_key32(most - off) : 0u, bound = 0;
   for (int n = 0; n < topk; ++n) {
     bound = __reduce_max_sync(0xffffffffu, key);
     if (key == bound) key = 0;  // (with every lane that has it: the bound is then lower than need be)
@@ -262,44 +329,69 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
   uint32_t in = 0;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (i < mine && ro_key32(c[i] + its_off(i)) >= bound) in |= 1u << i;
+    if (i < here && ro_key32(c[i] + off) >= bound) in |= 1u << i;
   int at = __popc(in);
   const int own = at;
 #pragma unroll
-  for (int off = 1; off < 32; off <<= 1) {
-    const int up = __shfl_up_sync(0xffffffffu, at, off);
-    if (lane >= off) at += up;
+  for (int x = 1; x < 32; x <<= 1) {
+    const int up = __shfl_up_sync(0xffffffffu, at, x);
+    if (lane >= x) at += up;
   }
   const int n = __shfl_sync(0xffffffffu, at, 31);
   if (n > RO_SLOTS) return false;
   at -= own;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (in >> i & 1) slots[at++] = {c[i], its_off(i), first + i, l[i]};
+    if (in >> i & 1) {
+      RouteSlot& to = slots[at++];
+      to.c = c[i];
+      to.off = off;
+      to.id = first + i;
+      to.l = l[i];
+    }
   __syncwarp();
   RouteSlot me[2];
   int rank[2] = {0, 0};
   bool near = false;
-  float w[2] = {0.f, 0.f};
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    me[j] = {-INFINITY, 0.f, 0x7fffffff, 0.f};
     if (j * 32 >= n) continue;
-    if (j * 32 + lane < n) me[j] = slots[j * 32 + lane];
+    const bool one = j * 32 + lane < n;
+    me[j] = slots[one ? j * 32 + lane : 0];
     bool close = false;
+#pragma unroll 4
     for (int m = 0; m < n; ++m) {
       const RouteSlot it = slots[m];
       rank[j] += it.c > me[j].c || (it.c == me[j].c && it.id < me[j].id);
       close |= m != j * 32 + lane && fabsf(it.c - me[j].c) <= it.off + me[j].off;
     }
-    if (j * 32 + lane >= n) rank[j] = topk;
-    if (rank[j] < topk) {
-      near |= close;
-      w[j] = soft ? expf(me[j].l - top) / sum : 1.f / (1.f + expf(-me[j].l));
+    if (!one) rank[j] = RO_NONE;
+    near |= close && rank[j] < topk;
+  }
+  if (bias && __any_sync(0xffffffffu, near)) {  // these few in 64 bits
+    const double all = soft ? ro_sum64<NE>(l, mine, top) : 1.;
+    double v[2];
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j * 32 < n)
+        v[j] = ro_score(soft, me[j].l, top) / all + (double)bias[me[j].id];
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+      if (j * 32 + lane < n) slots[j * 32 + lane].exact = v[j];
+    __syncwarp();
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      if (j * 32 >= n || rank[j] == RO_NONE) continue;
+      rank[j] = 0;
+      for (int m = 0; m < n; ++m) rank[j] += slots[m].exact > v[j] || (slots[m].exact == v[j] && slots[m].id < me[j].id);
     }
   }
-  if (__any_sync(0xffffffffu, biased && near)) return false;
-  if (n <= 32) rank[1] = topk;
+  float w[2] = {0.f, 0.f};
+  if (n <= 32) rank[1] = RO_NONE;
+#pragma unroll
+  for (int j = 0; j < 2; ++j)
+    if (rank[j] < topk) w[j] = soft ? expf(me[j].l - top) / sum : 1.f / (1.f + expf(-me[j].l));
   if (r.renorm) {
     const float all = ro_warp_sum(w[0] + w[1]);
     if (all < 0x1p-100f) return false;  // (weights that f32 holds badly)

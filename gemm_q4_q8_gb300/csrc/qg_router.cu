@@ -129,7 +129,7 @@ __device__ __forceinline__ bool route_column_fast(const qg_route& r, const Route
     b[i] = bias && i < mine ? bias[first + i] : 0.f;
     l[i] = i < mine ? logits[first + i] : 0.f;
   }
-  return route_fast(r, deal, l, b, bias != nullptr, first, mine, topk, slots, ids, rw);
+  return route_fast(r, deal, l, b, bias, first, mine, topk, slots, ids, rw);
 }
 __device__ __forceinline__ void route_column(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
                                              RouteSlot* slots, int32_t* ids, float* rw) {
