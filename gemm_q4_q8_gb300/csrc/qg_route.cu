@@ -14,15 +14,8 @@ namespace {
 constexpr int RO_WARPS = 4;
 constexpr int RO_BLOCKS = 152 * 12;  // with more tokens than warps of these, each takes several in turn
 
-// One lane's experts of a row.
-template <int NE>
-__device__ __forceinline__ void load_row(const float* row, int first, int mine, float (&v)[NE]) {
-#pragma unroll
-  for (int i = 0; i < NE; ++i) v[i] = i < mine ? row[first + i] : 0.f;
-}
-
-// NE: experts of a lane, at most; 0: all in 64 bits
-template <int NE>
+// NE: experts of a lane, at most; 0: all in 64 bits. FULL: every lane has NE. WIDE: and their logits are aligned to 16 bytes.
+template <int NE, bool FULL, bool WIDE>
 __global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? 8 : 1)
     route_kernel(const __grid_constant__ qg_route r, const float* logits, int64_t stride, const float* bias, int ntok, int E,
                  int topk, int32_t* ids, float* rw) {
@@ -38,17 +31,25 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? 8 : 1)
   } else {
     __shared__ RouteSlot slots[RO_WARPS][RO_SLOTS];
     const RouteDeal deal = route_deal(r, E);
-    const int group = lane / deal.lanes, from = (lane & (deal.lanes - 1)) * deal.per;
-    const int first = group * deal.size + from;
-    const int mine = first < E ? max(0, min(deal.per, deal.size - from)) : 0;
+    int first, mine;
+    route_share(deal, E, first, mine);
     float b[NE], l[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) b[i] = 0.f;
-    if (bias) load_row(bias, first, mine, b);
+    for (int i = 0; i < NE; ++i) b[i] = bias && (FULL || i < mine) ? bias[first + i] : 0.f;
     for (; tok < ntok; tok += step) {
-      load_row(logits + tok * stride, first, mine, l);
-      if (!route_fast(r, deal, l, b, bias, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
-        route_exact(r, logits + tok * stride, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
+      const float* const row = logits + tok * stride;
+      if constexpr (WIDE) {
+#pragma unroll
+        for (int i = 0; i < NE; i += 4) {
+          const float4 x = *reinterpret_cast<const float4*>(row + first + i);
+          l[i] = x.x; l[i + 1] = x.y; l[i + 2] = x.z; l[i + 3] = x.w;
+        }
+      } else {
+#pragma unroll
+        for (int i = 0; i < NE; ++i) l[i] = FULL || i < mine ? row[first + i] : -INFINITY;
+      }
+      if (!route_fast<NE, FULL>(r, deal, l, b, row, bias, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
+        route_exact(r, row, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
       __syncwarp();  // the slots have been read
     }
   }
@@ -68,14 +69,21 @@ bool route_shape_ok(const qg_route& r, int E, int topk) {
 
 cudaError_t route_launch(const qg_route& r, const float* logits, int64_t stride, const float* bias, int ntok, int E, int topk,
                          int32_t* ids, float* rw, cudaStream_t s) {
-  const int per = route_deal(r, E).per;
-  const auto kern = per <= 1    ? route_kernel<1>
-                    : per <= 2  ? route_kernel<2>
-                    : per <= 4  ? route_kernel<4>
-                    : per <= 8  ? route_kernel<8>
-                    : per <= 16 ? route_kernel<16>
-                    : per <= 32 ? route_kernel<32>
-                                : route_kernel<0>;
+  const RouteDeal deal = route_deal(r, E);
+  const int per = deal.per;
+  const bool full = E == 32 * per, wide = full && per % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (ntok == 1 || stride % 4 == 0);
+  const auto kern = wide && per == 4    ? route_kernel<4, true, true>
+                    : wide && per == 8  ? route_kernel<8, true, true>
+                    : wide && per == 16 ? route_kernel<16, true, true>
+                    : wide && per == 32 ? route_kernel<32, true, true>
+                    : full && per == 2  ? route_kernel<2, true, false>
+                    : per <= 1          ? route_kernel<1, false, false>
+                    : per <= 2          ? route_kernel<2, false, false>
+                    : per <= 4          ? route_kernel<4, false, false>
+                    : per <= 8          ? route_kernel<8, false, false>
+                    : per <= 16         ? route_kernel<16, false, false>
+                    : per <= 32         ? route_kernel<32, false, false>
+                                        : route_kernel<0, false, false>;
   const int64_t blocks = ((int64_t)ntok + RO_WARPS - 1) / RO_WARPS;
   return launch_pdl(kern, dim3((unsigned)(blocks < RO_BLOCKS ? blocks : RO_BLOCKS)), dim3(RO_WARPS * 32),
                     (size_t)RO_WARPS * E * sizeof(double), s, 0, LC_L1, r, logits, stride, bias, ntok, E, topk, ids, rw);

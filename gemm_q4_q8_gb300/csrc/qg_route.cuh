@@ -145,6 +145,13 @@ __host__ __device__ inline RouteDeal route_deal(const qg_route& r, int E) {
   return d;
 }
 
+// A lane's: `mine` experts from id `first`.
+__device__ __forceinline__ void route_share(const RouteDeal& d, int E, int& first, int& mine) {
+  const int lane = threadIdx.x & 31, from = (lane & (d.lanes - 1)) * d.per;
+  first = lane / d.lanes * d.size + from;
+  mine = first < E ? max(0, min(d.per, d.size - from)) : 0;
+}
+
 __device__ __forceinline__ float ro_ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -166,85 +173,84 @@ __device__ __forceinline__ float ro_warp_sum(float v) {
   return v;
 }
 
+// An expert that may be among the k best: its c in 32 or in 64 bits.
 struct RouteSlot {
   union {
-    struct {
-      float c, off;  // an expert's c, and by how much it may be off
-    };
+    float c;
     double exact;
   };
   int id;
-  float l;
 };
+// A number of a key.
+__device__ __forceinline__ float ro_value(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
 // Scores in 64 bits (softmax: over the sum), of finite logits.
 static __device__ __noinline__ double ro_score(bool soft, float l, float top) {
   const double e = exp(soft ? (double)l - (double)top : -(double)l);
   return soft ? e : 1. / (1. + e);
 }
-template <int NE>
-__device__ __forceinline__ double ro_sum64(const float (&l)[NE], int mine, float top) {
+static __device__ __noinline__ double ro_sum64(const float* row, int first, int mine, float top) {
   double all = 0.;
-#pragma unroll 1
-  for (int i = 0; i < NE; ++i) {
-    float x = 0.f;
-#pragma unroll
-    for (int k = 0; k < NE; ++k) x = k == i ? l[k] : x;
-    const double e = ro_score(true, x, top);
-    if (i < mine) all += e;
-  }
+  for (int i = 0; i < mine; ++i) all += ro_score(true, row[first + i], top);
   return ro_warp_sum(all);
 }
 
-// l, b: this lane's experts (0 where it has fewer than NE), `mine` of them from id `first`; bias: all of them. False: not decided.
-template <int NE>
+// The experts of this lane: `mine` of them from id `first`, their logits l and biases b in registers (where there are fewer than NE:
+// -infinity and 0; FULL: there are not), the logits of all at `row`. False: not decided.
+template <int NE, bool FULL>
 __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& deal, const float (&l)[NE], const float (&b)[NE],
-                                           const float* bias, int first, int mine, int topk, RouteSlot* slots, int32_t* ids, float* rw) {
+                                           const float* row, const float* bias, int first, int mine, int topk, RouteSlot* slots,
+                                           int32_t* ids, float* rw) {
   const int lane = threadIdx.x & 31;
   const bool grouped = r.top_group < r.n_group, soft = r.score == QG_SCORE_SOFTMAX;
+  auto here = [&](int i) { return FULL || i < mine; };
+  // the largest of the logits, and how large they are
+  float most = -INFINITY, size = 0.f;
   bool odd = false;
 #pragma unroll
-  for (int i = 0; i < NE; ++i) odd |= !(fabsf(l[i]) < INFINITY) || !(fabsf(b[i]) < INFINITY);
+  for (int i = 0; i < NE; ++i) {
+    most = fmaxf(most, l[i]);
+    odd |= here(i) && !(fabsf(l[i]) + fabsf(b[i]) < INFINITY);
+    size = fmaxf(size, here(i) ? fabsf(l[i]) : 0.f);
+  }
   if (__any_sync(0xffffffffu, odd)) return false;
   float top = 0.f, sum = 1.f;
   if (soft) {
-    top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (i < mine) top = fmaxf(top, l[i]);
-    const uint32_t k = __reduce_max_sync(0xffffffffu, top == -INFINITY ? 0u : ro_key32(top));
-    top = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
-    if (bias || grouped || !r.renorm) {  // (else only ratios are wanted)
+    top = ro_value(__reduce_max_sync(0xffffffffu, ro_key32(most)));
+    size = fmaxf(size, 0.f) + fabsf(top);  // (not less than |l - top|)
+    if (bias || grouped || !r.renorm) {    // (else only ratios are wanted)
       float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int i = 0; i < NE; ++i)
-        if (i < mine) part[i & 3] += expf(l[i] - top);
+      for (int i = 0; i < NE; ++i) part[i & 3] += expf(l[i] - top);
       sum = ro_warp_sum((part[0] + part[1]) + (part[2] + part[3]));
     }
   }
-  // c, and a bound on the errors of the lane's. Sigmoid: the exponent is off by |l| 2^-23.4 (its factor and product), ex2, sum and
-  // reciprocal by less than 2^-21 together. Softmax: the exponent by |l - top| 2^-24, expf by 2^-22, and the sum by its additions, at
-  // most 15 2^-24, the same 2^-22 and the exponents' mean error, below 7 2^-24 (an entropy). The bounds are twice that and more.
+  // c, and a bound on the errors of all. Sigmoid: the exponent is off by |l| 2^-23.4 (its factor and product), ex2, sum and reciprocal
+  // by less than 2^-21 together. Softmax: the exponent by |l - top| 2^-24 more, expf by 2^-22, and the sum by its additions, at most
+  // 15 2^-24, the same 2^-22 and the exponents' mean error, below 7 2^-24 (an entropy). The bounds are twice that and more.
   float c[NE], off = 0.f;
   if (bias || grouped) {
     const float inv = ro_rcp(sum);
+    float p_most = 0.f, b_most = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) {
       const float p = soft ? ro_ex2((l[i] - top) * 1.44269504f) * inv : ro_rcp(1.f + ro_ex2(l[i] * -1.44269504f));
-      c[i] = p + b[i];
-      if (i < mine) off = fmaxf(off, fmaf(p, fmaf(fabsf(l[i] - top), 0x1p-22f, soft ? 0x1p-18f : 0x1p-20f), fmaf(fabsf(c[i]), 0x1p-22f, 0x1p-120f)));
+      p_most = fmaxf(p_most, p);
+      b_most = fmaxf(b_most, fabsf(b[i]));
+      c[i] = here(i) ? p + b[i] : -INFINITY;
     }
+    off = fmaf(p_most, fmaf(size, 0x1p-21f, soft ? 0x1p-18f : 0x1p-20f), fmaf(p_most + b_most, 0x1p-22f, 0x1p-120f));
+    off = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(off)));
   }
   bool open = true;
   if (grouped) {
     // the group's two largest, by its lanes
     float v0 = -INFINITY, v1 = -INFINITY;
 #pragma unroll
-    for (int i = 0; i < NE; ++i)
-      if (i < mine) {
-        v1 = fmaxf(v1, fminf(v0, c[i]));
-        v0 = fmaxf(v0, c[i]);
-      }
+    for (int i = 0; i < NE; ++i) {
+      v1 = fmaxf(v1, fminf(v0, c[i]));
+      v0 = fmaxf(v0, c[i]);
+    }
     for (int x = deal.lanes >> 1; x >= 1; x >>= 1) {
       const float u0 = __shfl_xor_sync(0xffffffffu, v0, x), u1 = __shfl_xor_sync(0xffffffffu, v1, x);
       v1 = fmaxf(fminf(v0, u0), fmaxf(v1, u1));
@@ -252,48 +258,38 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
     }
     const float worth = r.group_top == 2 ? v0 + v1 : v0;
     int ahead = 0;
+#pragma unroll 4
     for (int h = 0; h < r.n_group; ++h) ahead += __shfl_sync(0xffffffffu, worth, h * deal.lanes) > worth;
+    const bool there = lane < r.n_group * deal.lanes;
     open = ahead < r.top_group;
     // the least of those that stay and the most of the others: further apart than both may be off?
-    const bool there = lane < r.n_group * deal.lanes;
     const uint32_t k = ro_key32(worth);
-    const uint32_t in = __reduce_min_sync(0xffffffffu, there && open ? k : 0xffffffffu);
+    const float last = ro_value(__reduce_min_sync(0xffffffffu, there && open ? k : 0xffffffffu));
     const uint32_t out = __reduce_max_sync(0xffffffffu, there && !open ? k : 0u);
-    const uint32_t err = __reduce_max_sync(0xffffffffu, __float_as_uint(fmaf(2.f, off, there ? fabsf(worth) * 0x1p-22f : 0.f)));
+    const float reach = fmaf(4.f, off, fabsf(last) * 0x1p-21f);  // twice the error of a worth
     const int n_in = __popc(__ballot_sync(0xffffffffu, there && open));
-    auto value = [](uint32_t x) { return __uint_as_float(x & 0x80000000u ? x ^ 0x80000000u : ~x); };
-    const float reach = 2.f * __uint_as_float(err);
-    const float last = value(in), next = n_in > r.top_group * deal.lanes ? last : value(out);  // (groups equal at the border are all open)
+    const float next = n_in > r.top_group * deal.lanes ? last : ro_value(out);  // (groups equal at the border are all open)
     if (last - next <= reach) {
       // Above the next one by more than the errors: stays. Below the last one by more: does not. Those between in 64 bits, of each
       // the experts that may be its largest.
       const bool above = there && worth > next + reach, close = there && !above && worth >= last - reach;
-      const double all = soft ? ro_sum64<NE>(l, mine, top) : 1.;
+      const double all = soft ? ro_sum64(row, first, mine, top) : 1.;
       double t0 = -INFINITY, t1 = -INFINITY;
       uint32_t todo = 0;
 #pragma unroll
       for (int i = 0; i < NE; ++i)
-        if (close && i < mine && c[i] + reach >= (r.group_top == 2 ? v1 : v0)) todo |= 1u << i;
-      while (__any_sync(0xffffffffu, todo)) {
-        const int k = __ffs(todo) - 1;
-        float x = 0.f, bx = 0.f;
-#pragma unroll
-        for (int i = 0; i < NE; ++i)
-          if (i == k) {
-            x = l[i];
-            bx = b[i];
-          }
-        if (todo) {
-          const double v = ro_score(soft, x, top) / all + (double)bx;
-          if (v > t0) {
-            t1 = t0;
-            t0 = v;
-          } else if (v > t1) {
-            t1 = v;
-          }
+        if (close && here(i) && c[i] + reach >= (r.group_top == 2 ? v1 : v0)) todo |= 1u << i;
+      for (; todo; todo &= todo - 1) {
+        const int e = first + __ffs(todo) - 1;
+        const double v = ro_score(soft, row[e], top) / all + (bias ? (double)bias[e] : 0.);
+        if (v > t0) {
+          t1 = t0;
+          t0 = v;
+        } else if (v > t1) {
+          t1 = v;
         }
-        todo &= todo - 1;
       }
+      __syncwarp();
       for (int x = deal.lanes >> 1; x >= 1; x >>= 1) {
         const double u0 = __shfl_xor_sync(0xffffffffu, t0, x), u1 = __shfl_xor_sync(0xffffffffu, t1, x);
         t1 = t0 > u0 ? (u0 > t1 ? u0 : t1) : (t0 > u1 ? t0 : u1);
@@ -314,22 +310,22 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
     off = 0.f;
 #pragma unroll
     for (int i = 0; i < NE; ++i) c[i] = l[i];
-  }
-  const int here = open ? mine : 0;
-  // the k-th largest of the lanes' maxima (of their lower bounds)
-  float most = -INFINITY;
+  } else {
+    most = -INFINITY;
 #pragma unroll
-  for (int i = 0; i < NE; ++i)
-    if (i < here) most = fmaxf(most, c[i]);
-  uint32_t key = here > 0 ? ro_key32(most - off) : 0u, bound = 0;
+    for (int i = 0; i < NE; ++i) most = fmaxf(most, c[i]);
+  }
+  // the k-th largest of the lanes' maxima, less what it may be off and what the others may be
+  uint32_t key = open && most > -INFINITY ? ro_key32(most) : 0u, bound = 0;
   for (int n = 0; n < topk; ++n) {
     bound = __reduce_max_sync(0xffffffffu, key);
     if (key == bound) key = 0;  // (with every lane that has it: the bound is then lower than need be)
   }
+  const float least = open ? (bound ? ro_value(bound) - 2.f * off : -3.402823466e38f) : INFINITY;
   uint32_t in = 0;
 #pragma unroll
   for (int i = 0; i < NE; ++i)
-    if (i < here && ro_key32(c[i] + off) >= bound) in |= 1u << i;
+    if (c[i] >= least) in |= 1u << i;
   int at = __popc(in);
   const int own = at;
 #pragma unroll
@@ -339,74 +335,72 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
   }
   const int n = __shfl_sync(0xffffffffu, at, 31);
   if (n > RO_SLOTS) return false;
-  at -= own;
+  RouteSlot* to = slots + (at - own);
 #pragma unroll
   for (int i = 0; i < NE; ++i)
     if (in >> i & 1) {
-      RouteSlot& to = slots[at++];
-      to.c = c[i];
-      to.off = off;
-      to.id = first + i;
-      to.l = l[i];
+      to->c = c[i];
+      to->id = first + i;
+      ++to;
     }
   __syncwarp();
-  RouteSlot me[2];
-  int rank[2] = {0, 0};
+  // each lane's one or two: how many are ahead, and whether another is too near to tell
+  int rank[2] = {RO_NONE, RO_NONE}, id[2] = {0, 0};
   bool near = false;
+  const float reach = 2.f * off;
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
-    if (j * 32 >= n) continue;
+    if (j * 32 >= n) break;
     const bool one = j * 32 + lane < n;
-    me[j] = slots[one ? j * 32 + lane : 0];
-    bool close = false;
+    const float mine_c = one ? slots[j * 32 + lane].c : INFINITY;
+    id[j] = one ? slots[j * 32 + lane].id : 0;
+    int ahead = 0, close = 0;
 #pragma unroll 4
     for (int m = 0; m < n; ++m) {
-      const RouteSlot it = slots[m];
-      rank[j] += it.c > me[j].c || (it.c == me[j].c && it.id < me[j].id);
-      close |= m != j * 32 + lane && fabsf(it.c - me[j].c) <= it.off + me[j].off;
+      const float d = slots[m].c - mine_c;
+      ahead += d > 0.f;
+      close += fabsf(d) <= reach;
     }
-    if (!one) rank[j] = RO_NONE;
-    near |= close && rank[j] < topk;
+    if (one) rank[j] = ahead;
+    near |= one && close > 1 && ahead < topk;
   }
-  if (bias && __any_sync(0xffffffffu, near)) {  // these few in 64 bits
-    const double all = soft ? ro_sum64<NE>(l, mine, top) : 1.;
+  if (__any_sync(0xffffffffu, near)) {  // these few in 64 bits (without a bias: equal ones by their ids)
+    const double all = soft && bias ? ro_sum64(row, first, mine, top) : 1.;
     double v[2];
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (j * 32 < n)
-        v[j] = ro_score(soft, me[j].l, top) / all + (double)bias[me[j].id];
+      if (rank[j] != RO_NONE) v[j] = bias ? ro_score(soft, row[id[j]], top) / all + (double)bias[id[j]] : (double)row[id[j]];
     __syncwarp();
 #pragma unroll
     for (int j = 0; j < 2; ++j)
-      if (j * 32 + lane < n) slots[j * 32 + lane].exact = v[j];
+      if (rank[j] != RO_NONE) slots[j * 32 + lane].exact = v[j];
     __syncwarp();
 #pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      if (j * 32 >= n || rank[j] == RO_NONE) continue;
-      rank[j] = 0;
-      for (int m = 0; m < n; ++m) rank[j] += slots[m].exact > v[j] || (slots[m].exact == v[j] && slots[m].id < me[j].id);
-    }
+    for (int j = 0; j < 2; ++j)
+      if (rank[j] != RO_NONE) {
+        rank[j] = 0;
+        for (int m = 0; m < n; ++m) rank[j] += slots[m].exact > v[j] || (slots[m].exact == v[j] && slots[m].id < id[j]);
+      }
   }
-  float w[2] = {0.f, 0.f};
-  if (n <= 32) rank[1] = RO_NONE;
+  // (the weights' errors: expf 2^-22, the sums and the reciprocals below 2^-22 each)
+  float w[2] = {0.f, 0.f}, all = 0.f;
+  const float inv = soft ? ro_rcp(sum) : 1.f;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
-    if (rank[j] < topk) w[j] = soft ? expf(me[j].l - top) / sum : 1.f / (1.f + expf(-me[j].l));
-  if (r.renorm) {
-    const float all = ro_warp_sum(w[0] + w[1]);
-    if (all < 0x1p-100f) return false;  // (weights that f32 holds badly)
-    w[0] /= all;
-    w[1] /= all;
-  }
-  bool small = false;
-#pragma unroll
-  for (int j = 0; j < 2; ++j) small |= rank[j] < topk && w[j] < 0x1p-100f;
+    if (rank[j] < topk) {
+      const float x = row[id[j]];
+      w[j] = soft ? expf(x - top) * inv : ro_rcp(1.f + expf(-x));
+    }
+  all = ro_warp_sum(w[0] + w[1]);
+  const float by = r.renorm ? ro_rcp(all) : 1.f;
+  // weights that f32 holds badly, or their reciprocal's
+  const bool small = (rank[0] < topk && w[0] < 0x1p-100f) || (rank[1] < topk && w[1] < 0x1p-100f);
   if (__any_sync(0xffffffffu, small)) return false;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (rank[j] < topk) {
-      ids[rank[j]] = me[j].id;
-      rw[rank[j]] = w[j] * r.scale;
+      ids[rank[j]] = id[j];
+      rw[rank[j]] = w[j] * by * r.scale;
     }
   __syncwarp();
   return true;

@@ -121,15 +121,15 @@ struct Plan {
 template <int NE>
 __device__ __forceinline__ bool route_column_fast(const qg_route& r, const RouteDeal& deal, const float* logits, const float* bias, int E,
                                                   int topk, RouteSlot* slots, int32_t* ids, float* rw) {
-  const int lane = threadIdx.x & 31, from = (lane & (deal.lanes - 1)) * deal.per, first = lane / deal.lanes * deal.size + from;
-  const int mine = first < E ? max(0, min(deal.per, deal.size - from)) : 0;
+  int first, mine;
+  route_share(deal, E, first, mine);
   float b[NE], l[NE];
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     b[i] = bias && i < mine ? bias[first + i] : 0.f;
-    l[i] = i < mine ? logits[first + i] : 0.f;
+    l[i] = i < mine ? logits[first + i] : -INFINITY;
   }
-  return route_fast(r, deal, l, b, bias, first, mine, topk, slots, ids, rw);
+  return route_fast<NE, false>(r, deal, l, b, logits, bias, first, mine, topk, slots, ids, rw);
 }
 __device__ __forceinline__ void route_column(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
                                              RouteSlot* slots, int32_t* ids, float* rw) {
