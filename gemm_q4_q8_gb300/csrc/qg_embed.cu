@@ -1,6 +1,6 @@
-// qg_embed.cu -- embedding lookup: rows of a matrix in the library's layout by token id, times a scale (qembed). A thread
-// makes eight neighbouring elements at a time. For Q8_0 and Q4_0 it reads the 16 stored bytes that hold them (its neighbours
-// read the same ones) and takes every second byte, as the halves of a group lie byte by byte; a weight, an integer times its
+// qg_embed.cu -- embedding lookup: rows of a matrix in the library's layout by token id, times a scale (qembed). A lane makes
+// units of neighbouring elements that it stores in one access, 4 f32 or 8 f16. For Q8_0 and Q4_0 it reads the 8 or 16 stored
+// bytes that hold them and takes every second one, as the halves of a group lie byte by byte; a weight, an integer times its
 // f16 scale, is exact in f32, then multiplied by the call's scale and rounded.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -13,49 +13,89 @@ namespace qg {
 
 namespace {
 
-constexpr int EM_THREADS = 128;
+constexpr int EM_WARPS = 4;
 
-template <int QT, class TO>
-__global__ void __launch_bounds__(EM_THREADS)
-    embed_kernel(const void* q, const uint16_t* scl, int rows, int k, const int32_t* ids, float scale, TO* y, int64_t ys,
-                 int32_t* err) {
+__device__ __forceinline__ void store_unit(float* p, const float (&v)[4]) { *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]); }
+__device__ __forceinline__ void store_unit(__half* p, const float (&v)[8]) { store8(p, v); }
+
+// U: units of a lane, whose loads are in flight together. A warp makes 32 U units of a token's row.
+template <int QT, class TO, int U>
+__global__ void __launch_bounds__(EM_WARPS * 32)
+    embed_kernel(const void* q, const uint16_t* scl, int rows, int k, const int32_t* ids, int64_t pieces, int per_tok, float scale, TO* y,
+                 int64_t ys, int32_t* err) {
+  constexpr int E = 16 / sizeof(TO);  // elements of a unit; twice as many bytes hold them
   pdl_trigger();
   pdl_wait();
-  const int tok = blockIdx.x, id = ids[tok];
+  const int lane = threadIdx.x & 31;
+  const int64_t piece = (int64_t)blockIdx.x * EM_WARPS + (threadIdx.x >> 5);
+  if (piece >= pieces) return;
+  const int64_t tok = per_tok == 1 ? piece : piece / per_tok;
+  const int part = (int)(piece - tok * per_tok), id = ids[tok];
   const bool bad = id < 0 || id >= rows;
-  if (bad && err && blockIdx.y == 0 && threadIdx.x == 0) atomicOr(err, QG_EMBED_BAD_ID);
+  if (bad && err && part == 0 && lane == 0) atomicOr(err, QG_EMBED_BAD_ID);
   TO* const out = y + tok * ys;
-  for (int i = blockIdx.y * EM_THREADS + threadIdx.x; i < k / 8; i += gridDim.y * EM_THREADS) {
-    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-    if (!bad) {
-      if constexpr (QT == QG_F16) {
-        load8(static_cast<const __half*>(q) + (size_t)id * k + 8 * i, v);
+  const int first = part * (32 * U) + lane, units = k / E;
+  uint32_t b[U][E / 2];
+  uint16_t d[U];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] *= scale;
-      } else {
-        // eighth i of the row: of Q8_0 half i % 2 of group i / 2; of Q4_0 half i % 2 of block i / 4, its low or high bits
-        const uint4 b = *reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(q) +
-                                                        (QT == QG_Q8_0 ? (size_t)id * k + 16 * (i / 2) : (size_t)id * (k / 2) + 16 * (i / 4)));
-        const float d = h2f(scl[(size_t)id * (k / 32) + i / 4]);
-        const uint32_t w[4] = {b.x, b.y, b.z, b.w};
-        const int shift = 8 * (i & 1) + (QT == QG_Q8_0 ? 0 : 4 * ((i >> 1) & 1));
+  for (int j = 0; j < U; ++j) {
+    const int i = first + 32 * j, e = E * i;  // its first element
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const uint32_t u = w[e >> 1] >> (shift + 16 * (e & 1));
-          const int n = QT == QG_Q8_0 ? (int)(int8_t)(u & 0xff) : (int)(u & 15) - 8;
-          v[e] = (float)n * d * scale;
-        }
+    for (int x = 0; x < E / 2; ++x) b[j][x] = 0;
+    d[j] = 0;
+    if (bad || i >= units) continue;
+    const size_t at = QT == QG_F16    ? ((size_t)id * k + e) * 2
+                      : QT == QG_Q8_0 ? (size_t)id * k + (e & ~15) + 2 * (e & 7)
+                                      : (size_t)id * (k / 2) + e / 32 * 16 + 2 * (e & 7);
+    const uint8_t* const p = static_cast<const uint8_t*>(q) + at;
+    if constexpr (E == 8) {
+      const uint4 x = *reinterpret_cast<const uint4*>(p);
+      b[j][0] = x.x; b[j][1] = x.y; b[j][2] = x.z; b[j][3] = x.w;
+    } else {
+      const uint2 x = *reinterpret_cast<const uint2*>(p);
+      b[j][0] = x.x; b[j][1] = x.y;
+    }
+    if constexpr (QT != QG_F16) d[j] = scl[(size_t)id * (k / 32) + e / 32];
+  }
+#pragma unroll
+  for (int j = 0; j < U; ++j) {
+    const int i = first + 32 * j, e = E * i;
+    if (i >= units) continue;
+    float v[E];
+    if constexpr (QT == QG_F16) {
+#pragma unroll
+      for (int x = 0; x < E / 2; ++x) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&b[j][x]));
+        v[2 * x] = f.x * scale;
+        v[2 * x + 1] = f.y * scale;
+      }
+    } else {
+      const float f = h2f(d[j]);
+      const int shift = (e & 8) + (QT == QG_Q8_0 ? 0 : (e & 16) / 4);  // the half of the group; of Q4_0 its low or high bits
+#pragma unroll
+      for (int x = 0; x < E; ++x) {
+        const uint32_t u = b[j][x >> 1] >> (shift + 16 * (x & 1));
+        const int n = QT == QG_Q8_0 ? (int)(int8_t)(u & 0xff) : (int)(u & 15) - 8;
+        v[x] = bad ? 0.f : (float)n * f * scale;
       }
     }
-    store8(out + 8 * i, v);
+    store_unit(out + e, v);
   }
+}
+
+template <int QT, class TO, int U>
+cudaError_t embed_u(const EmbedArgs& a, cudaStream_t s) {
+  const int64_t units = (int64_t)a.k * sizeof(TO) / 16;
+  const int per_tok = (int)((units + 32 * U - 1) / (32 * U));
+  const int64_t pieces = (int64_t)a.ntok * per_tok;
+  return launch_pdl(embed_kernel<QT, TO, U>, dim3((unsigned)((pieces + EM_WARPS - 1) / EM_WARPS)), dim3(EM_WARPS * 32), 0, s, 0, LC_L1, a.q,
+                    a.scl, a.rows, a.k, a.ids, pieces, per_tok, a.scale, static_cast<TO*>(a.y), a.ys, a.err);
 }
 
 template <int QT, class TO>
 cudaError_t embed_go(const EmbedArgs& a, cudaStream_t s) {
-  const int parts = (a.k / 8 + EM_THREADS - 1) / EM_THREADS;
-  return launch_pdl(embed_kernel<QT, TO>, dim3((unsigned)a.ntok, (unsigned)parts), dim3(EM_THREADS), 0, s, 0, LC_L1, a.q, a.scl, a.rows, a.k,
-                    a.ids, a.scale, static_cast<TO*>(a.y), a.ys, a.err);
+  // one unit a lane where that makes no more warps than the machine holds at a time
+  return (int64_t)a.ntok * a.k * sizeof(TO) <= (int64_t)152 * 64 * 512 ? embed_u<QT, TO, 1>(a, s) : embed_u<QT, TO, 4>(a, s);
 }
 
 template <class TO>
