@@ -7,7 +7,9 @@
 // Squares that leave the range of f32 (elements beyond 10^18, or all below 10^-17 with an eps as small) are summed again in
 // 64 bits: a row that needs it shows by its sum.
 //
-// Bound by memory.
+// Bound by memory: 8,191 rows of 5,120 f32 with the residual, to f16 and f32: 84.6 us, 587 MB, the rate of a large copy; without it 38.6 us,
+// 252 MB, 96% of it. To Q8_0 by its instructions, 90 for eight elements: 20,011 rows of 2,048 f16 in 33 us, where the bytes take 18.5. One
+// row of 5,120: 2.5 us, the launch, two trips to memory and one barrier.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -58,9 +60,12 @@ __device__ __forceinline__ A row_sum(A v, int lanes, A* part) {
   return v;
 }
 
-// YT: the type of y. VEC: rows in groups of eight elements, 16-byte aligned. U: such groups of a thread.
-template <class TI, int YT, bool VEC, int U, bool BLOCK>
+// YT: the type of y. ROWS: SINGLE, any rows, element by element; EIGHTS, in groups of eight elements, 16-byte aligned; FULL, and
+// every thread of a block has U such groups.
+enum { SINGLE, EIGHTS, FULL };
+template <class TI, int YT, int ROWS, int U, bool BLOCK>
 __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(const __grid_constant__ NormParams<TI> p, int lanes) {
+  constexpr bool VEC = ROWS != SINGLE;
   __shared__ float part[BLOCK ? 32 : 1];
   __shared__ double part64[BLOCK ? 32 : 1];
   pdl_trigger();
@@ -76,7 +81,7 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
   TI* const sum = p.sum ? p.sum + tok * p.ss + head * p.n : nullptr;
   // element e of the thread's group c; ok: is it one
   auto at = [&](int c, int e) { return VEC ? (c * width + t) * 8 + e : (c * 8 + e) * width + t; };
-  auto ok = [&](int i) { return live && i < p.n; };
+  auto ok = [&](int i) { return ROWS == FULL || (live && i < p.n); };
 
   float v[U][8];
 #pragma unroll
@@ -117,12 +122,15 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
       }
     }
   }
-  float ss = 0.f;
+  float2 sq = make_float2(0.f, 0.f);
 #pragma unroll
   for (int c = 0; c < U; ++c)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(v[c][e], v[c][e], ss);
-  ss = row_sum<BLOCK>(ss, lanes, part);
+    for (int e = 0; e < 8; e += 2) {
+      const float2 x = make_float2(v[c][e], v[c][e + 1]);
+      sq = fma2(x, x, sq);
+    }
+  const float ss = row_sum<BLOCK>(sq.x + sq.y, lanes, part);
   const float mean = ss / (float)p.n + p.eps;
   float r = 1.f / sqrtf(mean);
   const bool wide = live && !(ss <= 0x1p120f && mean >= 0x1p-100f);  // (NaN, too)
@@ -150,7 +158,12 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
       float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
       if (p.w && ok(i)) load8(p.w + i, g);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = v[c][e] * r * (g[e] + p.w_add);
+      for (int e = 0; e < 8; e += 2) {
+        const float2 x = mul2(mul2(make_float2(v[c][e], v[c][e + 1]), make_float2(r, r)),
+                              sub2(make_float2(g[e], g[e + 1]), make_float2(-p.w_add, -p.w_add)));
+        y[e] = x.x;
+        y[e + 1] = x.y;
+      }
       if constexpr (YT == QG_Q8_0) {
         uint32_t q[2];
         const uint32_t bits = q8_block(y, q);
@@ -180,28 +193,30 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
   }
 }
 
-template <class TI, int YT, bool VEC, int U>
+template <class TI, int YT, int ROWS, int U>
 cudaError_t norm_u(const NormParams<TI>& p, cudaStream_t s) {
   const int eights = (p.n + 7) / 8, need = (eights + U - 1) / U;
   if (need <= 32) {
     int lanes = 4;
     while (lanes < need) lanes *= 2;
     const int per = NM_WARP_THREADS / lanes;
-    return launch_pdl(norm_kernel<TI, YT, VEC, U, false>, dim3((p.rows + per - 1) / per), dim3(NM_WARP_THREADS), 0, s, 0,
+    return launch_pdl(norm_kernel<TI, YT, ROWS, U, false>, dim3((p.rows + per - 1) / per), dim3(NM_WARP_THREADS), 0, s, 0,
                       LC_L1, p, lanes);
   }
-  return launch_pdl(norm_kernel<TI, YT, VEC, U, true>, dim3(p.rows), dim3((need + 31) / 32 * 32), 0, s, 0, LC_L1, p, 0);
+  // (without the tests 20,011 rows of 2,048 made Q8_0 and read back take 52.9 us instead of 54.0, one token of 5,120 2.5 instead of 2.7)
+  const auto kern = ROWS == EIGHTS && p.n % (8 * 32 * U) == 0 ? norm_kernel<TI, YT, FULL, U, true> : norm_kernel<TI, YT, ROWS, U, true>;
+  return launch_pdl(kern, dim3(p.rows), dim3((need + 31) / 32 * 32), 0, s, 0, LC_L1, p, 0);
 }
 
 // Groups of eight a thread. Few rows: one, the shortest way through a row. Many: as many as keep the loads of other rows in flight
 // behind a row's sums, four, or two where add is read, too (8,191 rows of 5,120, f32 to f16: 38.9 us with four, 45.2 with two, 61.1 with
 // one; with add 88.3, 84.7 and 90.0). Rows read element by element: one (108.7 us for rows of 5,119 with add, 115 and 176).
-template <class TI, int YT, bool VEC>
-cudaError_t norm_vec(const NormParams<TI>& p, cudaStream_t s) {
+template <class TI, int YT, int ROWS>
+cudaError_t norm_rows(const NormParams<TI>& p, cudaStream_t s) {
   const int eights = (p.n + 7) / 8;
-  if (eights <= 1024 && (!VEC || p.rows <= 152)) return norm_u<TI, YT, VEC, 1>(p, s);
-  if (eights <= 2048 && (!VEC || p.add || eights < 16)) return norm_u<TI, YT, VEC, 2>(p, s);
-  return norm_u<TI, YT, VEC, 4>(p, s);
+  if (eights <= 1024 && (ROWS == SINGLE || p.rows <= 152)) return norm_u<TI, YT, ROWS, 1>(p, s);
+  if (eights <= 2048 && (ROWS == SINGLE || p.add || eights < 16)) return norm_u<TI, YT, ROWS, 2>(p, s);
+  return norm_u<TI, YT, ROWS, 4>(p, s);
 }
 
 template <class TI>
@@ -217,9 +232,9 @@ cudaError_t norm_typed(const NormArgs& a, cudaStream_t s) {
   p.w_add = a.w_add; p.eps = a.eps;
   p.heads = a.heads; p.n = a.n;
   p.rows = (uint32_t)a.ntok * a.heads;
-  if (a.yt == QG_Q8_0) return norm_vec<TI, QG_Q8_0, true>(p, s);
-  if (a.vec) return a.yt == QG_F16 ? norm_vec<TI, QG_F16, true>(p, s) : norm_vec<TI, QG_F32, true>(p, s);
-  return a.yt == QG_F16 ? norm_vec<TI, QG_F16, false>(p, s) : norm_vec<TI, QG_F32, false>(p, s);
+  if (a.yt == QG_Q8_0) return norm_rows<TI, QG_Q8_0, EIGHTS>(p, s);
+  if (a.vec) return a.yt == QG_F16 ? norm_rows<TI, QG_F16, EIGHTS>(p, s) : norm_rows<TI, QG_F32, EIGHTS>(p, s);
+  return a.yt == QG_F16 ? norm_rows<TI, QG_F16, SINGLE>(p, s) : norm_rows<TI, QG_F32, SINGLE>(p, s);
 }
 
 }  // namespace
