@@ -48,6 +48,7 @@ __device__ __forceinline__ double ro_warp_sum(double v) {
 // By a whole warp. c: shared, a double for each expert; done with when the call returns.
 static __device__ __noinline__ void route_exact(const qg_route& r, const float* logits, const float* bias, int E, int topk, double* c,
                                             int32_t* ids, float* rw) {
+  __syncwarp();  // (functions that are called: their lanes come together first)
   const int lane = threadIdx.x & 31;
   // softmax: the largest logit and the sum, NaN left out
   double top = -INFINITY, sum = 1.;
@@ -192,6 +193,7 @@ static __device__ __noinline__ double ro_score(bool soft, float l, float top) {
 static __device__ __noinline__ double ro_sum64(const float* row, int first, int mine, float top) {
   double all = 0.;
   for (int i = 0; i < mine; ++i) all += ro_score(true, row[first + i], top);
+  __syncwarp();
   return ro_warp_sum(all);
 }
 
@@ -201,6 +203,7 @@ template <int NE, bool FULL>
 __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& deal, const float (&l)[NE], const float (&b)[NE],
                                            const float* row, const float* bias, int first, int mine, int topk, RouteSlot* slots,
                                            int32_t* ids, float* rw) {
+  __syncwarp();
   const int lane = threadIdx.x & 31;
   const bool grouped = r.top_group < r.n_group, soft = r.score == QG_SCORE_SOFTMAX;
   auto here = [&](int i) { return FULL || i < mine; };

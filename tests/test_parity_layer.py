@@ -450,6 +450,65 @@ def test_route_many_tokens():
     assert ((rw.double() - w).abs() <= 2.0 ** -19 * w).all()
 
 
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("plan", range(len(PLANS)))
+@pytest.mark.parametrize("e,k", [(256, 8), (128, 6), (512, 10), (256, 32), (64, 4), (40, 4), (250, 9), (100, 16), (1024, 8), (8, 2), (504, 3)])
+def test_route_many_tokens_as_few(e, k, plan, biased):
+    """A call of many tokens decides as calls of few do: ordinary tokens, equal and nearly equal experts, NaN and infinities; and a few
+    of them as the plain form."""
+    plan = dict(PLANS[plan])
+    if e % plan.get("n_group", 1):
+        plan["n_group"], plan["top_group"] = 2, 1
+    if plan.get("group_top", 1) > e // plan.get("n_group", 1):
+        plan["group_top"] = 1
+    k = min(k, plan.get("top_group", 1) * (e // plan.get("n_group", 1)))
+    n = 2600
+    g = rng(17, e, k)
+    x = (g.standard_normal((n, e)) * 1.5).astype(np.float32)
+    x[::7] = np.round(x[::7])            # many equal ones
+    x[1::50] = 0
+    x[2::101, e // 2], x[3::103, 0], x[4::107, e - 1] = np.nan, np.inf, -np.inf
+    x[5::109] *= 40                      # weights next to nothing
+    bias = (g.standard_normal(e) * 0.1).astype(np.float32) if biased else None
+    if biased:
+        x[6::7, 1] = x[6::7, 0]
+        bias[1] = np.nextafter(bias[0], np.float32(9))  # a pair that only 64 bits tell apart
+    dx, db = cuda(x), None if bias is None else cuda(bias)
+    ids, i_ok = banded((n, k), torch.int32)
+    rw, r_ok = banded((n, k), torch.float32)
+    made = qg.qroute_plan(**plan)
+    qg.qmoe_route(made, dx, k, ids, rw, bias=db)
+    assert i_ok() and r_ok()
+    few, fw = torch.empty_like(ids), torch.empty_like(rw)
+    for a in range(0, n, 1000):
+        qg.qmoe_route(made, dx[a:a + 1000], k, few[a:a + 1000], fw[a:a + 1000], bias=db)
+    assert torch.equal(ids, few)
+    a, b = host(rw).astype(np.float64), host(fw).astype(np.float64)
+    assert np.array_equal(np.isnan(a), np.isnan(b))
+    assert (np.abs(np.nan_to_num(a - b)) <= 2.0 ** -18 * np.abs(np.nan_to_num(b)) + 2.0 ** -125).all()
+    for t in (0, 1, 2, 3, 4, 5, 6, 13, 20, 51, 103, 2599):
+        with np.errstate(invalid="ignore"):
+            want, w, near = ref.route(x[t], bias, k, **plan)
+        if near > 1e-14:
+            assert np.array_equal(host(ids)[t], want), t
+            weights_within(host(rw)[t], w, f"token {t}")
+
+
+def test_route_biases_not_finite_for_many_tokens():
+    """A bias that is not finite: every token in 64 bits."""
+    n, e, k = 2100, 64, 4
+    g = rng(18)
+    x = g.standard_normal((n, e)).astype(np.float32)
+    bias = (g.standard_normal(e) * 0.1).astype(np.float32)
+    bias[3], bias[10], bias[20] = np.inf, -np.inf, np.nan
+    ids, rw = torch.empty((n, k), dtype=torch.int32, device="cuda"), torch.empty((n, k), device="cuda")
+    qg.qmoe_route(qg.qroute_plan("sigmoid"), cuda(x), k, ids, rw, bias=cuda(bias))
+    for t in range(0, n, 191):
+        want, w, _ = ref.route(x[t], bias, k, "sigmoid")
+        assert np.array_equal(host(ids)[t], want)
+        weights_within(host(rw)[t], w)
+
+
 @pytest.mark.parametrize("e,hidden,ncols,k", [(256, 2048, 1, 8), (256, 2048, 16, 8), (1024, 768, 3, 32), (7, 33, 2, 7), (64, 8192, 16, 8),
                                               (64, 8190, 13, 8), (40, 128, 5, 4), (512, 5120, 2, 10)])
 @pytest.mark.parametrize("plan", [0, 1, 4, 5])
