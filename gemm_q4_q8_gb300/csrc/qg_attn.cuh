@@ -114,7 +114,7 @@ struct AttnCfg {
   static constexpr int NB = D / 32 / TEAM;      // blocks of a warp
   static constexpr int ACC = NT * NB * 8;       // accumulator registers
   static constexpr int RECORD = kv_record_bytes(TYPE, D), STAGE = (RECORD + 127) / 128 * 128;
-  static constexpr bool QSMEM = NT * NB > 4;  // Q fragments read from shared memory each time, not kept in registers
+  static constexpr bool QSMEM = NT * NB > 4 || TYPE == QG_Q4_1;  // Q fragments read from shared memory each time, not kept in registers
   static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
   // dimensions joined at a time (32 also where 64 would leave one stage less)
   static constexpr int OD = NT > 2 || (NT == 1 && RECORD == 8192) ? 32 : 64;
@@ -1184,11 +1184,11 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             }
             const float e0 = lo_f32(d[blk]), e1 = hi_f32(d[blk]);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-              const float2 lo = mul2(make_float2(w[nt][0], w[nt][1]), make_float2(e0, e0));
-              const float2 hi = mul2(make_float2(w[nt][2], w[nt][3]), make_float2(e1, e1));
-              const uint32_t b0 = transpose8(pack_f16(lo.x, lo.y));
-              const uint32_t b1 = transpose8(pack_f16(hi.x, hi.y));
+            for (int nt = 0; nt < NT; ++nt) {  // (pairs of tokens: e0 and e1 are next to each other as they come)
+              const float2 r0 = mul2(make_float2(w[nt][0], w[nt][2]), make_float2(e0, e1));
+              const float2 r1 = mul2(make_float2(w[nt][1], w[nt][3]), make_float2(e0, e1));
+              const uint32_t b0 = transpose8(pack_f16(r0.x, r1.x));
+              const uint32_t b1 = transpose8(pack_f16(r0.y, r1.y));
               mma16816_acc(o[blk][nt][0], v0, b0, b1);
               mma16816_acc(o[blk][nt][1], v1, b0, b1);
             }
