@@ -366,9 +366,7 @@ def _floats(t, name, n):
     """Address of n contiguous float32, None for None."""
     if t is None:
         return None
-    if _ELEM is None:
-        _dtypes()
-    if _ELEM.get(t.dtype) != QG_F32 or t.numel() != n or not t.is_contiguous():
+    if _elem(t, name) != QG_F32 or t.numel() != n or not t.is_contiguous():
         raise ValueError(f"{name}: {n} contiguous float32 expected, got {t.dtype} {tuple(t.shape)}")
     return t.data_ptr()
 
@@ -426,8 +424,10 @@ def qembed(qtype, q, scl, ids, y, scale=1.0, err_flag=None, stream=None):
         _check("qembed", st)
 
 
-def _vectors(t, shape, name):
-    """Token stride of a tensor [ntok, n] or [ntok, heads, n] whose vectors of a token are neighbours."""
+def _vectors(t, shape, row, name):
+    """Token stride of a tensor [ntok, n] or [ntok, heads, n] whose vectors of a token, `row` elements, are neighbours."""
+    if t.shape == shape and t.is_contiguous():
+        return row
     if len(shape) == 3:
         return _rows(t, shape, name)
     if t.shape != shape or (shape[1] > 1 and t.stride(1) != 1):
@@ -441,26 +441,35 @@ def qrms_norm(x, w, y, eps=1e-6, add=None, sum_out=None, w_add=0.0, y_scl=None, 
     x), or with y_scl Q8_0 rows: y int8 and y_scl f16 [ntok(, heads), n / 32], contiguous."""
     if _ELEM is None:
         _dtypes()
-    shape, kind = x.shape, _elem(x, "x")
-    if len(shape) not in (2, 3):
-        raise ValueError(f"x: [ntok, n] or [ntok, heads, n] expected, got {tuple(shape)}")
-    ntok, n = shape[0], shape[-1]
-    heads = shape[1] if len(shape) == 3 else 1
-    for t, name in ((add, "add"), (sum_out, "sum_out")):
-        if t is not None and t.dtype != x.dtype:
-            raise ValueError(f"{name}: {x.dtype} expected, as x, got {t.dtype}")
-    if y_scl is None:
-        yt, ys = _elem(y, "y"), _vectors(y, shape, "y")
+    shape, dtype, heads = x.shape, x.dtype, 1
+    if len(shape) == 3:
+        ntok, heads, n = shape
+    elif len(shape) == 2:
+        ntok, n = shape
     else:
-        yt, ys = Q8_0, 0
+        raise ValueError(f"x: [ntok, n] or [ntok, heads, n] expected, got {tuple(shape)}")
+    row = heads * n
+    kind, xs = _elem(x, "x"), _vectors(x, shape, row, "x")
+    ap = sp = a_stride = s_stride = None
+    if add is not None:
+        if add.dtype != dtype:
+            raise ValueError(f"add: {dtype} expected, as x, got {add.dtype}")
+        ap, a_stride = add.data_ptr(), _vectors(add, shape, row, "add")
+    if sum_out is not None:
+        if sum_out.dtype != dtype:
+            raise ValueError(f"sum_out: {dtype} expected, as x, got {sum_out.dtype}")
+        sp, s_stride = sum_out.data_ptr(), _vectors(sum_out, shape, row, "sum_out")
+    scales = None
+    if y_scl is None:
+        yt, ys = _elem(y, "y"), _vectors(y, shape, row, "y")
+    else:
+        yt, ys, scales = Q8_0, 0, y_scl.data_ptr()
         if y.shape != shape or y.element_size() != 1 or not y.is_contiguous():
             raise ValueError(f"y: contiguous int8 {tuple(shape)} expected, got {y.dtype} {tuple(y.shape)}")
         if y_scl.element_size() != 2 or y_scl.numel() != ntok * heads * (n // 32) or not y_scl.is_contiguous():
             raise ValueError(f"y_scl: {ntok * heads} x {n // 32} contiguous f16 expected, got {y_scl.dtype} {tuple(y_scl.shape)}")
-    st = (_lib or load()).qrms_norm(kind, x.data_ptr(), _vectors(x, shape, "x"), _ptr(add),
-                                    0 if add is None else _vectors(add, shape, "add"), _ptr(sum_out),
-                                    0 if sum_out is None else _vectors(sum_out, shape, "sum_out"), _floats(w, "w", n), w_add,
-                                    eps, ntok, heads, n, yt, y.data_ptr(), ys, _ptr(y_scl), _stream(stream))
+    st = (_lib or load()).qrms_norm(kind, x.data_ptr(), xs, ap, a_stride or 0, sp, s_stride or 0, _floats(w, "w", n), w_add, eps, ntok,
+                                    heads, n, yt, y.data_ptr(), ys, scales, _stream(stream))
     if st:
         _check("qrms_norm", st)
 
