@@ -329,7 +329,8 @@ struct Spot {
 // Q4_1. m is the largest f16 not above the block's smallest element, d the smallest f16 h with 15 h >= r, r = largest - m
 // (f32): as for Q8_0, r times a little more than 1/15, rounded up, is h or the f16 behind it, and 15 h is exact. The quant
 // is the integer nearest to (x - m) / d, two f32 operations; by an approximate reciprocal it is off by less than 15 * 1.5
-// 2^-23 = 2.7e-6, and only next to a half is the division needed.
+// 2^-23 = 2.7e-6, and only next to a half is the division needed. Elements count as within +-65504, so that d stays below 2^14 and
+// m + 8 d, which the attention takes as an f16, is one.
 __device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot, int d, const float (&y)[8]) {
   float lo = y[0], hi = y[0];  // an infinity or a NaN stays one
 #pragma unroll
@@ -344,16 +345,13 @@ __device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot
   }
   const bool bad = !(fabsf(lo) <= 3.402823466e38f) || !(fabsf(hi) <= 3.402823466e38f);
   uint32_t m_bits = __half_as_ushort(__float2half_rd(lo));
-  bool clamp = m_bits == 0xFC00;
-  if (clamp) m_bits = 0xFBFF;
+  const bool clamp = m_bits == 0xFC00 || hi > 65504.f;
+  if (m_bits == 0xFC00) m_bits = 0xFBFF;
+  hi = fminf(hi, 65504.f);
   const float m = __half2float(__ushort_as_half((uint16_t)m_bits)), r = fmaxf(hi - m, 0.f);  // (below 0 where m is -65504 and x far below)
   uint32_t bits = __half_as_ushort(__float2half_ru(r * 0x1.111112p-4f));
   if (bits == 0 && r > 0.f) bits = 1;
   if (bits && 15.f * __half2float(__ushort_as_half((uint16_t)(bits - 1))) >= r) --bits;
-  if (bits > 0x7BFF) {
-    bits = 0x7BFF;
-    clamp = true;
-  }
   uint32_t w = 0;
   if (!bad && bits != 0) {
     const float ds = __half2float(__ushort_as_half((uint16_t)bits)), magic = 12582912.f;

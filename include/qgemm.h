@@ -323,7 +323,8 @@ qg_status qembed(qg_type t, const void *q, const uint16_t *scl, int rows, int k,
  *   n    : 1..32768, for QG_Q8_0 a multiple of 32; n_heads >= 1; strides >= n_heads * n
  *          (ignored when ntok <= 1)
  * Sums are f32 (64 bits where the squares leave its range); a vector's result depends on
- * nothing but the vector, n, the alignment and whether there are more than 152 vectors.
+ * nothing but the vector, n, the alignment, whether there are more than 152 vectors and
+ * whether add is given.
  * Each pointer aligned to its elements; for QG_Q8_0 all 16-byte aligned and the strides
  * multiples of 8 elements (QG_ERR_ALIGN). Rows that begin at multiples of 16 bytes, with
  * w so aligned, too, are read and written in wide accesses.
@@ -436,11 +437,12 @@ qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride
  * max |x| / 127 rounded up to f16 (at most 65504), q the integer nearest to
  * x / d (ties to even, within +-127). A block with a NaN or an infinity gets
  * d = NaN, so that it is not silently lost.
- * Q4_1 blocks (the same 32 elements, value q * d + m): m is the largest f16 not
- * above min x (at least -65504), d the smallest f16 >= 0 with 15 d >= max x - m (at
- * most 65504; the difference in f32), q the integer nearest to (x - m) / d (f32
+ * Q4_1 blocks (the same 32 elements, value q * d + m; one beyond +-65504 counts as
+ * that): m is the largest f16 not above min x, d the smallest f16 >= 0 with 15 d >=
+ * max x - m (the difference in f32), q the integer nearest to (x - m) / d (f32
  * operations, ties to even, within 0..15; 0 where d is 0). A block with a NaN or an
- * infinity gets d = NaN.
+ * infinity gets d = NaN. A cache that is written in another way keeps m + 8 d within
+ * +-65504.
  *   type       : QG_F16, QG_Q8_0 or QG_Q4_1 (QG_ERR_TYPE)
  *   n_kv_heads : 1..256; head_dim: 64, 128 or 256; page_size: 16, 32, 64, 128
  *                or 256; n_pages >= 1; n_seq: 1..1024; max_pages >= 1, with
@@ -529,10 +531,10 @@ qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *p
  * Tokens that a row does not see (padding of the last page, later columns,
  * outside the window) have no effect on it, whatever their bytes hold.
  * Scores, softmax sums and the weighted sum are f32; a weight (times the
- * block's scale for Q8_0) is rounded to f16 before it meets its value: by at
- * most 2^-11 of itself, or 2^-30 of the largest weight (times the largest
- * scale). For Q4_1 it is rounded before it meets the block's m, and again when it
- * has been multiplied by the block's d. y is rounded to f16 once. Results are the same from run to run. The
+ * block's scale for Q8_0, its d for Q4_1) is rounded to f16 before it meets its
+ * value: by at most 2^-11 of itself, or 2^-30 of the largest weight (times the
+ * largest scale). For Q4_1 q - 8 is what it meets; the weight alone, rounded, meets
+ * m + 8 d, rounded to f16, too. y is rounded to f16 once. Results are the same from run to run. The
  * order of the sums depends on lens, window and the sizes, max_pages among
  * them: a column of a wider call need not equal the one-column call bit for
  * bit, nor a call over a wider page table the same call over a narrow one.

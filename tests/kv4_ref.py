@@ -31,7 +31,7 @@ def quantise(x):
     """(q, d, m) of f32 x [..., 32]: whole numbers 0 to 15, f16, f16. The documented rule in f32 operations."""
     x = np.asarray(x, np.float32)
     bad = ~np.isfinite(x).all(-1)
-    x = np.where(bad[..., None], np.float32(0), x)
+    x = np.clip(np.where(bad[..., None], np.float32(0), x), np.float32(-65504), np.float32(65504))
     m = below(x.min(-1))
     d = step_of(x.max(-1) - m.astype(np.float32))
     m32, d32 = m.astype(np.float32)[..., None], d.astype(np.float32)[..., None]

@@ -139,7 +139,8 @@ def test_append_not_finite():
     ko, vo = host(ko), host(vo)
     assert np.isnan(ko[0, 0, :32]).all() and np.isnan(ko[1, 1, 32:]).all() and np.isnan(vo[2, 0, 32:]).all()
     low = np.float32(ref.below(v[3, 1, :32].min()))
-    assert vo[3, 1, 0] == np.float32(15 * 65504.0 + low) and (vo[3, 1, 1:32] == low).all()
+    # 1e30 counts as 65504: a range of 65504 to 65508, d the f16 behind 4367 to 4367.2
+    assert vo[3, 1, 0] == np.float32(15 * 4368.0 + low) and (vo[3, 1, 1:32] == low).all()
     # m = -65504; the others lie within 4 of 0, so d is the f16 behind 65508 / 15 = 4367.2 (steps of 4): 4368, and they take
     # the quant 15 (65500 / 4368 = 14.9954): 15 * 4368 - 65504 = 16
     assert vo[4, 0, 0] == -65504 and np.abs(v[4, 0, 1:32]).max() < 4 and (vo[4, 0, 1:32] == 16).all()
@@ -429,6 +430,31 @@ def test_attention_one_large_value_among_small_ones(where, large):
     assert_within(y, want, bound, "one large value")
     rest = slice(32, None) if where == "block" else slice(None)
     assert (bound[..., rest] < 1e-3).all()  # (the values are of 0.1)
+
+
+@pytest.mark.parametrize("d", [64, 256])
+def test_attention_values_past_the_largest_f16(d):
+    """Blocks between -65504 and far above 65504, and all above it: what is stored, and the sums of m + 8 d, stay in f16's range."""
+    n, kv = 60, 2
+    c = Cache(kv, d, 16, 1, 4)
+    g = rng(23)
+    k, v = g.standard_normal((2, n, kv, d)).astype(np.float32)
+    v[0::4, :, :32] *= np.float32(1e6)
+    v[1::4, 0], v[2::4, 1] = 1e5, -3e38
+    v[3::4, :, 5] = 2e6
+    pos = np.arange(n, dtype=np.int32)
+    qg.qkv_append(c.c, cuda(k), cuda(v), cuda(pos))
+    c.host = host(c.pool)
+    ks, vs = np.empty((2, 3, n, kv, d))
+    for j in range(n):
+        for h in range(kv):
+            ks[:, j, h], vs[:, j, h] = c.get(0, j, h)
+    assert np.isfinite(vs).all() and np.abs(vs[0] + vs[1]).max() <= 65504 + 131008 * 2.0 ** -10
+    q = (g.standard_normal((1, 1, 6, d)) * 0.1).astype(np.float16)
+    y, _ = attend(c, q, [n])
+    want, bound = ref.attention(q, [ks], [vs], [n], 1, 0, d ** -0.5)
+    assert np.isfinite(y).all()
+    assert_within(y, want, bound, f"dim {d}")
 
 
 def test_attention_constant_blocks():
