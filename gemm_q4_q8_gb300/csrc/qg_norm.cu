@@ -13,6 +13,8 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include <type_traits>
+
 #include "qg_blocks.cuh"
 #include "qg_common.cuh"
 #include "qg_internal.h"
@@ -31,7 +33,7 @@ struct NormParams {
   void* y;
   uint16_t* scl;
   int64_t xs, as, ss, ys;
-  float w_add, eps;
+  float w_add, eps, inv_n;
   uint32_t heads, rows;
   int n;
 };
@@ -131,8 +133,8 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
       sq = fma2(x, x, sq);
     }
   const float ss = row_sum<BLOCK>(sq.x + sq.y, lanes, part);
-  const float mean = ss / (float)p.n + p.eps;
-  float r = 1.f / sqrtf(mean);
+  const float mean = fmaf(ss, p.inv_n, p.eps);
+  float r = rsqrtf(mean);  // (off by 2 steps at most)
   const bool wide = live && !(ss <= 0x1p120f && mean >= 0x1p-100f);  // (NaN, too)
   if (__builtin_expect(BLOCK ? wide : __any_sync(0xffffffffu, wide), 0)) {
     double s = 0;
@@ -150,33 +152,55 @@ __global__ void __launch_bounds__(BLOCK ? 1024 : NM_WARP_THREADS) norm_kernel(co
       r = 1.f;
     }
   }
+  // group c's normed elements (VEC)
+  auto normed = [&](int c, float (&y)[8]) {
+    const int i = at(c, 0);
+    float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (p.w && ok(i)) load8(p.w + i, g);
+    if (p.w_add != 0.f)
 #pragma unroll
-  for (int c = 0; c < U; ++c) {
-    float y[8];
-    if constexpr (VEC) {
-      const int i = at(c, 0);
-      float g[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
-      if (p.w && ok(i)) load8(p.w + i, g);
+      for (int e = 0; e < 8; ++e) g[e] += p.w_add;
 #pragma unroll
-      for (int e = 0; e < 8; e += 2) {
-        const float2 x = mul2(mul2(make_float2(v[c][e], v[c][e + 1]), make_float2(r, r)),
-                              sub2(make_float2(g[e], g[e + 1]), make_float2(-p.w_add, -p.w_add)));
-        y[e] = x.x;
-        y[e + 1] = x.y;
-      }
-      if constexpr (YT == QG_Q8_0) {
+    for (int e = 0; e < 8; e += 2) {
+      const float2 x = mul2(mul2(make_float2(v[c][e], v[c][e + 1]), make_float2(r, r)), make_float2(g[e], g[e + 1]));
+      y[e] = x.x;
+      y[e + 1] = x.y;
+    }
+  };
+  if constexpr (YT == QG_Q8_0) {
+    auto blocks = [&](auto tame) {  // the largest magnitude
+      float most = 0.f;
+#pragma unroll
+      for (int c = 0; c < U; ++c) {
+        const int i = at(c, 0);
+        float y[8], top;
         uint32_t q[2];
-        const uint32_t bits = q8_block(y, q);
+        normed(c, y);
+        const uint32_t bits = q8_block<0, decltype(tame)::value>(y, q, top);
+        most = max_nan(most, top);
         // stored order: of each 16 bytes the two halves byte by byte, a half a lane
         const bool second = t & 1;
         const uint32_t got = __shfl_xor_sync(0xffffffffu, second ? q[0] : q[1], 1);
         const uint32_t a = second ? got : q[0], b = second ? q[1] : got;
         if (ok(i)) {
           reinterpret_cast<uint2*>(static_cast<int8_t*>(p.y) + (int64_t)row * p.n)[i >> 3] =
-              make_uint2(__byte_perm(a, b, 0x5140) ^ 0x80808080u, __byte_perm(a, b, 0x7362) ^ 0x80808080u);
+              make_uint2(__byte_perm(a, b, 0x5140), __byte_perm(a, b, 0x7362));
           if ((t & 3) == 0) p.scl[(int64_t)row * (p.n >> 5) + (i >> 5)] = (uint16_t)bits;
         }
-      } else if (ok(i)) {
+      }
+      return most;
+    };
+    const float most = blocks(std::true_type());
+    if (__builtin_expect(__any_sync(0xffffffffu, !(most <= Q8_TOP)), 0)) blocks(std::false_type());
+    return;
+  }
+#pragma unroll
+  for (int c = 0; c < U; ++c) {
+    float y[8];
+    if constexpr (VEC) {
+      const int i = at(c, 0);
+      normed(c, y);
+      if (ok(i)) {
         if constexpr (YT == QG_F16) store8(static_cast<__half*>(p.y) + tok * p.ys + head * p.n + i, y);
         if constexpr (YT == QG_F32) store8(static_cast<float*>(p.y) + tok * p.ys + head * p.n + i, y);
       }
@@ -229,7 +253,7 @@ cudaError_t norm_typed(const NormArgs& a, cudaStream_t s) {
   p.y = a.y;
   p.scl = a.scl;
   p.xs = a.xs; p.as = a.as; p.ss = a.ss; p.ys = a.ys;
-  p.w_add = a.w_add; p.eps = a.eps;
+  p.w_add = a.w_add; p.eps = a.eps; p.inv_n = (float)(1. / a.n);
   p.heads = a.heads; p.n = a.n;
   p.rows = (uint32_t)a.ntok * a.heads;
   if (a.yt == QG_Q8_0) return norm_rows<TI, QG_Q8_0, EIGHTS>(p, s);

@@ -328,16 +328,12 @@ struct Spot {
 
 // Q4_1. m is the largest f16 not above the block's smallest element, d the smallest f16 h with 15 h >= r, r = largest - m
 // (f32): as for Q8_0, r times a little more than 1/15, rounded up, is h or the f16 behind it, and 15 h is exact. The quant
-// is the integer nearest to (x - m) / d, two f32 operations; by an approximate reciprocal it is off by less than 15 * 1.5
-// 2^-23 = 2.7e-6, and only next to a half is the division needed. Elements count as within +-65504, so that d stays below 2^14 and
+// is the integer nearest to (x - m) / d, two f32 operations. Elements count as within +-65504, so that d stays below 2^14 and
 // m + 8 d, which the attention takes as an f16, is one.
 __device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot, int d, const float (&y)[8]) {
-  float lo = y[0], hi = y[0];  // an infinity or a NaN stays one
-#pragma unroll
-  for (int e = 1; e < 8; ++e) {
-    lo = min_nan(lo, y[e]);
-    hi = max_nan(hi, y[e]);
-  }
+  // (an infinity or a NaN stays one)
+  float lo = min_nan(min_nan(y[0], y[1], y[2]), min_nan(y[3], y[4], y[5]), min_nan(y[6], y[7]));
+  float hi = max_nan(max_nan(y[0], y[1], y[2]), max_nan(y[3], y[4], y[5]), max_nan(y[6], y[7]));
 #pragma unroll
   for (int x = 1; x <= 2; ++x) {
     lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, x));
@@ -357,17 +353,15 @@ __device__ __forceinline__ void put8_q4(uint8_t* half, const Spot<QG_Q4_1>& spot
     const float ds = __half2float(__ushort_as_half((uint16_t)bits)), magic = 12582912.f;
     float inv;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(inv) : "f"(ds));
-    float b[8], off = 0.f;
+    float b[8];
 #pragma unroll
     for (int e = 0; e < 8; e += 2) {
-      const float2 q = mul2(sub2(make_float2(y[e], y[e + 1]), make_float2(m, m)), make_float2(inv, inv));
+      const float2 q = quotients(sub2(make_float2(y[e], y[e + 1]), make_float2(m, m)), ds, inv);
       const float2 n = sub2(q, make_float2(-magic, -magic));
-      const float2 x = sub2(q, sub2(n, make_float2(magic, magic)));
-      off = fmaxf(off, fmaxf(fabsf(x.x), fabsf(x.y)));
       b[e] = n.x;
       b[e + 1] = n.y;
     }
-    if (off > 0.49999f || clamp)
+    if (clamp)
 #pragma unroll
       for (int e = 0; e < 8; ++e) b[e] = fminf(fmaxf(__fdiv_rn(y[e] - m, ds), 0.f), 15.f) + magic;
     uint32_t n[2];
@@ -399,7 +393,8 @@ __device__ __forceinline__ void put8(uint8_t* half, const Spot<TYPE>& spot, int 
     if (half) store8(reinterpret_cast<__half*>(half + spot.at), y);
   } else {
     uint32_t w[2];
-    const uint32_t bits = q8_block(y, w);
+    float top;
+    const uint32_t bits = q8_block<128, false>(y, w, top);
     if (half) {
       *reinterpret_cast<uint2*>(half + spot.at) = make_uint2(w[0], w[1]);
       if (spot.scale_at >= 0) *reinterpret_cast<uint16_t*>(half + spot.scale_at) = (uint16_t)bits;
