@@ -57,6 +57,14 @@
 // to f16 (so V itself is never rounded); a power of two that follows the largest
 // scale seen keeps that product in the normal range of f16.
 //
+// Q4_1: an element is q d + m, q from 0 to 15. Keys: sum_d Q_d k_d = d sum_d Q_d q_d + m sum_d Q_d by blocks. A masked word is two
+// quants as f16 subnormals, the high nibbles 16 times as large (one row tile: a sum of their own, times 1/16; more: shifted). The
+// blocks' sums of queries are made once an item, as two f16 each scaled by row, and one small product with the blocks' m starts the
+// scores. Values: sum_j w_j v_j = sum_j (w_j d_j) (q_j - 8) + sum_j w_j (m_j + 8 d_j). The second part is one product a record for all
+// blocks, of weights and m + 8 d, both rounded to f16; in the first w d is rounded once, as in Q8_0, and q - 8 is exact (one packed
+// subtraction of subnormals; q itself would make both parts several times the answer, and cost twice the error, 5.9e-4 instead of
+// 2.6e-4 off 64 bits).
+//
 // Weights are rounded to f16 because the matrix product with the values takes both
 // factors in one type, and values are f16 (or integers that f16 holds): half a step,
 // 2^-11 of a weight, or 2^-32 of its run's largest (Q8_0, times the largest scale: 2^-30). Their sum is of the unrounded ones. Scores,
@@ -66,7 +74,10 @@
 // 8 rows: by memory, at 6.1 TB/s in f16 (131,071 tokens of 8 kv
 // heads of 128 in 88 us; the bytes alone take 79 at the rate of a large copy), and
 // nearly so in Q8_0 (64 ragged sequences, 279 MB, in 50 us, issue slots half
-// used). More rows: by the latency of the instructions between two matrix
+// used). Q4_1, one tile: by instructions, 363 a warp and record of 2,560 bytes, with 16 warps an SM and two thirds of the issue slots
+// used: the records alone at 82% of the copy rate, and 11 us around them (262,143 tokens of 8 kv heads of 128, 336 MB: 70.6 us,
+// 4.7 TB/s; 64 ragged sequences, 286 MB: 68.3). Two records a step 68.1 and 70.3; five CTAs an SM 73 to 79, as the registers
+// do not suffice. More rows: by the latency of the instructions between two matrix
 // products, with the 8 to 16 warps that the accumulators leave room for (Q8_0, 32 rows of heads
 // of 256: 800 instructions a record and tile of 16 rows, issue slots 38% and
 // tensor pipe 25% used, 38 us for 82 MB). One short sequence: by the chain of
@@ -104,7 +115,8 @@ constexpr int AT_CLUSTER_UNITS = 3;
 constexpr float AT_SLACK = 8.f;  // a score may pass its row's reference by this much (log 2)
 // f16: every weight is 2^7 times as large, in numerators and sums alike. The largest then lies between 2^7 and 2^15, and what
 // rounding to f16 takes from small ones (up to 2^-25 below its normals) is 2^-32 of it: a first token far above 30,000 others,
-// whose sum the answer is, else cost those of its warp a quarter of their weight. (Q8_0: wmul below does this.)
+// whose sum the answer is, else cost those of its warp a quarter of their weight. Q4_1 needs it where weights meet m + 8 d. (Q8_0:
+// wmul below does this.)
 constexpr float at_lift(int type) { return type == QG_Q8_0 ? 0.f : 7.f; }
 
 template <int TYPE, int D, int NT>
@@ -114,7 +126,8 @@ struct AttnCfg {
   static constexpr int NB = D / 32 / TEAM;      // blocks of a warp
   static constexpr int ACC = NT * NB * 8;       // accumulator registers
   static constexpr int RECORD = kv_record_bytes(TYPE, D), STAGE = (RECORD + 127) / 128 * 128;
-  static constexpr bool QSMEM = NT * NB > 4 || TYPE == QG_Q4_1;  // Q fragments read from shared memory each time, not kept in registers
+  // Q fragments read from shared memory each time, not kept in registers (Q4_1: 262,143 tokens 71.7 us with registers, 70.5 without)
+  static constexpr bool QSMEM = NT * NB > 4 || TYPE == QG_Q4_1;
   static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
   // dimensions joined at a time (32 also where 64 would leave one stage less)
   static constexpr int OD = NT > 2 || (NT == 1 && RECORD == 8192) ? 32 : 64;

@@ -2,6 +2,10 @@
 // units of neighbouring elements that it stores in one access, 4 f32 or 8 f16. For Q8_0 and Q4_0 it reads the 8 or 16 stored
 // bytes that hold them and takes every second one, as the halves of a group lie byte by byte; a weight, an integer times its
 // f16 scale, is exact in f32, then multiplied by the call's scale and rounded.
+//
+// Bound by memory where there are many rows: 20,011 of 2,048 from Q8_0, 208 MB, to f32 31.6 us, 97% of the rate of a large copy; to f16 20.2, 92%.
+// 4,095 rows, 42 MB that stay in L2: 8.6 us, issue slots 66% used (the floor of a copy is 6.3). One row: 1.5 us, the launch and
+// two loads, the second at the first one's place.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -94,7 +98,8 @@ cudaError_t embed_u(const EmbedArgs& a, cudaStream_t s) {
 
 template <int QT, class TO>
 cudaError_t embed_go(const EmbedArgs& a, cudaStream_t s) {
-  // one unit a lane where that makes no more warps than the machine holds at a time
+  // one unit a lane where that makes no more warps than the machine holds at a time; else four (4,095 rows of 2,048: 8.6 us, 9.8 with
+  // 16 neighbouring elements a lane and access)
   return (int64_t)a.ntok * a.k * sizeof(TO) <= (int64_t)152 * 64 * 512 ? embed_u<QT, TO, 1>(a, s) : embed_u<QT, TO, 4>(a, s);
 }
 

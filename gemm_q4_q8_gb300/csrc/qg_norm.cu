@@ -8,8 +8,9 @@
 // 64 bits: a row that needs it shows by its sum.
 //
 // Bound by memory: 8,191 rows of 5,120 f32 with the residual, to f16 and f32: 84.6 us, 587 MB, the rate of a large copy; without it 38.6 us,
-// 252 MB, 96% of it. To Q8_0 by its instructions, 90 for eight elements: 20,011 rows of 2,048 f16 in 33 us, where the bytes take 18.5. One
-// row of 5,120: 2.5 us, the launch, two trips to memory and one barrier.
+// 252 MB, 96% of it. To Q8_0 by its instructions, 140 for eight elements of a lane: 20,011 rows of 2,048 f16 in 28.5 us, where the bytes
+// take 18.5, with 28 warps an SM and two thirds of the issue slots used (read back in 20.2 more: 48.7; groups of eight a thread: two
+// 54.4, eight, whose registers halve the warps, 67.3). One row of 5,120: 2.5 us, the launch, two trips to memory and one barrier.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
@@ -227,19 +228,22 @@ cudaError_t norm_u(const NormParams<TI>& p, cudaStream_t s) {
     return launch_pdl(norm_kernel<TI, YT, ROWS, U, false>, dim3((p.rows + per - 1) / per), dim3(NM_WARP_THREADS), 0, s, 0,
                       LC_L1, p, lanes);
   }
-  // (without the tests 20,011 rows of 2,048 made Q8_0 and read back take 52.9 us instead of 54.0, one token of 5,120 2.5 instead of 2.7)
+  // (without the tests 20,011 rows of 2,048 made Q8_0 and read back took 52.9 us instead of 54.0, one token of 5,120 2.5 instead of 2.7)
   const auto kern = ROWS == EIGHTS && p.n % (8 * 32 * U) == 0 ? norm_kernel<TI, YT, FULL, U, true> : norm_kernel<TI, YT, ROWS, U, true>;
   return launch_pdl(kern, dim3(p.rows), dim3((need + 31) / 32 * 32), 0, s, 0, LC_L1, p, 0);
 }
 
-// Groups of eight a thread. Few rows: one, the shortest way through a row. Many: as many as keep the loads of other rows in flight
-// behind a row's sums, four, or two where add is read, too (8,191 rows of 5,120, f32 to f16: 38.9 us with four, 45.2 with two, 61.1 with
-// one; with add 88.3, 84.7 and 90.0). Rows read element by element: one (108.7 us for rows of 5,119 with add, 115 and 176).
+// Groups of eight a thread. Few rows, 1,280 threads an SM at most: one, the shortest way through a row (5,120 f32 elements with add: 150
+// rows 3.5 us, with two groups 3.8; 300: 3.8 and 4.5; 400, above the bound, 5.7 and 4.8). Many: as many as keep the loads of other rows
+// in flight behind a row's sums, four, or two where add is read, too (8,191 rows, to f16: 38.5 us with four, 45.2 with two, 61.1
+// with one; with add 88.3, 84.8 and 90.0); of rows of 64 elements or fewer two, as four leave lanes without any (240,000 rows of
+// 64: 17.1 us, 21.1 with four; of 96: 28.0, 24.7). Rows read element by element: one (108.7 us for rows of 5,119 with add, 115 and
+// 176).
 template <class TI, int YT, int ROWS>
 cudaError_t norm_rows(const NormParams<TI>& p, cudaStream_t s) {
   const int eights = (p.n + 7) / 8;
-  if (eights <= 1024 && (ROWS == SINGLE || p.rows <= 152)) return norm_u<TI, YT, ROWS, 1>(p, s);
-  if (eights <= 2048 && (ROWS == SINGLE || p.add || eights < 16)) return norm_u<TI, YT, ROWS, 2>(p, s);
+  if (eights <= 1024 && (ROWS == SINGLE || (int64_t)p.rows * eights <= 152 * 1280)) return norm_u<TI, YT, ROWS, 1>(p, s);
+  if (eights <= 2048 && (ROWS == SINGLE || p.add || eights <= 8)) return norm_u<TI, YT, ROWS, 2>(p, s);
   return norm_u<TI, YT, ROWS, 4>(p, s);
 }
 

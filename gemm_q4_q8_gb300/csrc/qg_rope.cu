@@ -21,7 +21,7 @@
 // Bound by memory: 4 bytes read and 2 (f16) or 17/16 (Q8_0) written an element.
 // qrope, 8,191 tokens of 40 heads of 128, f32 to f16: 40.1 us, 6.3 TB/s. qkv_append,
 // 16,382 tokens of 40 + 8 + 8 heads into Q8_0 blocks: 112 us, 5.7 TB/s, waiting for
-// rows (46% of the issue slots used, 36 warps an SM).
+// rows (46% of the issue slots used, 36 warps an SM); into Q4_1 blocks 118 us (without its stores at all it takes 112).
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 

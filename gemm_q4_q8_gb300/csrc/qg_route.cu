@@ -1,4 +1,9 @@
 // qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token (qg_route.cuh).
+//
+// Bound by instructions: 770 a token of 256 experts in 8 groups, two thirds of the issue slots used: 16,383 tokens in 18.0 us, where
+// their 18 MB would take 2.6. Without bias and groups 11 us, 512 experts 34, 1,000 tokens 6.4. Eight or sixteen lanes a token instead of a
+// warp: 22.6 and 25.2 us, as the k best one after the other then are a chain for few tokens at a time; the next token's logits
+// loaded ahead: no gain.
 #include <cuda_runtime.h>
 
 #include <cmath>

@@ -323,8 +323,8 @@ qg_status qembed(qg_type t, const void *q, const uint16_t *scl, int rows, int k,
  *   n    : 1..32768, for QG_Q8_0 a multiple of 32; n_heads >= 1; strides >= n_heads * n
  *          (ignored when ntok <= 1)
  * Sums are f32 (64 bits where the squares leave its range); a vector's result depends on
- * nothing but the vector, n, the alignment, whether there are more than 152 vectors and
- * whether add is given.
+ * nothing but the vector, n, the alignment, whether all vectors together have more than
+ * 1,556,480 elements (each counted up to a multiple of 8) and whether add is given.
  * Each pointer aligned to its elements; for QG_Q8_0 all 16-byte aligned and the strides
  * multiples of 8 elements (QG_ERR_ALIGN). Rows that begin at multiples of 16 bytes, with
  * w so aligned, too, are read and written in wide accesses.
