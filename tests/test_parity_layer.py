@@ -214,6 +214,34 @@ def test_norm_to_q8_blocks_where_the_last_bit_decides():
     np.testing.assert_array_equal(ref.unstored(host(q).view(np.uint8)).view(np.int8).reshape(-1, 32), wq)
 
 
+@pytest.mark.parametrize("n", [32, 96, 256, 2048, 5120])
+@pytest.mark.parametrize("rows", [7, 1600])
+def test_norm_to_q8_rows_next_to_odd_ones(n, rows):
+    """Rows with a NaN, an infinity, nothing at all or blocks that saturate leave the others' bytes as they are."""
+    g = rng(18, n)
+    x = g.standard_normal((rows, n)).astype(np.float32)
+    w = (1 + 0.2 * g.standard_normal(n)).astype(np.float32)
+    w[n - 1] = 1e12  # times 0, but in one row
+    x[:, n - 1] = 0
+
+    def run():
+        q = torch.empty((rows, n), dtype=torch.int8, device="cuda")
+        scl = torch.empty((rows, n // 32), dtype=torch.float16, device="cuda")
+        qg.qrms_norm(cuda(x), cuda(w), q, y_scl=scl, eps=0.0)
+        return host(q), host(scl)
+
+    q0, s0 = run()
+    assert np.isfinite(s0).all()
+    x[1, 3], x[2, n // 2], x[4], x[5, n - 1] = np.nan, np.inf, 0, 2.0
+    q1, s1 = run()
+    rest = [i for i in range(rows) if i not in (1, 2, 4, 5)]
+    np.testing.assert_array_equal(q1[rest], q0[rest])
+    np.testing.assert_array_equal(s1[rest], s0[rest])
+    assert np.isnan(s1[1]).all() and np.isnan(s1[4]).all()
+    assert [bool(b) for b in np.isnan(s1[2])] == [i == n // 2 // 32 for i in range(n // 32)]
+    assert s1[5, -1] == 65504 and ref.unstored(q1.view(np.uint8)).view(np.int8)[5, n - 1] == 127
+
+
 def test_norm_rows_score_as_an_index():
     """Normed rows as a Q8_0 matrix: qgemv_q8_0 scores a query against them."""
     import oracle
