@@ -137,6 +137,8 @@ __device__ __forceinline__ void route_column(const qg_route& r, const float* log
   bool done = false;
   if (deal.per <= 8)
     done = route_column_fast<8>(r, deal, logits, bias, E, topk, slots, ids, rw);
+  else if (deal.per <= 16)  // (512 experts: 7.9 us, 9.5 as 32 a lane)
+    done = route_column_fast<16>(r, deal, logits, bias, E, topk, slots, ids, rw);
   else if (deal.per <= 32)
     done = route_column_fast<32>(r, deal, logits, bias, E, topk, slots, ids, rw);
   if (!done) route_exact(r, logits, bias, E, topk, c, ids, rw);
