@@ -31,7 +31,7 @@ bool attn_shape_ok(int n_seq, int n_heads, int n_kv_heads, int head_dim, int nco
 // The kernel numbers an item's units, and its at_pad places behind them, in 32 bits: no more than a whole number of 32 tokens,
 // a partly filled unit and 7 places.
 bool attn_size_ok(const qg_kvcache& c, int n_heads, int ncols) {
-  static_assert(at_unit(256, 4) >= 32 && at_unit(64, 8) >= 32 && at_pad(1) <= 7 && at_pad(8) <= 7, "units + 8 are enough");
+  static_assert(at_unit(256, 4) >= 32 && at_unit(64, 8) >= 32 && at_pad(QG_Q4_1, 1) <= 7 && at_pad(QG_F16, 8) <= 7, "units + 8 are enough");
   const int rows = n_heads / c.n_kv_heads * ncols, nt = tiles_of(c.type, rows, c.head_dim);
   const int64_t tiles = (rows + 8 * nt - 1) / (8 * nt);
   const int64_t units = (int64_t)c.max_pages * c.page_size / 32 + 8;

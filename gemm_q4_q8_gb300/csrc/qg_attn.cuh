@@ -76,7 +76,7 @@
 // nearly so in Q8_0 (64 ragged sequences, 279 MB, in 50 us, issue slots half
 // used). Q4_1, one tile: by instructions, 363 a warp and record of 2,560 bytes, with 16 warps an SM and two thirds of the issue slots
 // used: the records alone at 82% of the copy rate, and 11 us around them (262,143 tokens of 8 kv heads of 128, 336 MB: 70.6 us,
-// 4.7 TB/s; 64 ragged sequences, 286 MB: 68.3). Two records a step 68.1 and 70.3; five CTAs an SM 73 to 79, as the registers
+// 4.7 TB/s; 64 ragged sequences, 286 MB: 64.5). Two records a step 68.1 and 70.3; five CTAs an SM 73 to 79, as the registers
 // do not suffice. More rows: by the latency of the instructions between two matrix
 // products, with the 8 to 16 warps that the accumulators leave room for (Q8_0, 32 rows of heads
 // of 256: 800 instructions a record and tile of 16 rows, issue slots 38% and
@@ -466,7 +466,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     if constexpr (CLUSTER)
       return ClusterRun<UNIT>(a, p.tiles, rank, ctas);
     else
-      return Runs<AT_THREADS, UNIT, at_pad(NT), C::GRID>(a, p.tiles, s_runs, s_part, cta == 0);
+      return Runs<AT_THREADS, UNIT, at_pad(TYPE, NT), C::GRID>(a, p.tiles, s_runs, s_part, cta == 0);
   }();
   if (cta >= runs.N) return;
   const int items = runs.items;
@@ -1485,7 +1485,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
 // Joins the parts of the items that are cut. blockIdx.x is an item (by_item) or, where there are more items than CTAs of
 // the main kernel, one of those CTAs: the last item that starts in its run is the only one that may be cut. WIDE: a CTA
 // joins a row and its warps share the parts out, for few items of many parts; otherwise a warp joins a row.
-template <int D, int ROWS, bool WIDE, int GRID>
+template <int D, int ROWS, bool WIDE, int GRID, int PAD>
 __global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kernel(const __grid_constant__ AttnDev p, int by_item) {
   constexpr int THREADS = WIDE ? 256 : 128, WARPS = THREADS / 32;
   constexpr int V = D / 32;               // dimensions of a lane
@@ -1500,7 +1500,7 @@ __global__ void __launch_bounds__(WIDE ? 256 : 128, WIDE ? 3 : 8) attn_join_kern
   const int row = WIDE ? blockIdx.y : blockIdx.y * WARPS + warp;
   pdl_trigger();
   // The main kernel lets this one start once what came before it is complete; so before pdl_wait only its parts are not.
-  const Runs<THREADS, at_unit(D, ROWS / 8), at_pad(ROWS / 8), GRID> runs(p.a, p.tiles, s_runs, s_part, false);
+  const Runs<THREADS, at_unit(D, ROWS / 8), PAD, GRID> runs(p.a, p.tiles, s_runs, s_part, false);
   Unit x;
   int c0 = blockIdx.x, n = 0;
   if (by_item) {
@@ -1646,7 +1646,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
                         n_items * ctas <= AT_SMS ? LC_SMEM : LC_FULL, p);
     }
   }
-  most = (most + at_pad(NT)) * n_items;
+  most = (most + at_pad(TYPE, NT)) * n_items;
   const int grid = most < C::GRID ? (int)most : C::GRID;
   const bool early = grid <= AT_SMS;
   const bool by_item = n_items <= grid, wide = n_items <= 4 * AT_SMS / tile_rows;
@@ -1657,7 +1657,7 @@ cudaError_t attn_typed(const AttnArgs& a, cudaStream_t s) {
   const size_t smem = C::smem(a.c.n_seq);
   cudaError_t e = prepare_kernel((const void*)attn_kernel<TYPE, D, NT, false>, smem, false);
   if (e != cudaSuccess) return e;
-  const auto join = wide ? attn_join_kernel<D, C::ROWS, true, C::GRID> : attn_join_kernel<D, C::ROWS, false, C::GRID>;
+  const auto join = wide ? attn_join_kernel<D, C::ROWS, true, C::GRID, at_pad(TYPE, NT)> : attn_join_kernel<D, C::ROWS, false, C::GRID, at_pad(TYPE, NT)>;
   e = launch_pdl(attn_kernel<TYPE, D, NT, false>, dim3(grid), dim3(AT_THREADS), smem, s, 0, early ? LC_SMEM : LC_FULL, p);
   if (e != cudaSuccess) return e;
   const dim3 join_grid(by_item ? n_items : grid, wide ? tile_rows : (tile_rows + 3) / 4);

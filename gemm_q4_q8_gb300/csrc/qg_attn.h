@@ -21,8 +21,9 @@ __host__ __device__ constexpr int at_team(int d, int nt) { return d == 256 && nt
 // Tokens of a unit: a record of 16 for every team of the CTA.
 __host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_team(d, nt) * KV_GROUP; }
 // An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
-// the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64).
-__host__ __device__ constexpr int at_pad(int nt) { return nt == 1 ? 2 : 4; }
+// the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64). Q4_1, 64
+// ragged sequences, 8 heads of 128: 68.4 us with 2, 64.5 with 3, 65.4 with 4, 66.2 with 5; 16 rows 96.9 with 3, 94.3 with 4, 97.8 with 6.
+__host__ __device__ constexpr int at_pad(int type, int nt) { return nt > 1 ? 4 : type == QG_Q4_1 ? 3 : 2; }
 
 cudaError_t attn_launch_64(const AttnArgs& a, int nt, cudaStream_t s);
 cudaError_t attn_launch_128(const AttnArgs& a, int nt, cudaStream_t s);
