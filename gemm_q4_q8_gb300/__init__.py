@@ -377,10 +377,11 @@ def qmoe_route(plan, logits, topk, ids_out, rw_out, bias=None, stream=None):
     if _ELEM is None:
         _dtypes()
     ntok, e = logits.shape
-    if _ELEM.get(logits.dtype) != QG_F32 or (e > 1 and logits.stride(1) != 1):
-        raise ValueError(f"logits: float32 rows expected, got {logits.dtype} with strides {logits.stride()}")
+    if _ELEM.get(logits.dtype) != QG_F32:
+        raise ValueError(f"logits: float32 expected, got {logits.dtype}")
+    stride = _vectors(logits, logits.shape, e, "logits")
     n = ntok * topk
-    st = (_lib or load()).qmoe_route(plan, logits.data_ptr(), logits.stride(0), _floats(bias, "bias", e), ntok, e, topk,
+    st = (_lib or load()).qmoe_route(plan, logits.data_ptr(), stride, _floats(bias, "bias", e), ntok, e, topk,
                                      _int32s(ids_out, "ids_out", n), _floats(rw_out, "rw_out", n), _stream(stream))
     if st:
         _check("qmoe_route", st)
@@ -407,19 +408,20 @@ def qembed(qtype, q, scl, ids, y, scale=1.0, err_flag=None, stream=None):
     if _ELEM is None:
         _dtypes()
     rows, k = q.shape
+    if not q.is_contiguous() or (q.dtype != _FLOAT16 if qtype == QG_F16 else q.element_size() != 1):
+        raise ValueError(f"q: contiguous rows of type {qtype} expected, got {q.dtype} {tuple(q.shape)}")
     if qtype == Q4_0:
         k *= 2
-    nbytes = rows * k // 2 if qtype == Q4_0 else rows * k * (2 if qtype == QG_F16 else 1)
-    if not q.is_contiguous() or q.nbytes != nbytes or (qtype == QG_F16 and q.dtype != _FLOAT16):
-        raise ValueError(f"q: contiguous rows of type {qtype} expected, got {q.dtype} {tuple(q.shape)}")
-    if scl is not None and (not scl.is_contiguous() or scl.nbytes != rows * (k // 32) * 2):
-        raise ValueError(f"scl: {rows} x {k // 32} contiguous f16 bits expected, got {scl.dtype} {tuple(scl.shape)}")
+    sp = None
+    if scl is not None:
+        if scl.numel() != rows * (k // 32) or scl.element_size() != 2 or not scl.is_contiguous():
+            raise ValueError(f"scl: {rows} x {k // 32} contiguous f16 bits expected, got {scl.dtype} {tuple(scl.shape)}")
+        sp = scl.data_ptr()
     ntok = ids.numel()
-    kind = _elem(y, "y")
-    if y.shape != (ntok, k) or (k > 1 and y.stride(1) != 1):
-        raise ValueError(f"y: {ntok} rows of {k} expected, got {tuple(y.shape)} with strides {y.stride()}")
-    st = (_lib or load()).qembed(int(qtype), q.data_ptr(), _ptr(scl), rows, k, _int32s(ids, "ids", ntok), ntok, scale, kind,
-                                 y.data_ptr(), y.stride(0), _flag(err_flag), _stream(stream))
+    kind, shape = _elem(y, "y"), (ntok, k)
+    stride = _vectors(y, shape, k, "y")
+    st = (_lib or load()).qembed(int(qtype), q.data_ptr(), sp, rows, k, _int32s(ids, "ids", ntok), ntok, scale, kind,
+                                 y.data_ptr(), stride, _flag(err_flag), _stream(stream))
     if st:
         _check("qembed", st)
 
@@ -449,17 +451,23 @@ def qrms_norm(x, w, y, eps=1e-6, add=None, sum_out=None, w_add=0.0, y_scl=None, 
     else:
         raise ValueError(f"x: [ntok, n] or [ntok, heads, n] expected, got {tuple(shape)}")
     row = heads * n
-    kind, xs = _elem(x, "x"), _vectors(x, shape, row, "x")
-    ap = sp = a_stride = s_stride = None
+    kind, xs = _elem(x, "x"), row if x.is_contiguous() else _vectors(x, shape, row, "x")
+    ap = sp = scales = None
+    a_stride = s_stride = row
     if add is not None:
         if add.dtype != dtype:
             raise ValueError(f"add: {dtype} expected, as x, got {add.dtype}")
-        ap, a_stride = add.data_ptr(), _vectors(add, shape, row, "add")
-    if sum_out is not None:
+        ap = add.data_ptr()
+        if add.shape != shape or not add.is_contiguous():
+            a_stride = _vectors(add, shape, row, "add")
+    if sum_out is x:
+        sp, s_stride = x.data_ptr(), xs
+    elif sum_out is not None:
         if sum_out.dtype != dtype:
             raise ValueError(f"sum_out: {dtype} expected, as x, got {sum_out.dtype}")
-        sp, s_stride = sum_out.data_ptr(), _vectors(sum_out, shape, row, "sum_out")
-    scales = None
+        sp = sum_out.data_ptr()
+        if sum_out.shape != shape or not sum_out.is_contiguous():
+            s_stride = _vectors(sum_out, shape, row, "sum_out")
     if y_scl is None:
         yt, ys = _elem(y, "y"), _vectors(y, shape, row, "y")
     else:
@@ -468,7 +476,7 @@ def qrms_norm(x, w, y, eps=1e-6, add=None, sum_out=None, w_add=0.0, y_scl=None, 
             raise ValueError(f"y: contiguous int8 {tuple(shape)} expected, got {y.dtype} {tuple(y.shape)}")
         if y_scl.element_size() != 2 or y_scl.numel() != ntok * heads * (n // 32) or not y_scl.is_contiguous():
             raise ValueError(f"y_scl: {ntok * heads} x {n // 32} contiguous f16 expected, got {y_scl.dtype} {tuple(y_scl.shape)}")
-    st = (_lib or load()).qrms_norm(kind, x.data_ptr(), xs, ap, a_stride or 0, sp, s_stride or 0, _floats(w, "w", n), w_add, eps, ntok,
+    st = (_lib or load()).qrms_norm(kind, x.data_ptr(), xs, ap, a_stride, sp, s_stride, _floats(w, "w", n), w_add, eps, ntok,
                                     heads, n, yt, y.data_ptr(), ys, scales, _stream(stream))
     if st:
         _check("qrms_norm", st)

@@ -206,3 +206,24 @@ def test_binding_refusals():
         with pytest.raises(ValueError):
             f()
             pytest.fail(f"call {i}")
+
+
+def test_binding_refuses_rows_with_gaps():
+    """Rows whose elements are not neighbours, though their stride is that of contiguous ones."""
+    torch = pytest.importorskip("torch")
+    x, w = torch.zeros(4, 64), torch.zeros(64)
+    gap = torch.zeros(400).as_strided((4, 64), (64, 2))
+    heads = torch.zeros(600).as_strided((4, 2, 32), (64, 40, 1))
+    ids, rw = torch.zeros(4, 8, dtype=torch.int32), torch.zeros(4, 8)
+    plan = qg.qroute_plan()
+    q8, s8 = torch.zeros(10, 64, dtype=torch.int8), torch.zeros(10, 2, dtype=torch.float16)
+    calls = [lambda: qg.qrms_norm(gap, w, x, stream=0), lambda: qg.qrms_norm(x, w, gap, stream=0),
+             lambda: qg.qrms_norm(x, w, x, add=gap, stream=0), lambda: qg.qrms_norm(x, w, x, add=x, sum_out=gap, stream=0),
+             lambda: qg.qrms_norm(heads, w[:32], x.view(4, 2, 32), stream=0),
+             lambda: qg.qrms_norm(x.view(4, 2, 32), w[:32], heads, stream=0),
+             lambda: qg.qembed(qg.Q8_0, q8, s8, ids[0, :4], gap, stream=0),
+             lambda: qg.qmoe_route(plan, gap, 8, ids, rw, stream=0)]
+    for i, f in enumerate(calls):
+        with pytest.raises(ValueError):
+            f()
+            pytest.fail(f"call {i}")
