@@ -98,8 +98,8 @@ cudaError_t embed_u(const EmbedArgs& a, cudaStream_t s) {
 
 template <int QT, class TO>
 cudaError_t embed_go(const EmbedArgs& a, cudaStream_t s) {
-  // one unit a lane where that makes no more warps than the machine holds at a time; else four (4,095 rows of 2,048: 8.6 us, 9.8 with
-  // 16 neighbouring elements a lane and access)
+  // one unit a lane where that makes no more warps than the machine holds at a time; else four (one row of 5,120: 1.5 us, with four 1.65;
+  // 150 rows of 2,048 1.73 and 1.79; 1,000 4.5 and 3.1; 4,095 17.4 and 8.5, 9.8 where a lane's elements are 16 neighbours)
   return (int64_t)a.ntok * a.k * sizeof(TO) <= (int64_t)152 * 64 * 512 ? embed_u<QT, TO, 1>(a, s) : embed_u<QT, TO, 4>(a, s);
 }
 

@@ -1,7 +1,7 @@
 // qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token (qg_route.cuh).
 //
 // Bound by instructions: 770 a token of 256 experts in 8 groups, two thirds of the issue slots used: 16,383 tokens in 18.0 us, where
-// their 18 MB would take 2.6. Without bias and groups 11 us, 512 experts 34, 1,000 tokens 6.4. Eight or sixteen lanes a token instead of a
+// their 18 MB would take 2.6. Without bias and groups 11 us, 512 experts 31.5, 1,000 tokens 6.4. Eight or sixteen lanes a token instead of a
 // warp: 22.6 and 25.2 us, as the k best one after the other then are a chain for few tokens at a time; the next token's logits
 // loaded ahead: no gain.
 #include <cuda_runtime.h>
@@ -22,8 +22,8 @@ constexpr int RO_WARPS = 4;
 // all.
 constexpr int RO_PER_SM = 6, RO_BLOCKS = 152 * RO_PER_SM;
 
-// NE: experts of a lane, at most; 0: all in 64 bits. FULL: every lane has NE. WIDE: and their logits are aligned to 16 bytes.
-template <int NE, bool FULL, bool WIDE>
+// NE: experts of a lane, at most; 0: all in 64 bits. WIDE: every lane has NE, and their logits are aligned to 16 bytes.
+template <int NE, bool WIDE>
 __global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? RO_PER_SM : 1)
     route_kernel(const __grid_constant__ qg_route r, const float* logits, int64_t stride, const float* bias, int ntok, int E,
                  int topk, int32_t* ids, float* rw) {
@@ -43,7 +43,7 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? RO_PER_SM : 1)
     route_share(deal, E, first, mine);
     float b[NE], l[NE];
 #pragma unroll
-    for (int i = 0; i < NE; ++i) b[i] = bias && (FULL || i < mine) ? bias[first + i] : 0.f;
+    for (int i = 0; i < NE; ++i) b[i] = bias && (WIDE || i < mine) ? bias[first + i] : 0.f;
     for (; tok < ntok; tok += step) {
       const float* const row = logits + tok * stride;
       if constexpr (WIDE) {
@@ -54,9 +54,9 @@ __global__ void __launch_bounds__(RO_WARPS * 32, NE <= 8 ? RO_PER_SM : 1)
         }
       } else {
 #pragma unroll
-        for (int i = 0; i < NE; ++i) l[i] = FULL || i < mine ? row[first + i] : -INFINITY;
+        for (int i = 0; i < NE; ++i) l[i] = i < mine ? row[first + i] : -INFINITY;
       }
-      if (!route_fast<NE, FULL>(r, deal, l, b, row, bias, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
+      if (!route_fast<NE, WIDE>(r, deal, l, b, row, bias, first, mine, topk, slots[warp], ids + tok * topk, rw + tok * topk))
         route_exact(r, row, bias, E, topk, c, ids + tok * topk, rw + tok * topk);
       __syncwarp();  // the slots have been read
     }
@@ -79,19 +79,19 @@ cudaError_t route_launch(const qg_route& r, const float* logits, int64_t stride,
                          int32_t* ids, float* rw, cudaStream_t s) {
   const RouteDeal deal = route_deal(r, E);
   const int per = deal.per;
-  const bool full = E == 32 * per, wide = full && per % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (ntok == 1 || stride % 4 == 0);
-  const auto kern = wide && per == 4    ? route_kernel<4, true, true>
-                    : wide && per == 8  ? route_kernel<8, true, true>
-                    : wide && per == 16 ? route_kernel<16, true, true>
-                    : wide && per == 32 ? route_kernel<32, true, true>
-                    : full && per == 2  ? route_kernel<2, true, false>
-                    : per <= 1          ? route_kernel<1, false, false>
-                    : per <= 2          ? route_kernel<2, false, false>
-                    : per <= 4          ? route_kernel<4, false, false>
-                    : per <= 8          ? route_kernel<8, false, false>
-                    : per <= 16         ? route_kernel<16, false, false>
-                    : per <= 32         ? route_kernel<32, false, false>
-                                        : route_kernel<0, false, false>;
+  // (16,383 tokens of 256 experts 17.9 us, 19.2 without; 128 14.9 and 15.3; 512 31.5 and 36.2)
+  const bool wide = E == 32 * per && per % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (ntok == 1 || stride % 4 == 0);
+  const auto kern = wide && per == 4    ? route_kernel<4, true>
+                    : wide && per == 8  ? route_kernel<8, true>
+                    : wide && per == 16 ? route_kernel<16, true>
+                    : wide && per == 32 ? route_kernel<32, true>
+                    : per <= 1          ? route_kernel<1, false>
+                    : per <= 2          ? route_kernel<2, false>
+                    : per <= 4          ? route_kernel<4, false>
+                    : per <= 8          ? route_kernel<8, false>
+                    : per <= 16         ? route_kernel<16, false>
+                    : per <= 32         ? route_kernel<32, false>
+                                        : route_kernel<0, false>;
   const int64_t blocks = ((int64_t)ntok + RO_WARPS - 1) / RO_WARPS;
   return launch_pdl(kern, dim3((unsigned)(blocks < RO_BLOCKS ? blocks : RO_BLOCKS)), dim3(RO_WARPS * 32),
                     (size_t)RO_WARPS * E * sizeof(double), s, 0, LC_L1, r, logits, stride, bias, ntok, E, topk, ids, rw);
