@@ -185,6 +185,12 @@ struct RouteSlot {
 // A number of a key.
 __device__ __forceinline__ float ro_value(uint32_t key) { return __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key); }
 
+// exp(x - y), with what rounding the difference leaves (half a step of 32 to 64 is 2^-19).
+__device__ __forceinline__ float ro_exp_diff(float x, float y) {
+  const float d = x - y, v = d - x, left = (x - (d - v)) - (y + v), e = expf(d);
+  return fmaf(e, left, e);
+}
+
 // Scores in 64 bits (softmax: over the sum), of finite logits.
 static __device__ __noinline__ double ro_score(bool soft, float l, float top) {
   const double e = exp(soft ? (double)l - (double)top : -(double)l);
@@ -385,14 +391,15 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
         for (int m = 0; m < n; ++m) rank[j] += slots[m].exact > v[j] || (slots[m].exact == v[j] && slots[m].id < id[j]);
       }
   }
-  // (the weights' errors: expf 2^-22, the sums and the reciprocals below 2^-22 each)
+  // (the weights' errors: expf 2^-22, the sums and the reciprocals below 2^-22 each; in the softmax's sum the differences' roundings
+  // count by their terms)
   float w[2] = {0.f, 0.f}, all = 0.f;
   const float inv = soft ? ro_rcp(sum) : 1.f;
 #pragma unroll
   for (int j = 0; j < 2; ++j)
     if (rank[j] < topk) {
       const float x = row[id[j]];
-      w[j] = soft ? expf(x - top) * inv : ro_rcp(1.f + expf(-x));
+      w[j] = soft ? ro_exp_diff(x, top) * inv : ro_rcp(1.f + expf(-x));
     }
   all = ro_warp_sum(w[0] + w[1]);
   const float by = r.renorm ? ro_rcp(all) : 1.f;

@@ -411,6 +411,17 @@ def test_route_choice_is_that_of_64_bits(score):
     assert seen > n // 2
 
 
+@pytest.mark.parametrize("renorm", [True, False])
+def test_route_weights_far_below_the_largest(renorm):
+    """Logits 32 to 64 below the largest: their difference in f32 is off by up to 2^-19, which the weights must not be."""
+    g = rng(43)
+    logits = g.uniform(-33, 28, (100, 64)).astype(np.float32)
+    logits[:, 0] = np.float32(30) + (np.float32(2.0) ** -19) * g.integers(0, 999, 100).astype(np.float32)
+    logits[:, 1] = -20  # the difference has a half step left where the largest is an odd number of steps
+    check_route(logits, None, 32, renorm=renorm)
+    check_route(logits, (0.01 * g.standard_normal(64)).astype(np.float32), 32, renorm=renorm)
+
+
 def test_route_saturated_sigmoids():
     """Sigmoids that f32 rounds to 1: still in order with a bias; without one in the order of the logits, past 64 bits' end."""
     x = np.linspace(12, 30, 64).astype(np.float32)[None]
