@@ -13,6 +13,8 @@
 // route_fast. The lanes of a warp are dealt to the groups, and a group's experts in runs to its lanes, in registers. The k-th
 // largest of the lanes' maxima is a bound below which no expert can be among the k best; what is above it, a few more than
 // k, goes to shared memory, one or two for each lane, which counts how many are ahead.
+//
+// The numbers of route_fast stay within f32's: logits of 2^126 and more, whose differences may not, are routed in 64 bits.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -219,7 +221,7 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
 #pragma unroll
   for (int i = 0; i < NE; ++i) {
     most = fmaxf(most, l[i]);
-    odd |= here(i) && !(fabsf(l[i]) + fabsf(b[i]) < INFINITY);
+    odd |= here(i) && !(fabsf(l[i]) < 0x1p126f && fabsf(b[i]) < INFINITY);
     size = fmaxf(size, here(i) ? fabsf(l[i]) : 0.f);
   }
   if (__any_sync(0xffffffffu, odd)) return false;
@@ -343,7 +345,7 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
     if (lane >= x) at += up;
   }
   const int n = __shfl_sync(0xffffffffu, at, 31);
-  if (n > RO_SLOTS) return false;
+  if (n > RO_SLOTS || n < topk) return false;  // (nothing is left unwritten)
   RouteSlot* to = slots + (at - own);
 #pragma unroll
   for (int i = 0; i < NE; ++i)

@@ -1,0 +1,87 @@
+"""GPU parity of the routing by a plan at the ends of f32's range, through both of its calls, against the plain 64-bit form."""
+import numpy as np
+import pytest
+
+import layer_ref as ref
+from helpers import assert_within, host
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+import gemm_q4_q8_gb300 as qg  # noqa: E402
+
+MOST = np.finfo(np.float32).max
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from gemm_q4_q8_gb300 import build
+    build.build()
+
+
+def rng(*key):
+    return np.random.Generator(np.random.PCG64(list(key)))
+
+
+def cuda(a):
+    return torch.from_numpy(np.ascontiguousarray(a)).cuda()
+
+
+def against(ids, rw, logits, bias, k, plan):
+    """ids equal, weights within 2^-19 of themselves, as documented. (Where two c that decide differ by less than 1e-14, two
+    exponentials in 64 bits may order them either way.)"""
+    for t in range(len(logits)):
+        with np.errstate(all="ignore"):
+            want, w, near = ref.route(logits[t], bias, k, **plan)
+        assert (ids[t] >= 0).all() and (ids[t] < logits.shape[1]).all(), (t, ids[t])
+        if near > 1e-14:
+            assert np.array_equal(ids[t], want), (t, ids[t], want)
+            assert np.array_equal(np.isnan(rw[t]), np.isnan(w)), (t, rw[t], w)
+            w = np.nan_to_num(w)
+            assert_within(np.nan_to_num(rw[t]), w, 2.0 ** -19 * np.abs(w) + 2.0 ** -126, f"token {t}")
+
+
+def check(logits, bias, k, **plan):
+    """At most 16 tokens, by qmoe_route and by qmoe_router_planned, whose columns are one-hot: weights [experts, column] are the logits."""
+    n, e = logits.shape
+    made, b = qg.qroute_plan(**plan), None if bias is None else cuda(bias)
+    for fused in (False, True):
+        ids = torch.full((n, k), -1, dtype=torch.int32, device="cuda")
+        rw = torch.full((n, k), -1.0, device="cuda")
+        if fused:
+            w = np.zeros((e, 16), np.float32)
+            w[:, :n] = logits.T
+            lg = torch.empty((n, e), device="cuda")
+            qg.qmoe_router_planned(made, cuda(w), torch.eye(16, dtype=torch.float16, device="cuda")[:n].contiguous(), k, ids, rw, bias=b,
+                                   logits_out=lg)
+            assert np.array_equal(host(lg), logits)
+        else:
+            qg.qmoe_route(made, cuda(logits), k, ids, rw, bias=b)
+        against(host(ids), host(rw), logits, bias, k, plan)
+
+
+SIZES = [(64, 4), (50, 25), (256, 8), (300, 32), (512, 10), (1000, 6)]
+SCORES = ["softmax", "sigmoid"]
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("e,k", SIZES)
+def test_logits_whose_differences_leave_f32(e, k, score):
+    """Finite logits up to the largest: a few of both signs, all of them, alike and not."""
+    g = rng(1, e)
+    x = g.standard_normal((9, e)).astype(np.float32)
+    x[0, 3], x[0, 4] = 3e38, -3e38
+    x[1, 7], x[1, e - 8] = MOST, -MOST
+    x[2] = np.where(np.arange(e) % 2, MOST, -MOST)
+    x[3, 1] = -MOST
+    x[4, ::3] = 2e38
+    x[5] *= 1e38
+    x[6] = MOST
+    x[7] = -MOST
+    x[8, :] = np.linspace(-float(MOST), float(MOST), e).astype(np.float32)
+    for bias in (None, (0.1 * g.standard_normal(e)).astype(np.float32)):
+        for plan in ({}, dict(renorm=False), dict(n_group=2, top_group=1, group_top=2), dict(n_group=2, top_group=1, group_top=1, scale=2.5)):
+            check(x, bias, k, score=score, **plan)
