@@ -45,7 +45,8 @@ def against(ids, rw, logits, bias, k, plan):
 
 
 def check(logits, bias, k, **plan):
-    """At most 16 tokens, by qmoe_route and by qmoe_router_planned, whose columns are one-hot: weights [experts, column] are the logits."""
+    """At most 16 tokens, by qmoe_route and by qmoe_router_planned, whose columns are one-hot: weights [experts, column] are the logits
+    (of experts whose weights are finite: 0 times an infinity is NaN), and the routing is that of the logits it made."""
     n, e = logits.shape
     made, b = qg.qroute_plan(**plan), None if bias is None else cuda(bias)
     for fused in (False, True):
@@ -57,10 +58,13 @@ def check(logits, bias, k, **plan):
             lg = torch.empty((n, e), device="cuda")
             qg.qmoe_router_planned(made, cuda(w), torch.eye(16, dtype=torch.float16, device="cuda")[:n].contiguous(), k, ids, rw, bias=b,
                                    logits_out=lg)
-            assert np.array_equal(host(lg), logits)
+            finite = np.isfinite(w).all(1)
+            assert np.array_equal(host(lg)[:, finite], logits[:, finite])
+            made_of = host(lg)
         else:
             qg.qmoe_route(made, cuda(logits), k, ids, rw, bias=b)
-        against(host(ids), host(rw), logits, bias, k, plan)
+            made_of = logits
+        against(host(ids), host(rw), made_of, bias, k, plan)
 
 
 SIZES = [(64, 4), (50, 25), (256, 8), (300, 32), (512, 10), (1000, 6)]
@@ -78,7 +82,8 @@ def test_logits_whose_differences_leave_f32(e, k, score):
     x[2] = np.where(np.arange(e) % 2, MOST, -MOST)
     x[3, 1] = -MOST
     x[4, ::3] = 2e38
-    x[5] *= 1e38
+    with np.errstate(over="ignore"):
+        x[5] *= 1e38  # (some of them infinite)
     x[6] = MOST
     x[7] = -MOST
     x[8, :] = np.linspace(-float(MOST), float(MOST), e).astype(np.float32)
