@@ -332,7 +332,8 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
     bound = __reduce_max_sync(0xffffffffu, key);
     if (key == bound) key = 0;  // (with every lane that has it: the bound is then lower than need be)
   }
-  const float least = open ? (bound ? ro_value(bound) - 2.f * off : -3.402823466e38f) : INFINITY;
+  // (not below f32's least number: -infinity would let in experts that are not there)
+  const float least = open ? (bound ? fmaxf(ro_value(bound) - 2.f * off, -3.402823466e38f) : -3.402823466e38f) : INFINITY;
   uint32_t in = 0;
 #pragma unroll
   for (int i = 0; i < NE; ++i)

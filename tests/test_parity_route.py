@@ -90,3 +90,16 @@ def test_logits_whose_differences_leave_f32(e, k, score):
     for bias in (None, (0.1 * g.standard_normal(e)).astype(np.float32)):
         for plan in ({}, dict(renorm=False), dict(n_group=2, top_group=1, group_top=2), dict(n_group=2, top_group=1, group_top=1, scale=2.5)):
             check(x, bias, k, score=score, **plan)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("e,k", SIZES + [(40, 4), (50, 3), (20, 2), (63, 6)])
+def test_biases_at_the_least_number(e, k, score):
+    """All experts but a few shut out by f32's least number, so that such ones are chosen, too; and all of them."""
+    g = rng(2, e)
+    x = g.standard_normal((5, e)).astype(np.float32)
+    for n_open in (0, 1, k - 1, k):
+        bias = np.full(e, -MOST, np.float32)
+        bias[g.permutation(e)[:n_open]] = 0.1
+        for plan in ({}, dict(renorm=False), dict(n_group=3 if e % 2 else 2, top_group=1, group_top=1)):
+            check(x, bias, k, score=score, **plan)
