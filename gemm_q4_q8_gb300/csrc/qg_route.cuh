@@ -14,7 +14,8 @@
 // largest of the lanes' maxima is a bound below which no expert can be among the k best; what is above it, a few more than
 // k, goes to shared memory, one or two for each lane, which counts how many are ahead.
 //
-// The numbers of route_fast stay within f32's: logits of 2^126 and more, whose differences may not, are routed in 64 bits.
+// The numbers of route_fast stay within f32's: logits of 2^126 and more, whose differences may not, are routed in 64 bits, and a
+// group's worth is halved, as the sum of two c may not either.
 #pragma once
 #include <cuda_runtime.h>
 #include <stdint.h>
@@ -267,7 +268,7 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
       v1 = fmaxf(fminf(v0, u0), fmaxf(v1, u1));
       v0 = fmaxf(v0, u0);
     }
-    const float worth = r.group_top == 2 ? v0 + v1 : v0;
+    const float worth = r.group_top == 2 ? 0.5f * v0 + 0.5f * v1 : v0;
     int ahead = 0;
 #pragma unroll 4
     for (int h = 0; h < r.n_group; ++h) ahead += __shfl_sync(0xffffffffu, worth, h * deal.lanes) > worth;
@@ -280,7 +281,7 @@ __device__ __forceinline__ bool route_fast(const qg_route& r, const RouteDeal& d
     const float reach = fmaf(4.f, off, fabsf(last) * 0x1p-21f);  // twice the error of a worth
     const int n_in = __popc(__ballot_sync(0xffffffffu, there && open));
     const float next = n_in > r.top_group * deal.lanes ? last : ro_value(out);  // (groups equal at the border are all open)
-    if (last - next <= reach) {
+    if (!(last - next > reach)) {
       // Above the next one by more than the errors: stays. Below the last one by more: does not. Those between in 64 bits, of each
       // the experts that may be its largest.
       const bool above = there && worth > next + reach, close = there && !above && worth >= last - reach;

@@ -103,3 +103,23 @@ def test_biases_at_the_least_number(e, k, score):
         bias[g.permutation(e)[:n_open]] = 0.1
         for plan in ({}, dict(renorm=False), dict(n_group=3 if e % 2 else 2, top_group=1, group_top=1)):
             check(x, bias, k, score=score, **plan)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("value", [2e38, MOST, 1e30, -1e30, -2e38, -MOST])
+@pytest.mark.parametrize("e,k,groups", [(64, 4, 8), (256, 8, 8), (300, 10, 12), (40, 6, 5), (1000, 8, 4)])
+def test_groups_whose_sums_leave_f32(e, k, groups, value, score):
+    """Two experts of a group with biases of this size, one group kept; two such groups; all experts; and all below the least number
+    in sum, one group above the others."""
+    g = rng(3, e)
+    x = g.standard_normal((5, e)).astype(np.float32)
+    size = e // groups
+    two, four, rest = ((0.1 * g.standard_normal(e)).astype(np.float32) for _ in range(3))
+    two[2 * size:2 * size + 2] = value
+    four[2 * size:2 * size + 2] = four[4 * size:4 * size + 2] = value
+    rest[:] = value
+    rest[3 * size:4 * size] = np.float32(value) * np.float32(0.9)
+    for bias in (two, four, np.full(e, value, np.float32), rest):
+        for keep in (1, 2):
+            for best in (1, 2):
+                check(x, bias, k, score=score, n_group=groups, top_group=keep, group_top=best)
