@@ -123,3 +123,29 @@ def test_groups_whose_sums_leave_f32(e, k, groups, value, score):
         for keep in (1, 2):
             for best in (1, 2):
                 check(x, bias, k, score=score, n_group=groups, top_group=keep, group_top=best)
+
+
+@pytest.mark.parametrize("score", SCORES)
+@pytest.mark.parametrize("value", [-1e2, -1e4, -1e6, -1e9, -1e30, -MOST, -np.inf])
+@pytest.mark.parametrize("e,k,groups", [(64, 4, 8), (256, 8, 8), (300, 10, 12), (40, 6, 5), (1000, 8, 4)])
+def test_experts_shut_out(e, k, groups, value, score):
+    """One expert, a group, all but one of a group, half of all and all but k shut out by their bias or by their logit, among experts that
+    are equal or so near that only 64 bits tell them apart."""
+    g = rng(4, e)
+    x = g.standard_normal((8, e)).astype(np.float32)
+    x[1] = np.round(x[1])
+    x[2] = 0
+    x[3:5, 1::2] = x[3:5, ::2]
+    size, n = e // groups, np.arange(e)
+    alive = g.permutation(e)
+    kept = np.zeros(e, bool)
+    kept[alive[:k]] = True
+    for shut in (n == 5, n // size == 1, (n // size == 1) & (n != size), alive < e // 2, ~kept):
+        bias = (0.1 * g.standard_normal(e)).astype(np.float32)
+        bias[1::2] = np.nextafter(bias[::2], np.float32(9))  # pairs that f32 scores do not tell apart
+        masked = np.where(shut, np.float32(value), bias)
+        low = np.where(shut, np.float32(value), x)
+        for plan in ({}, dict(renorm=False), dict(n_group=groups, top_group=2, group_top=2), dict(n_group=groups, top_group=2, group_top=1)):
+            check(x, masked, k, score=score, **plan)
+            check(low, bias, k, score=score, **plan)
+            check(low, None, k, score=score, **plan)
