@@ -773,7 +773,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
     auto ref = [&](int nt, int c) { return limit[nt][c] == -INFINITY ? -INFINITY : z[nt][c]; };
     // Q8_0: weights are multiplied by their scale and by wmul = 2^(7-e), so that they stay below 2^15
     // for scales up to wmax = 2^e; larger scales move e up. wback = 1 / wmul. Q4_1: the same with
-    // 2^-e, weights being 2^7 times as large from the start.
+    // 2^-e, weights being 2^7 times as large from the start, and |d|, which another writer's blocks may have of either sign.
     float wmul = 1.f, wmax = 0.f, wback = 1.f;
     // Q4_1: om[nt][c] of block g (c < 2): sum of weights times m + 8 d, of row 8 nt + 2t + c
     float om[TYPE == QG_Q4_1 ? NT : 1][4];
@@ -1149,14 +1149,14 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
           uint32_t d0, d1;
           lds64(vb + scales + blk * 32 + (g >> 1) * 8, d0, d1);
           d[blk] = __byte_perm(d0, d1, g & 1 ? 0x7632u : 0x5410u);
-          big = __hmax2(big, *reinterpret_cast<__half2*>(&d[blk]));
+          big = __hmax2(big, __habs2(*reinterpret_cast<__half2*>(&d[blk])));
         }
         float dmax = fmaxf(__low2float(big), __high2float(big));
         if (__builtin_expect(__any_sync(0xffffffffu, dmax > wmax), 0)) {
           dmax = wmax;  // again without infinities, which would cost the others their bits
 #pragma unroll
           for (int blk = 0; blk < NB; ++blk) {
-            const float x = lo_f32(d[blk]), y = hi_f32(d[blk]);
+            const float x = fabsf(lo_f32(d[blk])), y = fabsf(hi_f32(d[blk]));
             if (x <= 65504.f) dmax = fmaxf(dmax, x);
             if (y <= 65504.f) dmax = fmaxf(dmax, y);
           }

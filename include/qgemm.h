@@ -442,7 +442,7 @@ qg_status qrope(const qg_rope *plan, qg_type xt, const void *x, int64_t x_stride
  * max x - m (the difference in f32), q the integer nearest to (x - m) / d (f32
  * operations, ties to even, within 0..15; 0 where d is 0). A block with a NaN or an
  * infinity gets d = NaN. A cache that is written in another way keeps m + 8 d within
- * +-65504.
+ * +-65504; its d may have either sign.
  *   type       : QG_F16, QG_Q8_0 or QG_Q4_1 (QG_ERR_TYPE)
  *   n_kv_heads : 1..256; head_dim: 64, 128 or 256; page_size: 16, 32, 64, 128
  *                or 256; n_pages >= 1; n_seq: 1..1024; max_pages >= 1, with
