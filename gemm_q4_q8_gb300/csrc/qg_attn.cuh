@@ -62,8 +62,9 @@
 // blocks' sums of queries are made once an item, as two f16 each scaled by row, and one small product with the blocks' m starts the
 // scores. Values: sum_j w_j v_j = sum_j (w_j d_j) (q_j - 8) + sum_j w_j (m_j + 8 d_j). The second part is one product a record for all
 // blocks, of weights and m + 8 d, both rounded to f16; in the first w d is rounded once, as in Q8_0, and q - 8 is exact (one packed
-// subtraction of subnormals; q itself would make both parts several times the answer, and cost twice the error, 5.9e-4 instead of
-// 2.6e-4 off 64 bits).
+// subtraction of subnormals; q itself would make both parts several times the answer). Off 64 bits: 5.9e-4 with q itself and a weight
+// that is rounded to f16 before d meets it, 2.6e-4 with neither. The one rounding alone, of 262,143 random tokens: 3.6e-4 without
+// it, 3.1e-4 with it, in the same time at heads of 128 (81 us from memory) and 256, 54 and 56 us at heads of 64.
 //
 // Weights are rounded to f16 because the matrix product with the values takes both
 // factors in one type, and values are f16 (or integers that f16 holds): half a step,
@@ -126,7 +127,8 @@ struct AttnCfg {
   static constexpr int NB = D / 32 / TEAM;      // blocks of a warp
   static constexpr int ACC = NT * NB * 8;       // accumulator registers
   static constexpr int RECORD = kv_record_bytes(TYPE, D), STAGE = (RECORD + 127) / 128 * 128;
-  // Q fragments read from shared memory each time, not kept in registers (Q4_1: 262,143 tokens 71.7 us with registers, 70.5 without)
+  // Q fragments read from shared memory each time, not kept in registers (Q4_1, one row tile: 262,143 tokens of heads of
+  // 128 71.7 us with registers, 70.5 without; heads of 64, long and ragged, as long either way)
   static constexpr bool QSMEM = NT * NB > 4 || TYPE == QG_Q4_1;
   static constexpr int QPITCH = QSMEM ? 2 * D + 64 : 2 * D;  // bytes of a row of Q (+64: no bank conflicts)
   // dimensions joined at a time (32 also where 64 would leave one stage less)
@@ -1188,7 +1190,7 @@ __global__ void __launch_bounds__(AT_THREADS, AttnCfg<TYPE, D, NT>::CPS)
             nibbles<NIB_LO>(v[2 * h], v[2 * h + 1], v0);
             nibbles<NIB_HI>(v[2 * h], v[2 * h + 1], v1);  // 16 times their values: taken off at the item's end
             // Less 8, exact: the sums of quants themselves would be many times what is left of them when m joins, and each product's
-            // rounding would weigh twice as much. (By two more products with -8 a block: 76.8 us instead of 73.8 for 262,143 tokens
+            // rounding would weigh as much more. (By two more products with -8 a block: 76.8 us instead of 73.8 for 262,143 tokens
             // of 8 heads of 128, and 3.4e-4 instead of 2.6e-4 off 64 bits.)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {

@@ -23,6 +23,7 @@ __host__ __device__ constexpr int at_unit(int d, int nt) { return AT_WARPS / at_
 // An item's end (four warps' sums joined, the next queries taken up) costs a CTA about as much as this many units, and
 // the runs are cut as if it were that many more (measured: 1.2 units at 8 rows of heads of 128, 4.3 at 32 rows of 64). Q4_1, 64
 // ragged sequences, 8 heads of 128: 68.4 us with 2, 64.5 with 3, 65.4 with 4, 66.2 with 5; 16 rows 96.9 with 3, 94.3 with 4, 97.8 with 6.
+// Others of 32 to 8,192 tokens with 2, 3 and 4: 8 heads of 64 40.1, 36.0 and 36.0 us, 4 heads of 256 54.4, 50.3 and 48.3.
 __host__ __device__ constexpr int at_pad(int type, int nt) { return nt > 1 ? 4 : type == QG_Q4_1 ? 3 : 2; }
 
 cudaError_t attn_launch_64(const AttnArgs& a, int nt, cudaStream_t s);

@@ -3,7 +3,7 @@
 // bytes that hold them and takes every second one, as the halves of a group lie byte by byte; a weight, an integer times its
 // f16 scale, is exact in f32, then multiplied by the call's scale and rounded.
 //
-// Bound by memory where there are many rows: 20,011 of 2,048 from Q8_0, 208 MB, to f32 31.6 us, 97% of the rate of a large copy; to f16 20.2, 92%.
+// Bound by memory where there are many rows: 20,011 of 2,048 from Q8_0, 208 MB, to f32 32.0 us, 96% of the rate of a large copy; to f16 21.0, 88%.
 // 4,095 rows, 42 MB that stay in L2: 8.6 us, issue slots 66% used (the floor of a copy is 6.3). One row: 1.5 us, the launch and
 // two loads, the second at the first one's place.
 #include <cuda_fp16.h>

@@ -9,7 +9,7 @@
 //
 // Bound by memory: 8,191 rows of 5,120 f32 with the residual, to f16 and f32: 84.6 us, 587 MB, the rate of a large copy; without it 38.6 us,
 // 252 MB, 96% of it. To Q8_0 by its instructions, 140 for eight elements of a lane: 20,011 rows of 2,048 f16 in 28.5 us, where the bytes
-// take 18.5, with 28 warps an SM and two thirds of the issue slots used (read back in 20.2 more: 48.7; groups of eight a thread: two
+// take 18.5, with 28 warps an SM and two thirds of the issue slots used (read back in the rest of 48.7; groups of eight a thread: two
 // 54.4, eight, whose registers halve the warps, 67.3). One row of 5,120: 2.5 us, the launch, two trips to memory and one barrier.
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

@@ -1,7 +1,8 @@
 // qg_route.cu -- routing to experts from logits (qmoe_route): a warp a token (qg_route.cuh).
 //
-// Bound by instructions: 770 a token of 256 experts in 8 groups, two thirds of the issue slots used: 16,383 tokens in 18.0 us, where
-// their 18 MB would take 2.6. Without bias and groups 11 us, 512 experts 31.5, 1,000 tokens 6.4. Eight or sixteen lanes a token instead of a
+// Bound by instructions: 808 a token of 256 experts in 8 groups, 70% of the issue slots used: 16,383 tokens in 18.0 us, where
+// their 18 MB would take 2.6 (18.4 with one expert shut out by -1e9, or by -infinity). Without bias and groups 11.1 us, 512 experts
+// 31.5, 1,000 tokens 6.5; all of them in 64 bits, as a bias of NaN has it, 581. Eight or sixteen lanes a token instead of a
 // warp: 22.6 and 25.2 us, as the k best one after the other then are a chain for few tokens at a time; the next token's logits
 // loaded ahead: no gain.
 #include <cuda_runtime.h>
@@ -79,7 +80,7 @@ cudaError_t route_launch(const qg_route& r, const float* logits, int64_t stride,
                          int32_t* ids, float* rw, cudaStream_t s) {
   const RouteDeal deal = route_deal(r, E);
   const int per = deal.per;
-  // (16,383 tokens of 256 experts 17.9 us, 19.2 without; 128 14.9 and 15.3; 512 31.5 and 36.2)
+  // (16,383 tokens of 256 experts 17.9 us, 19.1 without; 128 15.5 and 16.0; 512 33.6 and 35.7; 1,024 64.6 and 90.6)
   const bool wide = E == 32 * per && per % 4 == 0 && (reinterpret_cast<uintptr_t>(logits) & 15) == 0 && (ntok == 1 || stride % 4 == 0);
   const auto kern = wide && per == 4    ? route_kernel<4, true>
                     : wide && per == 8  ? route_kernel<8, true>

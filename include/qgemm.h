@@ -255,7 +255,9 @@ qg_status qmoe_router(const float *w_router, const uint16_t *x, int n_expert, in
  * The choice is that of 64-bit arithmetic on the f32 logits and bias; without a bias
  * the experts' order is that of the logits. rw is within 2^-19 of its value. A NaN
  * logit ranks behind every number and is left out of the softmax's sum (where it is
- * chosen all the same, its weight is NaN); infinite logits count as alike.
+ * chosen all the same, its weight is NaN); infinite logits count as alike. A bias or a
+ * logit far below the others' (-1e9, the least f32, -infinity) shuts an expert out, which
+ * costs no time; where there are too few others it is chosen all the same.
  *   n_group: 1..32; top_group: 1..n_group; scale finite (QG_ERR_SHAPE)
  *   topk: 1..32; n_expert: 1..1024, a multiple of n_group; topk <= top_group *
  *   n_expert / n_group, and where top_group < n_group, group_top <= n_expert / n_group
@@ -329,7 +331,8 @@ qg_status qembed(qg_type t, const void *q, const uint16_t *scl, int rows, int k,
  * multiples of 8 elements (QG_ERR_ALIGN). Rows that begin at multiples of 16 bytes, with
  * w so aligned, too, are read and written in wide accesses.
  * sum may be x or add, and y may be x or add where it has their type and sum is
- * elsewhere or NULL, each with the same stride; any other overlap is QG_ERR_ALIAS.
+ * elsewhere or NULL, each with the same stride; any other overlap (of the ranges from
+ * the first to the last element, the gaps between rows included) is QG_ERR_ALIAS.
  * ------------------------------------------------------------------------- */
 #define QG_NORM_MAX 32768
 
