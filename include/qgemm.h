@@ -503,7 +503,8 @@ qg_status qkv_append(const qg_kvcache *cache, const qg_rope *rope, qg_type xt, c
                      const int32_t *pos, int ntok, int32_t *err_flag, cudaStream_t stream);
 
 /* Read tokens back: k_out, v_out [ntok][n_kv_heads][head_dim] of type yt
- * (QG_F16 or QG_F32; f16 rounds q * d once, both round q * d + m once). Keys come as stored (rotated).
+ * (QG_F16 or QG_F32; f16 rounds q * d once, both round q * d + m once; blocks that
+ * reach 65504 can come to 65520 and more, in f16 an infinity). Keys come as stored (rotated).
  * seq, pos as in qkv_append; padding and skipped tokens give zeros. k_out and
  * v_out may each be NULL (not wanted), 16-byte aligned. */
 qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *pos, int ntok,
@@ -532,11 +533,12 @@ qg_status qkv_read(const qg_kvcache *cache, const int32_t *seq, const int32_t *p
  *   ws    : device workspace of at least qattn_workspace_bytes(...) bytes,
  *           16-byte aligned; its contents on entry are ignored.
  * Tokens that a row does not see (padding of the last page, later columns,
- * outside the window) have no effect on it, whatever their bytes hold.
+ * outside the window) have no effect on it, whatever their bytes hold, but that the
+ * scales of those which other rows see are among the scales of the next sentence.
  * Scores, softmax sums and the weighted sum are f32; a weight (times the
  * block's scale for Q8_0, its d for Q4_1) is rounded to f16 before it meets its
  * value: by at most 2^-11 of itself, or 2^-30 of the largest weight (times the
- * largest scale). For Q4_1 q - 8 is what it meets; the weight alone, rounded, meets
+ * largest scale of the sequence's tokens). For Q4_1 q - 8 is what it meets; the weight alone, rounded, meets
  * m + 8 d, rounded to f16, too. y is rounded to f16 once. Results are the same from run to run. The
  * order of the sums depends on lens, window and the sizes, max_pages among
  * them: a column of a wider call need not equal the one-column call bit for
